@@ -339,6 +339,158 @@ sg_status sg_layer_copy_shard(const sg_layer* layer, int r, int what, void* dst,
 /* Release a layer and its device memory (NULL is ignored). */
 void sg_layer_free(sg_layer* layer);
 
+/* ---------------------------------------------------------------------------
+ * Mixture of experts.  A token goes through k of E experts, each a gated MLP
+ * whose layers are sharded over P ranks like any other layer here.  The
+ * router chooses (sg_moe_route) and groups the (token, choice) slots by
+ * expert; the grouped products (sg_experts_*) run every expert's rows in one
+ * launch; sg_moe_combine adds a token's results.  sg_moe_mlp is the chain.
+ *
+ * Grouped rows.  R rows, sorted by expert: rows offsets[e] .. offsets[e + 1] - 1
+ * are expert e's (offsets: E + 1 int32 on the device, not decreasing, NULL
+ * only when E == 1: every row is its).  Rows from offsets[E] on belong to no
+ * expert: they are not read, and outputs of theirs stay as they were.  What
+ * the index arrays hold is not checked on the host; contents outside their
+ * range never lead outside the caller's arrays.
+ * ------------------------------------------------------------------------- */
+typedef struct sg_experts sg_experts; /* opaque, owned by the library */
+
+/* Shard E dense linear layers over P ranks, each by the rules of
+ * sg_shard_linear (mode, segments, P); no bias.
+ *   weight (E, out_dims, in_dims) of dtype SG_BF16 or SG_F16, host or device
+ *   memory.  At most 1024 experts, dimensions below 2^24. */
+sg_status sg_shard_experts(const void* weight, sg_dtype dtype, int64_t E, int64_t out_dims, int64_t in_dims, int mode,
+                           int segments, int P, void* stream, sg_experts** out);
+
+/* The same from MXFP4 weights (sg_quantize_mxfp4's format along the inputs):
+ *   codes (E, out_dims, in_dims / 2), scales (E, out_dims, in_dims / 32) uint8.
+ * in_dims % 32 == 0 and, sharded-to-all, (in_dims / segments / P) % 32 == 0
+ * (SG_ERR_NOT_DIVISIBLE).  E == 1 is a plain MXFP4 layer.  Activations are
+ * bf16, the codes turned into bf16 exactly (unless scale times code leaves
+ * bf16's range), or MXFP4 themselves (a_scales below). */
+sg_status sg_shard_mxfp4_experts(const uint8_t* codes, const uint8_t* scales, int64_t E, int64_t out_dims,
+                                 int64_t in_dims, int mode, int segments, int P, void* stream, sg_experts** out);
+
+/* New weights (E, out_dims, in_dims) into a bf16 or fp16 layer, on the stream;
+ * nothing is allocated when they are in device memory. */
+sg_status sg_experts_update(sg_experts* layer, const void* weight, void* stream);
+
+/* Layer description (any output pointer may be NULL). */
+sg_status sg_experts_info(const sg_experts* layer, int64_t* E, int64_t* out_dims, int64_t* in_dims, int* mode,
+                          int* segments, int* P, sg_dtype* dtype, int* mxfp4);
+void sg_experts_free(sg_experts* layer); /* NULL is ignored */
+
+/* Grouped all-to-sharded product: y_r[m] = x[row(m)] W_{e(m), r}^T.
+ *   x        (T, in_dims) of the layer's dtype (bf16 for MXFP4 layers), row
+ *            stride ldx elements.
+ *   a_scales NULL, or (MXFP4 layers) the scales of MXFP4 activations: x is
+ *            then codes (T, in_dims / 2), a_scales (T, in_dims / 32), packed.
+ *   rows     NULL: row(m) = m; or (R) int32: row(m) = rows[m] / k (a plan's
+ *            slots).  A row outside 0 .. T - 1 reads zeros.
+ *   y        (P, R, n / P): n = out_dims, or with SG_EPI_SWIGLU (segments == 2,
+ *            [W_gate; W_up]) out_dims / 2 and silu(gate) * up, rounded once. */
+sg_status sg_experts_all_to_sharded(const sg_experts* layer, const void* x, const uint8_t* a_scales, int64_t T,
+                                    int64_t ldx, const int32_t* offsets, const int32_t* rows, int k, int64_t R,
+                                    void* y, int epilogue, sg_dtype y_dtype, void* stream);
+
+/* Grouped sharded-to-all product: y[m] = sum over r of h_r[m] W_{e(m), r}^T in
+ * rank order.  h (P, R, in_dims / P) of the layer's dtype, or MXFP4 codes
+ * (P, R, in_dims / P / 2) with h_scales (P, R, in_dims / P / 32); y (R, out_dims). */
+sg_status sg_experts_sharded_to_all(const sg_experts* layer, const void* h, const uint8_t* h_scales,
+                                    const int32_t* offsets, int64_t R, void* y, sg_dtype y_dtype, void* stream);
+
+/* Gradients of the two (bf16 and fp16 layers).
+ *   all-to-sharded: dy (P, R, out_dims / P) -> dx (R, in_dims), one row for
+ *     every grouped row (a token's are added by sg_moe_combine without
+ *     weights), summed over the ranks; dw (E, P, out_dims / P, in_dims), x and
+ *     rows as in the forward call (needed for dw only).
+ *   sharded-to-all: dy (R, out_dims) -> dh (P, R, in_dims / P);
+ *     dw (E, P, out_dims, in_dims / P).
+ * dw of an expert without rows is zero.  dx or dw may be NULL (not both). */
+sg_status sg_experts_all_to_sharded_backward(const sg_experts* layer, const void* x, int64_t T, int64_t ldx,
+                                             const void* dy, const int32_t* offsets, const int32_t* rows, int k,
+                                             int64_t R, void* dx, sg_dtype dx_dtype, void* dw, sg_dtype dw_dtype,
+                                             void* stream);
+sg_status sg_experts_sharded_to_all_backward(const sg_experts* layer, const void* h, const void* dy,
+                                             const int32_t* offsets, int64_t R, void* dh, sg_dtype dh_dtype, void* dw,
+                                             sg_dtype dw_dtype, void* stream);
+
+/* SwiGLU on its own, on rank-local rows [gate; up] (what an all-to-sharded
+ * layer with segments = 2 gives without the epilogue): gu (rows, 2 f) ->
+ * h (rows, f) = silu(gate) * up; dh (rows, f) -> dgu (rows, 2 f).  One dtype. */
+sg_status sg_swiglu(const void* gu, sg_dtype dtype, int64_t rows, int64_t f, void* h, void* stream);
+sg_status sg_swiglu_backward(const void* gu, const void* dh, sg_dtype dtype, int64_t rows, int64_t f, void* dgu,
+                             void* stream);
+
+/* Router.  For every token the k experts of the largest logits, in falling
+ * order, ties to the lowest expert; a logit of -inf (or NaN) closes the expert
+ * to the token, and a token with fewer than k open experts has dropped slots.
+ *   logits   (T, E) of dtype, row stride ld; E <= 1024, k <= 16.
+ *   weights  (T, k) fp32: the softmax over the token's open experts, with
+ *            normalize over its chosen ones; 0 for a dropped slot.
+ *   experts  (T, k) int32, -1 for a dropped slot.
+ * and the plan, slot s = t k + j:
+ *   offsets  (E + 1): the grouped rows of each expert.
+ *   rows     (T k): the slot of each grouped row, in slot order for each
+ *            expert; -1 behind the last.
+ *   slots    (T, k): the grouped row of each slot, -1 if dropped.
+ *   workspace sg_moe_route_workspace(T, E, k) bytes, no initial contents. */
+sg_status sg_moe_route(const void* logits, int64_t ld, sg_dtype dtype, int64_t T, int E, int k, int normalize,
+                       float* weights, int32_t* experts, int32_t* offsets, int32_t* rows, int32_t* slots,
+                       void* workspace, size_t ws_bytes, void* stream);
+size_t sg_moe_route_workspace(int64_t T, int E, int k);
+
+/* Its gradient: dweights (T, k) fp32 -> dlogits (T, E) of dtype, packed; 0 for
+ * closed experts.  weights and experts as sg_moe_route gave them; logits may
+ * be NULL with normalize. */
+sg_status sg_moe_route_backward(const void* logits, int64_t ld, sg_dtype dtype, int64_t T, int E, int k, int normalize,
+                                const float* weights, const int32_t* experts, const float* dweights, void* dlogits,
+                                void* stream);
+
+/* out[t] (T, D) = sum over j of weights[t][j] * y[slots[t][j]], in choice order,
+ * fp32, rounded once.  y (R, D); weights NULL: 1; slots outside 0 .. R - 1 are
+ * left out; k <= 16. */
+sg_status sg_moe_combine(const void* y, sg_dtype y_dtype, int64_t R, const int32_t* slots, const float* weights,
+                         int64_t T, int k, int64_t D, void* out, sg_dtype out_dtype, void* stream);
+
+/* Its gradient, dout, y and dy of one dtype: dy (R, D), dy[slots[t][j]] =
+ * weights[t][j] * dout[t], rows of no slot left as they were; dweights (T, k)
+ * fp32 = <dout[t], y[slots[t][j]]>, 0 for a slot left out.  Either may be NULL
+ * (not both).  A row may stand in slots once. */
+sg_status sg_moe_combine_backward(const void* dout, const void* y, sg_dtype dtype, int64_t R, const int32_t* slots,
+                                  const float* weights, int64_t T, int k, int64_t D, void* dy, float* dweights,
+                                  void* stream);
+
+/* The gated MLP over experts: y[t] = sum over t's slots of weight times
+ * down_e(silu(x[t] W_gate,e^T) * (x[t] W_up,e^T)).  h is stored in the layers'
+ * dtype, the down layer's rows in fp32; bitwise the chain of
+ * sg_experts_all_to_sharded (SWIGLU), sg_experts_sharded_to_all (fp32 y) and
+ * sg_moe_combine.
+ *   gate_up all-to-sharded with segments = 2, down sharded-to-all with
+ *   segments = 1, of one E, P and dtype (both MXFP4, or both not).
+ *   x (T, in_dims), row stride ldx; weights, offsets, rows, slots: a plan of
+ *   T tokens and k choices; y (T, out_dims of down).
+ *   workspace sg_moe_mlp_workspace(...) bytes, 16-byte aligned, no initial
+ *   contents; calls that share it must not overlap. */
+sg_status sg_moe_mlp(const sg_experts* gate_up, const sg_experts* down, const void* x, int64_t T, int64_t ldx,
+                     const float* weights, const int32_t* offsets, const int32_t* rows, const int32_t* slots, int k,
+                     void* y, sg_dtype y_dtype, void* workspace, size_t ws_bytes, void* stream);
+size_t sg_moe_mlp_workspace(const sg_experts* gate_up, const sg_experts* down, int64_t T, int k);
+
+/* MXFP4 (OCP Microscaling): blocks of 32 values share one E8M0 scale byte s,
+ * each value an E2M1 code (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign bit), worth
+ * code * 2^(s - 127).  Quantisation: s - 127 = floor(log2 max|x|) - 2, within
+ * -127 .. 127 (a block of zeros: -127); codes round to nearest even, above 6
+ * to 6; a block holding an infinity or a NaN: s = 255 (NaN), codes 0.
+ *   x (rows, cols) of dtype, row stride ldx; cols % 32 == 0.
+ *   codes (rows, cols / 2), value 2i of a row in the low half of byte i;
+ *   scales (rows, cols / 32). */
+sg_status sg_quantize_mxfp4(const void* x, sg_dtype dtype, int64_t rows, int64_t cols, int64_t ldx, uint8_t* codes,
+                            uint8_t* scales, void* stream);
+/* The values it stands for, rounded to dtype (exact in fp32); x packed. */
+sg_status sg_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, void* x,
+                              sg_dtype dtype, void* stream);
+
 /* Profiling: arm two hipEvent_t (created with timing enabled; either may be
  * NULL) for the next kernel this thread launches through the library, which
  * records start_event when that kernel begins and stop_event when it ends

@@ -17,6 +17,15 @@ kernels.  The entry points mirror include/shardgemm.h one to one:
     sharded_to_all_backward    sg_sharded_to_all_backward (sharded dx, dw)
     summa_matmul               sg_summa_matmul (+ sg_summa_workspace)
     summa_backward             sg_summa_backward (Matmul_ABT_2D / Matmul_ATB_2D)
+    shard_experts              sg_shard_experts; Experts.update: sg_experts_update
+    shard_mxfp4_experts        sg_shard_mxfp4_experts
+    experts_all_to_sharded     sg_experts_all_to_sharded (+ _backward)
+    experts_sharded_to_all     sg_experts_sharded_to_all (+ _backward)
+    swiglu                     sg_swiglu (+ _backward)
+    moe_route                  sg_moe_route (+ _backward): top-k experts and the grouping plan
+    moe_combine                sg_moe_combine (+ _backward): the weighted sum over a token's experts
+    moe_mlp                    sg_moe_mlp (+ sg_moe_mlp_workspace)
+    quantize_mxfp4             sg_quantize_mxfp4; dequantize_mxfp4: sg_dequantize_mxfp4
     Layer.info / Layer.shard   sg_layer_info / sg_layer_copy_shard
     time_next_launch           sg_time_next_launch (profiling)
 
@@ -27,6 +36,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -92,6 +102,26 @@ def lib():
             "sg_layer_info": ([P, P, P, P, P, P, P, P], I),
             "sg_layer_copy_shard": ([P, I, I, P, SZ, P], I),
             "sg_layer_free": ([P], None),
+            "sg_shard_experts": ([P, I, I64, I64, I64, I, I, I, P, PP], I),
+            "sg_shard_mxfp4_experts": ([P, P, I64, I64, I64, I, I, I, P, PP], I),
+            "sg_experts_update": ([P, P, P], I),
+            "sg_experts_info": ([P, P, P, P, P, P, P, P, P], I),
+            "sg_experts_free": ([P], None),
+            "sg_experts_all_to_sharded": ([P, P, P, I64, I64, P, P, I, I64, P, I, I, P], I),
+            "sg_experts_sharded_to_all": ([P, P, P, P, I64, P, I, P], I),
+            "sg_experts_all_to_sharded_backward": ([P, P, I64, I64, P, P, P, I, I64, P, I, P, I, P], I),
+            "sg_experts_sharded_to_all_backward": ([P, P, P, P, I64, P, I, P, I, P], I),
+            "sg_swiglu": ([P, I, I64, I64, P, P], I),
+            "sg_swiglu_backward": ([P, P, I, I64, I64, P, P], I),
+            "sg_moe_route": ([P, I64, I, I64, I, I, I, P, P, P, P, P, P, SZ, P], I),
+            "sg_moe_route_workspace": ([I64, I, I], SZ),
+            "sg_moe_route_backward": ([P, I64, I, I64, I, I, I, P, P, P, P, P], I),
+            "sg_moe_combine": ([P, I, I64, P, P, I64, I, I64, P, I, P], I),
+            "sg_moe_combine_backward": ([P, P, I, I64, P, P, I64, I, I64, P, P, P], I),
+            "sg_moe_mlp": ([P, P, P, I64, I64, P, P, P, P, I, P, I, P, SZ, P], I),
+            "sg_moe_mlp_workspace": ([P, P, I64, I], SZ),
+            "sg_quantize_mxfp4": ([P, I, I64, I64, I64, P, P, P], I),
+            "sg_dequantize_mxfp4": ([P, P, I64, I64, P, I, P], I),
             "sg_time_next_launch": ([P, P], I),
             "sg_last_error": ([], C.c_char_p),
         }
@@ -418,3 +448,376 @@ def summa_matmul(X: torch.Tensor, A: torch.Tensor, q: int, out: torch.Tensor | N
     _check(lib().sg_summa_matmul(_ptr(X), _ptr(A), _DT.get(X.dtype, -1), M, K, N, q, _ptr(out), int(accumulate),
                                  int(fused), ws_ptr, ws_bytes, _stream(X.device)))
     return out
+
+
+# ---- mixture of experts and MXFP4 -------------------------------------------
+# These calls run on the device of their tensors, whatever device is current,
+# on that device's current stream; workspaces come from torch's caching
+# allocator for each call, so calls on several streams, and captured graphs,
+# never share one.
+
+class Route(NamedTuple):
+    """A router's choices and the plan that groups its slots by expert (sg_moe_route)."""
+    weights: torch.Tensor   # (T, k) fp32
+    experts: torch.Tensor   # (T, k) int32, -1: dropped
+    offsets: torch.Tensor   # (E + 1) int32
+    rows: torch.Tensor      # (T k) int32, -1 behind the last
+    slots: torch.Tensor     # (T, k) int32, -1: dropped
+
+
+def _bad(message: str):
+    raise ShardGemmError(ERR_INVALID_ARG, message)
+
+
+def _want(t, name: str, shape=None, dtype=None, device=None, optional=False):
+    """One tensor argument: packed, of the shape (None: any extent), dtype and device asked for."""
+    if t is None:
+        if not optional:
+            _bad(f"{name} is None")
+        return None
+    if shape is not None and (t.dim() != len(shape) or any(w is not None and w != h for w, h in zip(shape, t.shape))):
+        _bad(f"{name} has shape {tuple(t.shape)}, not {tuple('any' if w is None else w for w in shape)}")
+    if dtype is not None and t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        _bad(f"{name} has dtype {t.dtype}")
+    if t.device.type != "cuda":
+        _bad(f"{name} is on {t.device}, not on a GPU")
+    if device is not None and t.device != device:
+        _bad(f"{name} is on {t.device}, not on {device}")
+    if not t.is_contiguous():
+        _bad(f"{name} is not contiguous")
+    return t
+
+
+def _matrix(t, name: str, width=None, dtype=None, device=None):
+    """A (rows, width) argument whose rows may be strided: the tensor and its row stride."""
+    if t.dim() != 2 or (width is not None and t.shape[1] != width):
+        _bad(f"{name} has shape {tuple(t.shape)}, not (any, {width})")
+    if dtype is not None and t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        _bad(f"{name} has dtype {t.dtype}")
+    if t.device.type != "cuda" or (device is not None and t.device != device):
+        _bad(f"{name} is on {t.device}, not on {device or 'a GPU'}")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1 or rows > 1 and t.stride(0) < cols:
+        _bad(f"{name} has strides {t.stride()}: its columns must be adjacent and its rows apart")
+    return t, (t.stride(0) if rows > 1 else cols)
+
+
+def _out(out, name: str, shape, dtype, device):
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return _want(out, name, shape, tuple(_DT), device)
+
+
+_FLOATS = tuple(_DT)
+
+
+class Experts:
+    """E sharded linear layers owned by the library (sg_experts*)."""
+
+    def __init__(self, handle: C.c_void_p, device: torch.device):
+        self._h = handle
+        self.device = device
+        e, o, i = C.c_int64(), C.c_int64(), C.c_int64()
+        m, s, p, d, q = C.c_int(), C.c_int(), C.c_int(), C.c_int(), C.c_int()
+        _check(lib().sg_experts_info(handle, C.byref(e), C.byref(o), C.byref(i), C.byref(m), C.byref(s), C.byref(p),
+                                     C.byref(d), C.byref(q)))
+        self.E, self.out_dims, self.in_dims = e.value, o.value, i.value
+        self.mode, self.segments, self.P = m.value, s.value, p.value
+        self.dtype = _TORCH_DT[d.value]
+        self.mx = bool(q.value)
+
+    @property
+    def handle(self):
+        if self._h is None:
+            _bad("the layer has been freed")
+        return self._h
+
+    def update(self, weight: torch.Tensor):
+        """New weights (E, out, in) into the layer, on the current stream."""
+        _want(weight, "weight", (self.E, self.out_dims, self.in_dims), self.dtype, self.device)
+        with torch.cuda.device(self.device):
+            _check(lib().sg_experts_update(self.handle, _ptr(weight), _stream(self.device)))
+
+    def free(self):
+        if self._h is not None and _lib is not None:
+            _lib.sg_experts_free(self._h)
+        self._h = None
+
+    def __del__(self):
+        try:
+            self.free()
+        except Exception:
+            pass
+
+
+def _experts(make, device) -> Experts:
+    device = device if device.type == "cuda" else torch.device("cuda", torch.cuda.current_device())
+    h = C.c_void_p()
+    with torch.cuda.device(device):
+        _check(make(_stream(device), C.byref(h)))
+    return Experts(h, device)
+
+
+def shard_experts(weight: torch.Tensor, sharding, segments: int = 1, P: int = 1) -> Experts:
+    """Shard E dense weights (E, out, in) over P ranks (sg_shard_experts)."""
+    if weight.dim() != 3:
+        _bad(f"weight has shape {tuple(weight.shape)}, not (E, out, in)")
+    E, o, i = weight.shape
+    weight = weight.contiguous()
+    return _experts(lambda s, h: lib().sg_shard_experts(_ptr(weight), _DT.get(weight.dtype, -1), E, o, i,
+                                                        _mode(sharding), segments, P, s, h), weight.device)
+
+
+def shard_mxfp4_experts(codes: torch.Tensor, scales: torch.Tensor, sharding, segments: int = 1, P: int = 1) -> Experts:
+    """Shard E MXFP4 weights (sg_shard_mxfp4_experts): codes (E, out, in / 2),
+    scales (E, out, in / 32) uint8, as quantize_mxfp4 gives them for (E, out, in)."""
+    if codes.dim() != 3 or scales.dim() != 3 or codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+        _bad("codes and scales must be (E, out, in / 2) and (E, out, in / 32) uint8")
+    E, o, half = codes.shape
+    if scales.shape != (E, o, half * 2 // 32) or codes.device != scales.device:
+        _bad(f"scales has shape {tuple(scales.shape)} for codes of shape {tuple(codes.shape)}")
+    codes, scales = codes.contiguous(), scales.contiguous()
+    return _experts(lambda s, h: lib().sg_shard_mxfp4_experts(_ptr(codes), _ptr(scales), E, o, half * 2,
+                                                              _mode(sharding), segments, P, s, h), codes.device)
+
+
+def _grouped(layer: Experts, offsets, rows, R):
+    _want(offsets, "offsets", (layer.E + 1,), torch.int32, layer.device, optional=layer.E == 1)
+    _want(rows, "rows", (R,), torch.int32, layer.device, optional=True)
+
+
+def experts_all_to_sharded(layer: Experts, x: torch.Tensor, offsets=None, rows=None, k: int = 1, swiglu: bool = False,
+                           x_scales=None, out_dtype=None, out: torch.Tensor | None = None) -> torch.Tensor:
+    """x (T, in) -> (P, R, n / P), rows grouped by expert (sg_experts_all_to_sharded);
+    n = out_dims, or out_dims / 2 with the SwiGLU epilogue.
+
+    rows: None (R = T, row m is x[m]) or the plan's slots, row m is x[rows[m] // k].
+    x_scales: x is MXFP4 codes (T, in / 2) with these scales (T, in / 32)."""
+    dev = layer.device
+    if x_scales is None:
+        x, ld = _matrix(x, "x", layer.in_dims, layer.dtype, dev)
+    else:
+        _want(x, "x", (None, layer.in_dims // 2), torch.uint8, dev)
+        _want(x_scales, "x_scales", (x.shape[0], layer.in_dims // 32), torch.uint8, dev)
+        ld = layer.in_dims
+    R = x.shape[0] if rows is None else rows.shape[0]
+    _grouped(layer, offsets, rows, R)
+    n = layer.out_dims // 2 if swiglu else layer.out_dims
+    out = _out(out, "out", (layer.P, R, n // layer.P), out_dtype or layer.dtype, dev)
+    with torch.cuda.device(dev):
+        _check(lib().sg_experts_all_to_sharded(layer.handle, _ptr(x), _ptr(x_scales), x.shape[0], ld, _ptr(offsets),
+                                               _ptr(rows), k, R, _ptr(out), EPI_SWIGLU if swiglu else EPI_NONE,
+                                               _DT[out.dtype], _stream(dev)))
+    return out
+
+
+def experts_sharded_to_all(layer: Experts, h: torch.Tensor, offsets=None, h_scales=None, out_dtype=None,
+                           out: torch.Tensor | None = None) -> torch.Tensor:
+    """h (P, R, in / P) -> (R, out): the ranks' partial sums added in rank order
+    (sg_experts_sharded_to_all).  h_scales: h is MXFP4 codes (P, R, in / P / 2)."""
+    dev, kr = layer.device, layer.in_dims // layer.P
+    if h_scales is None:
+        _want(h, "h", (layer.P, None, kr), layer.dtype, dev)
+    else:
+        _want(h, "h", (layer.P, None, kr // 2), torch.uint8, dev)
+        _want(h_scales, "h_scales", (layer.P, h.shape[1], kr // 32), torch.uint8, dev)
+    R = h.shape[1]
+    _grouped(layer, offsets, None, R)
+    out = _out(out, "out", (R, layer.out_dims), out_dtype or layer.dtype, dev)
+    with torch.cuda.device(dev):
+        _check(lib().sg_experts_sharded_to_all(layer.handle, _ptr(h), _ptr(h_scales), _ptr(offsets), R, _ptr(out),
+                                               _DT[out.dtype], _stream(dev)))
+    return out
+
+
+def experts_all_to_sharded_backward(layer: Experts, x: torch.Tensor | None, dy: torch.Tensor, offsets=None, rows=None,
+                                    k: int = 1, need_dx: bool = True, need_dw: bool = True, dx_dtype=None,
+                                    dw_dtype=torch.float32):
+    """dy (P, R, out / P) -> (dx (R, in), one row for every grouped row,
+    dw (E, P, out / P, in)); either may be skipped (None)."""
+    dev, n = layer.device, layer.out_dims // layer.P
+    _want(dy, "dy", (layer.P, None, n), layer.dtype, dev)
+    R, T, ld = dy.shape[1], 0, layer.in_dims
+    if need_dw:
+        x, ld = _matrix(x, "x", layer.in_dims, layer.dtype, dev)
+        T = x.shape[0]
+    _grouped(layer, offsets, rows, R)
+    dx = torch.empty((R, layer.in_dims), dtype=dx_dtype or layer.dtype, device=dev) if need_dx else None
+    dw = torch.empty((layer.E, layer.P, n, layer.in_dims), dtype=dw_dtype, device=dev) if need_dw else None
+    with torch.cuda.device(dev):
+        _check(lib().sg_experts_all_to_sharded_backward(
+            layer.handle, _ptr(x) if need_dw else None, T, ld, _ptr(dy), _ptr(offsets), _ptr(rows), k, R, _ptr(dx),
+            _DT.get(dx_dtype or layer.dtype, -1), _ptr(dw), _DT.get(dw_dtype, -1), _stream(dev)))
+    return dx, dw
+
+
+def experts_sharded_to_all_backward(layer: Experts, h: torch.Tensor | None, dy: torch.Tensor, offsets=None,
+                                    need_dx: bool = True, need_dw: bool = True, dx_dtype=None,
+                                    dw_dtype=torch.float32):
+    """dy (R, out) -> (dh (P, R, in / P), dw (E, P, out, in / P)); either may be skipped (None)."""
+    dev, kr = layer.device, layer.in_dims // layer.P
+    _want(dy, "dy", (None, layer.out_dims), layer.dtype, dev)
+    R = dy.shape[0]
+    if need_dw:
+        _want(h, "h", (layer.P, R, kr), layer.dtype, dev)
+    _grouped(layer, offsets, None, R)
+    dh = torch.empty((layer.P, R, kr), dtype=dx_dtype or layer.dtype, device=dev) if need_dx else None
+    dw = torch.empty((layer.E, layer.P, layer.out_dims, kr), dtype=dw_dtype, device=dev) if need_dw else None
+    with torch.cuda.device(dev):
+        _check(lib().sg_experts_sharded_to_all_backward(
+            layer.handle, _ptr(h) if need_dw else None, _ptr(dy), _ptr(offsets), R, _ptr(dh),
+            _DT.get(dx_dtype or layer.dtype, -1), _ptr(dw), _DT.get(dw_dtype, -1), _stream(dev)))
+    return dh, dw
+
+
+def swiglu(gu: torch.Tensor) -> torch.Tensor:
+    """(..., 2 f) rows [gate; up] -> (..., f) silu(gate) * up (sg_swiglu)."""
+    _want(gu, "gu", None, _FLOATS)
+    if gu.dim() < 1 or gu.shape[-1] % 2 or gu.shape[-1] == 0:
+        _bad(f"gu has shape {tuple(gu.shape)}: its rows must be [gate; up]")
+    f = gu.shape[-1] // 2
+    h = torch.empty((*gu.shape[:-1], f), dtype=gu.dtype, device=gu.device)
+    with torch.cuda.device(gu.device):
+        _check(lib().sg_swiglu(_ptr(gu), _DT[gu.dtype], gu.numel() // (2 * f), f, _ptr(h), _stream(gu.device)))
+    return h
+
+
+def swiglu_backward(gu: torch.Tensor, dh: torch.Tensor) -> torch.Tensor:
+    """Gradient of swiglu: dh (..., f) -> dgu (..., 2 f) (sg_swiglu_backward)."""
+    _want(gu, "gu", None, _FLOATS)
+    if gu.dim() < 1 or gu.shape[-1] % 2 or gu.shape[-1] == 0:
+        _bad(f"gu has shape {tuple(gu.shape)}: its rows must be [gate; up]")
+    f = gu.shape[-1] // 2
+    _want(dh, "dh", (*gu.shape[:-1], f), gu.dtype, gu.device)
+    dgu = torch.empty_like(gu)
+    with torch.cuda.device(gu.device):
+        _check(lib().sg_swiglu_backward(_ptr(gu), _ptr(dh), _DT[gu.dtype], gu.numel() // (2 * f), f, _ptr(dgu),
+                                        _stream(gu.device)))
+    return dgu
+
+
+def moe_route(logits: torch.Tensor, k: int, normalize: bool = True) -> Route:
+    """The k experts of every token and the plan that groups the slots
+    (sg_moe_route).  logits (T, E), -inf where an expert is closed to a token."""
+    logits, ld = _matrix(logits, "logits", None, _FLOATS)
+    T, E = logits.shape
+    dev = logits.device
+    need = int(lib().sg_moe_route_workspace(T, E, k))
+    n = max(T * k, 0)
+    buf = torch.empty((4 * n + E + 1 + need // 4,), dtype=torch.int32, device=dev)
+    w = buf[:n].view(torch.float32).view(T, -1) if n else buf.new_empty((T, max(k, 0)), dtype=torch.float32)
+    e, rows, slots = buf[n:2 * n].view(w.shape), buf[2 * n:3 * n], buf[3 * n:4 * n].view(w.shape)
+    offsets, ws = buf[4 * n:4 * n + E + 1], buf[4 * n + E + 1:]
+    with torch.cuda.device(dev):
+        _check(lib().sg_moe_route(_ptr(logits), ld, _DT[logits.dtype], T, E, k, int(normalize), _ptr(w), _ptr(e),
+                                  _ptr(offsets), _ptr(rows), _ptr(slots), _ptr(ws), need, _stream(dev)))
+    return Route(w, e, offsets, rows, slots)
+
+
+def moe_route_backward(logits: torch.Tensor, route: Route, dweights: torch.Tensor,
+                       normalize: bool = True) -> torch.Tensor:
+    """Gradient of the router's weights: dweights (T, k) -> dlogits (T, E) (sg_moe_route_backward)."""
+    logits, ld = _matrix(logits, "logits", None, _FLOATS)
+    T, E = logits.shape
+    dev = logits.device
+    k = route.weights.shape[-1]
+    _want(route.weights, "weights", (T, k), torch.float32, dev)
+    _want(route.experts, "experts", (T, k), torch.int32, dev)
+    _want(dweights, "dweights", (T, k), torch.float32, dev)
+    dz = torch.empty((T, E), dtype=logits.dtype, device=dev)
+    with torch.cuda.device(dev):
+        _check(lib().sg_moe_route_backward(_ptr(logits), ld, _DT[logits.dtype], T, E, k, int(normalize),
+                                           _ptr(route.weights), _ptr(route.experts), _ptr(dweights), _ptr(dz),
+                                           _stream(dev)))
+    return dz
+
+
+def moe_combine(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor | None = None, out_dtype=None,
+                out: torch.Tensor | None = None) -> torch.Tensor:
+    """(R, D) grouped rows -> (T, D): each token's rows, weighted and added
+    (sg_moe_combine).  weights None: 1."""
+    _want(y, "y", (None, None), _FLOATS)
+    dev = y.device
+    _want(slots, "slots", (None, None), torch.int32, dev)
+    T, k = slots.shape
+    _want(weights, "weights", (T, k), torch.float32, dev, optional=True)
+    out = _out(out, "out", (T, y.shape[1]), out_dtype or y.dtype, dev)
+    with torch.cuda.device(dev):
+        _check(lib().sg_moe_combine(_ptr(y), _DT[y.dtype], y.shape[0], _ptr(slots), _ptr(weights), T, k, y.shape[1],
+                                    _ptr(out), _DT[out.dtype], _stream(dev)))
+    return out
+
+
+def moe_combine_backward(dout: torch.Tensor, y: torch.Tensor, slots: torch.Tensor,
+                         weights: torch.Tensor | None = None, need_dy: bool = True, need_dweights: bool = True,
+                         dy: torch.Tensor | None = None):
+    """Gradient of moe_combine: dout (T, D) -> (dy (R, D), dweights (T, k));
+    either may be skipped (None).  Rows of no slot are left as they were in a
+    caller's dy, and are zero in a new one."""
+    _want(dout, "dout", (None, None), _FLOATS)
+    dev, (T, D) = dout.device, dout.shape
+    _want(y, "y", (None, D), dout.dtype, dev)
+    _want(slots, "slots", (T, None), torch.int32, dev)
+    k = slots.shape[1]
+    _want(weights, "weights", (T, k), torch.float32, dev, optional=True)
+    if need_dy:
+        dy = torch.zeros_like(y) if dy is None else _want(dy, "dy", tuple(y.shape), y.dtype, dev)
+    else:
+        dy = None
+    dw = torch.empty((T, k), dtype=torch.float32, device=dev) if need_dweights else None
+    with torch.cuda.device(dev):
+        _check(lib().sg_moe_combine_backward(_ptr(dout), _ptr(y), _DT[y.dtype], y.shape[0], _ptr(slots),
+                                             _ptr(weights), T, k, D, _ptr(dy), _ptr(dw), _stream(dev)))
+    return dy, dw
+
+
+def moe_mlp(gate_up: Experts, down: Experts, x: torch.Tensor, route: Route, out_dtype=None,
+            out: torch.Tensor | None = None) -> torch.Tensor:
+    """The gated MLP over experts: (T, in) -> (T, out) (sg_moe_mlp)."""
+    dev = gate_up.device
+    x, ld = _matrix(x, "x", gate_up.in_dims, gate_up.dtype, dev)
+    T, k = x.shape[0], route.slots.shape[-1]
+    _want(route.weights, "weights", (T, k), torch.float32, dev)
+    _want(route.slots, "slots", (T, k), torch.int32, dev)
+    _want(route.rows, "rows", (T * k,), torch.int32, dev)
+    _want(route.offsets, "offsets", (gate_up.E + 1,), torch.int32, dev)
+    out = _out(out, "out", (T, down.out_dims), out_dtype or down.dtype, dev)
+    need = int(lib().sg_moe_mlp_workspace(gate_up.handle, down.handle, T, k))
+    ws = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
+    with torch.cuda.device(dev):
+        _check(lib().sg_moe_mlp(gate_up.handle, down.handle, _ptr(x), T, ld, _ptr(route.weights), _ptr(route.offsets),
+                                _ptr(route.rows), _ptr(route.slots), k, _ptr(out), _DT[out.dtype], _ptr(ws), need,
+                                _stream(dev)))
+    return out
+
+
+def quantize_mxfp4(x: torch.Tensor):
+    """(..., n) values -> MXFP4 codes (..., n / 2) and scales (..., n / 32), uint8 (sg_quantize_mxfp4)."""
+    if x.dim() < 1:
+        _bad("x has no columns")
+    if x.dim() == 2:
+        m, ld = _matrix(x, "x", None, _FLOATS)
+    else:
+        m, ld = _want(x, "x", None, _FLOATS), x.shape[-1]
+    n = x.shape[-1]
+    rows = x.numel() // n if n else 0
+    codes = torch.empty((*x.shape[:-1], n // 2), dtype=torch.uint8, device=x.device)
+    scales = torch.empty((*x.shape[:-1], n // 32), dtype=torch.uint8, device=x.device)
+    with torch.cuda.device(x.device):
+        _check(lib().sg_quantize_mxfp4(_ptr(m), _DT[x.dtype], rows, n, ld, _ptr(codes), _ptr(scales),
+                                       _stream(x.device)))
+    return codes, scales
+
+
+def dequantize_mxfp4(codes: torch.Tensor, scales: torch.Tensor, out_dtype=torch.float32) -> torch.Tensor:
+    """The values that codes (..., n / 2) and scales (..., n / 32) stand for (sg_dequantize_mxfp4)."""
+    _want(codes, "codes", None, torch.uint8)
+    if codes.dim() < 1:
+        _bad("codes has no columns")
+    n = codes.shape[-1] * 2
+    _want(scales, "scales", (*codes.shape[:-1], n // 32), torch.uint8, codes.device)
+    x = torch.empty((*codes.shape[:-1], n), dtype=out_dtype, device=codes.device)
+    with torch.cuda.device(codes.device):
+        _check(lib().sg_dequantize_mxfp4(_ptr(codes), _ptr(scales), x.numel() // n if n else 0, n, _ptr(x),
+                                         _DT.get(out_dtype, -1), _stream(codes.device)))
+    return x

@@ -318,6 +318,8 @@ void set_weights(sg::Problem& p, const sg_layer* l) {
 
 }  // namespace
 
+std::string& sg::last_error() { return g_err; }
+
 extern "C" {
 
 const char* sg_last_error(void) { return g_err.c_str(); }

@@ -1,0 +1,188 @@
+// Mixture-of-experts products: what the entry points (experts_api.hip) hand to
+// the grouped kernels (experts.hip, experts_dw.hip).
+#pragma once
+
+#include "internal.h"
+
+namespace sg {
+
+// ---------------------------------------------------------------------------
+// One grouped product.  The rows m = 0 .. R-1 come grouped by expert: rows
+// offsets[e] .. offsets[e+1] - 1 belong to expert e (offsets null: E == 1 and
+// every row is its).  For a row m of expert e
+//
+//   out[m][n] = sum_s sum_{k < kl} A_s[row(m)][k] W_e[n][s kpad + k]
+//
+//  * A_s: segment s of the input, part s % a_pieces (each kl columns) of rank
+//    s / a_pieces, whose rows start at A + rank * a_rank elements, row stride
+//    lda; row(m) = m, or rows[m] / kdiv with a gather map (an index
+//    outside 0 .. T-1 reads zeros).  Rows are read below T.
+//  * W_e: fragment-major, 16-row blocks of `wsteps` steps: 16-bit weights,
+//    32 inputs a step (frag_offset); MXFP4 weights, 128 inputs a step
+//    (mx4_offset, mx4_scale_offset).  A segment's inputs are padded with zero
+//    weights to kpad, a multiple of 128 (MXFP4) or 64.
+//  * transposed (dx of the layer): W_e's rows are the contracted dimension:
+//    out[m][n] = sum_s sum_{k < kl} A_s[m][k] W_e[s kpad + k][n], kpad a
+//    multiple of 16 and segment s stored in rows s kpad .. + kl.
+//  * Output columns come in 16-column blocks: block b lies in piece b / bps at
+//    column 16 (b % bps) of its f columns; piece i is part i % S of rank i / S.
+//    Rank r's columns start at out + r * o_rank, row stride ldo.
+//  * swiglu: pieces 2r and 2r + 1 are rank r's gate and up rows; output block b
+//    is block b % bps of rank b / bps.
+// Rows behind offsets[E] are not written.
+// ---------------------------------------------------------------------------
+enum GroupedMode { G_BF16 = 0, G_F16 = 1, G_MX4 = 2, G_MX4A4 = 3 };
+
+struct Grouped {
+    int mode;  // GroupedMode: 16-bit x 16-bit, MXFP4 weights x bf16, MXFP4 x MXFP4
+    const void* A;
+    const uint8_t* a_scales;  // G_MX4A4: E8M0, one per 32 inputs, row stride kl / 32
+    int64_t lda, a_rank;      // elements
+    int a_pieces, nseg, kl, kpad;
+    const int32_t* offsets;
+    const int32_t* rows;
+    int kdiv, T, R, E;
+    const uint8_t* W;
+    int64_t w_expert;  // bytes from one expert's weights to the next
+    const uint8_t* wsc;
+    int64_t wsc_expert;
+    int wblocks, wsteps;  // 16-row blocks, steps a block
+    int transposed, swiglu;
+    int bps, f, S, nout;  // output blocks (of pairs with swiglu): nout
+    void* out;
+    int out_dtype;
+    int64_t ldo, o_rank;
+    int vec;  // rows of the output take 4-column vector stores
+};
+
+// Codes of an MXFP4 layer: the 16-row x 128-input block (block b, step st) is
+// 1 KB, lane l owning 16 bytes: the 32 codes of row l & 15, inputs 128 st + 32
+// (l >> 4) .. + 31, which is one scale block and its operand of one
+// v_mfma_scale_f32_16x16x128; input 2i in the low half of byte i.
+__host__ __device__ inline int64_t mx4_offset(int64_t block, int64_t st, int64_t nsteps) {
+    return (block * nsteps + st) * 1024;
+}
+// Their scales: for a 16-row block and a run of four steps 256 bytes, lane l's
+// four (one a step) adjacent.
+__host__ __device__ inline int64_t mx4_scale_runs(int64_t nsteps) { return (nsteps + 3) / 4; }
+__host__ __device__ inline int64_t mx4_scale_offset(int64_t block, int64_t st, int lane, int64_t nsteps) {
+    return ((block * mx4_scale_runs(nsteps) + (st >> 2)) * 64 + lane) * 4 + (st & 3);
+}
+
+// workgroups of 256 threads that one launch may have (2^32 threads)
+constexpr int64_t kMaxBlocks = 1 << 24;
+// hipErrorInvalidConfiguration: more workgroups than a launch may have
+hipError_t launch_grouped(const Grouped& p, hipStream_t s);
+
+// Weight gradients of a grouped layer: out[e][r][o][i] = sum over expert e's
+// rows m of G_r[m][o] X_r[row(m)][i]; zeros for an expert without rows.
+struct GroupedDw {
+    int f16;
+    const void* G;
+    int64_t ldg, g_rank;
+    const void* X;
+    int64_t ldx, x_rank;
+    const int32_t* offsets;
+    const int32_t* rows;
+    int kdiv, T, R, E, P, O, I;
+    void* out;
+    int out_dtype;
+    int vec;  // rows of the output take 4-column vector stores
+};
+hipError_t launch_grouped_dw(const GroupedDw& p, hipStream_t s);
+
+// Row-major expert weights -> the kernels' layout.
+struct ExpertsLayout {
+    int mode, S, P;       // sg_mode, segments, ranks
+    int64_t E, out, in;   // the unsharded layer
+    int64_t f, bps;       // columns and 16-row blocks of a piece (all-to-sharded: out / S / P; else out)
+    int64_t kl, kpad;     // inputs of a segment, padded
+    int64_t blocks, steps;
+};
+hipError_t experts_pack(void* dst, const void* src, const ExpertsLayout& l, hipStream_t s);
+hipError_t experts_pack_mx4(uint8_t* codes, uint8_t* scales, const uint8_t* src_codes, const uint8_t* src_scales,
+                            const ExpertsLayout& l, hipStream_t s);
+
+// Routing (route.hip)
+struct Route {
+    const void* logits;
+    int64_t ld;
+    int dtype, T, E, k, normalize;
+    float* weights;
+    int32_t *experts, *offsets, *rows, *slots;
+    int32_t* ws;
+};
+constexpr int kRouteMaxExperts = 1024, kRouteMaxK = 16;
+size_t route_workspace_ints(int64_t T, int E, int k);
+hipError_t launch_route(const Route& r, hipStream_t s);
+hipError_t launch_route_backward(const Route& r, const float* dweights, void* dlogits, int64_t ldd, hipStream_t s);
+hipError_t launch_combine(const void* y, int y_dtype, const int32_t* slots, const float* weights, int64_t T, int k,
+                          int64_t D, int64_t R, void* out, int out_dtype, hipStream_t s);
+hipError_t launch_combine_backward(const void* dout, const void* y, int dtype, const int32_t* slots,
+                                   const float* weights, int64_t T, int k, int64_t D, int64_t R, void* dy, float* dw,
+                                   hipStream_t s);
+// swiglu on (rows, 2 f) -> (rows, f); ldh: row stride of the output
+hipError_t launch_swiglu(const void* gu, int dtype, int64_t rows, int64_t f, void* h, hipStream_t s);
+hipError_t launch_swiglu_backward(const void* gu, const void* dh, int dtype, int64_t rows, int64_t f, void* dgu,
+                                  hipStream_t s);
+
+// MXFP4 (mxfp4.hip)
+hipError_t launch_quantize_mxfp4(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ld, uint8_t* codes,
+                                 uint8_t* scales, hipStream_t s);
+hipError_t launch_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, void* x,
+                                   int dtype, hipStream_t s);
+
+#ifdef __HIPCC__
+// ---- device helpers --------------------------------------------------------
+struct Slot {
+    int e, row0, nrows;  // expert (-1: none), first row, rows of the tile (at most TM)
+};
+
+// The `slot`-th tile of TM rows, counting expert after expert.  Every lane of
+// the wave calls it and gets the same answer; the offsets are clamped to
+// 0 .. R, so that no content of theirs leads out of the arrays.
+__device__ __forceinline__ Slot find_slot(const int32_t* offsets, int E, int R, int slot, int TM) {
+    if (!offsets) {
+        const int r0 = slot * TM;
+        return r0 < R ? Slot{0, r0, min(TM, R - r0)} : Slot{-1, 0, 0};
+    }
+    const int lane = threadIdx.x & 63;
+    int before = 0;
+    for (int e0 = 0; e0 < E; e0 += 64) {
+        const int e = e0 + lane;
+        int b = 0, n = 0;
+        if (e < E) {
+            b = min(max(offsets[e], 0), R);
+            n = max(min(offsets[e + 1], R) - b, 0);
+        }
+        const int t = (n + TM - 1) / TM;
+        int sum = t;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const int v = __shfl_up(sum, d);
+            if (lane >= d) sum += v;
+        }
+        const uint64_t hit = __ballot(before + sum > slot);
+        if (hit) {
+            const int l = __builtin_ctzll(hit);
+            const int first = before + __shfl(sum, l) - __shfl(t, l);
+            const int row = (slot - first) * TM;
+            const int bb = __shfl(b, l), nn = __shfl(n, l);
+            return Slot{__builtin_amdgcn_readfirstlane(e0 + l), __builtin_amdgcn_readfirstlane(bb + row),
+                        __builtin_amdgcn_readfirstlane(min(TM, nn - row))};
+        }
+        before += __shfl(sum, 63);
+    }
+    return Slot{-1, 0, 0};
+}
+
+// input row of grouped row m (-1: reads zeros)
+__device__ __forceinline__ int grouped_row(const int32_t* rows, int kdiv, int T, int m) {
+    if (!rows) return m < T ? m : -1;
+    const int s = rows[m];
+    const int t = s / kdiv;
+    return s >= 0 && t < T ? t : -1;
+}
+#endif
+
+}  // namespace sg

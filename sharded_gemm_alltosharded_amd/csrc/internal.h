@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <string>
 #include <type_traits>
 
 #include "../../include/shardgemm.h"
@@ -117,6 +118,9 @@ struct ArmedEvents {
     hipEvent_t start = nullptr, stop = nullptr;
 };
 ArmedEvents& armed_events();
+
+// the calling thread's sg_last_error() message
+std::string& last_error();
 
 #ifdef __HIPCC__
 template <typename K, typename... Args>

@@ -62,11 +62,11 @@ struct Grouped {
 __host__ __device__ inline int64_t mx4_offset(int64_t block, int64_t st, int64_t nsteps) {
     return (block * nsteps + st) * 1024;
 }
-// Their scales: for a 16-row block and a run of four steps 256 bytes, lane l's
-// four (one a step) adjacent.
+// Their scales: for a 16-row block and a run of four steps 16 rows x 16 bytes,
+// a row's four steps adjacent, four scale blocks (bytes) each.
 __host__ __device__ inline int64_t mx4_scale_runs(int64_t nsteps) { return (nsteps + 3) / 4; }
-__host__ __device__ inline int64_t mx4_scale_offset(int64_t block, int64_t st, int lane, int64_t nsteps) {
-    return ((block * mx4_scale_runs(nsteps) + (st >> 2)) * 64 + lane) * 4 + (st & 3);
+__host__ __device__ inline int64_t mx4_scale_offset(int64_t block, int64_t st, int row, int64_t nsteps) {
+    return ((block * mx4_scale_runs(nsteps) + (st >> 2)) * 16 + row) * 16 + (st & 3) * 4;
 }
 
 // workgroups of 256 threads that one launch may have (2^32 threads)

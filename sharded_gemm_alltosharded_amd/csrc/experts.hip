@@ -2,6 +2,8 @@
 // layout of an expert layer's weights.
 #include "experts.h"
 
+#define ALWAYS_INLINE __attribute__((always_inline))
+
 namespace sg {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -54,6 +56,21 @@ __device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t off) 
     return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
 }
 
+// one load of 16 (4) bytes a lane straight into LDS at to + 16 (4) lane
+__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, uint8_t* to) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)to, 16, voff, soff, 0, 0);
+}
+__device__ __forceinline__ void dma4(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, uint8_t* to) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)to, 4, voff, soff, 0, 0);
+}
+// every load, and every LDS write, of this wave has landed
+__device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0070); }
+
+__device__ __forceinline__ u32x2 read_tr(const uint8_t* p) {
+    return __builtin_bit_cast(
+        u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p));
+}
+
 // eight 16-bit inputs k .. k + 7 of a row, zeros from kl on and for row < 0;
 // any alignment
 __device__ __forceinline__ u32x4 load8_any(const uint16_t* a, int64_t row, int64_t lda, int k, int kl) {
@@ -63,33 +80,60 @@ __device__ __forceinline__ u32x4 load8_any(const uint16_t* a, int64_t row, int64
     return u32x4{h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16)};
 }
 
-// the 16-column output block ob of row m: this lane's columns 4 (lane >> 4) .. + 3
-__device__ __forceinline__ void store_block(const Grouped& p, int ob, int m, f32x4 v) {
-    const int piece = ob / p.bps, j = ob - piece * p.bps;
-    const int r = p.swiglu ? piece : piece / p.S;
-    const int s = p.swiglu ? 0 : piece - r * p.S;
-    const int c = 16 * j + 4 * ((threadIdx.x & 63) >> 4);
-    if (c >= p.f) return;
-    const int64_t o = (int64_t)r * p.o_rank + (int64_t)m * p.ldo + s * p.f + c;
-    if (p.vec) {  // f is a multiple of 4
-        if (p.out_dtype == SG_F32) {
-            *(f32x4*)((float*)p.out + o) = v;
-            return;
-        }
-        u32x2 w;
-        if (p.out_dtype == SG_BF16) {
-            w[0] = f32_to_bf16(v[0]) | ((uint32_t)f32_to_bf16(v[1]) << 16);
-            w[1] = f32_to_bf16(v[2]) | ((uint32_t)f32_to_bf16(v[3]) << 16);
-        } else {
-            w[0] = f32_to_f16(v[0]) | ((uint32_t)f32_to_f16(v[1]) << 16);
-            w[1] = f32_to_f16(v[2]) | ((uint32_t)f32_to_f16(v[3]) << 16);
-        }
-        *(u32x2*)((uint16_t*)p.out + o) = w;
-        return;
-    }
+__device__ __forceinline__ f32x4 swiglu4(f32x4 g, f32x4 u) {
+    f32x4 v;
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-        if (c + e < p.f) store_from_f32(p.out, p.out_dtype, o + e, v[e]);
+    for (int e = 0; e < 4; ++e) v[e] = silu_f32(g[e]) * u[e];
+    return v;
+}
+
+// Stores a wave's N x M result blocks: value(i, j) is this lane's four columns
+// 4 (lane >> 4) .. + 3 of output block ob0 + i, row row0 + 16 j + (lane & 15).
+// DT -1: any type and alignment.
+template <int DT, int N, int M, typename F>
+__device__ __forceinline__ void store_typed(const Grouped& p, int ob0, int row0, int nrows, F&& value) {
+    const int lane = threadIdx.x & 63;
+    static_for<0, N>([&](auto ic) {
+        constexpr int i = decltype(ic)::value;
+        const int ob = ob0 + i;
+        if (ob >= p.nout) return;
+        const int piece = ob / p.bps, blk = ob - piece * p.bps;
+        const int r = p.swiglu ? piece : piece / p.S, s = p.swiglu ? 0 : piece - r * p.S;
+        const int c = 16 * blk + 4 * (lane >> 4);
+        if (c >= p.f) return;
+        const int64_t base = (int64_t)r * p.o_rank + s * p.f + c;
+        static_for<0, M>([&](auto jc) {
+            constexpr int j = decltype(jc)::value;
+            const int m = 16 * j + (lane & 15);
+            if (m >= nrows) return;
+            const int64_t o = base + (int64_t)(row0 + m) * p.ldo;
+            const f32x4 v = value(ic, jc);
+            if constexpr (DT < 0) {  // any alignment
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (c + e < p.f) store_from_f32(p.out, p.out_dtype, o + e, v[e]);
+            } else if constexpr (DT == SG_F32) {
+                *(f32x4*)((float*)p.out + o) = v;
+            } else {
+                u32x2 w;
+                if constexpr (DT == SG_BF16) {
+                    w[0] = f32_to_bf16(v[0]) | ((uint32_t)f32_to_bf16(v[1]) << 16);
+                    w[1] = f32_to_bf16(v[2]) | ((uint32_t)f32_to_bf16(v[3]) << 16);
+                } else {
+                    w[0] = f32_to_f16(v[0]) | ((uint32_t)f32_to_f16(v[1]) << 16);
+                    w[1] = f32_to_f16(v[2]) | ((uint32_t)f32_to_f16(v[3]) << 16);
+                }
+                *(u32x2*)((uint16_t*)p.out + o) = w;
+            }
+        });
+    });
+}
+template <int N, int M, typename F>
+__device__ __forceinline__ void store_blocks(const Grouped& p, int ob0, int row0, int nrows, F&& value) {
+    if (!p.vec) store_typed<-1, N, M>(p, ob0, row0, nrows, value);
+    else if (p.out_dtype == SG_BF16) store_typed<SG_BF16, N, M>(p, ob0, row0, nrows, value);
+    else if (p.out_dtype == SG_F16) store_typed<SG_F16, N, M>(p, ob0, row0, nrows, value);
+    else store_typed<SG_F32, N, M>(p, ob0, row0, nrows, value);
 }
 
 // segment's first element of A
@@ -138,7 +182,7 @@ __global__ __launch_bounds__(256) void grouped_stream_kernel(Grouped p) {
         const int wb = weight_block(p, ob, SWIGLU ? i & 1 : 0);
         w[i] = p.W + (int64_t)s.e * p.w_expert + (int64_t)wb * p.wsteps * 1024 + lane * 16;
         if constexpr (MX)
-            ws[i] = p.wsc + (int64_t)s.e * p.wsc_expert + (int64_t)wb * mx4_scale_runs(p.wsteps) * 256 + lane * 4;
+            ws[i] = p.wsc + (int64_t)s.e * p.wsc_expert + mx4_scale_offset(wb, 0, lane & 15, p.wsteps);
     }
     int row[MB];
 #pragma unroll
@@ -183,7 +227,8 @@ __global__ __launch_bounds__(256) void grouped_stream_kernel(Grouped p) {
         for (int b = 0; b < MB; ++b) acc[i][b] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     u32x4 wf[4][NW], af[4][MB][AF];
-    uint32_t as[4][MB], wsc[NW], wsn[NW];
+    uint32_t as[4][MB];
+    u32x4 wsc[NW], wsn[NW];  // a run's scales of a weight row: a word a step, a byte a block
     auto load_step = [&](int st, int u) {
         const int c = min(st, steps - 1);
 #pragma unroll
@@ -195,7 +240,7 @@ __global__ __launch_bounds__(256) void grouped_stream_kernel(Grouped p) {
         if constexpr (MX) {
             const int c = min(run, runs - 1);
 #pragma unroll
-            for (int i = 0; i < NW; ++i) wsn[i] = *(const uint32_t*)(ws[i] + (int64_t)c * 256);
+            for (int i = 0; i < NW; ++i) wsn[i] = *(const u32x4*)(ws[i] + (int64_t)c * 256);
         }
     };
     if (run0 < run1) {
@@ -213,8 +258,7 @@ __global__ __launch_bounds__(256) void grouped_stream_kernel(Grouped p) {
 #pragma unroll
                 for (int i = 0; i < NW; ++i) {
                     if constexpr (MODE == G_MX4) {
-                        const uint32_t sb = (wsc[i] >> (8 * u)) & 255u;
-                        const float sc = e8m0_to_f32(sb);
+                        const float sc = e8m0_to_f32((wsc[i][u] >> (8 * (lane >> 4))) & 255u);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const u32x4 wv = mx4_to_bf16(wf[u][i][j], sc);
@@ -224,7 +268,7 @@ __global__ __launch_bounds__(256) void grouped_stream_kernel(Grouped p) {
                     } else if constexpr (MODE == G_MX4A4) {
 #pragma unroll
                         for (int b = 0; b < MB; ++b)
-                            acc[i][b] = mfma_mx4(wf[u][i], wsc[i] >> (8 * u), af[u][b][0], as[u][b], acc[i][b]);
+                            acc[i][b] = mfma_mx4(wf[u][i], wsc[i][u] >> (8 * (lane >> 4)), af[u][b][0], as[u][b], acc[i][b]);
                     } else {
 #pragma unroll
                         for (int b = 0; b < MB; ++b) acc[i][b] = mfma16<MODE == G_F16>(wf[u][i], af[u][b][0], acc[i][b]);
@@ -250,41 +294,60 @@ __global__ __launch_bounds__(256) void grouped_stream_kernel(Grouped p) {
 #pragma unroll
                 for (int b = 0; b < MB; ++b) acc[i][b] += red[(((q * NG + ng) * NW + i) * MB + b) * 64 + lane];
     }
-#pragma unroll
-    for (int n = 0; n < NB; ++n) {
-        if (ob0 + n >= p.nout) continue;
-#pragma unroll
-        for (int b = 0; b < MB; ++b) {
-            const int m = 16 * b + (lane & 15);
-            if (m >= s.nrows) continue;
-            f32x4 v;
-            if constexpr (SWIGLU) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = silu_f32(acc[2 * n][b][e]) * acc[2 * n + 1][b][e];
-            } else {
-                v = acc[n][b];
-            }
-            store_block(p, ob0 + n, s.row0 + m, v);
-        }
-    }
+    store_blocks<NB, MB>(p, ob0, s.row0, s.nrows, [&](auto ic, auto jc) {
+        constexpr int n = decltype(ic)::value, b = decltype(jc)::value;
+        if constexpr (!SWIGLU) return acc[n][b];
+        else return swiglu4(acc[2 * n][b], acc[2 * n + 1][b]);
+    });
 }
 
 // ---------------------------------------------------------------------------
-// Tile kernel: 128 rows x 128 weight rows (SwiGLU: 64 gate and the 64 matching
-// up rows; transposed: 128 columns of the weights), 64 contracted inputs a
-// tile, four waves of 64 x 64, operands staged through registers into two LDS
-// buffers.  The rows lie in LDS as 128-byte rows, chunks XOR-swizzled by
-// (row >> 1) & 7; weight fragments as stored, 1 KB each.  Transposed, the
-// contracted dimension runs down the weight's rows: ds_read_b64_tr_b16 hands
-// each lane four rows of one column.
+// Tile kernel: TM rows x BN weight rows (SwiGLU: BN / 2 gate and the BN / 2
+// matching up rows; transposed: BN columns of the weights), WM x WN waves, two
+// LDS stages.  Bound by the matrix unit for many rows of an expert.
+//
+// A k tile is 64 inputs (MXFP4 weights: 128; MXFP4 x MXFP4: 256, the same 128
+// bytes a row).  Its operands go from memory straight into the stage that the
+// k tile before left: one barrier a k tile, behind which every wave's loads of
+// it have landed; the next k tile's loads are issued between the two halves'
+// operand reads and MFMAs.  With two waves a SIMD the reads of one run beside
+// the MFMAs of the other; a raised wave priority around the MFMAs keeps them
+// back to back (256 x 256, 8192 x 28672 x 4096: 1.08 -> 1.28 PFLOP/s, where the
+// vendor library's product of that size reaches 1.37).  Each stage is an array
+// of its own, so that the compiler sees that reads of one do not wait for the
+// loads into the other.
+//
+// LDS: rows of A as 128 bytes (MXFP4 weights: 256), 16-byte chunks
+// XOR-swizzled by (row >> 1) & 7 (row & 15), so that the sixteen rows of an
+// operand read spread over all banks; weight fragments as stored, 1 KB each.
+// Transposed, the contracted dimension runs down the weight's rows:
+// ds_read_b64_tr_b16 hands each lane four rows of one column, and the odd
+// chunks of a fragment are stored four rows on, so that the two chunks of a
+// read lie in different banks.
 // ---------------------------------------------------------------------------
-template <bool F16, bool SWIGLU, bool TRANS, bool AL>
-__global__ __launch_bounds__(256) void grouped_tile_kernel(Grouped p, int slots, int tiles_n) {
-    constexpr int TM = 128;
-    __shared__ __attribute__((aligned(1024))) uint16_t sA[2][TM * 64], sW[2][16 * 512];
+template <int MODE, bool SWIGLU, bool TRANS, int TM, int BN, int WM, int WN, bool AL>
+__global__ __launch_bounds__(64 * WM * WN) void grouped_tile_kernel(Grouped p, int slots, int tiles_n) {
+    constexpr int NWV = WM * WN;
+    constexpr int NBM = TM / WM / 16, NBN = BN / WN / 16;
+    constexpr bool MX = MODE >= G_MX4, A4 = MODE == G_MX4A4;
+    constexpr int KT = A4 ? 256 : MX ? 128 : 64;
+    constexpr int KST = MX ? 128 : 32;              // inputs of a stored weight step
+    constexpr int ROWB = MODE == G_MX4 ? 256 : 128;  // bytes of a row of A in LDS
+    constexpr int CPR = ROWB / 16;                   // its chunks
+    constexpr int RPI = 64 / CPR;                    // rows of a 1 KB load
+    constexpr int LA = TM * ROWB / 1024 / NWV;       // loads of a wave
+    constexpr int FPB = MODE == G_MX4 ? 1 : 2;       // fragments of a weight block
+    constexpr int LW = BN / 16 * FPB / NWV;
+    constexpr int KK = MODE == G_MX4 ? 4 : 2;        // MFMA steps of a k tile
+    static_assert(LA * NWV * 1024 == TM * ROWB && LW * NWV * 16 == BN * FPB, "loads divide over the waves");
+    __shared__ __attribute__((aligned(1024))) uint8_t sA0[TM * ROWB], sA1[TM * ROWB], sW0[BN * FPB * 64],
+        sW1[BN * FPB * 64];
+    // MXFP4 scales of a k tile: four a weight row and step, four a row of A and step
+    __shared__ uint32_t sSW0[MX ? BN * FPB : 1], sSW1[MX ? BN * FPB : 1], sSA0[A4 ? TM * 2 : 1], sSA1[A4 ? TM * 2 : 1];
+
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wave_m = wave & 1, wave_n = wave >> 1;
+    const int wave_m = wave % WM, wave_n = wave / WM;
     const int tile = xcd_remap(blockIdx.x, slots * tiles_n);
     constexpr int GM = 4;
     const int g = tile / (GM * tiles_n), first = g * GM, gsz = min(GM, slots - first);
@@ -293,129 +356,213 @@ __global__ __launch_bounds__(256) void grouped_tile_kernel(Grouped p, int slots,
     if (s.e < 0) return;
     const int nt = tin / gsz;  // n tile
 
-    // rows this thread loads: (tid >> 3) + 32 i, chunk tid & 7
-    int row[4];
+    // load i of a wave: rows (i NWV + wave) RPI .. of A, chunk lane % CPR of them
+    uint32_t aoff[LA];
+    [[maybe_unused]] int arow[LA];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int m = (tid >> 3) + 32 * i;
-        row[i] = m < s.nrows ? grouped_row(p.rows, p.kdiv, p.T, s.row0 + m) : -1;
+    for (int i = 0; i < LA; ++i) {
+        const int m = (i * NWV + wave) * RPI + lane / CPR;
+        const int row = m < s.nrows ? grouped_row(p.rows, p.kdiv, p.T, s.row0 + m) : -1;
+        const int sw = ROWB == 128 ? (m >> 1) & 7 : m & 15;
+        const int ch = (lane % CPR) ^ sw;
+        arow[i] = row;
+        aoff[i] = row < 0 ? kOutside : (uint32_t)((A4 ? row * (p.lda / 2) : row * p.lda * 2) + ch * 16);
     }
+    auto chunk_of = [&](int i) {
+        const int m = (i * NWV + wave) * RPI + lane / CPR;
+        return (lane % CPR) ^ (ROWB == 128 ? (m >> 1) & 7 : m & 15);
+    };
+    constexpr int KPC = A4 ? 32 : 8;  // inputs of a chunk
     const uint8_t* W = p.W + (int64_t)s.e * p.w_expert;
-    const int kts = (p.kpad + 63) / 64, nkt = p.nseg * kts;
-    const int64_t a_bytes = ((int64_t)(p.T - 1) * p.lda + p.kl) * 2;
-
-    u32x4 ra[4], rw[4];
-    auto load = [&](int kt) {
-        const int seg = kt / kts, k0 = (kt - seg * kts) * 64;
-        const uint16_t* base = (const uint16_t*)p.A + seg_offset(p, seg);
-        const int k = k0 + 8 * (tid & 7);
+    const uint32_t wlane = (uint32_t)(TRANS ? lane ^ (((lane >> 4) & 1) << 2) : lane) * 16;
+    uint32_t wbase[LW];  // fragment's byte offset at k tile 0 (wave-uniform)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if constexpr (AL)
-                ra[i] = load16(buffer(base, a_bytes),
-                               row[i] >= 0 && k < p.kl ? (uint32_t)((row[i] * p.lda + k) * 2) : kOutside);
-            else
-                ra[i] = load8_any(base, row[i], p.lda, k, p.kl);
+    for (int i = 0; i < LW; ++i) {
+        const int f = i * NWV + wave;
+        if constexpr (TRANS) {
+            wbase[i] = 0;
+        } else {
+            const int b = f / FPB;
+            const int ob = SWIGLU ? nt * (BN / 32) + b / 2 : nt * (BN / 16) + b;
+            wbase[i] = ((uint32_t)weight_block(p, min(ob, p.nout - 1), SWIGLU ? b & 1 : 0) * p.wsteps + f % FPB) * 1024u;
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int f = 4 * i + wave;
-            int64_t at;
-            bool in = true;
-            if constexpr (TRANS) {
-                // fragment (block f >> 2 of the tile's four, step f & 3 of its four)
-                const int kb = k0 / 16 + (f >> 2), st = nt * 4 + (f & 3);
-                in = kb < p.kpad / 16 && st < p.wsteps;
-                at = ((int64_t)(seg * (p.kpad / 16) + kb) * p.wsteps + st) * 1024;
-            } else {
-                // fragment (block f >> 1 of the tile's eight, step f & 1 of its two)
-                int ob, half = 0;
-                if constexpr (SWIGLU) ob = nt * 4 + (f >> 2), half = (f >> 1) & 1;
-                else ob = nt * 8 + (f >> 1);
-                const int st = (seg * p.kpad + k0) / 32 + (f & 1);
-                at = ((int64_t)weight_block(p, min(ob, p.nout - 1), half) * p.wsteps + st) * 1024;
+    }
+    const int kts = (p.kpad + KT - 1) / KT, nkt = p.nseg * kts;
+    const int64_t a_bytes = A4 ? (int64_t)p.T * (p.lda / 2) : ((int64_t)(p.T - 1) * p.lda + p.kl) * 2;
+
+    // the k tile that is loaded next: its segment, first input, and the
+    // segment's first element of A
+    int iseg = 0, ik = 0, ipiece = 0;
+    int64_t irank = 0, ia = 0;
+    // (past the last k tile every load reads zeros, into a stage never read)
+    auto bytes = [&](int64_t n) ALWAYS_INLINE { return iseg < p.nseg ? n : 0; };
+    auto load_a = [&](uint8_t* sA, int i) ALWAYS_INLINE {
+        const int k = ik + chunk_of(i) * KPC;
+        uint8_t* to = sA + (i * NWV + wave) * 1024;
+        if constexpr (AL) {
+            const uint8_t* base = (const uint8_t*)p.A + (A4 ? ia / 2 : ia * 2);
+            uint32_t off = aoff[i];
+            if (ik + KT > p.kl && k >= p.kl) off = kOutside;
+            dma16(buffer(base, bytes(a_bytes)), off, (uint32_t)(A4 ? ik / 2 : ik * 2), to);
+        } else {
+            const uint16_t* base = (const uint16_t*)p.A + ia;
+            *(u32x4*)(to + lane * 16) = load8_any(base, iseg < p.nseg ? arow[i] : -1, p.lda, k, p.kl);
+        }
+    };
+    auto load_w = [&](uint8_t* sW, int i) ALWAYS_INLINE {
+        const int f = i * NWV + wave;
+        uint32_t off = wlane, at;
+        if constexpr (TRANS) {
+            const int kb = ik / 16 + f / (BN / 32), st = nt * (BN / 32) + f % (BN / 32);
+            at = ((uint32_t)(iseg * (p.kpad / 16) + kb) * p.wsteps + st) * 1024u;
+            if (kb >= p.kpad / 16 || st >= p.wsteps) off = kOutside, at = 0;
+        } else {
+            at = wbase[i] + (uint32_t)(iseg * p.kpad + ik) / KST * 1024u;
+            if (FPB * KST > KST && MX && ik + (f % FPB) * KST >= p.kpad) off = kOutside, at = 0;
+        }
+        dma16(buffer(W, bytes(p.w_expert)), off, at, sW + f * 1024);
+    };
+    // MXFP4: this lane's scales of a k tile, one load each: weight row lane & 15
+    // of (block, step) number wave * 4 + lane / 16, and row wave * 32 + lane / 2
+    // of A, step lane & 1
+    constexpr int SW = BN * FPB / 64;  // loads of a k tile's weight scales
+    static_assert(!MX || SW <= NWV, "one load a wave");
+    static_assert(!A4 || TM * 2 / 64 == NWV, "one load a wave");
+    [[maybe_unused]] uint32_t swoff = 0, saoff = kOutside;
+    [[maybe_unused]] const int ssub = (wave * 4 + (lane >> 4)) % FPB;
+    if constexpr (MX) {
+        const int b = (wave * 4 + (lane >> 4)) / FPB;
+        const int ob = SWIGLU ? nt * (BN / 32) + b / 2 : nt * (BN / 16) + b;
+        const int wb = weight_block(p, min(ob, p.nout - 1), SWIGLU ? b & 1 : 0);
+        swoff = (uint32_t)mx4_scale_offset(wb, 0, lane & 15, p.wsteps);
+    }
+    if constexpr (A4) {
+        const int m = wave * 32 + (lane >> 1);
+        const int row = m < s.nrows ? grouped_row(p.rows, p.kdiv, p.T, s.row0 + m) : -1;
+        if (row >= 0) saoff = (uint32_t)(row * (p.kl / 32)) + (lane & 1) * 4;
+    }
+    auto load_scales = [&](uint32_t* sSW, uint32_t* sSA) ALWAYS_INLINE {
+        if constexpr (MX) {
+            if (wave < SW) {
+                const int st = (iseg * p.kpad + ik) / 128 + ssub;
+                const uint32_t off = swoff + (st >> 2) * 256 + (st & 3) * 4;
+                dma4(buffer(p.wsc + (int64_t)s.e * p.wsc_expert, bytes(p.wsc_expert)),
+                     ik + ssub * 128 < p.kpad ? off : kOutside, 0, (uint8_t*)(sSW + wave * 64));
             }
-            rw[i] = in ? *(const u32x4*)(W + at + lane * 16) : u32x4{0, 0, 0, 0};
         }
+        if constexpr (A4)
+            dma4(buffer(p.a_scales + (int64_t)iseg * p.T * (p.kl / 32), bytes((int64_t)p.T * (p.kl / 32))),
+                 saoff != kOutside && ik + (lane & 1) * 128 < p.kl ? saoff + ik / 32 : kOutside, 0,
+                 (uint8_t*)(sSA + wave * 64));
     };
-    auto stage = [&](int buf) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int m = (tid >> 3) + 32 * i;
-            *(u32x4*)(sA[buf] + m * 64 + (((tid & 7) ^ ((m >> 1) & 7)) << 3)) = ra[i];
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) *(u32x4*)(sW[buf] + (4 * i + wave) * 512 + lane * 8) = rw[i];
+    auto advance = [&]() ALWAYS_INLINE {
+        ik += KT;
+        if (ik < p.kpad) return;
+        ik = 0;
+        ++iseg;
+        ia += p.kl;
+        if (++ipiece == p.a_pieces) ipiece = 0, irank += p.a_rank, ia = irank;
     };
 
-    f32x4 acc[4][4];
+    f32x4 acc[NBN][NBM];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < NBN; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < NBM; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     const int c16 = lane >> 4, r16 = lane & 15;
-    if (nkt > 0) {
-        load(0);
-        stage(0);
-        __syncthreads();
-        for (int t = 0; t < nkt; ++t) {
-            const int buf = t & 1;
-            if (t + 1 < nkt) load(t + 1);
+    const int amine = (wave_m * NBM * 16 + r16) * ROWB, asw = ROWB == 128 ? (r16 >> 1) & 7 : r16;
+    auto read = [&](const uint8_t* sA, const uint8_t* sW, const uint32_t* sSW, int kk, u32x4(&wf)[NBN], u32x4(&af)[NBM]) ALWAYS_INLINE {
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-                u32x4 wf[4], af[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if constexpr (TRANS) {
-                        // columns 16 (4 wave_n + i) .. of the tile; contracted rows 32 kk + 8 c16 ..
-                        const int nb = 4 * wave_n + i;
-                        const uint16_t* fr = sW[buf] + ((2 * kk + (c16 >> 1)) * 4 + (nb >> 1)) * 512;
-                        const int ch = 2 * (nb & 1) + ((r16 & 3) >> 1);
-                        const int rr = 8 * (c16 & 1) + (r16 >> 2);
-                        const uint16_t* a0 = fr + (rr + 16 * ch) * 8 + 4 * (r16 & 1);
-                        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                            (__attribute__((address_space(3))) s16x4*)a0);
-                        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                            (__attribute__((address_space(3))) s16x4*)(a0 + 4 * 8));
-                        const u32x2 l2 = __builtin_bit_cast(u32x2, lo), h2 = __builtin_bit_cast(u32x2, hi);
-                        wf[i] = u32x4{l2[0], l2[1], h2[0], h2[1]};
-                    } else {
-                        wf[i] = *(const u32x4*)(sW[buf] + ((4 * wave_n + i) * 2 + kk) * 512 + lane * 8);
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int m = wave_m * 64 + 16 * j + r16;
-                    af[j] = *(const u32x4*)(sA[buf] + m * 64 + (((4 * kk + c16) ^ ((m >> 1) & 7)) << 3));
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[i][j] = mfma16<F16>(wf[i], af[j], acc[i][j]);
-            }
-            if (t + 1 < nkt) stage(buf ^ 1);
-            __syncthreads();
-        }
-    }
-
-    static_for<0, (SWIGLU ? 2 : 4)>([&](auto ic) {
-        constexpr int i = decltype(ic)::value;
-        const int ob = SWIGLU ? nt * 4 + wave_n * 2 + i : nt * 8 + wave_n * 4 + i;
-        if (ob >= p.nout) return;
-        static_for<0, 4>([&](auto jc) {
-            constexpr int j = decltype(jc)::value;
-            const int m = wave_m * 64 + 16 * j + r16;
-            if (m >= s.nrows) return;
-            f32x4 v;
-            if constexpr (SWIGLU) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = silu_f32(acc[2 * i][j][e]) * acc[2 * i + 1][j][e];
+        for (int i = 0; i < NBN; ++i) {
+            const int nb = wave_n * NBN + i;
+            if constexpr (TRANS) {
+                // columns 16 nb .. of the tile, contracted rows 32 kk + 8 c16 ..
+                const uint8_t* fr = sW + ((2 * kk + (c16 >> 1)) * (BN / 32) + (nb >> 1)) * 1024;
+                const int ch = 2 * (nb & 1) + ((r16 & 3) >> 1);
+                const int rr = (8 * (c16 & 1) + (r16 >> 2)) ^ ((ch & 1) << 2);
+                const uint8_t* a0 = fr + (rr + 16 * ch) * 16 + 8 * (r16 & 1);
+                const uint8_t* a1 = fr + ((rr ^ 4) + 16 * ch) * 16 + 8 * (r16 & 1);
+                const u32x2 lo = read_tr(a0), hi = read_tr(a1);
+                wf[i] = u32x4{lo[0], lo[1], hi[0], hi[1]};
+            } else if constexpr (MODE == G_MX4) {
+                const uint32_t w = *(const uint32_t*)(sW + nb * 1024 + lane * 16 + 4 * kk);
+                wf[i] = mx4_to_bf16(w, e8m0_to_f32((sSW[nb * 16 + r16] >> (8 * c16)) & 255u));
             } else {
-                v = acc[i][j];
+                wf[i] = *(const u32x4*)(sW + (nb * FPB + kk) * 1024 + lane * 16);
             }
-            store_block(p, ob, s.row0 + m, v);
+        }
+#pragma unroll
+        for (int j = 0; j < NBM; ++j) {
+            const int ch = MODE == G_MX4 ? 4 * c16 + kk : 4 * kk + c16;
+            af[j] = *(const u32x4*)(sA + amine + j * 16 * ROWB + ((ch ^ asw) << 4));
+        }
+    };
+    auto multiply = [&](const uint32_t* sSW, const uint32_t* sSA, int kk, u32x4(&wf)[NBN], u32x4(&af)[NBM]) ALWAYS_INLINE {
+        uint32_t ws[NBN], as[NBM];
+        if constexpr (A4) {
+#pragma unroll
+            for (int i = 0; i < NBN; ++i) ws[i] = sSW[((wave_n * NBN + i) * 2 + kk) * 16 + r16] >> (8 * c16);
+#pragma unroll
+            for (int j = 0; j < NBM; ++j) as[j] = sSA[(wave_m * NBM * 16 + j * 16 + r16) * 2 + kk] >> (8 * c16);
+        }
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int j = 0; j < NBM; ++j)
+#pragma unroll
+            for (int i = 0; i < NBN; ++i) {
+                if constexpr (A4) acc[i][j] = mfma_mx4(wf[i], ws[i], af[j], as[j], acc[i][j]);
+                else acc[i][j] = mfma16<MODE == G_F16>(wf[i], af[j], acc[i][j]);
+            }
+        __builtin_amdgcn_s_setprio(0);
+    };
+    auto step = [&](const uint8_t* sA, const uint8_t* sW, const uint32_t* sSW, const uint32_t* sSA, uint8_t* nA,
+                    uint8_t* nW, uint32_t* nSW, uint32_t* nSA) ALWAYS_INLINE {
+        // this wave's loads of the k tile have landed; behind the barrier every
+        // wave's have, and every wave has read the k tile before
+        wait_loads();
+        __builtin_amdgcn_s_barrier();
+        u32x4 wf[NBN], af[NBM];
+        static_for<0, KK>([&](auto kc) ALWAYS_INLINE {
+            constexpr int kk = decltype(kc)::value;
+            read(sA, sW, sSW, kk, wf, af);
+            if constexpr (kk == 0) {
+                load_scales(nSW, nSA);
+#pragma unroll
+                for (int i = 0; i < LA; ++i) load_a(nA, i);
+            } else if constexpr (kk == 1) {
+#pragma unroll
+                for (int i = 0; i < LW; ++i) load_w(nW, i);
+                advance();
+            }
+            multiply(sSW, sSA, kk, wf, af);
         });
+        // MXFP4 x MXFP4: the operands of both halves do not fit the registers
+        // together, so each half's MFMAs come before the next half's reads
+        if constexpr (A4)
+            static_for<0, KK>([&](auto) ALWAYS_INLINE {
+                __builtin_amdgcn_sched_group_barrier(0x100, 2 * (NBN + NBM), 0);  // LDS reads
+                __builtin_amdgcn_sched_group_barrier(0x008, NBN * NBM, 0);        // MFMAs
+            });
+    };
+    load_scales(sSW0, sSA0);
+#pragma unroll
+    for (int i = 0; i < LA; ++i) load_a(sA0, i);
+#pragma unroll
+    for (int i = 0; i < LW; ++i) load_w(sW0, i);
+    advance();
+    for (int t = 0; t < nkt; t += 2) {
+        step(sA0, sW0, sSW0, sSA0, sA1, sW1, sSW1, sSA1);
+        if (t + 1 < nkt) step(sA1, sW1, sSW1, sSA1, sA0, sW0, sSW0, sSA0);
+    }
+    wait_loads();  // none may still be writing this workgroup's LDS when it ends
+
+    constexpr int NO = SWIGLU ? NBN / 2 : NBN;  // output blocks of a wave
+    const int m0 = wave_m * NBM * 16;
+    store_blocks<NO, NBM>(p, nt * NO * WN + wave_n * NO, s.row0 + m0, s.nrows - m0, [&](auto ic, auto jc) {
+        constexpr int i = decltype(ic)::value, j = decltype(jc)::value;
+        if constexpr (!SWIGLU) return acc[i][j];
+        else return swiglu4(acc[2 * i][j], acc[2 * i + 1][j]);
     });
 }
 
@@ -473,9 +620,10 @@ __global__ __launch_bounds__(256) void pack_mx4_kernel(uint8_t* codes, uint8_t* 
     }
     *(u32x4*)(codes + e * l.blocks * l.steps * 1024 + mx4_offset(b, st, l.steps) + lane * 16) = v;
     uint8_t* se = scales + e * l.blocks * mx4_scale_runs(l.steps) * 256;
-    se[mx4_scale_offset(b, st, lane, l.steps)] = s;
+    se[mx4_scale_offset(b, st, lane & 15, l.steps) + (lane >> 4)] = s;
     if (st == l.steps - 1)  // the rest of the last run is read and not used
-        for (int64_t i = l.steps; i < mx4_scale_runs(l.steps) * 4; ++i) se[mx4_scale_offset(b, i, lane, l.steps)] = 127;
+        for (int64_t i = l.steps; i < mx4_scale_runs(l.steps) * 4; ++i)
+            se[mx4_scale_offset(b, i, lane & 15, l.steps) + (lane >> 4)] = 127;
 }
 
 template <int MODE, bool SWIGLU, int MB, int NB, int KS, bool AL>
@@ -498,24 +646,36 @@ hipError_t stream_mode(const Grouped& p, hipStream_t s) {
     return stream_launch<MODE, SWIGLU, 2, NB, 1, AL>(p, s);
 }
 
-template <bool F16, bool SWIGLU, bool TRANS, bool AL>
+template <int MODE, bool SWIGLU, bool TRANS, int TM, int BN, int WM, int WN, bool AL>
 hipError_t tile_launch(const Grouped& p, hipStream_t s) {
-    const int64_t slots = p.R / 128 + (p.R < p.E ? p.R : p.E);
-    const int64_t tiles_n = (p.nout + (SWIGLU ? 3 : 7)) / (SWIGLU ? 4 : 8);
-    if (slots * tiles_n >= kMaxBlocks) return hipErrorInvalidConfiguration;
-    launch(grouped_tile_kernel<F16, SWIGLU, TRANS, AL>, dim3((unsigned)(slots * tiles_n)), dim3(256), 0, s, p,
-           (int)slots, (int)tiles_n);
+    constexpr int NB = SWIGLU ? BN / 32 : BN / 16;
+    const int64_t slots = p.R / TM + (p.R < p.E ? p.R : p.E);
+    const int64_t tiles_n = (p.nout + NB - 1) / NB;
+    if (slots * tiles_n >= kMaxBlocks / 2) return hipErrorInvalidConfiguration;
+    launch(grouped_tile_kernel<MODE, SWIGLU, TRANS, TM, BN, WM, WN, AL>, dim3((unsigned)(slots * tiles_n)),
+           dim3(64 * WM * WN), 0, s, p, (int)slots, (int)tiles_n);
     return hipGetLastError();
+}
+
+template <int MODE, bool SWIGLU, bool TRANS, bool AL>
+hipError_t tile_mode(const Grouped& p, hipStream_t s) {
+    if constexpr (!AL) {
+        return tile_launch<MODE, SWIGLU, TRANS, 128, 128, 2, 2, false>(p, s);
+    } else if constexpr (MODE == G_MX4) {
+        return tile_launch<MODE, SWIGLU, TRANS, 128, 256, 2, 4, true>(p, s);
+    } else {
+        if (p.R >= (int64_t)192 * p.E) return tile_launch<MODE, SWIGLU, TRANS, 256, 256, 2, 4, true>(p, s);
+        return tile_launch<MODE, SWIGLU, TRANS, 128, 128, 2, 2, true>(p, s);
+    }
 }
 
 template <int MODE, bool AL>
 hipError_t by_mode(const Grouped& p, hipStream_t s) {
-    if constexpr (MODE < G_MX4) {
-        constexpr bool F = MODE == G_F16;
-        if (p.transposed) return tile_launch<F, false, true, AL>(p, s);
-        if (p.R > (int64_t)32 * p.E)
-            return p.swiglu ? tile_launch<F, true, false, AL>(p, s) : tile_launch<F, false, false, AL>(p, s);
-    }
+    if constexpr (MODE < G_MX4)
+        if (p.transposed) return tile_mode<MODE, false, true, AL>(p, s);
+    // (an MXFP4 row's scales are staged four at a time)
+    const bool tiles = p.R > (int64_t)32 * p.E && (MODE != G_MX4A4 || (p.kl % 128 == 0 && (uintptr_t)p.a_scales % 4 == 0));
+    if (tiles) return p.swiglu ? tile_mode<MODE, true, false, AL>(p, s) : tile_mode<MODE, false, false, AL>(p, s);
     return p.swiglu ? stream_mode<MODE, true, AL>(p, s) : stream_mode<MODE, false, AL>(p, s);
 }
 

@@ -98,6 +98,8 @@ sg_status layout_of(int64_t E, int64_t out_dims, int64_t in_dims, int mode, int 
     l->steps = (col ? 1 : P) * l->kpad / (mx ? 128 : 32);
     if (E * l->blocks * l->steps >= sg::kMaxBlocks * 4)
         return fail(SG_ERR_UNSUPPORTED, "an expert layer above 64 GiB is not supported");
+    if (l->blocks * l->steps * 1024 > kMaxBytes)
+        return fail(SG_ERR_UNSUPPORTED, "an expert above 4 GiB is not supported");
     return SG_OK;
 }
 

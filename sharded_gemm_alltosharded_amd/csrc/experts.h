@@ -133,7 +133,61 @@ hipError_t launch_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scales, 
                                    int dtype, hipStream_t s);
 
 #ifdef __HIPCC__
+#define ALWAYS_INLINE __attribute__((always_inline))
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
 // ---- device helpers --------------------------------------------------------
+// D = rows x columns of 16: lane l gives 32 (k) / 4 = 8 values of row l & 15 of
+// w and of column l & 15 of a, and holds rows 4 (l >> 4) .. + 3 of column l & 15
+template <bool F16>
+__device__ __forceinline__ f32x4 mfma16(u32x4 w, u32x4 a, f32x4 c) {
+    if constexpr (F16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, w), __builtin_bit_cast(f16x8, a), c, 0,
+                                                      0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), __builtin_bit_cast(bf16x8, a),
+                                                       c, 0, 0, 0);
+}
+
+constexpr uint32_t kOutside = 0xfffffff0u;  // byte offset past every buffer: reads zeros
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, int64_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, (int)(uint32_t)bytes, 0x00020000);
+}
+__device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
+
+// one load of 16 (4) bytes a lane straight into LDS at to + 16 (4) lane
+__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, uint8_t* to) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)to, 16, voff, soff, 0, 0);
+}
+__device__ __forceinline__ void dma4(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, uint8_t* to) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)to, 4, voff, soff, 0, 0);
+}
+// every load, and every LDS write, of this wave has landed
+__device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0070); }
+
+__device__ __forceinline__ u32x2 read_tr(const uint8_t* p) {
+    return __builtin_bit_cast(
+        u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p));
+}
+
+// eight 16-bit inputs k .. k + 7 of a row, zeros from kl on and for row < 0;
+// any alignment
+__device__ __forceinline__ u32x4 load8_any(const uint16_t* a, int64_t row, int64_t lda, int k, int kl) {
+    uint32_t h[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = row >= 0 && k + e < kl ? a[row * lda + k + e] : 0;
+    return u32x4{h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16)};
+}
+
 struct Slot {
     int e, row0, nrows;  // expert (-1: none), first row, rows of the tile (at most TM)
 };

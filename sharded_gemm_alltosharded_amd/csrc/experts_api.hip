@@ -465,6 +465,7 @@ sg_status sg_experts_all_to_sharded_backward(const sg_experts* x, const void* a,
     if (!st && dw) st = check_gather(T, ldx, x->l.in, rows, k, R);
     if (!st) st = check_backward(x, a, dy, R, dx, dx_dtype, dw, dw_dtype);
     if (!st) st = check_bytes(R, x->l.f * x->l.S, 4);
+    if (!st && dw) st = check_bytes(T, ldx, 4);
     if (st) return st;
     const sg::ExpertsLayout& l = x->l;
     const int64_t n = l.f * l.S;  // columns of a rank
@@ -524,6 +525,7 @@ sg_status sg_experts_sharded_to_all_backward(const sg_experts* x, const void* h,
     if (!st) st = check_rows(x, offsets, R);
     if (!st) st = check_backward(x, h, dy, R, dh, dh_dtype, dw, dw_dtype);
     if (!st) st = check_bytes(R, x->l.out, 4);
+    if (!st) st = check_bytes(R, x->l.kl, 4);
     if (st) return st;
     const sg::ExpertsLayout& l = x->l;
     hipStream_t s = (hipStream_t)stream;

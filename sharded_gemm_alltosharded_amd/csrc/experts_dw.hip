@@ -10,50 +10,36 @@
 
 namespace sg {
 
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 namespace {
 
-template <bool F16>
-__device__ __forceinline__ f32x4 mfma16(u32x4 w, u32x4 a, f32x4 c) {
-    if constexpr (F16)
-        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, w), __builtin_bit_cast(f16x8, a), c, 0,
-                                                      0, 0);
-    else
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), __builtin_bit_cast(bf16x8, a),
-                                                       c, 0, 0, 0);
-}
-
-// A tile row is 256 bytes (128 columns) in LDS; its 32-byte pieces are
-// XOR-swizzled so that the sixteen rows one transposed read touches
-// (8 c + 0 .. 3 for c = 0 .. 3) spread over all eight.
+// A tile row's 32-byte pieces are XOR-swizzled in LDS so that the sixteen rows
+// one transposed read touches (8 c + 0 .. 3 for c = 0 .. 3) spread over all
+// banks.
 __device__ __forceinline__ int swz(int row) { return (row & 3) | (((row >> 3) & 1) << 2); }
 
-__device__ __forceinline__ u32x2 read_tr(const uint16_t* p) {
-    return __builtin_bit_cast(
-        u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p));
-}
-
-// 128 x 128 outputs, four waves of 64 x 64, 64 rows a tile, staged through
-// registers into two LDS buffers.
-template <bool F16, bool AL>
-__global__ __launch_bounds__(256) void grouped_dw_kernel(GroupedDw p, int tiles_o, int tiles_i) {
-    __shared__ __attribute__((aligned(1024))) uint16_t sG[2][64 * 128], sX[2][64 * 128];
+// TO x TI outputs, WO x WI waves, 64 contracted rows a tile, two LDS stages
+// filled straight from memory as in the grouped tile kernel (experts.hip).  The
+// gather map's entries are read two tiles ahead, so that no load waits for its
+// own address (4096 tokens, 8 experts, 28672 x 4096: 12.3 ms when it did).
+// Experts without rows get zeros.
+template <bool F16, int TO, int TI, int WO, int WI, bool AL>
+__global__ __launch_bounds__(64 * WO * WI) void grouped_dw_kernel(GroupedDw p, int tiles_o, int tiles_i) {
+    constexpr int NWV = WO * WI, NBO = TO / WO / 16, NBI = TI / WI / 16;
+    constexpr int LG = 64 * TO * 2 / 1024 / NWV, LX = 64 * TI * 2 / 1024 / NWV;  // 1 KB loads of a wave
+    constexpr int CG = TO / 8, CX = TI / 8;                                    // 16-byte chunks of a row
+    __shared__ __attribute__((aligned(1024))) uint8_t sG0[64 * TO * 2], sG1[64 * TO * 2], sX0[64 * TI * 2],
+        sX1[64 * TI * 2];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int tile = xcd_remap(blockIdx.x, gridDim.x);
     const int per = tiles_o * tiles_i;
     const int er = tile / per, tin = tile - er * per;
     const int e = er / p.P, r = er - e * p.P;
-    constexpr int GM = 8;
+    constexpr int GM = 4;
     const int g = tin / (GM * tiles_i), first = g * GM, gsz = min(GM, tiles_o - first);
     const int tt = tin - g * GM * tiles_i;
-    const int o0 = (first + tt % gsz) * 128, i0 = tt / gsz * 128;
+    const int o0 = (first + tt % gsz) * TO, i0 = tt / gsz * TI;
     int m0 = 0, m1 = p.R;
     if (p.offsets) {
         m0 = min(max(p.offsets[e], 0), p.R);
@@ -61,99 +47,129 @@ __global__ __launch_bounds__(256) void grouped_dw_kernel(GroupedDw p, int tiles_
     }
     const uint16_t* G = (const uint16_t*)p.G + r * p.g_rank;
     const uint16_t* X = (const uint16_t*)p.X + r * p.x_rank;
+    const __amdgpu_buffer_rsrc_t bg = buffer(G, ((int64_t)(p.R - 1) * p.ldg + p.O) * 2);
+    const __amdgpu_buffer_rsrc_t bx = buffer(X, ((int64_t)(p.T - 1) * p.ldx + p.I) * 2);
 
-    // thread: chunk tid & 15 (8 columns) of rows (tid >> 4) + 16 i
-    const int ch = tid & 15;
-    u32x4 rg[4], rx[4];
-    auto load8 = [&](const uint16_t* a, int64_t row, int64_t ld, int c, int n) -> u32x4 {
-        if constexpr (AL) {
-            if (row < 0 || c >= n) return u32x4{0, 0, 0, 0};
-            return *(const u32x4*)(a + row * ld + c);
-        } else {
-            uint32_t h[8];
+    // load i of a wave: tile row (i NWV + wave) 64 / C + lane / C, LDS chunk lane % C
+    int gcol[LG], xcol[LX], raw[LX];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) h[q] = row >= 0 && c + q < n ? a[row * ld + c + q] : 0;
-            return u32x4{h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16)};
+    for (int i = 0; i < LG; ++i) {
+        const int m = (i * NWV + wave) * (64 / CG) + lane / CG;
+        gcol[i] = o0 + 8 * ((lane % CG) ^ (swz(m) << 1));
+    }
+#pragma unroll
+    for (int i = 0; i < LX; ++i) {
+        const int m = (i * NWV + wave) * (64 / CX) + lane / CX;
+        xcol[i] = i0 + 8 * ((lane % CX) ^ (swz(m) << 1));
+    }
+    auto fetch_rows = [&](int mt) ALWAYS_INLINE {  // the gather map of tile mt
+        if (!p.rows) return;
+#pragma unroll
+        for (int i = 0; i < LX; ++i) {
+            const int m = mt + (i * NWV + wave) * (64 / CX) + lane / CX;
+            raw[i] = p.rows[min(m, p.R - 1)];
         }
     };
-    auto load = [&](int mt) {
+    auto load_g = [&](int mt, uint8_t* s) ALWAYS_INLINE {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int m = mt + (tid >> 4) + 16 * i;
-            rg[i] = load8(G, m < m1 ? m : -1, p.ldg, o0 + 8 * ch, p.O);
-            rx[i] = load8(X, m < m1 ? grouped_row(p.rows, p.kdiv, p.T, m) : -1, p.ldx, i0 + 8 * ch, p.I);
+        for (int i = 0; i < LG; ++i) {
+            const int m = mt + (i * NWV + wave) * (64 / CG) + lane / CG;
+            uint8_t* to = s + (i * NWV + wave) * 1024;
+            if constexpr (AL)
+                dma16(bg, m < m1 && gcol[i] < p.O ? (uint32_t)((m * p.ldg + gcol[i]) * 2) : kOutside, 0, to);
+            else
+                *(u32x4*)(to + lane * 16) = load8_any(G, m < m1 ? m : -1, p.ldg, gcol[i], p.O);
         }
     };
-    auto stage = [&](int buf) {
+    auto load_x = [&](int mt, uint8_t* s) ALWAYS_INLINE {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int m = (tid >> 4) + 16 * i;
-            const int at = m * 128 + ((ch ^ (swz(m) << 1)) << 3);
-            *(u32x4*)(sG[buf] + at) = rg[i];
-            *(u32x4*)(sX[buf] + at) = rx[i];
+        for (int i = 0; i < LX; ++i) {
+            const int m = mt + (i * NWV + wave) * (64 / CX) + lane / CX;
+            uint8_t* to = s + (i * NWV + wave) * 1024;
+            int row = m;
+            if (p.rows) row = raw[i] < 0 ? -1 : (int)((uint32_t)raw[i] / (uint32_t)p.kdiv);
+            if (m >= m1 || row >= p.T) row = -1;
+            if constexpr (AL)
+                dma16(bx, row >= 0 && xcol[i] < p.I ? (uint32_t)((row * p.ldx + xcol[i]) * 2) : kOutside, 0, to);
+            else
+                *(u32x4*)(to + lane * 16) = load8_any(X, row, p.ldx, xcol[i], p.I);
         }
     };
 
-    f32x4 acc[4][4];
+    f32x4 acc[NBI][NBO];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < NBI; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < NBO; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     const int c16 = lane >> 4, r16 = lane & 15;
-    const int wo = (wave & 1) * 64, wi = (wave >> 1) * 64;
-    // operand of columns col .. col + 15: contracted rows 32 kk + 8 c16 + 0 .. 7
-    auto operand = [&](const uint16_t* s, int col, int kk) -> u32x4 {
-        const int row = 32 * kk + 8 * c16 + (r16 >> 2);
-        const int c = (col >> 3) + ((r16 & 3) >> 1);  // 16-byte chunk
-        const uint16_t* a = s + 4 * (r16 & 1);
-        const u32x2 lo = read_tr(a + row * 128 + ((c ^ (swz(row) << 1)) << 3));
-        const u32x2 hi = read_tr(a + (row + 4) * 128 + ((c ^ (swz(row + 4) << 1)) << 3));
+    const int wo = (wave % WO) * (TO / WO), wi = (wave / WO) * (TI / WI);
+    // contracted rows 32 kk + 8 c16 + 0 .. 7 of columns col .. col + 15
+    auto operand = [&](const uint8_t* s, int rowb, int col, int kk) ALWAYS_INLINE -> u32x4 {
+        const int row = 32 * kk + 8 * c16 + (r16 >> 2);  // (row + 4 has the same swizzle)
+        const int c = (col >> 3) + ((r16 & 3) >> 1);
+        const uint8_t* a = s + row * rowb + ((c ^ (swz(row) << 1)) << 4) + 8 * (r16 & 1);
+        const u32x2 lo = read_tr(a), hi = read_tr(a + 4 * rowb);
         return u32x4{lo[0], lo[1], hi[0], hi[1]};
     };
-
-    if (m0 < m1) {
-        load(m0);
-        stage(0);
-        __syncthreads();
-        int buf = 0;
-        for (int mt = m0; mt < m1; mt += 64, buf ^= 1) {
-            if (mt + 64 < m1) load(mt + 64);
+    auto step = [&](int mt, const uint8_t* sG, const uint8_t* sX, uint8_t* nG, uint8_t* nX) ALWAYS_INLINE {
+        wait_loads();  // this wave's loads have landed; behind the barrier every wave's
+        __builtin_amdgcn_s_barrier();
+        static_for<0, 2>([&](auto kc) ALWAYS_INLINE {
+            constexpr int kk = decltype(kc)::value;
+            u32x4 gf[NBO], xf[NBI];
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-                u32x4 gf[4], xf[4];
+            for (int i = 0; i < NBI; ++i) xf[i] = operand(sX, TI * 2, wi + 16 * i, kk);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    xf[i] = operand(sX[buf], wi + 16 * i, kk);
-                    gf[i] = operand(sG[buf], wo + 16 * i, kk);
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[i][j] = mfma16<F16>(xf[i], gf[j], acc[i][j]);
+            for (int j = 0; j < NBO; ++j) gf[j] = operand(sG, TO * 2, wo + 16 * j, kk);
+            // (past the last tile: zeros, into a stage never read)
+            if constexpr (kk == 0) load_x(mt + 64, nX);
+            else {
+                load_g(mt + 64, nG);
+                fetch_rows(mt + 128);
             }
-            if (mt + 64 < m1) stage(buf ^ 1);
-            __syncthreads();
+            __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+            for (int j = 0; j < NBO; ++j)
+#pragma unroll
+                for (int i = 0; i < NBI; ++i) acc[i][j] = mfma16<F16>(xf[i], gf[j], acc[i][j]);
+            __builtin_amdgcn_s_setprio(0);
+        });
+    };
+    if (m0 < m1) {
+        fetch_rows(m0);
+        load_x(m0, sX0);
+        load_g(m0, sG0);
+        fetch_rows(m0 + 64);
+        for (int mt = m0; mt < m1; mt += 128) {
+            step(mt, sG0, sX0, sG1, sX1);
+            if (mt + 64 < m1) step(mt + 64, sG1, sX1, sG0, sX0);
         }
+        wait_loads();  // none may still be writing this workgroup's LDS when it ends
     }
 
     // lane: output row o = .. + r16, columns 4 c16 .. + 3 of each block
     const int64_t base = (int64_t)er * p.O * p.I;
-    static_for<0, 4>([&](auto jc) {
-        constexpr int j = decltype(jc)::value;
-        const int o = o0 + wo + 16 * j + r16;
-        if (o >= p.O) return;
-        static_for<0, 4>([&](auto ic) {
-            constexpr int i = decltype(ic)::value;
-            const int c = i0 + wi + 16 * i + 4 * c16;
-            if (c >= p.I) return;
-            const int64_t at = base + (int64_t)o * p.I + c;
-            const f32x4 v = acc[i][j];
-            if (p.vec) {
-                if (p.out_dtype == SG_F32) {
+    auto put = [&](auto dt) ALWAYS_INLINE {
+        constexpr int DT = decltype(dt)::value;  // -1: any type and alignment
+        static_for<0, NBO>([&](auto jc) {
+            constexpr int j = decltype(jc)::value;
+            const int o = o0 + wo + 16 * j + r16;
+            if (o >= p.O) return;
+            static_for<0, NBI>([&](auto ic) {
+                constexpr int i = decltype(ic)::value;
+                const int c = i0 + wi + 16 * i + 4 * c16;
+                if (c >= p.I) return;
+                const int64_t at = base + (int64_t)o * p.I + c;
+                const f32x4 v = acc[i][j];
+                if constexpr (DT < 0) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (c + q < p.I) store_from_f32(p.out, p.out_dtype, at + q, v[q]);
+                } else if constexpr (DT == SG_F32) {
                     *(f32x4*)((float*)p.out + at) = v;
                 } else {
                     u32x2 w;
-                    if (p.out_dtype == SG_BF16) {
+                    if constexpr (DT == SG_BF16) {
                         w[0] = f32_to_bf16(v[0]) | ((uint32_t)f32_to_bf16(v[1]) << 16);
                         w[1] = f32_to_bf16(v[2]) | ((uint32_t)f32_to_bf16(v[3]) << 16);
                     } else {
@@ -162,32 +178,39 @@ __global__ __launch_bounds__(256) void grouped_dw_kernel(GroupedDw p, int tiles_
                     }
                     *(u32x2*)((uint16_t*)p.out + at) = w;
                 }
-            } else {
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    if (c + q < p.I) store_from_f32(p.out, p.out_dtype, at + q, v[q]);
-            }
+            });
         });
-    });
+    };
+    if (!p.vec) put(std::integral_constant<int, -1>{});
+    else if (p.out_dtype == SG_BF16) put(std::integral_constant<int, SG_BF16>{});
+    else if (p.out_dtype == SG_F16) put(std::integral_constant<int, SG_F16>{});
+    else put(std::integral_constant<int, SG_F32>{});
+}
+
+template <bool F16, int TO, int TI, int WO, int WI, bool AL>
+hipError_t dw_launch(const GroupedDw& p, hipStream_t s) {
+    const int64_t to = (p.O + TO - 1) / TO, ti = (p.I + TI - 1) / TI;
+    const int64_t blocks = (int64_t)p.E * p.P * to * ti;
+    if (blocks >= kMaxBlocks / 2) return hipErrorInvalidConfiguration;
+    launch(grouped_dw_kernel<F16, TO, TI, WO, WI, AL>, dim3((unsigned)blocks), dim3(64 * WO * WI), 0, s, p, (int)to,
+           (int)ti);
+    return hipGetLastError();
+}
+
+template <bool F16>
+hipError_t dw_type(const GroupedDw& p, hipStream_t s) {
+    const bool al = (uintptr_t)p.G % 16 == 0 && (uintptr_t)p.X % 16 == 0 && p.ldg % 8 == 0 && p.ldx % 8 == 0 &&
+                    p.g_rank % 8 == 0 && p.x_rank % 8 == 0 && p.O % 8 == 0 && p.I % 8 == 0;
+    if (!al) return dw_launch<F16, 128, 128, 2, 2, false>(p, s);
+    const int64_t big = (int64_t)p.E * p.P * ((p.O + 255) / 256) * ((p.I + 255) / 256);
+    if (big >= 2 * device_cus()) return dw_launch<F16, 256, 256, 2, 4, true>(p, s);
+    return dw_launch<F16, 128, 128, 2, 2, true>(p, s);
 }
 
 }  // namespace
 
 hipError_t launch_grouped_dw(const GroupedDw& p, hipStream_t s) {
-    const int64_t to = (p.O + 127) / 128, ti = (p.I + 127) / 128;
-    const int64_t blocks = (int64_t)p.E * p.P * to * ti;
-    if (blocks >= kMaxBlocks) return hipErrorInvalidConfiguration;
-    const dim3 grid((unsigned)blocks);
-    const bool al = (uintptr_t)p.G % 16 == 0 && (uintptr_t)p.X % 16 == 0 && p.ldg % 8 == 0 && p.ldx % 8 == 0 &&
-                    p.g_rank % 8 == 0 && p.x_rank % 8 == 0 && p.O % 8 == 0 && p.I % 8 == 0;
-    auto go = [&](auto f16, auto a) {
-        launch(grouped_dw_kernel<decltype(f16)::value, decltype(a)::value>, grid, dim3(256), 0, s, p, (int)to, (int)ti);
-    };
-    using T = std::true_type;
-    using F = std::false_type;
-    if (p.f16) al ? go(T{}, T{}) : go(T{}, F{});
-    else al ? go(F{}, T{}) : go(F{}, F{});
-    return hipGetLastError();
+    return p.f16 ? dw_type<true>(p, s) : dw_type<false>(p, s);
 }
 
 }  // namespace sg

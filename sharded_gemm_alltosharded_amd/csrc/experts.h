@@ -230,6 +230,20 @@ __device__ __forceinline__ Slot find_slot(const int32_t* offsets, int E, int R, 
     return Slot{-1, 0, 0};
 }
 
+// how many tiles of TM rows there are
+__device__ __forceinline__ int count_slots(const int32_t* offsets, int E, int R, int TM) {
+    if (!offsets) return (R + TM - 1) / TM;
+    const int lane = threadIdx.x & 63;
+    int t = 0;
+    for (int e = lane; e < E; e += 64) {
+        const int b = min(max(offsets[e], 0), R);
+        t += (max(min(offsets[e + 1], R) - b, 0) + TM - 1) / TM;
+    }
+#pragma unroll
+    for (int d = 32; d; d >>= 1) t += __shfl_xor(t, d);
+    return __builtin_amdgcn_readfirstlane(t);
+}
+
 // input row of grouped row m (-1: reads zeros)
 __device__ __forceinline__ int grouped_row(const int32_t* rows, int kdiv, int T, int m) {
     if (!rows) return m < T ? m : -1;

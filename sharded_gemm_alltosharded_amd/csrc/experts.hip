@@ -295,6 +295,11 @@ __global__ __launch_bounds__(64 * WM * WN) void grouped_tile_kernel(Grouped p, i
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wave_m = wave % WM, wave_n = wave / WM;
+    // The launch has room for every way the rows may fall on the experts; the
+    // tiles that there are, not that room, are dealt out to the XCDs.  (Falling
+    // offsets could count more: those are left out.)
+    slots = min(slots, count_slots(p.offsets, p.E, p.R, TM));
+    if ((int)blockIdx.x >= slots * tiles_n) return;
     const int tile = xcd_remap(blockIdx.x, slots * tiles_n);
     constexpr int GM = 4;
     const int g = tile / (GM * tiles_n), first = g * GM, gsz = min(GM, slots - first);

@@ -32,9 +32,11 @@ __global__ __launch_bounds__(64 * WO * WI) void grouped_dw_kernel(GroupedDw p, i
         sX1[64 * TI * 2];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int tile = xcd_remap(blockIdx.x, gridDim.x);
-    const int per = tiles_o * tiles_i;
-    const int er = tile / per, tin = tile - er * per;
+    // every XCD takes a run of tiles of every expert: experts differ in rows
+    // (whole experts to an XCD: 4.5 ms where this takes 2.4)
+    const int per = tiles_o * tiles_i, run = (per + 7) / 8;
+    const int er = (blockIdx.x / 8) / run, tin = (blockIdx.x % 8) * run + (blockIdx.x / 8) % run;
+    if (tin >= per) return;
     const int e = er / p.P, r = er - e * p.P;
     constexpr int GM = 4;
     const int g = tin / (GM * tiles_i), first = g * GM, gsz = min(GM, tiles_o - first);
@@ -190,7 +192,7 @@ __global__ __launch_bounds__(64 * WO * WI) void grouped_dw_kernel(GroupedDw p, i
 template <bool F16, int TO, int TI, int WO, int WI, bool AL>
 hipError_t dw_launch(const GroupedDw& p, hipStream_t s) {
     const int64_t to = (p.O + TO - 1) / TO, ti = (p.I + TI - 1) / TI;
-    const int64_t blocks = (int64_t)p.E * p.P * to * ti;
+    const int64_t blocks = (int64_t)p.E * p.P * ((to * ti + 7) / 8 * 8);
     if (blocks >= kMaxBlocks / 2) return hipErrorInvalidConfiguration;
     launch(grouped_dw_kernel<F16, TO, TI, WO, WI, AL>, dim3((unsigned)blocks), dim3(64 * WO * WI), 0, s, p, (int)to,
            (int)ti);

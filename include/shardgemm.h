@@ -434,7 +434,8 @@ sg_status sg_swiglu_backward(const void* gu, const void* dh, sg_dtype dtype, int
  *   rows     (T k): the slot of each grouped row, in slot order for each
  *            expert; -1 behind the last.
  *   slots    (T, k): the grouped row of each slot, -1 if dropped.
- *   workspace sg_moe_route_workspace(T, E, k) bytes, no initial contents. */
+ *   workspace sg_moe_route_workspace(T, E, k) bytes (0 for few slots), no
+ *            initial contents; calls that share it must not overlap. */
 sg_status sg_moe_route(const void* logits, int64_t ld, sg_dtype dtype, int64_t T, int E, int k, int normalize,
                        float* weights, int32_t* experts, int32_t* offsets, int32_t* rows, int32_t* slots,
                        void* workspace, size_t ws_bytes, void* stream);

@@ -469,17 +469,39 @@ def _bad(message: str):
     raise ShardGemmError(ERR_INVALID_ARG, message)
 
 
+_FLOATS = tuple(_DT)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _run(fn, dev: torch.device, *args):
+    """fn(*args, stream) on dev's current stream, with dev current.  (These calls
+    are short: with the public stream object and an unconditional device guard
+    the binding took longer than the kernels of a decoding step.)"""
+    i = dev.index
+    if torch.cuda.current_device() != i:
+        with torch.cuda.device(i):
+            return _run(fn, dev, *args)
+    rc = fn(*args, _raw_stream(i) if _raw_stream is not None else torch.cuda.current_stream(i).cuda_stream)
+    if rc != OK:
+        _check(rc)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
 def _want(t, name: str, shape=None, dtype=None, device=None, optional=False):
     """One tensor argument: packed, of the shape (None: any extent), dtype and device asked for."""
     if t is None:
         if not optional:
             _bad(f"{name} is None")
         return None
-    if shape is not None and (t.dim() != len(shape) or any(w is not None and w != h for w, h in zip(shape, t.shape))):
+    if shape is not None and tuple(t.shape) != shape and (
+            t.dim() != len(shape) or any(w is not None and w != h for w, h in zip(shape, t.shape))):
         _bad(f"{name} has shape {tuple(t.shape)}, not {tuple('any' if w is None else w for w in shape)}")
-    if dtype is not None and t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+    if dtype is not None and t.dtype is not dtype and t.dtype not in (dtype if isinstance(dtype, tuple) else ()):
         _bad(f"{name} has dtype {t.dtype}")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         _bad(f"{name} is on {t.device}, not on a GPU")
     if device is not None and t.device != device:
         _bad(f"{name} is on {t.device}, not on {device}")
@@ -488,27 +510,28 @@ def _want(t, name: str, shape=None, dtype=None, device=None, optional=False):
     return t
 
 
-def _matrix(t, name: str, width=None, dtype=None, device=None):
-    """A (rows, width) argument whose rows may be strided: the tensor and its row stride."""
+def _matrix(t, name: str, width=None, dtype=_FLOATS, device=None):
+    """A (rows, width) argument whose rows may be strided: its row stride."""
     if t.dim() != 2 or (width is not None and t.shape[1] != width):
         _bad(f"{name} has shape {tuple(t.shape)}, not (any, {width})")
-    if dtype is not None and t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+    if t.dtype is not dtype and t.dtype not in (dtype if isinstance(dtype, tuple) else ()):
         _bad(f"{name} has dtype {t.dtype}")
-    if t.device.type != "cuda" or (device is not None and t.device != device):
+    if not t.is_cuda or (device is not None and t.device != device):
         _bad(f"{name} is on {t.device}, not on {device or 'a GPU'}")
     rows, cols = t.shape
+    if t.is_contiguous():
+        return cols
     if cols > 1 and t.stride(1) != 1 or rows > 1 and t.stride(0) < cols:
         _bad(f"{name} has strides {t.stride()}: its columns must be adjacent and its rows apart")
-    return t, (t.stride(0) if rows > 1 else cols)
+    return t.stride(0) if rows > 1 else cols
 
 
 def _out(out, name: str, shape, dtype, device):
     if out is None:
+        if dtype not in _DT:
+            _bad(f"{name} cannot be {dtype}")
         return torch.empty(shape, dtype=dtype, device=device)
-    return _want(out, name, shape, tuple(_DT), device)
-
-
-_FLOATS = tuple(_DT)
+    return _want(out, name, shape, _FLOATS, device)
 
 
 class Experts:
@@ -535,8 +558,7 @@ class Experts:
     def update(self, weight: torch.Tensor):
         """New weights (E, out, in) into the layer, on the current stream."""
         _want(weight, "weight", (self.E, self.out_dims, self.in_dims), self.dtype, self.device)
-        with torch.cuda.device(self.device):
-            _check(lib().sg_experts_update(self.handle, _ptr(weight), _stream(self.device)))
+        _run(lib().sg_experts_update, self.device, self.handle, _at(weight))
 
     def free(self):
         if self._h is not None and _lib is not None:
@@ -595,7 +617,7 @@ def experts_all_to_sharded(layer: Experts, x: torch.Tensor, offsets=None, rows=N
     x_scales: x is MXFP4 codes (T, in / 2) with these scales (T, in / 32)."""
     dev = layer.device
     if x_scales is None:
-        x, ld = _matrix(x, "x", layer.in_dims, layer.dtype, dev)
+        ld = _matrix(x, "x", layer.in_dims, layer.dtype, dev)
     else:
         _want(x, "x", (None, layer.in_dims // 2), torch.uint8, dev)
         _want(x_scales, "x_scales", (x.shape[0], layer.in_dims // 32), torch.uint8, dev)
@@ -604,10 +626,8 @@ def experts_all_to_sharded(layer: Experts, x: torch.Tensor, offsets=None, rows=N
     _grouped(layer, offsets, rows, R)
     n = layer.out_dims // 2 if swiglu else layer.out_dims
     out = _out(out, "out", (layer.P, R, n // layer.P), out_dtype or layer.dtype, dev)
-    with torch.cuda.device(dev):
-        _check(lib().sg_experts_all_to_sharded(layer.handle, _ptr(x), _ptr(x_scales), x.shape[0], ld, _ptr(offsets),
-                                               _ptr(rows), k, R, _ptr(out), EPI_SWIGLU if swiglu else EPI_NONE,
-                                               _DT[out.dtype], _stream(dev)))
+    _run(lib().sg_experts_all_to_sharded, dev, layer.handle, _at(x), _at(x_scales), x.shape[0], ld, _at(offsets),
+         _at(rows), k, R, _at(out), EPI_SWIGLU if swiglu else EPI_NONE, _DT[out.dtype])
     return out
 
 
@@ -624,9 +644,8 @@ def experts_sharded_to_all(layer: Experts, h: torch.Tensor, offsets=None, h_scal
     R = h.shape[1]
     _grouped(layer, offsets, None, R)
     out = _out(out, "out", (R, layer.out_dims), out_dtype or layer.dtype, dev)
-    with torch.cuda.device(dev):
-        _check(lib().sg_experts_sharded_to_all(layer.handle, _ptr(h), _ptr(h_scales), _ptr(offsets), R, _ptr(out),
-                                               _DT[out.dtype], _stream(dev)))
+    _run(lib().sg_experts_sharded_to_all, dev, layer.handle, _at(h), _at(h_scales), _at(offsets), R, _at(out),
+         _DT[out.dtype])
     return out
 
 
@@ -639,15 +658,13 @@ def experts_all_to_sharded_backward(layer: Experts, x: torch.Tensor | None, dy: 
     _want(dy, "dy", (layer.P, None, n), layer.dtype, dev)
     R, T, ld = dy.shape[1], 0, layer.in_dims
     if need_dw:
-        x, ld = _matrix(x, "x", layer.in_dims, layer.dtype, dev)
+        ld = _matrix(x, "x", layer.in_dims, layer.dtype, dev)
         T = x.shape[0]
     _grouped(layer, offsets, rows, R)
-    dx = torch.empty((R, layer.in_dims), dtype=dx_dtype or layer.dtype, device=dev) if need_dx else None
-    dw = torch.empty((layer.E, layer.P, n, layer.in_dims), dtype=dw_dtype, device=dev) if need_dw else None
-    with torch.cuda.device(dev):
-        _check(lib().sg_experts_all_to_sharded_backward(
-            layer.handle, _ptr(x) if need_dw else None, T, ld, _ptr(dy), _ptr(offsets), _ptr(rows), k, R, _ptr(dx),
-            _DT.get(dx_dtype or layer.dtype, -1), _ptr(dw), _DT.get(dw_dtype, -1), _stream(dev)))
+    dx = _out(None, "dx", (R, layer.in_dims), dx_dtype or layer.dtype, dev) if need_dx else None
+    dw = _out(None, "dw", (layer.E, layer.P, n, layer.in_dims), dw_dtype, dev) if need_dw else None
+    _run(lib().sg_experts_all_to_sharded_backward, dev, layer.handle, _at(x) if need_dw else None, T, ld, _at(dy),
+         _at(offsets), _at(rows), k, R, _at(dx), _DT.get(dx_dtype or layer.dtype, -1), _at(dw), _DT.get(dw_dtype, -1))
     return dx, dw
 
 
@@ -661,12 +678,10 @@ def experts_sharded_to_all_backward(layer: Experts, h: torch.Tensor | None, dy: 
     if need_dw:
         _want(h, "h", (layer.P, R, kr), layer.dtype, dev)
     _grouped(layer, offsets, None, R)
-    dh = torch.empty((layer.P, R, kr), dtype=dx_dtype or layer.dtype, device=dev) if need_dx else None
-    dw = torch.empty((layer.E, layer.P, layer.out_dims, kr), dtype=dw_dtype, device=dev) if need_dw else None
-    with torch.cuda.device(dev):
-        _check(lib().sg_experts_sharded_to_all_backward(
-            layer.handle, _ptr(h) if need_dw else None, _ptr(dy), _ptr(offsets), R, _ptr(dh),
-            _DT.get(dx_dtype or layer.dtype, -1), _ptr(dw), _DT.get(dw_dtype, -1), _stream(dev)))
+    dh = _out(None, "dx", (layer.P, R, kr), dx_dtype or layer.dtype, dev) if need_dx else None
+    dw = _out(None, "dw", (layer.E, layer.P, layer.out_dims, kr), dw_dtype, dev) if need_dw else None
+    _run(lib().sg_experts_sharded_to_all_backward, dev, layer.handle, _at(h) if need_dw else None, _at(dy),
+         _at(offsets), R, _at(dh), _DT.get(dx_dtype or layer.dtype, -1), _at(dw), _DT.get(dw_dtype, -1))
     return dh, dw
 
 
@@ -677,8 +692,7 @@ def swiglu(gu: torch.Tensor) -> torch.Tensor:
         _bad(f"gu has shape {tuple(gu.shape)}: its rows must be [gate; up]")
     f = gu.shape[-1] // 2
     h = torch.empty((*gu.shape[:-1], f), dtype=gu.dtype, device=gu.device)
-    with torch.cuda.device(gu.device):
-        _check(lib().sg_swiglu(_ptr(gu), _DT[gu.dtype], gu.numel() // (2 * f), f, _ptr(h), _stream(gu.device)))
+    _run(lib().sg_swiglu, gu.device, _at(gu), _DT[gu.dtype], gu.numel() // (2 * f), f, _at(h))
     return h
 
 
@@ -690,34 +704,32 @@ def swiglu_backward(gu: torch.Tensor, dh: torch.Tensor) -> torch.Tensor:
     f = gu.shape[-1] // 2
     _want(dh, "dh", (*gu.shape[:-1], f), gu.dtype, gu.device)
     dgu = torch.empty_like(gu)
-    with torch.cuda.device(gu.device):
-        _check(lib().sg_swiglu_backward(_ptr(gu), _ptr(dh), _DT[gu.dtype], gu.numel() // (2 * f), f, _ptr(dgu),
-                                        _stream(gu.device)))
+    _run(lib().sg_swiglu_backward, gu.device, _at(gu), _at(dh), _DT[gu.dtype], gu.numel() // (2 * f), f, _at(dgu))
     return dgu
 
 
 def moe_route(logits: torch.Tensor, k: int, normalize: bool = True) -> Route:
     """The k experts of every token and the plan that groups the slots
     (sg_moe_route).  logits (T, E), -inf where an expert is closed to a token."""
-    logits, ld = _matrix(logits, "logits", None, _FLOATS)
+    ld = _matrix(logits, "logits")
     T, E = logits.shape
-    dev = logits.device
-    need = int(lib().sg_moe_route_workspace(T, E, k))
+    dev, L = logits.device, lib()
     n = max(T * k, 0)
+    # one allocation; the workspace (none for few slots) may end it: only this call uses it
+    need = L.sg_moe_route_workspace(T, E, k)
     buf = torch.empty((4 * n + E + 1 + need // 4,), dtype=torch.int32, device=dev)
-    w = buf[:n].view(torch.float32).view(T, -1) if n else buf.new_empty((T, max(k, 0)), dtype=torch.float32)
-    e, rows, slots = buf[n:2 * n].view(w.shape), buf[2 * n:3 * n], buf[3 * n:4 * n].view(w.shape)
-    offsets, ws = buf[4 * n:4 * n + E + 1], buf[4 * n + E + 1:]
-    with torch.cuda.device(dev):
-        _check(lib().sg_moe_route(_ptr(logits), ld, _DT[logits.dtype], T, E, k, int(normalize), _ptr(w), _ptr(e),
-                                  _ptr(offsets), _ptr(rows), _ptr(slots), _ptr(ws), need, _stream(dev)))
+    w, e, rows, slots, offsets, ws = buf.split_with_sizes((n, n, n, n, E + 1, need // 4))
+    shape = (T, max(k, 0))
+    w, e, slots = w.view(torch.float32).view(shape), e.view(shape), slots.view(shape)
+    _run(L.sg_moe_route, dev, _at(logits), ld, _DT[logits.dtype], T, E, k, int(normalize), _at(w), _at(e), _at(offsets),
+         _at(rows), _at(slots), _at(ws), need)
     return Route(w, e, offsets, rows, slots)
 
 
 def moe_route_backward(logits: torch.Tensor, route: Route, dweights: torch.Tensor,
                        normalize: bool = True) -> torch.Tensor:
     """Gradient of the router's weights: dweights (T, k) -> dlogits (T, E) (sg_moe_route_backward)."""
-    logits, ld = _matrix(logits, "logits", None, _FLOATS)
+    ld = _matrix(logits, "logits")
     T, E = logits.shape
     dev = logits.device
     k = route.weights.shape[-1]
@@ -725,10 +737,8 @@ def moe_route_backward(logits: torch.Tensor, route: Route, dweights: torch.Tenso
     _want(route.experts, "experts", (T, k), torch.int32, dev)
     _want(dweights, "dweights", (T, k), torch.float32, dev)
     dz = torch.empty((T, E), dtype=logits.dtype, device=dev)
-    with torch.cuda.device(dev):
-        _check(lib().sg_moe_route_backward(_ptr(logits), ld, _DT[logits.dtype], T, E, k, int(normalize),
-                                           _ptr(route.weights), _ptr(route.experts), _ptr(dweights), _ptr(dz),
-                                           _stream(dev)))
+    _run(lib().sg_moe_route_backward, dev, _at(logits), ld, _DT[logits.dtype], T, E, k, int(normalize),
+         _at(route.weights), _at(route.experts), _at(dweights), _at(dz))
     return dz
 
 
@@ -742,9 +752,8 @@ def moe_combine(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor | No
     T, k = slots.shape
     _want(weights, "weights", (T, k), torch.float32, dev, optional=True)
     out = _out(out, "out", (T, y.shape[1]), out_dtype or y.dtype, dev)
-    with torch.cuda.device(dev):
-        _check(lib().sg_moe_combine(_ptr(y), _DT[y.dtype], y.shape[0], _ptr(slots), _ptr(weights), T, k, y.shape[1],
-                                    _ptr(out), _DT[out.dtype], _stream(dev)))
+    _run(lib().sg_moe_combine, dev, _at(y), _DT[y.dtype], y.shape[0], _at(slots), _at(weights), T, k, y.shape[1],
+         _at(out), _DT[out.dtype])
     return out
 
 
@@ -765,9 +774,8 @@ def moe_combine_backward(dout: torch.Tensor, y: torch.Tensor, slots: torch.Tenso
     else:
         dy = None
     dw = torch.empty((T, k), dtype=torch.float32, device=dev) if need_dweights else None
-    with torch.cuda.device(dev):
-        _check(lib().sg_moe_combine_backward(_ptr(dout), _ptr(y), _DT[y.dtype], y.shape[0], _ptr(slots),
-                                             _ptr(weights), T, k, D, _ptr(dy), _ptr(dw), _stream(dev)))
+    _run(lib().sg_moe_combine_backward, dev, _at(dout), _at(y), _DT[y.dtype], y.shape[0], _at(slots), _at(weights), T, k,
+         D, _at(dy), _at(dw))
     return dy, dw
 
 
@@ -775,19 +783,18 @@ def moe_mlp(gate_up: Experts, down: Experts, x: torch.Tensor, route: Route, out_
             out: torch.Tensor | None = None) -> torch.Tensor:
     """The gated MLP over experts: (T, in) -> (T, out) (sg_moe_mlp)."""
     dev = gate_up.device
-    x, ld = _matrix(x, "x", gate_up.in_dims, gate_up.dtype, dev)
+    ld = _matrix(x, "x", gate_up.in_dims, gate_up.dtype, dev)
     T, k = x.shape[0], route.slots.shape[-1]
     _want(route.weights, "weights", (T, k), torch.float32, dev)
     _want(route.slots, "slots", (T, k), torch.int32, dev)
     _want(route.rows, "rows", (T * k,), torch.int32, dev)
     _want(route.offsets, "offsets", (gate_up.E + 1,), torch.int32, dev)
     out = _out(out, "out", (T, down.out_dims), out_dtype or down.dtype, dev)
-    need = int(lib().sg_moe_mlp_workspace(gate_up.handle, down.handle, T, k))
+    L = lib()
+    need = L.sg_moe_mlp_workspace(gate_up.handle, down.handle, T, k)
     ws = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
-    with torch.cuda.device(dev):
-        _check(lib().sg_moe_mlp(gate_up.handle, down.handle, _ptr(x), T, ld, _ptr(route.weights), _ptr(route.offsets),
-                                _ptr(route.rows), _ptr(route.slots), k, _ptr(out), _DT[out.dtype], _ptr(ws), need,
-                                _stream(dev)))
+    _run(L.sg_moe_mlp, dev, gate_up.handle, down.handle, _at(x), T, ld, _at(route.weights), _at(route.offsets),
+         _at(route.rows), _at(route.slots), k, _at(out), _DT[out.dtype], _at(ws), need)
     return out
 
 
@@ -795,17 +802,16 @@ def quantize_mxfp4(x: torch.Tensor):
     """(..., n) values -> MXFP4 codes (..., n / 2) and scales (..., n / 32), uint8 (sg_quantize_mxfp4)."""
     if x.dim() < 1:
         _bad("x has no columns")
-    if x.dim() == 2:
-        m, ld = _matrix(x, "x", None, _FLOATS)
-    else:
-        m, ld = _want(x, "x", None, _FLOATS), x.shape[-1]
     n = x.shape[-1]
+    if x.dim() == 2:
+        ld = _matrix(x, "x")
+    else:
+        _want(x, "x", None, _FLOATS)
+        ld = n
     rows = x.numel() // n if n else 0
     codes = torch.empty((*x.shape[:-1], n // 2), dtype=torch.uint8, device=x.device)
     scales = torch.empty((*x.shape[:-1], n // 32), dtype=torch.uint8, device=x.device)
-    with torch.cuda.device(x.device):
-        _check(lib().sg_quantize_mxfp4(_ptr(m), _DT[x.dtype], rows, n, ld, _ptr(codes), _ptr(scales),
-                                       _stream(x.device)))
+    _run(lib().sg_quantize_mxfp4, x.device, _at(x), _DT[x.dtype], rows, n, ld, _at(codes), _at(scales))
     return codes, scales
 
 
@@ -816,8 +822,7 @@ def dequantize_mxfp4(codes: torch.Tensor, scales: torch.Tensor, out_dtype=torch.
         _bad("codes has no columns")
     n = codes.shape[-1] * 2
     _want(scales, "scales", (*codes.shape[:-1], n // 32), torch.uint8, codes.device)
-    x = torch.empty((*codes.shape[:-1], n), dtype=out_dtype, device=codes.device)
-    with torch.cuda.device(codes.device):
-        _check(lib().sg_dequantize_mxfp4(_ptr(codes), _ptr(scales), x.numel() // n if n else 0, n, _ptr(x),
-                                         _DT.get(out_dtype, -1), _stream(codes.device)))
+    x = _out(None, "out", (*codes.shape[:-1], n), out_dtype, codes.device)
+    _run(lib().sg_dequantize_mxfp4, codes.device, _at(codes), _at(scales), x.numel() // n if n else 0, n, _at(x),
+         _DT[out_dtype])
     return x

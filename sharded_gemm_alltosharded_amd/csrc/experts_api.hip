@@ -591,7 +591,7 @@ sg_status sg_moe_route(const void* logits, int64_t ld, sg_dtype dtype, int64_t T
     if (!offsets || (T && (!logits || !weights || !experts || !rows || !slots)))
         return fail(SG_ERR_INVALID_ARG, "the logits and every output must not be NULL");
     const size_t need = sg_moe_route_workspace(T, E, k);
-    if (T && (!workspace || ws_bytes < need || !aligned(workspace, 4)))
+    if (need && (!workspace || ws_bytes < need || !aligned(workspace, 4)))
         return fail(SG_ERR_WORKSPACE, "sg_moe_route needs %zu bytes of workspace (got %zu)", need,
                     workspace ? ws_bytes : (size_t)0);
     r.logits = logits;

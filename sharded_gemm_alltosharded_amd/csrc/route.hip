@@ -511,6 +511,8 @@ __global__ __launch_bounds__(256) void swiglu_kernel(const void* gu, const void*
     }
 }
 
+bool small(int64_t T, int E, int k) { return T * k <= kSmallSlots && T <= 256 && E <= kSmallExperts; }
+
 int chunk_tokens_of(int64_t T, int k) {
     // about 256 slots a chunk, at most 1024 chunks
     int64_t c = (256 + k - 1) / k;
@@ -520,7 +522,7 @@ int chunk_tokens_of(int64_t T, int k) {
 
 template <int V>
 void route_v(const Route& r, hipStream_t s) {
-    if ((int64_t)r.T * r.k <= kSmallSlots && r.T <= 256 && r.E <= kSmallExperts) {
+    if (small(r.T, r.E, r.k)) {
         launch(route_small_kernel<V>, dim3(1), dim3(1024), 0, s, r);
         return;
     }
@@ -536,6 +538,7 @@ bool al16(const void* p) { return (uintptr_t)p % 16 == 0; }
 }  // namespace
 
 size_t route_workspace_ints(int64_t T, int E, int k) {
+    if (small(T, E, k)) return 0;
     const int64_t ct = chunk_tokens_of(T, k);
     return (size_t)((T + ct - 1) / ct) * E;
 }

@@ -105,9 +105,9 @@ __device__ __forceinline__ int weight_block(const Grouped& p, int ob, int i) {
 // output blocks (their sums are added in wave order through LDS), 4 / KS groups
 // stand side by side.  Steps come in runs of four, a run of loads ahead.
 // ---------------------------------------------------------------------------
-template <int MODE, bool SWIGLU, int MB, int NB, int KS, bool AL>
-__global__ __launch_bounds__(256) void grouped_stream_kernel(Grouped p) {
-    constexpr int NG = 4 / KS, NW = SWIGLU ? 2 * NB : NB;
+template <int MODE, bool SWIGLU, int MB, int NB, int KS, int NWV, bool AL>
+__global__ __launch_bounds__(64 * NWV) void grouped_stream_kernel(Grouped p) {
+    constexpr int NG = NWV / KS, NW = SWIGLU ? 2 * NB : NB;
     constexpr bool MX = MODE >= G_MX4;
     constexpr int KST = MX ? 128 : 32;               // inputs of a step
     constexpr int AF = MODE == G_MX4 ? 4 : 1;        // 16-byte operands of a step and 16 rows
@@ -272,9 +272,9 @@ __global__ __launch_bounds__(256) void grouped_stream_kernel(Grouped p) {
 // chunks of a fragment are stored four rows on, so that the two chunks of a
 // read lie in different banks.
 // ---------------------------------------------------------------------------
-template <int MODE, bool SWIGLU, bool TRANS, int TM, int BN, int WM, int WN, bool AL>
-__global__ __launch_bounds__(64 * WM * WN) void grouped_tile_kernel(Grouped p, int slots, int tiles_n) {
-    constexpr int NWV = WM * WN;
+template <int MODE, bool SWIGLU, bool TRANS, int TM, int BN, bool AL>
+__global__ __launch_bounds__(512) void grouped_tile_kernel(Grouped p, int slots, int tiles_n) {
+    constexpr int WM = 2, WN = 4, NWV = WM * WN;
     constexpr int NBM = TM / WM / 16, NBN = BN / WN / 16;
     constexpr bool MX = MODE >= G_MX4, A4 = MODE == G_MX4A4;
     constexpr int KT = A4 ? 256 : MX ? 128 : 64;
@@ -294,7 +294,9 @@ __global__ __launch_bounds__(64 * WM * WN) void grouped_tile_kernel(Grouped p, i
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wave_m = wave % WM, wave_n = wave / WM;
+    // (the WM waves of one column stand on one SIMD: where the tile has rows for
+    // one of them only, it has the SIMD for itself)
+    const int wave_m = wave / WN, wave_n = wave % WN;
     // The launch has room for every way the rows may fall on the experts; the
     // tiles that there are, not that room, are dealt out to the XCDs.  (Falling
     // offsets could count more: those are left out.)
@@ -379,7 +381,8 @@ __global__ __launch_bounds__(64 * WM * WN) void grouped_tile_kernel(Grouped p, i
     // of A, step lane & 1
     constexpr int SW = BN * FPB / 64;  // loads of a k tile's weight scales
     static_assert(!MX || SW <= NWV, "one load a wave");
-    static_assert(!A4 || TM * 2 / 64 == NWV, "one load a wave");
+    constexpr int SA = TM * 2 / 64;    // and of the rows' scales
+    static_assert(!A4 || SA <= NWV, "one load a wave");
     [[maybe_unused]] uint32_t swoff = 0, saoff = kOutside;
     [[maybe_unused]] const int ssub = (wave * 4 + (lane >> 4)) % FPB;
     if constexpr (MX) {
@@ -403,7 +406,7 @@ __global__ __launch_bounds__(64 * WM * WN) void grouped_tile_kernel(Grouped p, i
             }
         }
         if constexpr (A4)
-            dma4(buffer(p.a_scales + (int64_t)iseg * p.T * (p.kl / 32), bytes((int64_t)p.T * (p.kl / 32))),
+            if (wave < SA) dma4(buffer(p.a_scales + (int64_t)iseg * p.T * (p.kl / 32), bytes((int64_t)p.T * (p.kl / 32))),
                  saoff != kOutside && ik + (lane & 1) * 128 < p.kl ? saoff + ik / 32 : kOutside, 0,
                  (uint8_t*)(sSA + wave * 64));
     };
@@ -468,6 +471,14 @@ __global__ __launch_bounds__(64 * WM * WN) void grouped_tile_kernel(Grouped p, i
             }
         __builtin_amdgcn_s_setprio(0);
     };
+    auto issue = [&](uint8_t* nA, uint8_t* nW, uint32_t* nSW, uint32_t* nSA) ALWAYS_INLINE {
+        load_scales(nSW, nSA);
+#pragma unroll
+        for (int i = 0; i < LA; ++i) load_a(nA, i);
+#pragma unroll
+        for (int i = 0; i < LW; ++i) load_w(nW, i);
+        advance();
+    };
     auto step = [&](const uint8_t* sA, const uint8_t* sW, const uint32_t* sSW, const uint32_t* sSA, uint8_t* nA,
                     uint8_t* nW, uint32_t* nSW, uint32_t* nSA) ALWAYS_INLINE {
         // this wave's loads of the k tile have landed; behind the barrier every
@@ -475,37 +486,38 @@ __global__ __launch_bounds__(64 * WM * WN) void grouped_tile_kernel(Grouped p, i
         wait_loads();
         __builtin_amdgcn_s_barrier();
         u32x4 wf[NBN], af[NBM];
+        if constexpr (A4) issue(nA, nW, nSW, nSA);
         static_for<0, KK>([&](auto kc) ALWAYS_INLINE {
             constexpr int kk = decltype(kc)::value;
             read(sA, sW, sSW, kk, wf, af);
-            if constexpr (kk == 0) {
+            if constexpr (!A4 && kk == 0) {
                 load_scales(nSW, nSA);
 #pragma unroll
                 for (int i = 0; i < LA; ++i) load_a(nA, i);
-            } else if constexpr (kk == 1) {
+            } else if constexpr (!A4 && kk == 1) {
 #pragma unroll
                 for (int i = 0; i < LW; ++i) load_w(nW, i);
                 advance();
             }
             multiply(sSW, sSA, kk, wf, af);
         });
-        // MXFP4 x MXFP4: the operands of both halves do not fit the registers
-        // together, so each half's MFMAs come before the next half's reads
-        if constexpr (A4)
-            static_for<0, KK>([&](auto) ALWAYS_INLINE {
-                __builtin_amdgcn_sched_group_barrier(0x100, 2 * (NBN + NBM), 0);  // LDS reads
-                __builtin_amdgcn_sched_group_barrier(0x008, NBN * NBM, 0);        // MFMAs
-            });
     };
-    load_scales(sSW0, sSA0);
-#pragma unroll
-    for (int i = 0; i < LA; ++i) load_a(sA0, i);
-#pragma unroll
-    for (int i = 0; i < LW; ++i) load_w(sW0, i);
-    advance();
-    for (int t = 0; t < nkt; t += 2) {
-        step(sA0, sW0, sSW0, sSA0, sA1, sW1, sSW1, sSA1);
-        if (t + 1 < nkt) step(sA1, sW1, sSW1, sSA1, sA0, sW0, sSW0, sSA0);
+    auto load_step = [&](uint8_t* nA, uint8_t* nW, uint32_t* nSW, uint32_t* nSA) ALWAYS_INLINE {
+        wait_loads();
+        __builtin_amdgcn_s_barrier();
+        issue(nA, nW, nSW, nSA);
+    };
+    issue(sA0, sW0, sSW0, sSA0);
+    if (wave_m * NBM * 16 < s.nrows) {
+        for (int t = 0; t < nkt; t += 2) {
+            step(sA0, sW0, sSW0, sSA0, sA1, sW1, sSW1, sSA1);
+            if (t + 1 < nkt) step(sA1, sW1, sSW1, sSA1, sA0, sW0, sSW0, sSA0);
+        }
+    } else {  // none of the wave's rows is there: its share of the loads is all
+        for (int t = 0; t < nkt; t += 2) {
+            load_step(sA1, sW1, sSW1, sSA1);
+            if (t + 1 < nkt) load_step(sA0, sW0, sSW0, sSA0);
+        }
     }
     wait_loads();  // none may still be writing this workgroup's LDS when it ends
 
@@ -578,46 +590,78 @@ __global__ __launch_bounds__(256) void pack_mx4_kernel(uint8_t* codes, uint8_t* 
             se[mx4_scale_offset(b, i, lane & 15, l.steps) + (lane >> 4)] = 127;
 }
 
-template <int MODE, bool SWIGLU, int MB, int NB, int KS, bool AL>
+template <int MODE, bool SWIGLU, int MB, int NB, int KS, int NWV, bool AL>
 hipError_t stream_launch(const Grouped& p, hipStream_t s) {
-    constexpr int per = 4 / KS * NB;
+    constexpr int per = NWV / KS * NB;
     const int64_t groups = (p.nout + per - 1) / per;
     const int64_t slots = p.R / (16 * MB) + (p.R < p.E ? p.R : p.E);
-    if (groups * slots >= kMaxBlocks) return hipErrorInvalidConfiguration;
-    launch(grouped_stream_kernel<MODE, SWIGLU, MB, NB, KS, AL>, dim3((unsigned)(groups * slots)), dim3(256), 0, s, p);
+    if (groups * slots >= kMaxBlocks * 4 / NWV) return hipErrorInvalidConfiguration;
+    launch(grouped_stream_kernel<MODE, SWIGLU, MB, NB, KS, NWV, AL>, dim3((unsigned)(groups * slots)), dim3(64 * NWV),
+           0, s, p);
     return hipGetLastError();
 }
 
+// How many output blocks a wave takes, and how many waves share their inputs.
+// 16-bit weights: few blocks and many waves (us, two rows and 32 rows of 8
+// experts of the decode MLP, then 32 rows of 64 experts of 2048 x 1024):
+//   gate|up  eight waves a pair of blocks   72 201 37   one wave for two pairs  108 211 52
+//   down     eight waves for two blocks     44 108 22   four waves              69 107 22
+//            four waves for four blocks     87 115 22
+// MXFP4 weights spend more on turning codes into operands, which a wider group
+// shares out over no more rows but which fewer waves repeat less often: the
+// widest group, and the fewest waves that give every compute unit seven (gate|up
+// of 32 rows, two pairs a wave: 83 us, one pair and eight waves: 158 us; down,
+// four waves for four blocks 49 us, eight for two 67 us).
 template <int MODE, bool SWIGLU, bool AL>
 hipError_t stream_mode(const Grouped& p, hipStream_t s) {
     constexpr int NB = SWIGLU ? 2 : 4;
-    if (p.R <= (int64_t)16 * p.E) {
-        if (p.nout <= 256) return stream_launch<MODE, SWIGLU, 1, NB / 2, 4, AL>(p, s);
-        return stream_launch<MODE, SWIGLU, 1, NB, 1, AL>(p, s);
+    const int64_t blocks = (int64_t)p.nout * (p.R < p.E ? p.R : p.E), want = 7 * (int64_t)device_cus();
+    // (MXFP4 activations whose scales the tiles cannot take come here with any rows)
+    if constexpr (MODE == G_MX4A4)
+        if (p.R > (int64_t)8 * p.E) return stream_launch<MODE, SWIGLU, 2, NB, 1, 4, AL>(p, s);
+    if constexpr (MODE < G_MX4) {
+        if constexpr (!SWIGLU && AL)
+            if (blocks * 2 > want) return stream_launch<MODE, SWIGLU, 1, NB / 2, 4, 4, AL>(p, s);
+    } else if constexpr (AL) {
+        if (blocks / NB >= want) return stream_launch<MODE, SWIGLU, 1, NB, 1, 4, AL>(p, s);
+        if (blocks / NB * 2 >= want) return stream_launch<MODE, SWIGLU, 1, NB, 2, 4, AL>(p, s);
+        if (blocks / NB * 4 >= want) return stream_launch<MODE, SWIGLU, 1, NB, 4, 4, AL>(p, s);
+        if (blocks / NB * 8 >= want) return stream_launch<MODE, SWIGLU, 1, NB, 8, 8, AL>(p, s);
     }
-    return stream_launch<MODE, SWIGLU, 2, NB, 1, AL>(p, s);
+    return stream_launch<MODE, SWIGLU, 1, NB / 2, 8, 8, AL>(p, s);
 }
 
-template <int MODE, bool SWIGLU, bool TRANS, int TM, int BN, int WM, int WN, bool AL>
+template <int MODE, bool SWIGLU, bool TRANS, int TM, int BN, bool AL>
 hipError_t tile_launch(const Grouped& p, hipStream_t s) {
     constexpr int NB = SWIGLU ? BN / 32 : BN / 16;
     const int64_t slots = p.R / TM + (p.R < p.E ? p.R : p.E);
     const int64_t tiles_n = (p.nout + NB - 1) / NB;
     if (slots * tiles_n >= kMaxBlocks / 2) return hipErrorInvalidConfiguration;
-    launch(grouped_tile_kernel<MODE, SWIGLU, TRANS, TM, BN, WM, WN, AL>, dim3((unsigned)(slots * tiles_n)),
-           dim3(64 * WM * WN), 0, s, p, (int)slots, (int)tiles_n);
+    launch(grouped_tile_kernel<MODE, SWIGLU, TRANS, TM, BN, AL>, dim3((unsigned)(slots * tiles_n)), dim3(512), 0, s, p,
+           (int)slots, (int)tiles_n);
     return hipGetLastError();
 }
 
+// Tile by the rows of an expert, m = R / E on average (they differ: half as
+// much again is reckoned with), and by whether the tiles fill the chip.  Times
+// in us on bf16 experts, 64 x 128 / 128 x 128 / 256 x 256 tiles:
+//   8 x (28672 x 4096, SwiGLU)  m = 32: 339 335 407   96: 440 378 434  128: 604 471 464   256: 1010 765 717
+//   8 x (4096 x 14336)          m = 32: 200 204 318   96: 229 237 323  192: 434 271 360   256: 476 498 385
+//   32 x (2048 x 2048, SwiGLU)  m = 32:  55  55  62   48:  66  57  64  128:  88  84  72   256: 146 118 125
 template <int MODE, bool SWIGLU, bool TRANS, bool AL>
 hipError_t tile_mode(const Grouped& p, hipStream_t s) {
     if constexpr (!AL) {
-        return tile_launch<MODE, SWIGLU, TRANS, 128, 128, 2, 2, false>(p, s);
+        return tile_launch<MODE, SWIGLU, TRANS, 128, 128, false>(p, s);
     } else if constexpr (MODE == G_MX4) {
-        return tile_launch<MODE, SWIGLU, TRANS, 128, 256, 2, 4, true>(p, s);
+        return tile_launch<MODE, SWIGLU, TRANS, 64, 128, true>(p, s);
     } else {
-        if (p.R >= (int64_t)192 * p.E) return tile_launch<MODE, SWIGLU, TRANS, 256, 256, 2, 4, true>(p, s);
-        return tile_launch<MODE, SWIGLU, TRANS, 128, 128, 2, 2, true>(p, s);
+        // (MXFP4 products are so short that a wave of tiles more costs them a
+        // wider tile's gain: 512 rows of 8 experts, gate|up 461 429, down 221 256)
+        const int64_t tiles = (p.R / 256 + p.E / 2) * ((p.nout + 15) / 16) * (SWIGLU ? 2 : 1);
+        if (p.R >= (int64_t)128 * p.E && tiles * 10 >= (int64_t)device_cus() * (MODE == G_MX4A4 ? 40 : 7))
+            return tile_launch<MODE, SWIGLU, TRANS, 256, 256, true>(p, s);
+        if (p.R > (int64_t)40 * p.E) return tile_launch<MODE, SWIGLU, TRANS, 128, 128, true>(p, s);
+        return tile_launch<MODE, SWIGLU, TRANS, 64, 128, true>(p, s);
     }
 }
 
@@ -626,7 +670,7 @@ hipError_t by_mode(const Grouped& p, hipStream_t s) {
     if constexpr (MODE < G_MX4)
         if (p.transposed) return tile_mode<MODE, false, true, AL>(p, s);
     // (an MXFP4 row's scales are staged four at a time)
-    const bool tiles = p.R > (int64_t)32 * p.E && (MODE != G_MX4A4 || (p.kl % 128 == 0 && (uintptr_t)p.a_scales % 4 == 0));
+    const bool tiles = p.R > (int64_t)8 * p.E && (MODE != G_MX4A4 || (p.kl % 128 == 0 && (uintptr_t)p.a_scales % 4 == 0));
     if (tiles) return p.swiglu ? tile_mode<MODE, true, false, AL>(p, s) : tile_mode<MODE, false, false, AL>(p, s);
     return p.swiglu ? stream_mode<MODE, true, AL>(p, s) : stream_mode<MODE, false, AL>(p, s);
 }

@@ -272,43 +272,38 @@ __global__ __launch_bounds__(64 * NWV) void grouped_stream_kernel(Grouped p) {
 // chunks of a fragment are stored four rows on, so that the two chunks of a
 // read lie in different banks.
 // ---------------------------------------------------------------------------
+template <int MODE, int TM, int BN>
+struct TileShape {
+    static constexpr int ROWB = MODE == G_MX4 ? 256 : 128;  // bytes of a row of A in LDS
+    static constexpr int FPB = MODE == G_MX4 ? 1 : 2;       // fragments of a weight block
+    static constexpr int A = TM * ROWB, W = BN * FPB * 64;  // bytes of a stage
+    // scales of a stage, in words: four a weight row and step, four a row of A and step
+    static constexpr int SW = MODE >= G_MX4 ? BN * FPB : 1, SA = MODE == G_MX4A4 ? TM * 2 : 1;
+};
+
+// n tile nt of the rows of one slot; the stages may be larger than needed
 template <int MODE, bool SWIGLU, bool TRANS, int TM, int BN, bool AL>
-__global__ __launch_bounds__(512) void grouped_tile_kernel(Grouped p, int slots, int tiles_n) {
+__device__ __forceinline__ void grouped_tile(const Grouped& p, const Slot s, const int nt, uint8_t* sA0, uint8_t* sA1,
+                                             uint8_t* sW0, uint8_t* sW1, uint32_t* sSW0, uint32_t* sSW1, uint32_t* sSA0,
+                                             uint32_t* sSA1) {
+    using Shape = TileShape<MODE, TM, BN>;
     constexpr int WM = 2, WN = 4, NWV = WM * WN;
     constexpr int NBM = TM / WM / 16, NBN = BN / WN / 16;
     constexpr bool MX = MODE >= G_MX4, A4 = MODE == G_MX4A4;
     constexpr int KT = A4 ? 256 : MX ? 128 : 64;
-    constexpr int KST = MX ? 128 : 32;              // inputs of a stored weight step
-    constexpr int ROWB = MODE == G_MX4 ? 256 : 128;  // bytes of a row of A in LDS
-    constexpr int CPR = ROWB / 16;                   // its chunks
-    constexpr int RPI = 64 / CPR;                    // rows of a 1 KB load
-    constexpr int LA = TM * ROWB / 1024 / NWV;       // loads of a wave
-    constexpr int FPB = MODE == G_MX4 ? 1 : 2;       // fragments of a weight block
+    constexpr int KST = MX ? 128 : 32;  // inputs of a stored weight step
+    constexpr int ROWB = Shape::ROWB, FPB = Shape::FPB;
+    constexpr int CPR = ROWB / 16;                // chunks of a row
+    constexpr int RPI = 64 / CPR;                 // rows of a 1 KB load
+    constexpr int LA = TM * ROWB / 1024 / NWV;    // loads of a wave
     constexpr int LW = BN / 16 * FPB / NWV;
-    constexpr int KK = MODE == G_MX4 ? 4 : 2;        // MFMA steps of a k tile
+    constexpr int KK = MODE == G_MX4 ? 4 : 2;     // MFMA steps of a k tile
     static_assert(LA * NWV * 1024 == TM * ROWB && LW * NWV * 16 == BN * FPB, "loads divide over the waves");
-    __shared__ __attribute__((aligned(1024))) uint8_t sA0[TM * ROWB], sA1[TM * ROWB], sW0[BN * FPB * 64],
-        sW1[BN * FPB * 64];
-    // MXFP4 scales of a k tile: four a weight row and step, four a row of A and step
-    __shared__ uint32_t sSW0[MX ? BN * FPB : 1], sSW1[MX ? BN * FPB : 1], sSA0[A4 ? TM * 2 : 1], sSA1[A4 ? TM * 2 : 1];
-
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     // (the WM waves of one column stand on one SIMD: where the tile has rows for
     // one of them only, it has the SIMD for itself)
     const int wave_m = wave / WN, wave_n = wave % WN;
-    // The launch has room for every way the rows may fall on the experts; the
-    // tiles that there are, not that room, are dealt out to the XCDs.  (Falling
-    // offsets could count more: those are left out.)
-    slots = min(slots, count_slots(p.offsets, p.E, p.R, TM));
-    if ((int)blockIdx.x >= slots * tiles_n) return;
-    const int tile = xcd_remap(blockIdx.x, slots * tiles_n);
-    constexpr int GM = 4;
-    const int g = tile / (GM * tiles_n), first = g * GM, gsz = min(GM, slots - first);
-    const int tin = tile - g * GM * tiles_n;
-    const Slot s = find_slot(p.offsets, p.E, p.R, first + tin % gsz, TM);
-    if (s.e < 0) return;
-    const int nt = tin / gsz;  // n tile
 
     // load i of a wave: rows (i NWV + wave) RPI .. of A, chunk lane % CPR of them
     uint32_t aoff[LA];
@@ -530,6 +525,48 @@ __global__ __launch_bounds__(512) void grouped_tile_kernel(Grouped p, int slots,
     });
 }
 
+template <int MODE, bool SWIGLU, bool TRANS, int TM, int BN, bool AL>
+__global__ __launch_bounds__(512) void grouped_tile_kernel(Grouped p, int slots, int tiles_n, int cus) {
+    using Shape = TileShape<MODE, TM, BN>;
+    __shared__ __attribute__((aligned(1024))) uint8_t sA0[Shape::A], sA1[Shape::A], sW0[Shape::W], sW1[Shape::W];
+    __shared__ uint32_t sSW0[Shape::SW], sSW1[Shape::SW], sSA0[Shape::SA], sSA1[Shape::SA];
+    // The launch has room for every way the rows may fall on the experts; the
+    // tiles that there are, not that room, are dealt out to the XCDs.  (Falling
+    // offsets could count more: those are left out.)
+    slots = min(slots, count_slots(p.offsets, p.E, p.R, TM));
+    int tiles = slots * tiles_n, rest = 0;
+    // 256 x 256 tiles take a compute unit each.  Where the last time round the
+    // chip would leave half of it idle or more, its tiles are cut into quarters
+    // (down projection of 4096 tokens, 2.25 times round: 1168 -> 1024 us).
+    if constexpr (TM == 256) {
+        rest = tiles % cus;
+        if (rest * 2 > cus) rest = 0;
+        tiles -= rest;
+    }
+    auto slot_of = [&](int tile, int& nt) {
+        constexpr int GM = 4;
+        const int g = tile / (GM * tiles_n), first = g * GM, gsz = min(GM, slots - first);
+        const int tin = tile - g * GM * tiles_n;
+        nt = tin / gsz;
+        return find_slot(p.offsets, p.E, p.R, first + tin % gsz, TM);
+    };
+    int nt;
+    if ((int)blockIdx.x < tiles) {
+        const Slot s = slot_of(xcd_remap(blockIdx.x, tiles), nt);
+        if (s.e < 0) return;
+        grouped_tile<MODE, SWIGLU, TRANS, TM, BN, AL>(p, s, nt, sA0, sA1, sW0, sW1, sSW0, sSW1, sSA0, sSA1);
+    } else if constexpr (TM == 256) {
+        if ((int)blockIdx.x >= tiles + 4 * rest) return;
+        const int q = xcd_remap(blockIdx.x - tiles, 4 * rest);
+        Slot s = slot_of(tiles + q / 4, nt);
+        s.row0 += (q & 1) * 128;
+        s.nrows = min(s.nrows - (q & 1) * 128, 128);
+        if (s.e < 0 || s.nrows <= 0) return;
+        grouped_tile<MODE, SWIGLU, TRANS, 128, BN / 2, AL>(p, s, 2 * nt + ((q >> 1) & 1), sA0, sA1, sW0, sW1, sSW0, sSW1,
+                                                           sSA0, sSA1);
+    }
+}
+
 // ---- layout -----------------------------------------------------------------
 // where stored row n of an expert and stored input q come from (-1: padding)
 __device__ __forceinline__ int64_t source_row(const ExpertsLayout& l, int64_t n) {
@@ -547,13 +584,19 @@ __device__ __forceinline__ int64_t source_col(const ExpertsLayout& l, int64_t q)
     return s * (l.in / l.S) + r * part + (c - s * part);
 }
 
-__global__ __launch_bounds__(256) void pack_kernel(uint16_t* dst, const uint16_t* src, ExpertsLayout l, int64_t frags) {
+__global__ __launch_bounds__(256) void pack_kernel(uint16_t* dst, const uint16_t* src, ExpertsLayout l, int64_t frags,
+                                                   bool whole) {
     const int64_t fr = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
     if (fr >= frags) return;
     const int lane = threadIdx.x & 63;
     const int64_t st = fr % l.steps, b = (fr / l.steps) % l.blocks, e = fr / (l.steps * l.blocks);
     const int64_t row = source_row(l, b * 16 + (lane & 15)), q = st * 32 + 8 * (lane >> 4);
     const uint16_t* from = src + (e * l.out + row) * l.in;
+    if (whole) {  // eight inputs lie together, 16-byte aligned
+        const int64_t c = row >= 0 ? source_col(l, q) : -1;
+        *(u32x4*)(dst + fr * 512 + lane * 8) = c >= 0 ? *(const u32x4*)(from + c) : u32x4{0, 0, 0, 0};
+        return;
+    }
     uint32_t h[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -636,9 +679,11 @@ hipError_t tile_launch(const Grouped& p, hipStream_t s) {
     constexpr int NB = SWIGLU ? BN / 32 : BN / 16;
     const int64_t slots = p.R / TM + (p.R < p.E ? p.R : p.E);
     const int64_t tiles_n = (p.nout + NB - 1) / NB;
-    if (slots * tiles_n >= kMaxBlocks / 2) return hipErrorInvalidConfiguration;
-    launch(grouped_tile_kernel<MODE, SWIGLU, TRANS, TM, BN, AL>, dim3((unsigned)(slots * tiles_n)), dim3(512), 0, s, p,
-           (int)slots, (int)tiles_n);
+    const int cus = device_cus();
+    const int64_t blocks = slots * tiles_n + (TM == 256 ? 3 * (cus / 2) : 0);
+    if (blocks >= kMaxBlocks / 2) return hipErrorInvalidConfiguration;
+    launch(grouped_tile_kernel<MODE, SWIGLU, TRANS, TM, BN, AL>, dim3((unsigned)blocks), dim3(512), 0, s, p, (int)slots,
+           (int)tiles_n, cus);
     return hipGetLastError();
 }
 
@@ -690,8 +735,9 @@ hipError_t launch_grouped(const Grouped& p, hipStream_t s) {
 
 hipError_t experts_pack(void* dst, const void* src, const ExpertsLayout& l, hipStream_t s) {
     const int64_t frags = l.E * l.blocks * l.steps;
+    const int64_t part = l.mode == SG_ALL_TO_SHARDED ? l.in : l.in / l.S / l.P;
     launch(pack_kernel, dim3((unsigned)((frags + 3) / 4)), dim3(256), 0, s, (uint16_t*)dst, (const uint16_t*)src, l,
-           frags);
+           frags, part % 8 == 0 && (uintptr_t)src % 16 == 0);
     return hipGetLastError();
 }
 

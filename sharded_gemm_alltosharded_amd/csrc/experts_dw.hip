@@ -203,10 +203,13 @@ template <bool F16>
 hipError_t dw_type(const GroupedDw& p, hipStream_t s) {
     const bool al = (uintptr_t)p.G % 16 == 0 && (uintptr_t)p.X % 16 == 0 && p.ldg % 8 == 0 && p.ldx % 8 == 0 &&
                     p.g_rank % 8 == 0 && p.x_rank % 8 == 0 && p.O % 8 == 0 && p.I % 8 == 0;
-    if (!al) return dw_launch<F16, 128, 128, 2, 2, false>(p, s);
+    if (!al) return dw_launch<F16, 128, 128, 2, 4, false>(p, s);
+    // the wide tile where its tiles go round the chip several times (8 experts
+    // of 28672 x 4096: 2.30 ms, 2.72 on the narrow one; 32 of 1024 x 704 over
+    // 1500 x 4 rows, twice round: 35 us, 28 on the narrow one)
     const int64_t big = (int64_t)p.E * p.P * ((p.O + 255) / 256) * ((p.I + 255) / 256);
-    if (big >= 2 * device_cus()) return dw_launch<F16, 256, 256, 2, 4, true>(p, s);
-    return dw_launch<F16, 128, 128, 2, 2, true>(p, s);
+    if (big >= 4 * device_cus()) return dw_launch<F16, 256, 256, 2, 4, true>(p, s);
+    return dw_launch<F16, 128, 128, 2, 4, true>(p, s);
 }
 
 }  // namespace

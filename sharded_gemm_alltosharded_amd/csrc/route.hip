@@ -191,13 +191,13 @@ __global__ __launch_bounds__(1024) void route_small_kernel(Route r) {
 // Chunks of consecutive tokens; ws[chunk][expert] holds the chunk's counts,
 // after the scan the chunk's first row of that expert.
 template <int V>
-__global__ __launch_bounds__(256) void route_choose_kernel(Route r, int chunk_tokens) {
+__global__ __launch_bounds__(1024) void route_choose_kernel(Route r, int chunk_tokens) {
     __shared__ int count[kRouteMaxExperts];
     const int tid = threadIdx.x, wave = tid >> 6;
-    for (int i = tid; i < r.E; i += 256) count[i] = 0;
+    for (int i = tid; i < r.E; i += 1024) count[i] = 0;
     __syncthreads();
     const int t0 = blockIdx.x * chunk_tokens, t1 = min(t0 + chunk_tokens, r.T);
-    for (int t = t0 + wave; t < t1; t += 4)
+    for (int t = t0 + wave; t < t1; t += 16)
         choose<V>(r, t, [&](int j, int e, float w) {
             const int64_t s = (int64_t)t * r.k + j;
             r.experts[s] = e;
@@ -205,7 +205,7 @@ __global__ __launch_bounds__(256) void route_choose_kernel(Route r, int chunk_to
             if (e >= 0) atomicAdd(&count[e], 1);  // counts: no order in them
         });
     __syncthreads();
-    for (int i = tid; i < r.E; i += 256) r.ws[(int64_t)blockIdx.x * r.E + i] = count[i];
+    for (int i = tid; i < r.E; i += 1024) r.ws[(int64_t)blockIdx.x * r.E + i] = count[i];
 }
 
 // One workgroup: thread (part, e) walks a part of the chunks of expert e.
@@ -410,15 +410,21 @@ __global__ __launch_bounds__(256) void combine_kernel(const void* y, const int32
     const int64_t c = ((int64_t)(blockIdx.x - t * per_token) * blockDim.x + threadIdx.x) * 8;
     if (c >= D) return;
     float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll 4
-    for (int j = 0; j < k; ++j) {
-        const int64_t row = slots[t * k + j];
-        if (row < 0 || row >= R) continue;
-        const float w = weights ? weights[t * k + j] : 1.f;
-        float v[8];
-        load_cols<YT, VEC>(y, row, D, c, v);
+    for (int j0 = 0; j0 < k; j0 += 4) {  // four rows' loads at once
+        float v[4][8], w[4];
+        bool in[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] = fmaf(w, v[e], acc[e]);
+        for (int j = 0; j < 4; ++j) {
+            const int64_t s = t * k + min(j0 + j, k - 1), row = slots[s];
+            in[j] = j0 + j < k && row >= 0 && row < R;
+            w[j] = weights ? weights[s] : 1.f;
+            if (in[j]) load_cols<YT, VEC>(y, row, D, c, v[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (in[j])
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc[e] = fmaf(w[j], v[j][e], acc[e]);
     }
     store_cols<OT, VEC>(out, t, D, c, acc);
 }
@@ -528,7 +534,7 @@ void route_v(const Route& r, hipStream_t s) {
     }
     const int ct = chunk_tokens_of(r.T, r.k);
     const int chunks = (r.T + ct - 1) / ct;
-    launch(route_choose_kernel<V>, dim3(chunks), dim3(256), 0, s, r, ct);
+    launch(route_choose_kernel<V>, dim3(chunks), dim3(1024), 0, s, r, ct);
     launch(route_scan_kernel, dim3(1), dim3(1024), 0, s, r, chunks);
     launch(route_place_kernel, dim3(chunks), dim3(64), 0, s, r, ct);
 }

@@ -345,6 +345,59 @@ def test_experts_row_backward(case):
                 ref.close(gw[e, r], d, ref.sum_bound(m, b - a), f"dw {dt} {e} {r}")
 
 
+# the wide tiles, their quarters and the narrow ones, on rows that end inside
+# them: E, R, in, out / P / S, P, S, dtype
+WIDE = [
+    (1, 2600, 96, 2304, 1, 2, BF), (1, 2600, 72, 1500, 3, 1, HF), (3, 2000, 64, 2104, 1, 2, HF),
+    (2, 4700, 136, 1024, 2, 2, BF), (5, 3000, 200, 3000, 1, 1, BF), (1, 700, 64, 16392, 1, 1, HF),
+]
+
+
+@pytest.mark.parametrize("E,R,K,f,P,S,dtype", WIDE)
+def test_experts_wide_tiles(E, R, K, f, P, S, dtype):
+    """Sampled rows of the products, and of both gradients, at sizes that take the widest tiles."""
+    g = gen(R + f)
+    n = f * P * S
+    w, x = normal(g, (E, n, K), dtype, 1 / math.sqrt(K)), normal(g, (R, K), dtype)
+    off = offsets_of(g, E, R, empty=False)
+    order = ref.shard_rows(n, S, P)
+    col = sg.shard_experts(w.cuda(), "all-to-sharded", segments=S, P=P)
+    pick = torch.unique(torch.cat([torch.randint(0, R, (40,), generator=g), off[1:-1].long(), off[1:].long() - 1,
+                                   torch.tensor([0, 127, 128, 255, 256, R - 1])]))
+    pick = pick[pick < R]
+    expert = torch.searchsorted(off[1:].contiguous(), pick.int(), right=True)
+    y = torch.stack([w[e].double() @ x[r].double() for r, e in zip(pick, expert)])
+    mag = torch.stack([w[e].double().abs() @ x[r].double().abs() for r, e in zip(pick, expert)])
+    res, bound = torch.stack([y[:, o] for o in order]), torch.stack([mag[:, o] for o in order])
+    got = sg.experts_all_to_sharded(col, x.cuda(), off.cuda(), out_dtype=F32)
+    ref.close(got[:, pick.cuda()], res, ref.sum_bound(bound, K), "column")
+    if S == 2:
+        h = sg.experts_all_to_sharded(col, x.cuda(), off.cuda(), swiglu=True)
+        (a, b), (ma, mb) = res.split(f, -1), bound.split(f, -1)
+        ref.close(h[:, pick.cuda()], ref.silu(a) * b, ref.swiglu_bound(a, b, ma, mb, K), "swiglu")
+    # the same weights transposed: dx of a layer whose inputs are the wide side
+    row = sg.shard_experts(w.transpose(1, 2).contiguous().cuda(), "sharded-to-all", segments=S, P=P)
+    dh, dw = sg.experts_sharded_to_all_backward(row, got.to(dtype), x.cuda(), off.cuda(), dx_dtype=F32)
+    ref.close(dh[:, pick.cuda()], res, ref.sum_bound(bound, K), "dh")
+    o = torch.randint(0, K, (5,), generator=g)
+    for e in range(E):
+        a, b = int(off[e]), int(off[e + 1])
+        hs = got[:, a:b].to(dtype).double().cpu()
+        for r in range(P):
+            d = x[a:b, o].double().T @ hs[r]
+            m = x[a:b, o].double().abs().T @ hs[r].abs()
+            ref.close(dw[e, r][o.cuda()], d, ref.sum_bound(m, b - a), f"dw {e} {r}")
+    # and back: the wide side summed over
+    dy = normal(g, (P, R, f * S), dtype)
+    full = torch.zeros((len(pick), n), dtype=torch.float64)
+    for r, q in enumerate(order):
+        full[:, q] = dy[r, pick].double()
+    dx, _ = sg.experts_all_to_sharded_backward(col, None, dy.cuda(), off.cuda(), need_dw=False, dx_dtype=F32)
+    want = torch.stack([full[i] @ w[e].double() for i, e in enumerate(expert)])
+    mag = torch.stack([full[i].abs() @ w[e].double().abs() for i, e in enumerate(expert)])
+    ref.close(dx[pick.cuda()], want, ref.sum_bound(mag, n), "dx")
+
+
 @pytest.mark.parametrize("R", [0, 1, 16, 40, 129, 400])
 def test_experts_rows_behind_the_last_stay(R):
     g = gen(R)

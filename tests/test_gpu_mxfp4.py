@@ -134,6 +134,38 @@ def test_mxfp4_column(E, R, K, f, P, S, acts):
             ref.close(got, ref.silu(a) * b, ref.swiglu_bound(a, b, ma, mb, K), f"column swiglu {dt}")
 
 
+@pytest.mark.parametrize("acts", [16, 4])
+@pytest.mark.parametrize("E,R,K,f,P,S", [(1, 4200, 128, 8200, 2, 1), (3, 6000, 384, 3000, 1, 2), (1, 900, 640, 4100, 1, 2),
+                                         (2, 300, 256, 9000, 1, 1)])
+def test_mxfp4_wide_tiles(E, R, K, f, P, S, acts):
+    """Sampled rows at sizes that take the widest tiles and their quarters."""
+    g = gen(R)
+    n = f * P * S
+    codes, scales = mx_weights(g, E, n, K)
+    w = ref.decode(codes, scales)
+    layer = sg.shard_mxfp4_experts(codes.cuda(), scales.cuda(), "all-to-sharded", segments=S, P=P)
+    x = normal(g, (R, K), BF)
+    off = offsets_of(g, E, R, empty=False)
+    pick = torch.unique(torch.cat([torch.randint(0, R, (30,), generator=g), off[1:].long() - 1,
+                                   torch.tensor([0, 127, 128, 255, 256])]))
+    expert = torch.searchsorted(off[1:].contiguous(), pick.int(), right=True)
+    if acts == 4:
+        xc, xs = sg.quantize_mxfp4(x.cuda())
+        args, kw, xv = (xc,), {"x_scales": xs}, ref.decode(*ref.encode(x[pick]))
+    else:
+        args, kw, xv = (x.cuda(),), {}, x[pick].double()
+    y = torch.stack([w[e] @ v for v, e in zip(xv, expert)])
+    mag = torch.stack([w[e].abs() @ v.abs() for v, e in zip(xv, expert)])
+    order = ref.shard_rows(n, S, P)
+    res, bound = torch.stack([y[:, o] for o in order]), torch.stack([mag[:, o] for o in order])
+    got = sg.experts_all_to_sharded(layer, *args, off.cuda(), out_dtype=F32, **kw)
+    ref.close(got[:, pick.cuda()], res, ref.sum_bound(bound, K), "column")
+    if S == 2:
+        got = sg.experts_all_to_sharded(layer, *args, off.cuda(), swiglu=True, out_dtype=BF, **kw)
+        (a, b), (ma, mb) = res.split(f, -1), bound.split(f, -1)
+        ref.close(got[:, pick.cuda()], ref.silu(a) * b, ref.swiglu_bound(a, b, ma, mb, K), "swiglu")
+
+
 ROWS = [  # E, R, out, in / P, P
     (1, 1, 1, 32, 1), (1, 150, 64, 96, 2), (3, 5, 20, 160, 1), (4, 64, 33, 64, 3), (8, 100, 250, 32, 4),
     (3, 900, 300, 288, 2), (40, 70, 64, 128, 1),

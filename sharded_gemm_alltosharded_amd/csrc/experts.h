@@ -85,9 +85,11 @@ struct GroupedDw {
     const int32_t* offsets;
     const int32_t* rows;
     int kdiv, T, R, E, P, O, I;
+    uint32_t kmul;  // set by the launch
+    int kshift;
     void* out;
     int out_dtype;
-    int vec;  // rows of the output take 4-column vector stores
+    int vec;  // rows of the output take 8-column vector stores
 };
 hipError_t launch_grouped_dw(const GroupedDw& p, hipStream_t s);
 
@@ -172,7 +174,18 @@ __device__ __forceinline__ void dma4(__amdgpu_buffer_rsrc_t r, uint32_t voff, ui
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)to, 4, voff, soff, 0, 0);
 }
 // every load, and every LDS write, of this wave has landed
-__device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0070); }
+__device__ __forceinline__ void wait_loads() {
+    __builtin_amdgcn_s_waitcnt(0x0070);
+    asm volatile("" ::: "memory");
+}
+// ... and, behind the barrier, of every wave of the workgroup; no access to
+// memory is moved over it
+__device__ __forceinline__ void stage_barrier() {
+    asm volatile("" ::: "memory");
+    wait_loads();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
 
 __device__ __forceinline__ u32x2 read_tr(const uint8_t* p) {
     return __builtin_bit_cast(
@@ -222,6 +235,9 @@ __device__ __forceinline__ Slot find_slot(const int32_t* offsets, int E, int R, 
             const int first = before + __shfl(sum, l) - __shfl(t, l);
             const int row = (slot - first) * TM;
             const int bb = __shfl(b, l), nn = __shfl(n, l);
+            // (falling offsets can count more tiles than an int holds)
+            if (__builtin_amdgcn_readfirstlane(row) < 0 || __builtin_amdgcn_readfirstlane(row - nn) >= 0)
+                return Slot{-1, 0, 0};
             return Slot{__builtin_amdgcn_readfirstlane(e0 + l), __builtin_amdgcn_readfirstlane(bb + row),
                         __builtin_amdgcn_readfirstlane(min(TM, nn - row))};
         }

@@ -422,7 +422,8 @@ __device__ __forceinline__ void grouped_tile(const Grouped& p, const Slot s, con
 
     const int c16 = lane >> 4, r16 = lane & 15;
     const int amine = (wave_m * NBM * 16 + r16) * ROWB, asw = ROWB == 128 ? (r16 >> 1) & 7 : r16;
-    auto read = [&](const uint8_t* sA, const uint8_t* sW, const uint32_t* sSW, int kk, u32x4(&wf)[NBN], u32x4(&af)[NBM]) ALWAYS_INLINE {
+    auto read = [&](const uint8_t* sA, const uint8_t* sW, const u32x4(&codes)[NBN], const float(&scale)[NBN], int kk,
+                    u32x4(&wf)[NBN], u32x4(&af)[NBM]) ALWAYS_INLINE {
 #pragma unroll
         for (int i = 0; i < NBN; ++i) {
             const int nb = wave_n * NBN + i;
@@ -436,8 +437,7 @@ __device__ __forceinline__ void grouped_tile(const Grouped& p, const Slot s, con
                 const u32x2 lo = read_tr(a0), hi = read_tr(a1);
                 wf[i] = u32x4{lo[0], lo[1], hi[0], hi[1]};
             } else if constexpr (MODE == G_MX4) {
-                const uint32_t w = *(const uint32_t*)(sW + nb * 1024 + lane * 16 + 4 * kk);
-                wf[i] = mx4_to_bf16(w, e8m0_to_f32((sSW[nb * 16 + r16] >> (8 * c16)) & 255u));
+                wf[i] = mx4_to_bf16(codes[i][kk], scale[i]);
             } else {
                 wf[i] = *(const u32x4*)(sW + (nb * FPB + kk) * 1024 + lane * 16);
             }
@@ -478,13 +478,22 @@ __device__ __forceinline__ void grouped_tile(const Grouped& p, const Slot s, con
                     uint8_t* nW, uint32_t* nSW, uint32_t* nSA) ALWAYS_INLINE {
         // this wave's loads of the k tile have landed; behind the barrier every
         // wave's have, and every wave has read the k tile before
-        wait_loads();
-        __builtin_amdgcn_s_barrier();
+        stage_barrier();
         u32x4 wf[NBN], af[NBM];
+        // MXFP4 weights: a lane's 32 codes and their scale serve the k tile's four steps
+        [[maybe_unused]] u32x4 codes[NBN];
+        [[maybe_unused]] float scale[NBN];
+        if constexpr (MODE == G_MX4) {
+#pragma unroll
+            for (int i = 0; i < NBN; ++i) {
+                codes[i] = *(const u32x4*)(sW + (wave_n * NBN + i) * 1024 + lane * 16);
+                scale[i] = e8m0_to_f32((sSW[(wave_n * NBN + i) * 16 + r16] >> (8 * c16)) & 255u);
+            }
+        }
         if constexpr (A4) issue(nA, nW, nSW, nSA);
         static_for<0, KK>([&](auto kc) ALWAYS_INLINE {
             constexpr int kk = decltype(kc)::value;
-            read(sA, sW, sSW, kk, wf, af);
+            read(sA, sW, codes, scale, kk, wf, af);
             if constexpr (!A4 && kk == 0) {
                 load_scales(nSW, nSA);
 #pragma unroll
@@ -498,8 +507,7 @@ __device__ __forceinline__ void grouped_tile(const Grouped& p, const Slot s, con
         });
     };
     auto load_step = [&](uint8_t* nA, uint8_t* nW, uint32_t* nSW, uint32_t* nSA) ALWAYS_INLINE {
-        wait_loads();
-        __builtin_amdgcn_s_barrier();
+        stage_barrier();
         issue(nA, nW, nSW, nSA);
     };
     issue(sA0, sW0, sSW0, sSA0);
@@ -698,6 +706,12 @@ hipError_t tile_mode(const Grouped& p, hipStream_t s) {
     if constexpr (!AL) {
         return tile_launch<MODE, SWIGLU, TRANS, 128, 128, false>(p, s);
     } else if constexpr (MODE == G_MX4) {
+        // (turning codes into operands costs the narrow tile as much as its few
+        // rows' products; gate|up, 64 x 128 / 128 x 256:  m = 64: 185 222  256: 552 531  1024: 1987 1742,
+        // down  64: 126 174  256: 280 364  1024: 960 938)
+        const int64_t tiles = (p.R / 128 + p.E / 2) * ((p.nout + 15) / 16) * (SWIGLU ? 2 : 1);
+        if (p.R >= (int64_t)192 * p.E && tiles >= (int64_t)device_cus() * 6)
+            return tile_launch<MODE, SWIGLU, TRANS, 128, 256, true>(p, s);
         return tile_launch<MODE, SWIGLU, TRANS, 64, 128, true>(p, s);
     } else {
         // (MXFP4 products are so short that a wave of tiles more costs them a

@@ -360,10 +360,14 @@ sg_status sg_experts_info(const sg_experts* x, int64_t* E, int64_t* out_dims, in
 
 void sg_experts_free(sg_experts* x) {
     if (!x) return;
+    int d = x->device;
+    (void)hipGetDevice(&d);
+    if (d != x->device) (void)hipSetDevice(x->device);
     // kernels queued on any stream may still read the weights
     (void)hipDeviceSynchronize();
     if (x->w) (void)hipFree(x->w);
     if (x->wsc) (void)hipFree(x->wsc);
+    if (d != x->device) (void)hipSetDevice(d);
     delete x;
 }
 
@@ -511,7 +515,7 @@ sg_status sg_experts_all_to_sharded_backward(const sg_experts* x, const void* a,
         p.I = (int)l.in;
         p.out = dw;
         p.out_dtype = dw_dtype;
-        p.vec = l.in % 4 == 0 && aligned(dw, 16);
+        p.vec = l.in % 8 == 0 && aligned(dw, 16);
         st = launched(sg::launch_grouped_dw(p, s), "sg_experts_all_to_sharded_backward dw");
     }
     return st;
@@ -568,7 +572,7 @@ sg_status sg_experts_sharded_to_all_backward(const sg_experts* x, const void* h,
         p.I = (int)l.kl;
         p.out = dw;
         p.out_dtype = dw_dtype;
-        p.vec = l.kl % 4 == 0 && aligned(dw, 16);
+        p.vec = l.kl % 8 == 0 && aligned(dw, 16);
         st = launched(sg::launch_grouped_dw(p, s), "sg_experts_sharded_to_all_backward dw");
     }
     return st;

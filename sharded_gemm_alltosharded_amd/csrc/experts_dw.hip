@@ -52,17 +52,22 @@ __global__ __launch_bounds__(64 * WO * WI) void grouped_dw_kernel(GroupedDw p, i
     const __amdgpu_buffer_rsrc_t bg = buffer(G, ((int64_t)(p.R - 1) * p.ldg + p.O) * 2);
     const __amdgpu_buffer_rsrc_t bx = buffer(X, ((int64_t)(p.T - 1) * p.ldx + p.I) * 2);
 
-    // load i of a wave: tile row (i NWV + wave) 64 / C + lane / C, LDS chunk lane % C
+    // load i of a wave: tile row (i NWV + wave) 64 / C + lane / C, LDS chunk lane
+    // % C.  Byte offsets within a tile stay in registers; the tile's own is a
+    // scalar, or with a gather map its row's product.
     int gcol[LG], xcol[LX], raw[LX];
+    uint32_t goff[LG], xoff[LX];
 #pragma unroll
     for (int i = 0; i < LG; ++i) {
         const int m = (i * NWV + wave) * (64 / CG) + lane / CG;
         gcol[i] = o0 + 8 * ((lane % CG) ^ (swz(m) << 1));
+        goff[i] = gcol[i] < p.O ? (uint32_t)((m * p.ldg + gcol[i]) * 2) : kOutside;
     }
 #pragma unroll
     for (int i = 0; i < LX; ++i) {
         const int m = (i * NWV + wave) * (64 / CX) + lane / CX;
         xcol[i] = i0 + 8 * ((lane % CX) ^ (swz(m) << 1));
+        xoff[i] = xcol[i] < p.I ? (uint32_t)(((p.rows ? 0 : m * p.ldx) + xcol[i]) * 2) : kOutside;
     }
     auto fetch_rows = [&](int mt) ALWAYS_INLINE {  // the gather map of tile mt
         if (!p.rows) return;
@@ -73,28 +78,31 @@ __global__ __launch_bounds__(64 * WO * WI) void grouped_dw_kernel(GroupedDw p, i
         }
     };
     auto load_g = [&](int mt, uint8_t* s) ALWAYS_INLINE {
+        const uint32_t at = mt < m1 ? (uint32_t)(mt * p.ldg * 2) : 0;
 #pragma unroll
         for (int i = 0; i < LG; ++i) {
             const int m = mt + (i * NWV + wave) * (64 / CG) + lane / CG;
             uint8_t* to = s + (i * NWV + wave) * 1024;
-            if constexpr (AL)
-                dma16(bg, m < m1 && gcol[i] < p.O ? (uint32_t)((m * p.ldg + gcol[i]) * 2) : kOutside, 0, to);
-            else
-                *(u32x4*)(to + lane * 16) = load8_any(G, m < m1 ? m : -1, p.ldg, gcol[i], p.O);
+            if constexpr (AL) dma16(bg, m < m1 ? goff[i] : kOutside, at, to);
+            else *(u32x4*)(to + lane * 16) = load8_any(G, m < m1 ? m : -1, p.ldg, gcol[i], p.O);
         }
     };
     auto load_x = [&](int mt, uint8_t* s) ALWAYS_INLINE {
+        const uint32_t at = p.rows || mt >= m1 ? 0 : (uint32_t)(mt * p.ldx * 2);
 #pragma unroll
         for (int i = 0; i < LX; ++i) {
             const int m = mt + (i * NWV + wave) * (64 / CX) + lane / CX;
             uint8_t* to = s + (i * NWV + wave) * 1024;
             int row = m;
-            if (p.rows) row = raw[i] < 0 ? -1 : (int)((uint32_t)raw[i] / (uint32_t)p.kdiv);
-            if (m >= m1 || row >= p.T) row = -1;
-            if constexpr (AL)
-                dma16(bx, row >= 0 && xcol[i] < p.I ? (uint32_t)((row * p.ldx + xcol[i]) * 2) : kOutside, 0, to);
-            else
-                *(u32x4*)(to + lane * 16) = load8_any(X, row, p.ldx, xcol[i], p.I);
+            if (p.rows) row = raw[i] < 0 ? -1 : p.kmul ? (int)(__umulhi((uint32_t)raw[i], p.kmul) >> p.kshift) : raw[i];
+            const bool in = m < m1 && row >= 0 && row < p.T;
+            if constexpr (AL) {
+                uint32_t off = xoff[i];
+                if (p.rows) off = xcol[i] < p.I ? off + (uint32_t)row * (uint32_t)(p.ldx * 2) : kOutside;
+                dma16(bx, in ? off : kOutside, at, to);
+            } else {
+                *(u32x4*)(to + lane * 16) = load8_any(X, in ? row : -1, p.ldx, xcol[i], p.I);
+            }
         }
     };
 
@@ -106,23 +114,34 @@ __global__ __launch_bounds__(64 * WO * WI) void grouped_dw_kernel(GroupedDw p, i
     const int c16 = lane >> 4, r16 = lane & 15;
     const int wo = (wave % WO) * (TO / WO), wi = (wave / WO) * (TI / WI);
     // contracted rows 32 kk + 8 c16 + 0 .. 7 of columns col .. col + 15
-    auto operand = [&](const uint8_t* s, int rowb, int col, int kk) ALWAYS_INLINE -> u32x4 {
+    auto operand = [&](const uint8_t* s, int col, int kk) ALWAYS_INLINE -> u32x4 {
+        constexpr int rowb = TO * 2;
         const int row = 32 * kk + 8 * c16 + (r16 >> 2);  // (row + 4 has the same swizzle)
         const int c = (col >> 3) + ((r16 & 3) >> 1);
         const uint8_t* a = s + row * rowb + ((c ^ (swz(row) << 1)) << 4) + 8 * (r16 & 1);
         const u32x2 lo = read_tr(a), hi = read_tr(a + 4 * rowb);
         return u32x4{lo[0], lo[1], hi[0], hi[1]};
     };
+    // X's columns are dealt to the MFMA's rows so that a lane ends up with eight
+    // adjacent ones of two blocks: block i, row 4 c + e is column 32 (i / 2) + 8 c
+    // + 4 (i % 2) + e of the wave's (16-byte stores in place of 8-byte ones)
+    auto operand_x = [&](const uint8_t* s, int i, int kk) ALWAYS_INLINE -> u32x4 {
+        constexpr int rowb = TI * 2;
+        const int row = 32 * kk + 8 * c16 + (r16 >> 2);
+        const int c = (wi >> 3) + 4 * (i >> 1) + (r16 & 3);
+        const uint8_t* a = s + row * rowb + ((c ^ (swz(row) << 1)) << 4) + 8 * (i & 1);
+        const u32x2 lo = read_tr(a), hi = read_tr(a + 4 * rowb);
+        return u32x4{lo[0], lo[1], hi[0], hi[1]};
+    };
     auto step = [&](int mt, const uint8_t* sG, const uint8_t* sX, uint8_t* nG, uint8_t* nX) ALWAYS_INLINE {
-        wait_loads();  // this wave's loads have landed; behind the barrier every wave's
-        __builtin_amdgcn_s_barrier();
+        stage_barrier();
         static_for<0, 2>([&](auto kc) ALWAYS_INLINE {
             constexpr int kk = decltype(kc)::value;
             u32x4 gf[NBO], xf[NBI];
 #pragma unroll
-            for (int i = 0; i < NBI; ++i) xf[i] = operand(sX, TI * 2, wi + 16 * i, kk);
+            for (int i = 0; i < NBI; ++i) xf[i] = operand_x(sX, i, kk);
 #pragma unroll
-            for (int j = 0; j < NBO; ++j) gf[j] = operand(sG, TO * 2, wo + 16 * j, kk);
+            for (int j = 0; j < NBO; ++j) gf[j] = operand(sG, wo + 16 * j, kk);
             // (past the last tile: zeros, into a stage never read)
             if constexpr (kk == 0) load_x(mt + 64, nX);
             else {
@@ -149,7 +168,6 @@ __global__ __launch_bounds__(64 * WO * WI) void grouped_dw_kernel(GroupedDw p, i
         wait_loads();  // none may still be writing this workgroup's LDS when it ends
     }
 
-    // lane: output row o = .. + r16, columns 4 c16 .. + 3 of each block
     const int64_t base = (int64_t)er * p.O * p.I;
     auto put = [&](auto dt) ALWAYS_INLINE {
         constexpr int DT = decltype(dt)::value;  // -1: any type and alignment
@@ -157,28 +175,24 @@ __global__ __launch_bounds__(64 * WO * WI) void grouped_dw_kernel(GroupedDw p, i
             constexpr int j = decltype(jc)::value;
             const int o = o0 + wo + 16 * j + r16;
             if (o >= p.O) return;
-            static_for<0, NBI>([&](auto ic) {
-                constexpr int i = decltype(ic)::value;
-                const int c = i0 + wi + 16 * i + 4 * c16;
+            static_for<0, NBI / 2>([&](auto ic) {
+                constexpr int i = 2 * decltype(ic)::value;
+                const int c = i0 + wi + 16 * i + 8 * c16;
                 if (c >= p.I) return;
                 const int64_t at = base + (int64_t)o * p.I + c;
-                const f32x4 v = acc[i][j];
+                const f32x4 v = acc[i][j], w = acc[i + 1][j];
                 if constexpr (DT < 0) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        if (c + q < p.I) store_from_f32(p.out, p.out_dtype, at + q, v[q]);
+                    for (int q = 0; q < 8; ++q)
+                        if (c + q < p.I) store_from_f32(p.out, p.out_dtype, at + q, q < 4 ? v[q & 3] : w[q & 3]);
                 } else if constexpr (DT == SG_F32) {
                     *(f32x4*)((float*)p.out + at) = v;
+                    *(f32x4*)((float*)p.out + at + 4) = w;
                 } else {
-                    u32x2 w;
-                    if constexpr (DT == SG_BF16) {
-                        w[0] = f32_to_bf16(v[0]) | ((uint32_t)f32_to_bf16(v[1]) << 16);
-                        w[1] = f32_to_bf16(v[2]) | ((uint32_t)f32_to_bf16(v[3]) << 16);
-                    } else {
-                        w[0] = f32_to_f16(v[0]) | ((uint32_t)f32_to_f16(v[1]) << 16);
-                        w[1] = f32_to_f16(v[2]) | ((uint32_t)f32_to_f16(v[3]) << 16);
-                    }
-                    *(u32x2*)((uint16_t*)p.out + at) = w;
+                    auto half = [](float f) { return (uint32_t)(DT == SG_BF16 ? f32_to_bf16(f) : f32_to_f16(f)); };
+                    *(u32x4*)((uint16_t*)p.out + at) =
+                        u32x4{half(v[0]) | (half(v[1]) << 16), half(v[2]) | (half(v[3]) << 16),
+                              half(w[0]) | (half(w[1]) << 16), half(w[2]) | (half(w[3]) << 16)};
                 }
             });
         });
@@ -214,7 +228,16 @@ hipError_t dw_type(const GroupedDw& p, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_grouped_dw(const GroupedDw& p, hipStream_t s) {
+hipError_t launch_grouped_dw(const GroupedDw& call, hipStream_t s) {
+    GroupedDw p = call;
+    // slot / kdiv as a multiplication: exact for slots below 2^31 (the error of
+    // kmul, at most kdiv, times a slot stays below 2^(32 + kshift))
+    if (p.kdiv > 1) {
+        int log = 31 - __builtin_clz((unsigned)p.kdiv);
+        if ((p.kdiv & (p.kdiv - 1)) == 0) --log;
+        p.kshift = log;
+        p.kmul = (uint32_t)((1ull << (32 + log)) / (unsigned)p.kdiv + 1);
+    }
     return p.f16 ? dw_type<true>(p, s) : dw_type<false>(p, s);
 }
 

@@ -214,21 +214,22 @@ def test_mxfp4_integers_exact(acts):
     assert torch.equal(got.double().cpu(), want)
 
 
+@pytest.mark.parametrize("R", [5, 100])
 @pytest.mark.parametrize("acts", [16, 4])
-def test_mxfp4_nan_scale(acts):
+def test_mxfp4_nan_scale(acts, R):
     g = gen(4)
     codes, scales = mx_weights(g, 1, 48, 128)
     codes[0, 7] = 0
     scales[0, 7, 2] = 255
     layer = sg.shard_mxfp4_experts(codes.cuda(), scales.cuda(), "all-to-sharded")
-    x = normal(g, (5, 128), BF).cuda()
+    x = normal(g, (R, 128), BF).cuda()
     if acts == 4:
         c, s = sg.quantize_mxfp4(x)
         s[3, 1] = 255
         got = sg.experts_all_to_sharded(layer, c, x_scales=s)
     else:
         got = sg.experts_all_to_sharded(layer, x)
-    nan = torch.zeros((1, 5, 48), dtype=torch.bool)
+    nan = torch.zeros((1, R, 48), dtype=torch.bool)
     nan[..., 7] = True
     if acts == 4:
         nan[0, 3] = True

@@ -205,60 +205,67 @@ struct Slot {
     int e, row0, nrows;  // expert (-1: none), first row, rows of the tile (at most TM)
 };
 
-// The `slot`-th tile of TM rows, counting expert after expert.  Every lane of
-// the wave calls it and gets the same answer; the offsets are clamped to
-// 0 .. R, so that no content of theirs leads out of the arrays.
-__device__ __forceinline__ Slot find_slot(const int32_t* offsets, int E, int R, int slot, int TM) {
-    if (!offsets) {
-        const int r0 = slot * TM;
-        return r0 < R ? Slot{0, r0, min(TM, R - r0)} : Slot{-1, 0, 0};
+// The tiles of TM rows that the experts' rows make up, counting expert after
+// expert.  Every lane of the wave takes part and gets the same answers; the
+// offsets are clamped to 0 .. R, so that no content of theirs leads out of the
+// arrays.  Up to 64 experts the offsets are read once, one a lane.
+struct SlotMap {
+    const int32_t* offsets;
+    int E, R, TM;
+    int b, n, t, sum;  // this lane's expert: first row, rows, tiles, tiles up to and with it
+
+    __device__ __forceinline__ SlotMap(const int32_t* o, int experts, int rows, int tile)
+        : offsets(o), E(experts), R(rows), TM(tile), b(0), n(0), t(0), sum(0) {
+        if (offsets) read(0);
     }
-    const int lane = threadIdx.x & 63;
-    int before = 0;
-    for (int e0 = 0; e0 < E; e0 += 64) {
-        const int e = e0 + lane;
-        int b = 0, n = 0;
+    __device__ __forceinline__ void read(int e0) {
+        const int lane = threadIdx.x & 63, e = e0 + lane;
+        b = n = 0;
         if (e < E) {
             b = min(max(offsets[e], 0), R);
             n = max(min(offsets[e + 1], R) - b, 0);
         }
-        const int t = (n + TM - 1) / TM;
-        int sum = t;
+        t = (n + TM - 1) / TM;
+        sum = t;
 #pragma unroll
         for (int d = 1; d < 64; d *= 2) {
             const int v = __shfl_up(sum, d);
             if (lane >= d) sum += v;
         }
-        const uint64_t hit = __ballot(before + sum > slot);
-        if (hit) {
-            const int l = __builtin_ctzll(hit);
-            const int first = before + __shfl(sum, l) - __shfl(t, l);
-            const int row = (slot - first) * TM;
-            const int bb = __shfl(b, l), nn = __shfl(n, l);
-            // (falling offsets can count more tiles than an int holds)
-            if (__builtin_amdgcn_readfirstlane(row) < 0 || __builtin_amdgcn_readfirstlane(row - nn) >= 0)
-                return Slot{-1, 0, 0};
-            return Slot{__builtin_amdgcn_readfirstlane(e0 + l), __builtin_amdgcn_readfirstlane(bb + row),
-                        __builtin_amdgcn_readfirstlane(min(TM, nn - row))};
+    }
+    __device__ __forceinline__ int count() {
+        if (!offsets) return (R + TM - 1) / TM;
+        int total = 0;
+        for (int e0 = 0; e0 < E; e0 += 64) {
+            if (E > 64) read(e0);
+            total += __shfl(sum, 63);
         }
-        before += __shfl(sum, 63);
+        return __builtin_amdgcn_readfirstlane(total);
     }
-    return Slot{-1, 0, 0};
-}
-
-// how many tiles of TM rows there are
-__device__ __forceinline__ int count_slots(const int32_t* offsets, int E, int R, int TM) {
-    if (!offsets) return (R + TM - 1) / TM;
-    const int lane = threadIdx.x & 63;
-    int t = 0;
-    for (int e = lane; e < E; e += 64) {
-        const int b = min(max(offsets[e], 0), R);
-        t += (max(min(offsets[e + 1], R) - b, 0) + TM - 1) / TM;
+    __device__ __forceinline__ Slot find(int slot) {
+        if (!offsets) {
+            const int r0 = slot * TM;
+            return r0 < R ? Slot{0, r0, min(TM, R - r0)} : Slot{-1, 0, 0};
+        }
+        int before = 0;
+        for (int e0 = 0; e0 < E; e0 += 64) {
+            if (E > 64) read(e0);
+            const uint64_t hit = __ballot(before + sum > slot);
+            if (hit) {
+                const int l = __builtin_ctzll(hit);
+                const int first = before + __shfl(sum, l) - __shfl(t, l);
+                const int row = __builtin_amdgcn_readfirstlane((slot - first) * TM);
+                const int bb = __builtin_amdgcn_readfirstlane(__shfl(b, l));
+                const int nn = __builtin_amdgcn_readfirstlane(__shfl(n, l));
+                // (falling offsets can count more tiles than an int holds)
+                if (row < 0 || row >= nn) return Slot{-1, 0, 0};
+                return Slot{__builtin_amdgcn_readfirstlane(e0 + l), bb + row, min(TM, nn - row)};
+            }
+            before += __shfl(sum, 63);
+        }
+        return Slot{-1, 0, 0};
     }
-#pragma unroll
-    for (int d = 32; d; d >>= 1) t += __shfl_xor(t, d);
-    return __builtin_amdgcn_readfirstlane(t);
-}
+};
 
 // input row of grouped row m (-1: reads zeros)
 __device__ __forceinline__ int grouped_row(const int32_t* rows, int kdiv, int T, int m) {

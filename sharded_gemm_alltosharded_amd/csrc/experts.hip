@@ -27,10 +27,25 @@ __device__ __forceinline__ u32x4 mx4_to_bf16(uint32_t w, float scale) {
     return r;
 }
 
+// silu(g) u.  For 16-bit results (NEAR) on the hardware's exponential and
+// reciprocal, off by a few fp32 half steps, far below the result's own rounding:
+// e^-z = 2^t 2^r with t = -z log2 e rounded and r what the rounding left (beyond
+// |t| = 100 the result is 0 or z but for 2^-100, and r would be infinite).
+template <bool NEAR>
 __device__ __forceinline__ f32x4 swiglu4(f32x4 g, f32x4 u) {
     f32x4 v;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = silu_f32(g[e]) * u[e];
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (NEAR) {
+            const float z = g[i], t = -1.44269504f * z;
+            const float r = fabsf(t) < 100.f ? fmaf(-1.44269504f, z, -t) : 0.f;
+            float e = __builtin_amdgcn_exp2f(t);
+            e = fmaf(e * r, 0.693147181f, e);
+            v[i] = z * __builtin_amdgcn_rcpf(1.0f + e) * u[i];
+        } else {
+            v[i] = silu_f32(g[i]) * u[i];
+        }
+    }
     return v;
 }
 
@@ -54,7 +69,9 @@ __device__ __forceinline__ void store_typed(const Grouped& p, int ob0, int row0,
             const int m = 16 * j + (lane & 15);
             if (m >= nrows) return;
             const int64_t o = base + (int64_t)(row0 + m) * p.ldo;
-            const f32x4 v = value(ic, jc);
+            f32x4 v;  // (of the type alone: alignment does not change a result)
+            if (DT < 0 ? p.out_dtype != SG_F32 : DT != SG_F32) v = value(ic, jc, std::true_type{});
+            else v = value(ic, jc, std::false_type{});
             if constexpr (DT < 0) {  // any alignment
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
@@ -117,7 +134,7 @@ __global__ __launch_bounds__(64 * NWV) void grouped_stream_kernel(Grouped p) {
     const int kw = wave % KS, ng = wave / KS;
     const int groups = (p.nout + NG * NB - 1) / (NG * NB);
     const int si = blockIdx.x / groups;
-    const Slot s = find_slot(p.offsets, p.E, p.R, si, 16 * MB);
+    const Slot s = SlotMap(p.offsets, p.E, p.R, 16 * MB).find(si);
     if (s.e < 0) return;
     const int ob0 = ((blockIdx.x - si * groups) * NG + ng) * NB;
 
@@ -241,10 +258,10 @@ __global__ __launch_bounds__(64 * NWV) void grouped_stream_kernel(Grouped p) {
 #pragma unroll
                 for (int b = 0; b < MB; ++b) acc[i][b] += red[(((q * NG + ng) * NW + i) * MB + b) * 64 + lane];
     }
-    store_blocks<NB, MB>(p, ob0, s.row0, s.nrows, [&](auto ic, auto jc) {
+    store_blocks<NB, MB>(p, ob0, s.row0, s.nrows, [&](auto ic, auto jc, auto near) {
         constexpr int n = decltype(ic)::value, b = decltype(jc)::value;
         if constexpr (!SWIGLU) return acc[n][b];
-        else return swiglu4(acc[2 * n][b], acc[2 * n + 1][b]);
+        else return swiglu4<decltype(near)::value>(acc[2 * n][b], acc[2 * n + 1][b]);
     });
 }
 
@@ -526,10 +543,10 @@ __device__ __forceinline__ void grouped_tile(const Grouped& p, const Slot s, con
 
     constexpr int NO = SWIGLU ? NBN / 2 : NBN;  // output blocks of a wave
     const int m0 = wave_m * NBM * 16;
-    store_blocks<NO, NBM>(p, nt * NO * WN + wave_n * NO, s.row0 + m0, s.nrows - m0, [&](auto ic, auto jc) {
+    store_blocks<NO, NBM>(p, nt * NO * WN + wave_n * NO, s.row0 + m0, s.nrows - m0, [&](auto ic, auto jc, auto near) {
         constexpr int i = decltype(ic)::value, j = decltype(jc)::value;
         if constexpr (!SWIGLU) return acc[i][j];
-        else return swiglu4(acc[2 * i][j], acc[2 * i + 1][j]);
+        else return swiglu4<decltype(near)::value>(acc[2 * i][j], acc[2 * i + 1][j]);
     });
 }
 
@@ -541,7 +558,8 @@ __global__ __launch_bounds__(512) void grouped_tile_kernel(Grouped p, int slots,
     // The launch has room for every way the rows may fall on the experts; the
     // tiles that there are, not that room, are dealt out to the XCDs.  (Falling
     // offsets could count more: those are left out.)
-    slots = min(slots, count_slots(p.offsets, p.E, p.R, TM));
+    SlotMap map(p.offsets, p.E, p.R, TM);
+    slots = min(slots, map.count());
     int tiles = slots * tiles_n, rest = 0;
     // 256 x 256 tiles take a compute unit each.  Where the last time round the
     // chip would leave half of it idle or more, its tiles are cut into quarters
@@ -556,7 +574,7 @@ __global__ __launch_bounds__(512) void grouped_tile_kernel(Grouped p, int slots,
         const int g = tile / (GM * tiles_n), first = g * GM, gsz = min(GM, slots - first);
         const int tin = tile - g * GM * tiles_n;
         nt = tin / gsz;
-        return find_slot(p.offsets, p.E, p.R, first + tin % gsz, TM);
+        return map.find(first + tin % gsz);
     };
     int nt;
     if ((int)blockIdx.x < tiles) {
@@ -671,7 +689,7 @@ hipError_t stream_mode(const Grouped& p, hipStream_t s) {
     if constexpr (MODE == G_MX4A4)
         if (p.R > (int64_t)8 * p.E) return stream_launch<MODE, SWIGLU, 2, NB, 1, 4, AL>(p, s);
     if constexpr (MODE < G_MX4) {
-        if constexpr (!SWIGLU && AL)
+        if constexpr (!SWIGLU)
             if (blocks * 2 > want) return stream_launch<MODE, SWIGLU, 1, NB / 2, 4, 4, AL>(p, s);
     } else if constexpr (AL) {
         if (blocks / NB >= want) return stream_launch<MODE, SWIGLU, 1, NB, 1, 4, AL>(p, s);

@@ -482,7 +482,7 @@ def test_experts_update():
 
 CHAIN = [  # T, E, k, D, F, P, dtype
     (1, 8, 2, 256, 512, 8, BF), (3, 4, 4, 64, 96, 1, HF), (33, 64, 4, 128, 64, 4, BF), (300, 5, 3, 200, 366, 2, BF),
-    (1000, 4, 2, 128, 256, 4, HF), (77, 3, 1, 70, 54, 2, BF),
+    (1000, 4, 2, 128, 256, 4, HF), (77, 3, 1, 70, 54, 2, BF), (20, 64, 2, 512, 74, 2, BF),
 ]
 
 

@@ -173,16 +173,18 @@ __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, uint32_t voff, u
 __device__ __forceinline__ void dma4(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, uint8_t* to) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)to, 4, voff, soff, 0, 0);
 }
-// every load, and every LDS write, of this wave has landed
+// every load of this wave but the last N, and every LDS write, has landed
+template <int N = 0>
 __device__ __forceinline__ void wait_loads() {
-    __builtin_amdgcn_s_waitcnt(0x0070);
+    __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | ((N >> 4) << 14));
     asm volatile("" ::: "memory");
 }
 // ... and, behind the barrier, of every wave of the workgroup; no access to
 // memory is moved over it
+template <int N = 0>
 __device__ __forceinline__ void stage_barrier() {
     asm volatile("" ::: "memory");
-    wait_loads();
+    wait_loads<N>();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 }

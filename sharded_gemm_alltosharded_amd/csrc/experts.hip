@@ -272,7 +272,7 @@ __global__ __launch_bounds__(64 * NWV) void grouped_stream_kernel(Grouped p) {
 //
 // A k tile is 64 inputs (MXFP4 weights: 128; MXFP4 x MXFP4: 256, the same 128
 // bytes a row).  Its operands go from memory straight into the stage that the
-// k tile before left: one barrier a k tile, behind which every wave's loads of
+// k tile before left (with four stages, three k tiles ahead): one barrier a k tile, behind which every wave's loads of
 // it have landed; the next k tile's loads are issued between the two halves'
 // operand reads and MFMAs.  With two waves a SIMD the reads of one run beside
 // the MFMAs of the other; a raised wave priority around the MFMAs keeps them
@@ -298,11 +298,16 @@ struct TileShape {
     static constexpr int SW = MODE >= G_MX4 ? BN * FPB : 1, SA = MODE == G_MX4A4 ? TM * 2 : 1;
 };
 
+template <int NS>
+struct Stages {
+    uint8_t *A[NS], *W[NS];
+    uint32_t *SW[NS], *SA[NS];
+};
+
 // n tile nt of the rows of one slot; the stages may be larger than needed
-template <int MODE, bool SWIGLU, bool TRANS, int TM, int BN, bool AL>
-__device__ __forceinline__ void grouped_tile(const Grouped& p, const Slot s, const int nt, uint8_t* sA0, uint8_t* sA1,
-                                             uint8_t* sW0, uint8_t* sW1, uint32_t* sSW0, uint32_t* sSW1, uint32_t* sSA0,
-                                             uint32_t* sSA1) {
+template <int MODE, bool SWIGLU, bool TRANS, int TM, int BN, int NS, bool AL>
+__device__ __forceinline__ void grouped_tile(const Grouped& p, const Slot s, const int nt, const Stages<NS>& stage) {
+    static_assert(AL || NS == 2, "rows staged through registers come one k tile ahead");
     using Shape = TileShape<MODE, TM, BN>;
     constexpr int WM = 2, WN = 4, NWV = WM * WN;
     constexpr int NBM = TM / WM / 16, NBN = BN / WN / 16;
@@ -491,11 +496,17 @@ __device__ __forceinline__ void grouped_tile(const Grouped& p, const Slot s, con
         for (int i = 0; i < LW; ++i) load_w(nW, i);
         advance();
     };
-    auto step = [&](const uint8_t* sA, const uint8_t* sW, const uint32_t* sSW, const uint32_t* sSA, uint8_t* nA,
-                    uint8_t* nW, uint32_t* nSW, uint32_t* nSA) ALWAYS_INLINE {
+    // (of the loads that may stay in flight, a wave's scales are not counted)
+    constexpr int LATER = (NS - 2) * (LA + LW);
+    auto step = [&](auto uc) ALWAYS_INLINE {
+        constexpr int u = decltype(uc)::value, next = (u + NS - 1) % NS;
+        const uint8_t *sA = stage.A[u], *sW = stage.W[u];
+        const uint32_t *sSW = stage.SW[u], *sSA = stage.SA[u];
+        uint8_t *nA = stage.A[next], *nW = stage.W[next];
+        uint32_t *nSW = stage.SW[next], *nSA = stage.SA[next];
         // this wave's loads of the k tile have landed; behind the barrier every
         // wave's have, and every wave has read the k tile before
-        stage_barrier();
+        stage_barrier<LATER>();
         u32x4 wf[NBN], af[NBM];
         // MXFP4 weights: a lane's 32 codes and their scale serve the k tile's four steps
         [[maybe_unused]] u32x4 codes[NBN];
@@ -523,21 +534,23 @@ __device__ __forceinline__ void grouped_tile(const Grouped& p, const Slot s, con
             multiply(sSW, sSA, kk, wf, af);
         });
     };
-    auto load_step = [&](uint8_t* nA, uint8_t* nW, uint32_t* nSW, uint32_t* nSA) ALWAYS_INLINE {
-        stage_barrier();
-        issue(nA, nW, nSW, nSA);
-    };
-    issue(sA0, sW0, sSW0, sSA0);
+    static_for<0, NS - 1>([&](auto uc) ALWAYS_INLINE {
+        constexpr int u = decltype(uc)::value;
+        issue(stage.A[u], stage.W[u], stage.SW[u], stage.SA[u]);
+    });
     if (wave_m * NBM * 16 < s.nrows) {
-        for (int t = 0; t < nkt; t += 2) {
-            step(sA0, sW0, sSW0, sSA0, sA1, sW1, sSW1, sSA1);
-            if (t + 1 < nkt) step(sA1, sW1, sSW1, sSA1, sA0, sW0, sSW0, sSA0);
-        }
+        for (int t = 0; t < nkt; t += NS)
+            static_for<0, NS>([&](auto uc) ALWAYS_INLINE {
+                if (decltype(uc)::value == 0 || t + decltype(uc)::value < nkt) step(uc);
+            });
     } else {  // none of the wave's rows is there: its share of the loads is all
-        for (int t = 0; t < nkt; t += 2) {
-            load_step(sA1, sW1, sSW1, sSA1);
-            if (t + 1 < nkt) load_step(sA0, sW0, sSW0, sSA0);
-        }
+        for (int t = 0; t < nkt; t += NS)
+            static_for<0, NS>([&](auto uc) ALWAYS_INLINE {
+                constexpr int u = decltype(uc)::value, next = (u + NS - 1) % NS;
+                if (u > 0 && t + u >= nkt) return;
+                stage_barrier<LATER>();
+                issue(stage.A[next], stage.W[next], stage.SW[next], stage.SA[next]);
+            });
     }
     wait_loads();  // none may still be writing this workgroup's LDS when it ends
 
@@ -550,11 +563,22 @@ __device__ __forceinline__ void grouped_tile(const Grouped& p, const Slot s, con
     });
 }
 
-template <int MODE, bool SWIGLU, bool TRANS, int TM, int BN, bool AL>
+template <int MODE, bool SWIGLU, bool TRANS, int TM, int BN, int NS, bool AL>
 __global__ __launch_bounds__(512) void grouped_tile_kernel(Grouped p, int slots, int tiles_n, int cus) {
     using Shape = TileShape<MODE, TM, BN>;
-    __shared__ __attribute__((aligned(1024))) uint8_t sA0[Shape::A], sA1[Shape::A], sW0[Shape::W], sW1[Shape::W];
-    __shared__ uint32_t sSW0[Shape::SW], sSW1[Shape::SW], sSA0[Shape::SA], sSA1[Shape::SA];
+    constexpr bool R = NS == 4;  // (a ring of four, or two)
+    static_assert(NS == 2 || NS == 4, "stages");
+    __shared__ __attribute__((aligned(1024))) uint8_t sA0[Shape::A], sA1[Shape::A], sW0[Shape::W], sW1[Shape::W],
+        sA2[R ? Shape::A : 4], sA3[R ? Shape::A : 4], sW2[R ? Shape::W : 4], sW3[R ? Shape::W : 4];
+    __shared__ uint32_t sSW0[Shape::SW], sSW1[Shape::SW], sSA0[Shape::SA], sSA1[Shape::SA], sSW2[R ? Shape::SW : 1],
+        sSW3[R ? Shape::SW : 1], sSA2[R ? Shape::SA : 1], sSA3[R ? Shape::SA : 1];
+    Stages<NS> stage;
+    stage.A[0] = sA0, stage.W[0] = sW0, stage.SW[0] = sSW0, stage.SA[0] = sSA0;
+    stage.A[1] = sA1, stage.W[1] = sW1, stage.SW[1] = sSW1, stage.SA[1] = sSA1;
+    if constexpr (R) {
+        stage.A[2] = sA2, stage.W[2] = sW2, stage.SW[2] = sSW2, stage.SA[2] = sSA2;
+        stage.A[3] = sA3, stage.W[3] = sW3, stage.SW[3] = sSW3, stage.SA[3] = sSA3;
+    }
     // The launch has room for every way the rows may fall on the experts; the
     // tiles that there are, not that room, are dealt out to the XCDs.  (Falling
     // offsets could count more: those are left out.)
@@ -580,7 +604,7 @@ __global__ __launch_bounds__(512) void grouped_tile_kernel(Grouped p, int slots,
     if ((int)blockIdx.x < tiles) {
         const Slot s = slot_of(xcd_remap(blockIdx.x, tiles), nt);
         if (s.e < 0) return;
-        grouped_tile<MODE, SWIGLU, TRANS, TM, BN, AL>(p, s, nt, sA0, sA1, sW0, sW1, sSW0, sSW1, sSA0, sSA1);
+        grouped_tile<MODE, SWIGLU, TRANS, TM, BN, NS, AL>(p, s, nt, stage);
     } else if constexpr (TM == 256) {
         if ((int)blockIdx.x >= tiles + 4 * rest) return;
         const int q = xcd_remap(blockIdx.x - tiles, 4 * rest);
@@ -588,8 +612,7 @@ __global__ __launch_bounds__(512) void grouped_tile_kernel(Grouped p, int slots,
         s.row0 += (q & 1) * 128;
         s.nrows = min(s.nrows - (q & 1) * 128, 128);
         if (s.e < 0 || s.nrows <= 0) return;
-        grouped_tile<MODE, SWIGLU, TRANS, 128, BN / 2, AL>(p, s, 2 * nt + ((q >> 1) & 1), sA0, sA1, sW0, sW1, sSW0, sSW1,
-                                                           sSA0, sSA1);
+        grouped_tile<MODE, SWIGLU, TRANS, 128, BN / 2, NS, AL>(p, s, 2 * nt + ((q >> 1) & 1), stage);
     }
 }
 
@@ -700,7 +723,7 @@ hipError_t stream_mode(const Grouped& p, hipStream_t s) {
     return stream_launch<MODE, SWIGLU, 1, NB / 2, 8, 8, AL>(p, s);
 }
 
-template <int MODE, bool SWIGLU, bool TRANS, int TM, int BN, bool AL>
+template <int MODE, bool SWIGLU, bool TRANS, int TM, int BN, int NS, bool AL>
 hipError_t tile_launch(const Grouped& p, hipStream_t s) {
     constexpr int NB = SWIGLU ? BN / 32 : BN / 16;
     const int64_t slots = p.R / TM + (p.R < p.E ? p.R : p.E);
@@ -708,9 +731,24 @@ hipError_t tile_launch(const Grouped& p, hipStream_t s) {
     const int cus = device_cus();
     const int64_t blocks = slots * tiles_n + (TM == 256 ? 3 * (cus / 2) : 0);
     if (blocks >= kMaxBlocks / 2) return hipErrorInvalidConfiguration;
-    launch(grouped_tile_kernel<MODE, SWIGLU, TRANS, TM, BN, AL>, dim3((unsigned)blocks), dim3(512), 0, s, p, (int)slots,
+    launch(grouped_tile_kernel<MODE, SWIGLU, TRANS, TM, BN, NS, AL>, dim3((unsigned)blocks), dim3(512), 0, s, p, (int)slots,
            (int)tiles_n, cus);
     return hipGetLastError();
+}
+
+// Whether tiles of TM rows and 128 weight rows hardly fill the chip once: they
+// then take four stages, which leave a compute unit room for one workgroup
+// instead of two or three.  us with two / four stages, 8 x (4096 x 14336), 256
+// tiles: m = 32: 200 / 156, 96: 238 / 180; MXFP4 m = 32: 113 / 87; 8 x (28672 x
+// 4096, SwiGLU), 1792 tiles: m = 32: 332 / 324, 128: 471 / 503; 32 x (2048 x 2048,
+// SwiGLU), 512 tiles: m = 64: 58 / 69.
+template <bool SWIGLU, int TM>
+bool few_tiles(const Grouped& p) {
+    const int64_t experts = p.R < p.E ? p.R : p.E;
+    // a quarter more rows than the average expert's are reckoned with
+    const int64_t slots = experts * ((p.R * (int64_t)5 / (4 * experts) + TM - 1) / TM);
+    const int64_t tiles = slots * ((p.nout + (SWIGLU ? 3 : 7)) / (SWIGLU ? 4 : 8));
+    return tiles * 5 <= (int64_t)device_cus() * 6;
 }
 
 // Tile by the rows of an expert, m = R / E on average (they differ: half as
@@ -722,23 +760,28 @@ hipError_t tile_launch(const Grouped& p, hipStream_t s) {
 template <int MODE, bool SWIGLU, bool TRANS, bool AL>
 hipError_t tile_mode(const Grouped& p, hipStream_t s) {
     if constexpr (!AL) {
-        return tile_launch<MODE, SWIGLU, TRANS, 128, 128, false>(p, s);
+        return tile_launch<MODE, SWIGLU, TRANS, 128, 128, 2, false>(p, s);
     } else if constexpr (MODE == G_MX4) {
         // (turning codes into operands costs the narrow tile as much as its few
         // rows' products; gate|up, 64 x 128 / 128 x 256:  m = 64: 185 222  256: 552 531  1024: 1987 1742,
         // down  64: 126 174  256: 280 364  1024: 960 938)
         const int64_t tiles = (p.R / 128 + p.E / 2) * ((p.nout + 15) / 16) * (SWIGLU ? 2 : 1);
         if (p.R >= (int64_t)192 * p.E && tiles >= (int64_t)device_cus() * 6)
-            return tile_launch<MODE, SWIGLU, TRANS, 128, 256, true>(p, s);
-        return tile_launch<MODE, SWIGLU, TRANS, 64, 128, true>(p, s);
+            return tile_launch<MODE, SWIGLU, TRANS, 128, 256, 2, true>(p, s);
+        if (few_tiles<SWIGLU, 64>(p)) return tile_launch<MODE, SWIGLU, TRANS, 64, 128, 4, true>(p, s);
+        return tile_launch<MODE, SWIGLU, TRANS, 64, 128, 2, true>(p, s);
     } else {
         // (MXFP4 products are so short that a wave of tiles more costs them a
         // wider tile's gain: 512 rows of 8 experts, gate|up 461 429, down 221 256)
         const int64_t tiles = (p.R / 256 + p.E / 2) * ((p.nout + 15) / 16) * (SWIGLU ? 2 : 1);
         if (p.R >= (int64_t)128 * p.E && tiles * 10 >= (int64_t)device_cus() * (MODE == G_MX4A4 ? 40 : 7))
-            return tile_launch<MODE, SWIGLU, TRANS, 256, 256, true>(p, s);
-        if (p.R > (int64_t)40 * p.E) return tile_launch<MODE, SWIGLU, TRANS, 128, 128, true>(p, s);
-        return tile_launch<MODE, SWIGLU, TRANS, 64, 128, true>(p, s);
+            return tile_launch<MODE, SWIGLU, TRANS, 256, 256, 2, true>(p, s);
+        if (p.R > (int64_t)40 * p.E) {
+            if (few_tiles<SWIGLU, 128>(p)) return tile_launch<MODE, SWIGLU, TRANS, 128, 128, 4, true>(p, s);
+            return tile_launch<MODE, SWIGLU, TRANS, 128, 128, 2, true>(p, s);
+        }
+        if (few_tiles<SWIGLU, 64>(p)) return tile_launch<MODE, SWIGLU, TRANS, 64, 128, 4, true>(p, s);
+        return tile_launch<MODE, SWIGLU, TRANS, 64, 128, 2, true>(p, s);
     }
 }
 

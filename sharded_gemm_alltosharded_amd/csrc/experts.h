@@ -52,7 +52,6 @@ struct Grouped {
     void* out;
     int out_dtype;
     int64_t ldo, o_rank;
-    int vec;  // rows of the output take 4-column vector stores
 };
 
 // Codes of an MXFP4 layer: the 16-row x 128-input block (block b, step st) is
@@ -89,7 +88,6 @@ struct GroupedDw {
     int kshift;
     void* out;
     int out_dtype;
-    int vec;  // rows of the output take 8-column vector stores
 };
 hipError_t launch_grouped_dw(const GroupedDw& p, hipStream_t s);
 
@@ -194,13 +192,63 @@ __device__ __forceinline__ u32x2 read_tr(const uint8_t* p) {
         u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p));
 }
 
-// eight 16-bit inputs k .. k + 7 of a row, zeros from kl on and for row < 0;
-// any alignment
-__device__ __forceinline__ u32x4 load8_any(const uint16_t* a, int64_t row, int64_t lda, int k, int kl) {
-    uint32_t h[8];
+// eight 16-bit inputs k .. k + 7 of a row, zeros from n on and for row < 0; any
+// alignment (a global load takes every address).  Row 0 is there, n >= 1.  The
+// last chunk of a row is read from the row's last eight inputs and shifted, so
+// that no lane branches and no load leaves its row.
+__device__ __forceinline__ u32x4 load8_any(const uint16_t* a, int64_t row, int64_t ld, int k, int n) {
+    const bool in = row >= 0 && k < n;
+    if (n < 8) {
+        uint32_t h[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) h[e] = row >= 0 && k + e < kl ? a[row * lda + k + e] : 0;
-    return u32x4{h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16)};
+        for (int e = 0; e < 8; ++e) h[e] = in && k + e < n ? a[row * ld + k + e] : 0;
+        return u32x4{h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16)};
+    }
+    const int over = max(k + 8 - n, 0);  // inputs of the chunk past the row's end
+    uint64_t v[2];
+    __builtin_memcpy(v, a + (in ? row * ld + k - over : 0), 16);
+    const uint64_t lo = over & 4 ? v[1] : v[0], hi = over & 4 ? 0 : v[1];
+    const int sh = 16 * (over & 3);
+    const uint64_t x = in ? (lo >> sh) | ((hi << 1) << (63 - sh)) : 0, y = in ? hi >> sh : 0;
+    return u32x4{(uint32_t)x, (uint32_t)(x >> 32), (uint32_t)y, (uint32_t)(y >> 32)};
+}
+
+// four (eight) results in adjacent columns, `left` of them in the row; any alignment
+template <int DT, int N>
+__device__ __forceinline__ void store_cols(void* out, int64_t at, const float (&v)[N], int left) {
+    if (left < N) {
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            if (e < left) store_from_f32(out, DT, at + e, v[e]);
+    } else if constexpr (DT == SG_F32) {
+        __builtin_memcpy((float*)out + at, v, 4 * N);
+    } else {
+        uint32_t w[N / 2];
+#pragma unroll
+        for (int e = 0; e < N / 2; ++e) {
+            const uint32_t lo = DT == SG_BF16 ? f32_to_bf16(v[2 * e]) : f32_to_f16(v[2 * e]);
+            const uint32_t hi = DT == SG_BF16 ? f32_to_bf16(v[2 * e + 1]) : f32_to_f16(v[2 * e + 1]);
+            w[e] = lo | (hi << 16);
+        }
+        __builtin_memcpy((uint16_t*)out + at, w, 2 * N);
+    }
+}
+
+// eight values of any type in adjacent columns, `left` of them in the row (the
+// others zero); any alignment
+template <int DT>
+__device__ __forceinline__ void load_cols(const void* x, int64_t at, float (&v)[8], int64_t left) {
+    if (left < 8) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = e < left ? load_as_f32(x, DT, at + e) : 0.f;
+    } else if constexpr (DT == SG_F32) {
+        __builtin_memcpy(v, (const float*)x + at, 32);
+    } else {
+        uint16_t h[8];
+        __builtin_memcpy(h, (const uint16_t*)x + at, 16);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = DT == SG_BF16 ? bf16_to_f32(h[e]) : f16_to_f32(h[e]);
+    }
 }
 
 struct Slot {

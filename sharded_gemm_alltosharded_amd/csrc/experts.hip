@@ -51,7 +51,6 @@ __device__ __forceinline__ f32x4 swiglu4(f32x4 g, f32x4 u) {
 
 // Stores a wave's N x M result blocks: value(i, j) is this lane's four columns
 // 4 (lane >> 4) .. + 3 of output block ob0 + i, row row0 + 16 j + (lane & 15).
-// DT -1: any type and alignment.
 template <int DT, int N, int M, typename F>
 __device__ __forceinline__ void store_typed(const Grouped& p, int ob0, int row0, int nrows, F&& value) {
     const int lane = threadIdx.x & 63;
@@ -68,34 +67,15 @@ __device__ __forceinline__ void store_typed(const Grouped& p, int ob0, int row0,
             constexpr int j = decltype(jc)::value;
             const int m = 16 * j + (lane & 15);
             if (m >= nrows) return;
-            const int64_t o = base + (int64_t)(row0 + m) * p.ldo;
-            f32x4 v;  // (of the type alone: alignment does not change a result)
-            if (DT < 0 ? p.out_dtype != SG_F32 : DT != SG_F32) v = value(ic, jc, std::true_type{});
-            else v = value(ic, jc, std::false_type{});
-            if constexpr (DT < 0) {  // any alignment
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (c + e < p.f) store_from_f32(p.out, p.out_dtype, o + e, v[e]);
-            } else if constexpr (DT == SG_F32) {
-                *(f32x4*)((float*)p.out + o) = v;
-            } else {
-                u32x2 w;
-                if constexpr (DT == SG_BF16) {
-                    w[0] = f32_to_bf16(v[0]) | ((uint32_t)f32_to_bf16(v[1]) << 16);
-                    w[1] = f32_to_bf16(v[2]) | ((uint32_t)f32_to_bf16(v[3]) << 16);
-                } else {
-                    w[0] = f32_to_f16(v[0]) | ((uint32_t)f32_to_f16(v[1]) << 16);
-                    w[1] = f32_to_f16(v[2]) | ((uint32_t)f32_to_f16(v[3]) << 16);
-                }
-                *(u32x2*)((uint16_t*)p.out + o) = w;
-            }
+            const f32x4 q = value(ic, jc, std::bool_constant<DT != SG_F32>{});
+            const float v[4] = {q[0], q[1], q[2], q[3]};
+            store_cols<DT>(p.out, base + (int64_t)(row0 + m) * p.ldo, v, p.f - c);
         });
     });
 }
 template <int N, int M, typename F>
 __device__ __forceinline__ void store_blocks(const Grouped& p, int ob0, int row0, int nrows, F&& value) {
-    if (!p.vec) store_typed<-1, N, M>(p, ob0, row0, nrows, value);
-    else if (p.out_dtype == SG_BF16) store_typed<SG_BF16, N, M>(p, ob0, row0, nrows, value);
+    if (p.out_dtype == SG_BF16) store_typed<SG_BF16, N, M>(p, ob0, row0, nrows, value);
     else if (p.out_dtype == SG_F16) store_typed<SG_F16, N, M>(p, ob0, row0, nrows, value);
     else store_typed<SG_F32, N, M>(p, ob0, row0, nrows, value);
 }
@@ -370,15 +350,22 @@ __device__ __forceinline__ void grouped_tile(const Grouped& p, const Slot s, con
     auto load_a = [&](uint8_t* sA, int i) ALWAYS_INLINE {
         const int k = ik + chunk_of(i) * KPC;
         uint8_t* to = sA + (i * NWV + wave) * 1024;
-        if constexpr (AL) {
-            const uint8_t* base = (const uint8_t*)p.A + (A4 ? ia / 2 : ia * 2);
-            uint32_t off = aoff[i];
-            if (ik + KT > p.kl && k >= p.kl) off = kOutside;
-            dma16(buffer(base, bytes(a_bytes)), off, (uint32_t)(A4 ? ik / 2 : ik * 2), to);
-        } else {
-            const uint16_t* base = (const uint16_t*)p.A + ia;
-            *(u32x4*)(to + lane * 16) = load8_any(base, iseg < p.nseg ? arow[i] : -1, p.lda, k, p.kl);
-        }
+        const uint8_t* base = (const uint8_t*)p.A + (A4 ? ia / 2 : ia * 2);
+        uint32_t off = aoff[i];
+        if (ik + KT > p.kl && k >= p.kl) off = kOutside;
+        dma16(buffer(base, bytes(a_bytes)), off, (uint32_t)(A4 ? ik / 2 : ik * 2), to);
+    };
+    // rows of any alignment: through registers, into LDS when the k tile at hand is done
+    [[maybe_unused]] u32x4 av[LA];
+    auto fetch_a = [&]() ALWAYS_INLINE {
+#pragma unroll
+        for (int i = 0; i < LA; ++i)
+            av[i] = load8_any((const uint16_t*)p.A + (iseg < p.nseg ? ia : 0), iseg < p.nseg ? arow[i] : -1, p.lda,
+                              ik + chunk_of(i) * KPC, p.kl);
+    };
+    auto put_a = [&](uint8_t* sA) ALWAYS_INLINE {
+#pragma unroll
+        for (int i = 0; i < LA; ++i) *(u32x4*)(sA + (i * NWV + wave) * 1024 + lane * 16) = av[i];
     };
     auto load_w = [&](uint8_t* sW, int i) ALWAYS_INLINE {
         const int f = i * NWV + wave;
@@ -490,8 +477,13 @@ __device__ __forceinline__ void grouped_tile(const Grouped& p, const Slot s, con
     };
     auto issue = [&](uint8_t* nA, uint8_t* nW, uint32_t* nSW, uint32_t* nSA) ALWAYS_INLINE {
         load_scales(nSW, nSA);
+        if constexpr (AL) {
 #pragma unroll
-        for (int i = 0; i < LA; ++i) load_a(nA, i);
+            for (int i = 0; i < LA; ++i) load_a(nA, i);
+        } else {
+            fetch_a();
+            put_a(nA);
+        }
 #pragma unroll
         for (int i = 0; i < LW; ++i) load_w(nW, i);
         advance();
@@ -524,8 +516,12 @@ __device__ __forceinline__ void grouped_tile(const Grouped& p, const Slot s, con
             read(sA, sW, codes, scale, kk, wf, af);
             if constexpr (!A4 && kk == 0) {
                 load_scales(nSW, nSA);
+                if constexpr (AL) {
 #pragma unroll
-                for (int i = 0; i < LA; ++i) load_a(nA, i);
+                    for (int i = 0; i < LA; ++i) load_a(nA, i);
+                } else {
+                    fetch_a();
+                }
             } else if constexpr (!A4 && kk == 1) {
 #pragma unroll
                 for (int i = 0; i < LW; ++i) load_w(nW, i);
@@ -533,6 +529,7 @@ __device__ __forceinline__ void grouped_tile(const Grouped& p, const Slot s, con
             }
             multiply(sSW, sSA, kk, wf, af);
         });
+        if constexpr (!AL) put_a(nA);
     };
     static_for<0, NS - 1>([&](auto uc) ALWAYS_INLINE {
         constexpr int u = decltype(uc)::value;

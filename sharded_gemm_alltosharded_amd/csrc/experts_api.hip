@@ -203,7 +203,6 @@ int mode_of(const sg_experts* x, const uint8_t* a_scales) {
 void set_out(sg::Grouped& p, void* y, sg_dtype dt) {
     p.out = y;
     p.out_dtype = dt;
-    p.vec = p.f % 4 == 0 && p.ldo % 4 == 0 && p.o_rank % 4 == 0 && aligned(y, 16);
 }
 
 // x (T, in) -> ranks' columns; ldh: columns of a rank's output row that are
@@ -515,7 +514,6 @@ sg_status sg_experts_all_to_sharded_backward(const sg_experts* x, const void* a,
         p.I = (int)l.in;
         p.out = dw;
         p.out_dtype = dw_dtype;
-        p.vec = l.in % 8 == 0 && aligned(dw, 16);
         st = launched(sg::launch_grouped_dw(p, s), "sg_experts_all_to_sharded_backward dw");
     }
     return st;
@@ -572,7 +570,6 @@ sg_status sg_experts_sharded_to_all_backward(const sg_experts* x, const void* h,
         p.I = (int)l.kl;
         p.out = dw;
         p.out_dtype = dw_dtype;
-        p.vec = l.kl % 8 == 0 && aligned(dw, 16);
         st = launched(sg::launch_grouped_dw(p, s), "sg_experts_sharded_to_all_backward dw");
     }
     return st;

@@ -77,14 +77,23 @@ __global__ __launch_bounds__(64 * WO * WI) void grouped_dw_kernel(GroupedDw p, i
             raw[i] = p.rows[min(m, p.R - 1)];
         }
     };
+    // (rows of any alignment go through registers, into LDS when the tile at hand is done)
+    [[maybe_unused]] u32x4 gv[LG], xv[LX];
+    auto put_rows = [&](uint8_t* g, uint8_t* x) ALWAYS_INLINE {
+        if constexpr (!AL) {
+#pragma unroll
+            for (int i = 0; i < LG; ++i) *(u32x4*)(g + (i * NWV + wave) * 1024 + lane * 16) = gv[i];
+#pragma unroll
+            for (int i = 0; i < LX; ++i) *(u32x4*)(x + (i * NWV + wave) * 1024 + lane * 16) = xv[i];
+        }
+    };
     auto load_g = [&](int mt, uint8_t* s) ALWAYS_INLINE {
         const uint32_t at = mt < m1 ? (uint32_t)(mt * p.ldg * 2) : 0;
 #pragma unroll
         for (int i = 0; i < LG; ++i) {
             const int m = mt + (i * NWV + wave) * (64 / CG) + lane / CG;
-            uint8_t* to = s + (i * NWV + wave) * 1024;
-            if constexpr (AL) dma16(bg, m < m1 ? goff[i] : kOutside, at, to);
-            else *(u32x4*)(to + lane * 16) = load8_any(G, m < m1 ? m : -1, p.ldg, gcol[i], p.O);
+            if constexpr (AL) dma16(bg, m < m1 ? goff[i] : kOutside, at, s + (i * NWV + wave) * 1024);
+            else gv[i] = load8_any(G, m < m1 ? m : -1, p.ldg, gcol[i], p.O);
         }
     };
     auto load_x = [&](int mt, uint8_t* s) ALWAYS_INLINE {
@@ -92,16 +101,15 @@ __global__ __launch_bounds__(64 * WO * WI) void grouped_dw_kernel(GroupedDw p, i
 #pragma unroll
         for (int i = 0; i < LX; ++i) {
             const int m = mt + (i * NWV + wave) * (64 / CX) + lane / CX;
-            uint8_t* to = s + (i * NWV + wave) * 1024;
             int row = m;
             if (p.rows) row = raw[i] < 0 ? -1 : p.kmul ? (int)(__umulhi((uint32_t)raw[i], p.kmul) >> p.kshift) : raw[i];
             const bool in = m < m1 && row >= 0 && row < p.T;
             if constexpr (AL) {
                 uint32_t off = xoff[i];
                 if (p.rows) off = xcol[i] < p.I ? off + (uint32_t)row * (uint32_t)(p.ldx * 2) : kOutside;
-                dma16(bx, in ? off : kOutside, at, to);
+                dma16(bx, in ? off : kOutside, at, s + (i * NWV + wave) * 1024);
             } else {
-                *(u32x4*)(to + lane * 16) = load8_any(X, in ? row : -1, p.ldx, xcol[i], p.I);
+                xv[i] = load8_any(X, in ? row : -1, p.ldx, xcol[i], p.I);
             }
         }
     };
@@ -155,11 +163,13 @@ __global__ __launch_bounds__(64 * WO * WI) void grouped_dw_kernel(GroupedDw p, i
                 for (int i = 0; i < NBI; ++i) acc[i][j] = mfma16<F16>(xf[i], gf[j], acc[i][j]);
             __builtin_amdgcn_s_setprio(0);
         });
+        put_rows(nG, nX);
     };
     if (m0 < m1) {
         fetch_rows(m0);
         load_x(m0, sX0);
         load_g(m0, sG0);
+        put_rows(sG0, sX0);
         fetch_rows(m0 + 64);
         for (int mt = m0; mt < m1; mt += 128) {
             step(mt, sG0, sX0, sG1, sX1);
@@ -170,7 +180,7 @@ __global__ __launch_bounds__(64 * WO * WI) void grouped_dw_kernel(GroupedDw p, i
 
     const int64_t base = (int64_t)er * p.O * p.I;
     auto put = [&](auto dt) ALWAYS_INLINE {
-        constexpr int DT = decltype(dt)::value;  // -1: any type and alignment
+        constexpr int DT = decltype(dt)::value;
         static_for<0, NBO>([&](auto jc) {
             constexpr int j = decltype(jc)::value;
             const int o = o0 + wo + 16 * j + r16;
@@ -179,26 +189,13 @@ __global__ __launch_bounds__(64 * WO * WI) void grouped_dw_kernel(GroupedDw p, i
                 constexpr int i = 2 * decltype(ic)::value;
                 const int c = i0 + wi + 16 * i + 8 * c16;
                 if (c >= p.I) return;
-                const int64_t at = base + (int64_t)o * p.I + c;
-                const f32x4 v = acc[i][j], w = acc[i + 1][j];
-                if constexpr (DT < 0) {
-#pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        if (c + q < p.I) store_from_f32(p.out, p.out_dtype, at + q, q < 4 ? v[q & 3] : w[q & 3]);
-                } else if constexpr (DT == SG_F32) {
-                    *(f32x4*)((float*)p.out + at) = v;
-                    *(f32x4*)((float*)p.out + at + 4) = w;
-                } else {
-                    auto half = [](float f) { return (uint32_t)(DT == SG_BF16 ? f32_to_bf16(f) : f32_to_f16(f)); };
-                    *(u32x4*)((uint16_t*)p.out + at) =
-                        u32x4{half(v[0]) | (half(v[1]) << 16), half(v[2]) | (half(v[3]) << 16),
-                              half(w[0]) | (half(w[1]) << 16), half(w[2]) | (half(w[3]) << 16)};
-                }
+                const f32x4 a = acc[i][j], b = acc[i + 1][j];
+                const float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+                store_cols<DT>(p.out, base + (int64_t)o * p.I + c, v, p.I - c);
             });
         });
     };
-    if (!p.vec) put(std::integral_constant<int, -1>{});
-    else if (p.out_dtype == SG_BF16) put(std::integral_constant<int, SG_BF16>{});
+    if (p.out_dtype == SG_BF16) put(std::integral_constant<int, SG_BF16>{});
     else if (p.out_dtype == SG_F16) put(std::integral_constant<int, SG_F16>{});
     else put(std::integral_constant<int, SG_F32>{});
 }

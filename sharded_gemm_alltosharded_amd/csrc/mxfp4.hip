@@ -16,33 +16,14 @@ namespace {
 
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
-template <int DT, bool AL>
-__device__ __forceinline__ void load8(const void* x, int64_t i, float (&v)[8]) {
-    if constexpr (!AL) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = load_as_f32(x, DT, i + e);
-    } else if constexpr (DT == SG_F32) {
-        const f32x4 a = *(const f32x4*)((const float*)x + i), b = *(const f32x4*)((const float*)x + i + 4);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = a[e], v[4 + e] = b[e];
-    } else {
-        const u32x4 w = *(const u32x4*)((const uint16_t*)x + i);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const uint16_t h = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
-            v[e] = DT == SG_BF16 ? bf16_to_f32(h) : f16_to_f32(h);
-        }
-    }
-}
-
-template <int DT, bool AL>
+template <int DT>
 __global__ __launch_bounds__(256) void quantize_kernel(const void* x, int64_t n8, int64_t cols8, int64_t ld,
                                                        uint8_t* codes, uint8_t* scales) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;  // which 8 values; n8 is a multiple of 4
     if (i >= n8) return;
     const int64_t row = i / cols8, c = i - row * cols8;
     float v[8];
-    load8<DT, AL>(x, row * ld + c * 8, v);
+    load_cols<DT>(x, row * ld + c * 8, v, 8);
     // magnitudes compare like their bit patterns; infinities and NaNs are the largest
     uint32_t m = 0;
 #pragma unroll
@@ -83,30 +64,14 @@ __global__ __launch_bounds__(256) void dequantize_kernel(const uint8_t* codes, c
     v[0] = a[0], v[1] = a[1], v[2] = b[0], v[3] = b[1], v[4] = c[0], v[5] = c[1], v[6] = d[0], v[7] = d[1];
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = s == 255 ? __builtin_nanf("") : ldexpf(v[e], s - 127);
-    if constexpr (DT == SG_F32) {
-        *(f32x4*)((float*)x + i * 8) = f32x4{v[0], v[1], v[2], v[3]};
-        *(f32x4*)((float*)x + i * 8 + 4) = f32x4{v[4], v[5], v[6], v[7]};
-    } else {
-        u32x4 o;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint32_t lo = DT == SG_BF16 ? f32_to_bf16(v[2 * e]) : f32_to_f16(v[2 * e]);
-            const uint32_t hi = DT == SG_BF16 ? f32_to_bf16(v[2 * e + 1]) : f32_to_f16(v[2 * e + 1]);
-            o[e] = lo | (hi << 16);
-        }
-        *(u32x4*)((uint16_t*)x + i * 8) = o;
-    }
+    store_cols<DT>(x, i * 8, v, 8);
 }
 
 template <int DT>
 void quantize(const void* x, int64_t rows, int64_t cols, int64_t ld, uint8_t* codes, uint8_t* scales, hipStream_t s) {
     const int64_t n8 = rows * (cols / 8);
     const dim3 grid((unsigned)((n8 + 255) / 256));
-    const size_t esz = DT == SG_F32 ? 4 : 2;
-    if ((uintptr_t)x % 16 == 0 && ld * esz % 16 == 0)
-        launch(quantize_kernel<DT, true>, grid, dim3(256), 0, s, x, n8, cols / 8, ld, codes, scales);
-    else
-        launch(quantize_kernel<DT, false>, grid, dim3(256), 0, s, x, n8, cols / 8, ld, codes, scales);
+    launch(quantize_kernel<DT>, grid, dim3(256), 0, s, x, n8, cols / 8, ld, codes, scales);
 }
 
 }  // namespace

@@ -354,56 +354,10 @@ __global__ __launch_bounds__(256) void route_backward_kernel(Route r, const floa
 // ---- weighted sum of a token's rows ----------------------------------------
 // out[t] = sum_j w[t][j] y[slots[t][j]] in choice order, dropped slots left
 // out.  Bound by HBM: every row read once, every output written once.  A
-// thread owns 8 (VEC) adjacent columns.
-template <int DT>
-__device__ __forceinline__ void load_vec8(const void* x, int64_t i, float (&v)[8]) {
-    if constexpr (DT == SG_F32) {
-        const f32x4 a = *(const f32x4*)((const float*)x + i), b = *(const f32x4*)((const float*)x + i + 4);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = a[e], v[4 + e] = b[e];
-    } else {
-        const u32x4 w = *(const u32x4*)((const uint16_t*)x + i);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const uint16_t h = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
-            v[e] = DT == SG_BF16 ? bf16_to_f32(h) : f16_to_f32(h);
-        }
-    }
-}
-template <int DT>
-__device__ __forceinline__ void store_vec8(void* x, int64_t i, const float (&v)[8]) {
-    if constexpr (DT == SG_F32) {
-        *(f32x4*)((float*)x + i) = f32x4{v[0], v[1], v[2], v[3]};
-        *(f32x4*)((float*)x + i + 4) = f32x4{v[4], v[5], v[6], v[7]};
-    } else {
-        u32x4 o;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint32_t lo = DT == SG_BF16 ? f32_to_bf16(v[2 * e]) : f32_to_f16(v[2 * e]);
-            const uint32_t hi = DT == SG_BF16 ? f32_to_bf16(v[2 * e + 1]) : f32_to_f16(v[2 * e + 1]);
-            o[e] = lo | (hi << 16);
-        }
-        *(u32x4*)((uint16_t*)x + i) = o;
-    }
-}
-// 8 columns from column c of a row of D: the part of them below D
-template <int DT, bool VEC>
-__device__ __forceinline__ void load_cols(const void* x, int64_t row, int64_t D, int64_t c, float (&v)[8]) {
-    if constexpr (VEC) load_vec8<DT>(x, row * D + c, v);
-    else
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = c + e < D ? load_as_f32(x, DT, row * D + c + e) : 0.f;
-}
-template <int DT, bool VEC>
-__device__ __forceinline__ void store_cols(void* x, int64_t row, int64_t D, int64_t c, const float (&v)[8]) {
-    if constexpr (VEC) store_vec8<DT>(x, row * D + c, v);
-    else
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (c + e < D) store_from_f32(x, DT, row * D + c + e, v[e]);
-}
-
-template <int YT, int OT, bool VEC>
+// thread owns 8 adjacent columns.
+// WHOLE: D is a multiple of 8 (with a branch for the row's end between them the
+// loads do not go out together: the gradient below 104 -> 161 us).
+template <int YT, int OT, bool WHOLE>
 __global__ __launch_bounds__(256) void combine_kernel(const void* y, const int32_t* slots, const float* weights, int k,
                                                       int64_t D, int64_t R, void* out, int per_token) {
     const int64_t t = blockIdx.x / per_token;
@@ -418,7 +372,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const void* y, const int32
             const int64_t s = t * k + min(j0 + j, k - 1), row = slots[s];
             in[j] = j0 + j < k && row >= 0 && row < R;
             w[j] = weights ? weights[s] : 1.f;
-            if (in[j]) load_cols<YT, VEC>(y, row, D, c, v[j]);
+            if (in[j]) load_cols<YT>(y, row * D + c, v[j], WHOLE ? 8 : D - c);
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -426,38 +380,42 @@ __global__ __launch_bounds__(256) void combine_kernel(const void* y, const int32
 #pragma unroll
                 for (int e = 0; e < 8; ++e) acc[e] = fmaf(w[j], v[j][e], acc[e]);
     }
-    store_cols<OT, VEC>(out, t, D, c, acc);
+    store_cols<OT>(out, t * D + c, acc, WHOLE ? 8 : (int)min(D - c, (int64_t)8));
 }
 
 // ---- its gradient -----------------------------------------------------------
 // dy[slots[t][j]] = w[t][j] dout[t], dw[t][j] = <dout[t], y[slots[t][j]]>.
 // One workgroup a token: its dout is read once per choice from the caches, the
 // rows of y once.  The dot products are summed over lanes in a fixed tree.
-template <int DT, bool VEC>
-__global__ __launch_bounds__(256) void combine_backward_kernel(const void* dout, const void* y, const int32_t* slots,
-                                                               const float* weights, int k, int64_t D, int64_t R,
+template <int DT, bool WHOLE>
+__global__ __launch_bounds__(256) void combine_backward_kernel(const void* dout, const void* y,
+                                                               const int32_t* __restrict__ slots,
+                                                               const float* __restrict__ weights, int k, int64_t D, int64_t R,
                                                                void* dy, float* dw) {
     __shared__ float part[kRouteMaxK][4];
     const int64_t t = blockIdx.x;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    // (lane j holds slot j: no load of it waits behind the rows')
+    const int mine = lane < k ? slots[t * k + lane] : -1;
+    const float wmine = lane < k && weights ? weights[t * k + lane] : 1.f;
     for (int j = 0; j < k; ++j) {
-        const int64_t row = slots[t * k + j];
+        const int64_t row = __builtin_amdgcn_readlane(mine, j);
         const bool ok = row >= 0 && row < R;
         float dot = 0.f;
         if (ok) {
-            const float w = weights ? weights[t * k + j] : 1.f;
+            const float w = __shfl(wmine, j);
             for (int64_t c = (int64_t)threadIdx.x * 8; c < D; c += 256 * 8) {
                 float g[8], v[8], o[8];
-                load_cols<DT, VEC>(dout, t, D, c, g);
+                load_cols<DT>(dout, t * D + c, g, WHOLE ? 8 : D - c);
                 if (dw) {
-                    load_cols<DT, VEC>(y, row, D, c, v);
+                    load_cols<DT>(y, row * D + c, v, WHOLE ? 8 : D - c);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) dot = fmaf(g[e], v[e], dot);
                 }
                 if (dy) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) o[e] = w * g[e];
-                    store_cols<DT, VEC>(dy, row, D, c, o);
+                    store_cols<DT>(dy, row * D + c, o, WHOLE ? 8 : (int)min(D - c, (int64_t)8));
                 }
             }
         }
@@ -477,26 +435,16 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(const void* dout,
 // ---- SwiGLU on stored gate | up rows ---------------------------------------
 // h = silu(g) u;  with s = 1 / (1 + e^-g): dg = dh u s (1 + g (1 - s)),
 // du = dh g s.  Bound by HBM.
-template <int DT, bool VEC, bool BWD>
+template <int DT, bool BWD, bool WHOLE>
 __global__ __launch_bounds__(256) void swiglu_kernel(const void* gu, const void* dh, int64_t rows, int64_t f,
                                                      int64_t fc, void* out) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= rows * fc) return;
     const int64_t row = i / fc, c = (i - row * fc) * 8;
+    const int left = WHOLE ? 8 : (int)min(f - c, (int64_t)8);
     float g[8], u[8], a[8], b[8];
-    auto part = [&](int64_t base, float (&v)[8], const void* p) {
-        if constexpr (VEC) load_vec8<DT>(p, base + c, v);
-        else
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = c + e < f ? load_as_f32(p, DT, base + c + e) : 0.f;
-    };
-    auto put = [&](int64_t base, const float (&v)[8]) {
-        if constexpr (VEC) store_vec8<DT>(out, base + c, v);
-        else
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (c + e < f) store_from_f32(out, DT, base + c + e, v[e]);
-    };
+    auto part = [&](int64_t base, float(&v)[8], const void* p) { load_cols<DT>(p, base + c, v, left); };
+    auto put = [&](int64_t base, const float(&v)[8]) { store_cols<DT>(out, base + c, v, left); };
     part(row * 2 * f, g, gu);
     part(row * 2 * f + f, u, gu);
     if constexpr (!BWD) {
@@ -539,8 +487,6 @@ void route_v(const Route& r, hipStream_t s) {
     launch(route_place_kernel, dim3(chunks), dim3(64), 0, s, r, ct);
 }
 
-bool al16(const void* p) { return (uintptr_t)p % 16 == 0; }
-
 }  // namespace
 
 size_t route_workspace_ints(int64_t T, int E, int k) {
@@ -573,10 +519,9 @@ hipError_t launch_combine(const void* y, int y_dtype, const int32_t* slots, cons
     const int threads = D >= 2048 ? 256 : D >= 1024 ? 128 : 64;
     const int per = (int)((D + threads * 8 - 1) / (threads * 8));
     const dim3 grid((unsigned)(T * per));
-    const bool vec = D % 8 == 0 && al16(y) && al16(out);
     auto go = [&](auto yt, auto ot) {
         constexpr int YT = decltype(yt)::value, OT = decltype(ot)::value;
-        if (vec) launch(combine_kernel<YT, OT, true>, grid, dim3(threads), 0, s, y, slots, weights, k, D, R, out, per);
+        if (D % 8 == 0) launch(combine_kernel<YT, OT, true>, grid, dim3(threads), 0, s, y, slots, weights, k, D, R, out, per);
         else launch(combine_kernel<YT, OT, false>, grid, dim3(threads), 0, s, y, slots, weights, k, D, R, out, per);
     };
     auto with_out = [&](auto yt) {
@@ -594,10 +539,9 @@ hipError_t launch_combine_backward(const void* dout, const void* y, int dtype, c
                                    const float* weights, int64_t T, int k, int64_t D, int64_t R, void* dy, float* dw,
                                    hipStream_t s) {
     const dim3 grid((unsigned)T);
-    const bool vec = D % 8 == 0 && al16(dout) && (!dw || al16(y)) && (!dy || al16(dy));
     auto go = [&](auto dt) {
         constexpr int DT = decltype(dt)::value;
-        if (vec) launch(combine_backward_kernel<DT, true>, grid, dim3(256), 0, s, dout, y, slots, weights, k, D, R, dy, dw);
+        if (D % 8 == 0) launch(combine_backward_kernel<DT, true>, grid, dim3(256), 0, s, dout, y, slots, weights, k, D, R, dy, dw);
         else launch(combine_backward_kernel<DT, false>, grid, dim3(256), 0, s, dout, y, slots, weights, k, D, R, dy, dw);
     };
     if (dtype == SG_F32) go(std::integral_constant<int, SG_F32>{});
@@ -611,11 +555,10 @@ static hipError_t swiglu_any(const void* gu, const void* dh, int dtype, int64_t 
                              hipStream_t s) {
     const int64_t fc = (f + 7) / 8;
     const dim3 grid((unsigned)((rows * fc + 255) / 256));
-    const bool vec = f % 8 == 0 && al16(gu) && al16(out) && (!BWD || al16(dh));
     auto go = [&](auto dt) {
         constexpr int DT = decltype(dt)::value;
-        if (vec) launch(swiglu_kernel<DT, true, BWD>, grid, dim3(256), 0, s, gu, dh, rows, f, fc, out);
-        else launch(swiglu_kernel<DT, false, BWD>, grid, dim3(256), 0, s, gu, dh, rows, f, fc, out);
+        if (f % 8 == 0) launch(swiglu_kernel<DT, BWD, true>, grid, dim3(256), 0, s, gu, dh, rows, f, fc, out);
+        else launch(swiglu_kernel<DT, BWD, false>, grid, dim3(256), 0, s, gu, dh, rows, f, fc, out);
     };
     if (dtype == SG_F32) go(std::integral_constant<int, SG_F32>{});
     else if (dtype == SG_BF16) go(std::integral_constant<int, SG_BF16>{});

@@ -358,7 +358,9 @@ typedef struct sg_experts sg_experts; /* opaque, owned by the library */
 /* Shard E dense linear layers over P ranks, each by the rules of
  * sg_shard_linear (mode, segments, P); no bias.
  *   weight (E, out_dims, in_dims) of dtype SG_BF16 or SG_F16, host or device
- *   memory.  At most 1024 experts, dimensions below 2^24. */
+ *   memory.  At most 1024 experts, dimensions of 2^24, 4 GiB an expert and 64
+ *   GiB a layer; calls take activation slices (one rank's rows) below 4 GiB
+ *   (else SG_ERR_UNSUPPORTED). */
 sg_status sg_shard_experts(const void* weight, sg_dtype dtype, int64_t E, int64_t out_dims, int64_t in_dims, int mode,
                            int segments, int P, void* stream, sg_experts** out);
 
@@ -425,7 +427,7 @@ sg_status sg_swiglu_backward(const void* gu, const void* dh, sg_dtype dtype, int
 /* Router.  For every token the k experts of the largest logits, in falling
  * order, ties to the lowest expert; a logit of -inf (or NaN) closes the expert
  * to the token, and a token with fewer than k open experts has dropped slots.
- *   logits   (T, E) of dtype, row stride ld; E <= 1024, k <= 16.
+ *   logits   (T, E) of dtype, row stride ld; E <= 1024, k <= 16, T <= 2^25.
  *   weights  (T, k) fp32: the softmax over the token's open experts, with
  *            normalize over its chosen ones; 0 for a dropped slot.
  *   experts  (T, k) int32, -1 for a dropped slot.

@@ -603,13 +603,15 @@ def shard_mxfp4_experts(codes: torch.Tensor, scales: torch.Tensor, sharding, seg
                                                               _mode(sharding), segments, P, s, h), codes.device)
 
 
-def _grouped(layer: Experts, offsets, rows, R):
+def _grouped(layer: Experts, offsets, rows, R, k=1):
+    if rows is not None and k is None:
+        _bad("rows are slots of k choices each: k is None")
     _want(offsets, "offsets", (layer.E + 1,), torch.int32, layer.device, optional=layer.E == 1)
     _want(rows, "rows", (R,), torch.int32, layer.device, optional=True)
 
 
-def experts_all_to_sharded(layer: Experts, x: torch.Tensor, offsets=None, rows=None, k: int = 1, swiglu: bool = False,
-                           x_scales=None, out_dtype=None, out: torch.Tensor | None = None) -> torch.Tensor:
+def experts_all_to_sharded(layer: Experts, x: torch.Tensor, offsets=None, rows=None, k: int | None = None,
+                           swiglu: bool = False, x_scales=None, out_dtype=None, out: torch.Tensor | None = None) -> torch.Tensor:
     """x (T, in) -> (P, R, n / P), rows grouped by expert (sg_experts_all_to_sharded);
     n = out_dims, or out_dims / 2 with the SwiGLU epilogue.
 
@@ -623,11 +625,11 @@ def experts_all_to_sharded(layer: Experts, x: torch.Tensor, offsets=None, rows=N
         _want(x_scales, "x_scales", (x.shape[0], layer.in_dims // 32), torch.uint8, dev)
         ld = layer.in_dims
     R = x.shape[0] if rows is None else rows.shape[0]
-    _grouped(layer, offsets, rows, R)
+    _grouped(layer, offsets, rows, R, k)
     n = layer.out_dims // 2 if swiglu else layer.out_dims
     out = _out(out, "out", (layer.P, R, n // layer.P), out_dtype or layer.dtype, dev)
     _run(lib().sg_experts_all_to_sharded, dev, layer.handle, _at(x), _at(x_scales), x.shape[0], ld, _at(offsets),
-         _at(rows), k, R, _at(out), EPI_SWIGLU if swiglu else EPI_NONE, _DT[out.dtype])
+         _at(rows), k or 1, R, _at(out), EPI_SWIGLU if swiglu else EPI_NONE, _DT[out.dtype])
     return out
 
 
@@ -650,7 +652,7 @@ def experts_sharded_to_all(layer: Experts, h: torch.Tensor, offsets=None, h_scal
 
 
 def experts_all_to_sharded_backward(layer: Experts, x: torch.Tensor | None, dy: torch.Tensor, offsets=None, rows=None,
-                                    k: int = 1, need_dx: bool = True, need_dw: bool = True, dx_dtype=None,
+                                    k: int | None = None, need_dx: bool = True, need_dw: bool = True, dx_dtype=None,
                                     dw_dtype=torch.float32):
     """dy (P, R, out / P) -> (dx (R, in), one row for every grouped row,
     dw (E, P, out / P, in)); either may be skipped (None)."""
@@ -660,11 +662,11 @@ def experts_all_to_sharded_backward(layer: Experts, x: torch.Tensor | None, dy: 
     if need_dw:
         ld = _matrix(x, "x", layer.in_dims, layer.dtype, dev)
         T = x.shape[0]
-    _grouped(layer, offsets, rows, R)
+    _grouped(layer, offsets, rows, R, k)
     dx = _out(None, "dx", (R, layer.in_dims), dx_dtype or layer.dtype, dev) if need_dx else None
     dw = _out(None, "dw", (layer.E, layer.P, n, layer.in_dims), dw_dtype, dev) if need_dw else None
     _run(lib().sg_experts_all_to_sharded_backward, dev, layer.handle, _at(x) if need_dw else None, T, ld, _at(dy),
-         _at(offsets), _at(rows), k, R, _at(dx), _DT.get(dx_dtype or layer.dtype, -1), _at(dw), _DT.get(dw_dtype, -1))
+         _at(offsets), _at(rows), k or 1, R, _at(dx), _DT.get(dx_dtype or layer.dtype, -1), _at(dw), _DT.get(dw_dtype, -1))
     return dx, dw
 
 

@@ -29,8 +29,9 @@ __device__ __forceinline__ u32x4 mx4_to_bf16(uint32_t w, float scale) {
 
 // silu(g) u.  For 16-bit results (NEAR) on the hardware's exponential and
 // reciprocal, off by a few fp32 half steps, far below the result's own rounding:
-// e^-z = 2^t 2^r with t = -z log2 e rounded and r what the rounding left (beyond
-// |t| = 100 the result is 0 or z but for 2^-100, and r would be infinite).
+// e^-z = 2^t 2^r with t = -z log2 e rounded and r what the rounding left.  Beyond
+// |t| = 100 r is left out: 2^t then tells z from 0 or from z alone, and for
+// infinite t there is no r.
 template <bool NEAR>
 __device__ __forceinline__ f32x4 swiglu4(f32x4 g, f32x4 u) {
     f32x4 v;
@@ -98,9 +99,9 @@ __device__ __forceinline__ int weight_block(const Grouped& p, int ob, int i) {
 // weights of the experts that have rows once.  Weights go from memory straight
 // into the registers of the MFMA that uses them (a step of a 16-row block is 1
 // KB contiguous, 16 bytes a lane); the rows of up to 16 MB tokens are the
-// other operand.  Four waves: KS of them split the inputs of one group of NB
-// output blocks (their sums are added in wave order through LDS), 4 / KS groups
-// stand side by side.  Steps come in runs of four, a run of loads ahead.
+// other operand.  KS of the NWV waves split the inputs of one group of NB output
+// blocks (their sums are added in wave order through LDS), NWV / KS groups stand
+// side by side.  Steps come in runs of four, a run of loads ahead.
 // ---------------------------------------------------------------------------
 template <int MODE, bool SWIGLU, int MB, int NB, int KS, int NWV, bool AL>
 __global__ __launch_bounds__(64 * NWV) void grouped_stream_kernel(Grouped p) {
@@ -247,16 +248,16 @@ __global__ __launch_bounds__(64 * NWV) void grouped_stream_kernel(Grouped p) {
 
 // ---------------------------------------------------------------------------
 // Tile kernel: TM rows x BN weight rows (SwiGLU: BN / 2 gate and the BN / 2
-// matching up rows; transposed: BN columns of the weights), WM x WN waves, two
-// LDS stages.  Bound by the matrix unit for many rows of an expert.
+// matching up rows; transposed: BN columns of the weights), 2 x 4 waves, two or
+// four LDS stages.  Bound by the matrix unit for many rows of an expert.
 //
 // A k tile is 64 inputs (MXFP4 weights: 128; MXFP4 x MXFP4: 256, the same 128
 // bytes a row).  Its operands go from memory straight into the stage that the
-// k tile before left (with four stages, three k tiles ahead): one barrier a k tile, behind which every wave's loads of
-// it have landed; the next k tile's loads are issued between the two halves'
-// operand reads and MFMAs.  With two waves a SIMD the reads of one run beside
-// the MFMAs of the other; a raised wave priority around the MFMAs keeps them
-// back to back (256 x 256, 8192 x 28672 x 4096: 1.08 -> 1.28 PFLOP/s, where the
+// k tile before left (with four stages, three k tiles ahead): one barrier a k
+// tile, behind which every wave's loads of it have landed; the next loads are
+// issued between the two halves' operand reads and MFMAs.  With two waves a SIMD
+// the reads of one run beside the MFMAs of the other; a raised wave priority
+// around the MFMAs keeps them back to back (256 x 256, 8192 x 28672 x 4096: 1.08 -> 1.28 PFLOP/s, where the
 // vendor library's product of that size reaches 1.37).  Each stage is an array
 // of its own, so that the compiler sees that reads of one do not wait for the
 // loads into the other.
@@ -409,10 +410,12 @@ __device__ __forceinline__ void grouped_tile(const Grouped& p, const Slot s, con
                      ik + ssub * 128 < p.kpad ? off : kOutside, 0, (uint8_t*)(sSW + wave * 64));
             }
         }
-        if constexpr (A4)
-            if (wave < SA) dma4(buffer(p.a_scales + (int64_t)iseg * p.T * (p.kl / 32), bytes((int64_t)p.T * (p.kl / 32))),
-                 saoff != kOutside && ik + (lane & 1) * 128 < p.kl ? saoff + ik / 32 : kOutside, 0,
-                 (uint8_t*)(sSA + wave * 64));
+        if constexpr (A4) {
+            if (wave < SA)
+                dma4(buffer(p.a_scales + (int64_t)iseg * p.T * (p.kl / 32), bytes((int64_t)p.T * (p.kl / 32))),
+                     saoff != kOutside && ik + (lane & 1) * 128 < p.kl ? saoff + ik / 32 : kOutside, 0,
+                     (uint8_t*)(sSA + wave * 64));
+        }
     };
     auto advance = [&]() ALWAYS_INLINE {
         ik += KT;

@@ -44,6 +44,7 @@ int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 bool aligned(const void* p, size_t n) { return (uintptr_t)p % n == 0; }
 
 constexpr int64_t kMaxRows = (int64_t)1 << 30;
+constexpr int64_t kMaxTokens = (int64_t)1 << 25;  // of a router's launch, a wave each
 constexpr int64_t kMaxBytes = 0xffff0000;  // what a 32-bit buffer offset reaches
 
 // device memory as it is, host memory through a copy that `tmp` then owns
@@ -293,7 +294,8 @@ sg_status check_route(const sg::Route& r, int64_t T, int64_t ld) {
     if (r.E > sg::kRouteMaxExperts || r.k > sg::kRouteMaxK)
         return fail(SG_ERR_UNSUPPORTED, "more than %d experts, or %d choices, are not supported", sg::kRouteMaxExperts,
                     sg::kRouteMaxK);
-    if (T > kMaxRows / r.k) return fail(SG_ERR_UNSUPPORTED, "more than 2^30 slots are not supported");
+    if (T > kMaxTokens || T > kMaxRows / r.k)
+        return fail(SG_ERR_UNSUPPORTED, "more than 2^25 tokens, or 2^30 slots, are not supported");
     if (ld < r.E) return fail(SG_ERR_INVALID_ARG, "row stride %lld of the logits is below E", (long long)ld);
     return SG_OK;
 }

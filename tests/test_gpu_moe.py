@@ -234,6 +234,7 @@ COLUMNS = [
     (1, 1, 8, 1, 1, 1, BF), (1, 200, 64, 16, 2, 2, BF), (3, 5, 32, 20, 1, 2, HF), (4, 64, 136, 33, 2, 2, BF),
     (8, 100, 62, 24, 4, 2, HF), (5, 700, 1000, 48, 2, 1, BF), (2, 300, 256, 130, 1, 2, HF), (6, 40, 520, 16, 8, 2, BF),
     (70, 90, 64, 16, 1, 2, BF), (4, 513, 320, 64, 3, 3, BF), (2, 1100, 192, 272, 1, 2, BF), (1, 300, 35, 7, 3, 2, BF),
+    (100, 1300, 72, 24, 1, 2, HF), (130, 2000, 33, 5, 2, 2, BF),
 ]
 
 
@@ -464,6 +465,48 @@ def test_experts_strided_x():
         for a, b in zip(sg.experts_all_to_sharded_backward(layer, x, dy, off),
                         sg.experts_all_to_sharded_backward(layer, x.contiguous(), dy, off)):
             assert torch.equal(a, b)
+
+
+def test_row_map_needs_its_k():
+    layer = sg.shard_experts(normal(gen(1), (1, 16, 64), BF).cuda(), "all-to-sharded")
+    x, rows = normal(gen(2), (4, 64), BF).cuda(), torch.zeros(8, dtype=torch.int32, device="cuda")
+    with pytest.raises(sg.ShardGemmError, match="k is None"):
+        sg.experts_all_to_sharded(layer, x, rows=rows)
+    with pytest.raises(sg.ShardGemmError, match="k is None"):
+        sg.experts_all_to_sharded_backward(layer, x, torch.zeros((1, 8, 16), dtype=BF, device="cuda"), rows=rows)
+
+
+def test_experts_refuse_what_does_not_fit():
+    """Refusals that need a layer: wrong mode, widths, dtypes, devices, scales and pairs."""
+    g = gen(3)
+    col = sg.shard_experts(normal(g, (2, 32, 64), BF).cuda(), "all-to-sharded", segments=2)
+    row = sg.shard_experts(normal(g, (2, 64, 16), BF).cuda(), "sharded-to-all")
+    one = sg.shard_experts(normal(g, (2, 32, 64), BF).cuda(), "all-to-sharded")
+    off = torch.tensor([0, 2, 4], dtype=torch.int32).cuda()
+    x = normal(g, (4, 64), BF).cuda()
+    bad = lambda code, f, *a, **k: pytest.raises(sg.ShardGemmError, f, *a, **k).value.code == code
+    assert bad(sg.ERR_BAD_MODE, sg.experts_all_to_sharded, row, x[:, :16].contiguous(), off)
+    assert bad(sg.ERR_INVALID_ARG, sg.experts_all_to_sharded, col, x[:, :32], off)
+    assert bad(sg.ERR_INVALID_ARG, sg.experts_all_to_sharded, col, x.float(), off)
+    assert bad(sg.ERR_INVALID_ARG, sg.experts_all_to_sharded, col, x.cpu(), off)
+    assert bad(sg.ERR_INVALID_ARG, sg.experts_all_to_sharded, col, x)  # no offsets for two experts
+    assert bad(sg.ERR_INVALID_ARG, sg.experts_all_to_sharded, col, x, off.long())
+    assert bad(sg.ERR_INVALID_ARG, sg.experts_all_to_sharded, col, x.t().contiguous().t(), off)
+    assert bad(sg.ERR_INVALID_ARG, sg.experts_all_to_sharded, one, x, off, swiglu=True)
+    codes, scales = sg.quantize_mxfp4(x)
+    assert bad(sg.ERR_INVALID_ARG, sg.experts_all_to_sharded, col, codes, off, x_scales=scales)
+    assert bad(sg.ERR_INVALID_ARG, sg.experts_sharded_to_all, row, x[None], off)
+    z = normal(g, (4, 2), F32).cuda()
+    r = sg.moe_route(z, 1)
+    assert bad(sg.ERR_INVALID_ARG, sg.moe_mlp, one, row, x, r)  # segments = 1
+    assert bad(sg.ERR_INVALID_ARG, sg.moe_mlp, row, col, x[:, :16].contiguous(), r)
+    assert bad(sg.ERR_NOT_DIVISIBLE, sg.quantize_mxfp4, x[:, :40])
+    mx = sg.shard_mxfp4_experts(*sg.quantize_mxfp4(normal(g, (2, 32, 64)).cuda()), "all-to-sharded", segments=2)
+    assert bad(sg.ERR_UNSUPPORTED, sg.experts_all_to_sharded_backward, mx, x, torch.zeros((1, 4, 32), dtype=BF,
+                                                                                       device="cuda"), off)
+    assert bad(sg.ERR_UNSUPPORTED, mx.update, normal(g, (2, 32, 64), BF).cuda())
+    col.free()
+    assert bad(sg.ERR_INVALID_ARG, sg.experts_all_to_sharded, col, x, off)
 
 
 def test_experts_update():

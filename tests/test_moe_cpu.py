@@ -88,7 +88,8 @@ def route(L, T=4, E=8, k=2, ld=None, dtype=sg.F32, logits=PTR, out=PTR, ws=PTR, 
     (dict(T=-1), sg.ERR_INVALID_ARG), (dict(k=0), sg.ERR_INVALID_ARG), (dict(k=9), sg.ERR_INVALID_ARG),
     (dict(E=0, k=1), sg.ERR_INVALID_ARG), (dict(ld=7), sg.ERR_INVALID_ARG), (dict(dtype=5), sg.ERR_INVALID_ARG),
     (dict(E=1025), sg.ERR_UNSUPPORTED), (dict(E=64, k=17), sg.ERR_UNSUPPORTED), (dict(T=1 << 62), sg.ERR_UNSUPPORTED),
-    (dict(T=1 << 30), sg.ERR_UNSUPPORTED), (dict(logits=None), sg.ERR_INVALID_ARG), (dict(out=None), sg.ERR_INVALID_ARG),
+    (dict(T=1 << 30), sg.ERR_UNSUPPORTED), (dict(T=(1 << 25) + 1, k=1), sg.ERR_UNSUPPORTED),
+    (dict(logits=None), sg.ERR_INVALID_ARG), (dict(out=None), sg.ERR_INVALID_ARG),
     (dict(T=5000, ws=None), sg.ERR_WORKSPACE), (dict(T=5000, bytes_=4), sg.ERR_WORKSPACE),
 ])
 def test_route_refuses(L, kw, code):

@@ -716,13 +716,14 @@ def moe_route(logits: torch.Tensor, k: int, normalize: bool = True) -> Route:
     ld = _matrix(logits, "logits")
     T, E = logits.shape
     dev, L = logits.device, lib()
-    n = max(T * k, 0)
+    if not 1 <= k <= E:
+        _bad(f"a router needs 1 <= k <= E (got k {k}, E {E})")
+    n = T * k
     # one allocation; the workspace (none for few slots) may end it: only this call uses it
     need = L.sg_moe_route_workspace(T, E, k)
     buf = torch.empty((4 * n + E + 1 + need // 4,), dtype=torch.int32, device=dev)
     w, e, rows, slots, offsets, ws = buf.split_with_sizes((n, n, n, n, E + 1, need // 4))
-    shape = (T, max(k, 0))
-    w, e, slots = w.view(torch.float32).view(shape), e.view(shape), slots.view(shape)
+    w, e, slots = w.view(torch.float32).view(T, k), e.view(T, k), slots.view(T, k)
     _run(L.sg_moe_route, dev, _at(logits), ld, _DT[logits.dtype], T, E, k, int(normalize), _at(w), _at(e), _at(offsets),
          _at(rows), _at(slots), _at(ws), need)
     return Route(w, e, offsets, rows, slots)
@@ -764,7 +765,7 @@ def moe_combine_backward(dout: torch.Tensor, y: torch.Tensor, slots: torch.Tenso
                          dy: torch.Tensor | None = None):
     """Gradient of moe_combine: dout (T, D) -> (dy (R, D), dweights (T, k));
     either may be skipped (None).  Rows of no slot are left as they were in a
-    caller's dy, and are zero in a new one."""
+    caller's dy, and are zero in a new one; a row may stand in slots once."""
     _want(dout, "dout", (None, None), _FLOATS)
     dev, (T, D) = dout.device, dout.shape
     _want(y, "y", (None, D), dout.dtype, dev)

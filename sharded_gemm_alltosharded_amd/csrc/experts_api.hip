@@ -303,7 +303,7 @@ sg_status check_route(const sg::Route& r, int64_t T, int64_t ld) {
 sg_status check_slots(int64_t T, int k, int64_t D, int64_t R) {
     if (T < 0 || k < 1 || D < 1 || R < 0) return fail(SG_ERR_INVALID_ARG, "need T >= 0, k >= 1, D >= 1, R >= 0");
     if (k > sg::kRouteMaxK) return fail(SG_ERR_UNSUPPORTED, "more than %d choices are not supported", sg::kRouteMaxK);
-    if (T > kMaxRows / k || R > kMaxRows || T * (D / 512 + 1) >= sg::kMaxBlocks)
+    if (D > kMaxRows || T > kMaxRows / k || R > kMaxRows || T * (D / 512 + 1) >= sg::kMaxBlocks)
         return fail(SG_ERR_UNSUPPORTED, "more rows than one launch takes");
     return SG_OK;
 }
@@ -449,7 +449,7 @@ sg_status sg_moe_mlp(const sg_experts* g, const sg_experts* d, const void* x, in
     return st;
 }
 
-static sg_status check_backward(const sg_experts* x, const void* in, const void* dy, int64_t R, const void* dx,
+static sg_status check_backward(const sg_experts* x, const void* in, int64_t T, const void* dy, int64_t R, const void* dx,
                                 sg_dtype dx_dtype, const void* dw, sg_dtype dw_dtype) {
     if (x->mx) return fail(SG_ERR_UNSUPPORTED, "MXFP4 experts have no backward pass");
     if (!dx && !dw) return fail(SG_ERR_INVALID_ARG, "dx and dw are both NULL");
@@ -457,6 +457,7 @@ static sg_status check_backward(const sg_experts* x, const void* in, const void*
     if (dw && !known(dw_dtype)) return fail(SG_ERR_INVALID_ARG, "unknown dw dtype %d", (int)dw_dtype);
     if (R > 0 && !dy) return fail(SG_ERR_INVALID_ARG, "dy is NULL");
     if (R > 0 && dw && !in) return fail(SG_ERR_INVALID_ARG, "dw needs x");
+    if (R > 0 && dw && T == 0) return fail(SG_ERR_INVALID_ARG, "%lld rows of no tokens", (long long)R);
     return SG_OK;
 }
 
@@ -468,7 +469,7 @@ sg_status sg_experts_all_to_sharded_backward(const sg_experts* x, const void* a,
     sg_status st = check_layer(x, SG_ALL_TO_SHARDED, "sg_experts_all_to_sharded_backward");
     if (!st) st = check_rows(x, offsets, R);
     if (!st && dw) st = check_gather(T, ldx, x->l.in, rows, k, R);
-    if (!st) st = check_backward(x, a, dy, R, dx, dx_dtype, dw, dw_dtype);
+    if (!st) st = check_backward(x, a, T, dy, R, dx, dx_dtype, dw, dw_dtype);
     if (!st) st = check_bytes(R, x->l.f * x->l.S, 4);
     if (!st && dw) st = check_bytes(T, ldx, 4);
     if (st) return st;
@@ -527,9 +528,9 @@ sg_status sg_experts_sharded_to_all_backward(const sg_experts* x, const void* h,
     sg::last_error().clear();
     sg_status st = check_layer(x, SG_SHARDED_TO_ALL, "sg_experts_sharded_to_all_backward");
     if (!st) st = check_rows(x, offsets, R);
-    if (!st) st = check_backward(x, h, dy, R, dh, dh_dtype, dw, dw_dtype);
+    if (!st) st = check_backward(x, h, R, dy, R, dh, dh_dtype, dw, dw_dtype);
     if (!st) st = check_bytes(R, x->l.out, 4);
-    if (!st) st = check_bytes(R, x->l.kl, 4);
+    if (!st && dw) st = check_bytes(R, x->l.kl, 4);
     if (st) return st;
     const sg::ExpertsLayout& l = x->l;
     hipStream_t s = (hipStream_t)stream;

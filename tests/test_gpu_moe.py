@@ -467,6 +467,55 @@ def test_experts_strided_x():
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("R", [6, 20, 150])
+def test_rows_of_no_token_read_zeros(R):
+    """Entries of the row map outside 0 .. T k - 1, and falling offsets, for few rows and for many."""
+    g = gen(R)
+    E, T, k, K, f = 3, 9, 2, 72, 40
+    w = normal(g, (E, f, K), BF, 0.1)
+    layer = sg.shard_experts(w.cuda(), "all-to-sharded")
+    x, off = normal(g, (T, K), BF).cuda(), offsets_of(g, E, R).cuda()
+    rows = torch.randint(0, T * k, (R,), generator=g, dtype=torch.int32)
+    out = torch.rand(R, generator=g) < 0.4
+    bad = torch.tensor([-1, T * k, 2**31 - 1, -2**31, -k], dtype=torch.int32)
+    rows[out] = bad[torch.randint(0, 5, (int(out.sum()),), generator=g)]
+    flat = torch.where(out[:, None], 0, x.cpu()[torch.where(out, 0, rows).long() // k])
+    y = sg.experts_all_to_sharded(layer, x, off, rows=rows.cuda(), k=k)
+    assert torch.equal(y, sg.experts_all_to_sharded(layer, flat.cuda(), off))
+    assert (y[:, out.cuda()] == 0).all()
+    dy = normal(g, (1, R, f), BF).cuda()
+    _, dw = sg.experts_all_to_sharded_backward(layer, x, dy, off, rows=rows.cuda(), k=k, need_dx=False)
+    assert torch.equal(dw, sg.experts_all_to_sharded_backward(layer, flat.cuda(), dy, off, need_dx=False)[1])
+    guard = torch.full((3, R, f), 7.0, dtype=BF, device="cuda")
+    sg.experts_all_to_sharded(layer, x, torch.tensor([0, R, 1, 2 * R], dtype=torch.int32).cuda(), rows=rows.cuda(), k=k,
+                              out=guard[1:2])
+    assert (guard[0] == 7).all() and (guard[2] == 7).all()
+
+
+def test_results_past_2_to_the_32():
+    """Arrays of more than 2^32 values: the last rows are where they belong."""
+    g = gen(11)
+    R, K, f = (1 << 17) + 40, 64, 1 << 15
+    w = normal(g, (1, f, K), BF, 0.2)
+    layer = sg.shard_experts(w.cuda(), "all-to-sharded", segments=2)
+    tail = normal(g, (64, K), BF).cuda()
+    x = torch.zeros((R, K), dtype=BF, device="cuda")
+    x[-64:] = tail
+    y = sg.experts_all_to_sharded(layer, x)
+    assert torch.equal(y[:, -64:], sg.experts_all_to_sharded(layer, tail)) and not y[0, : R - 64].any()
+    slots = torch.tensor([[R - 1, R - 64], [R - 5, -1]], dtype=torch.int32).cuda()
+    near = (slots - torch.where(slots >= 0, R - 64, 0)).int()
+    assert torch.equal(sg.moe_combine(y[0], slots), sg.moe_combine(y[0, -64:].contiguous(), near))
+    assert torch.equal(sg.swiglu(y[0])[-64:], sg.swiglu(y[0, -64:].contiguous()))
+    for a, b in zip(sg.quantize_mxfp4(y[0]), sg.quantize_mxfp4(y[0, -64:].contiguous())):
+        assert torch.equal(a[-64:], b)
+    down = sg.shard_experts(w.transpose(1, 2).contiguous().cuda(), "sharded-to-all")
+    dh, _ = sg.experts_sharded_to_all_backward(down, None, x, need_dw=False)
+    t, v = tail.cpu().double(), w[0].double()
+    for got in (y, dh):
+        ref.close(got[0, -64:], t @ v.T, ref.sum_bound(t.abs() @ v.abs().T, K), "last rows")
+
+
 def test_row_map_needs_its_k():
     layer = sg.shard_experts(normal(gen(1), (1, 16, 64), BF).cuda(), "all-to-sharded")
     x, rows = normal(gen(2), (4, 64), BF).cuda(), torch.zeros(8, dtype=torch.int32, device="cuda")

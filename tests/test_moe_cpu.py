@@ -115,7 +115,8 @@ def test_combine_refuses(L):
     for kw in (dict(R=-1), dict(T=-1), dict(k=0), dict(D=0), dict(yt=7), dict(ot=7), dict(y=None), dict(slots=None),
                dict(out=None)):
         assert call(**kw) == sg.ERR_INVALID_ARG, kw
-    for kw in (dict(k=17), dict(T=1 << 62), dict(T=1 << 25), dict(R=1 << 40)):
+    for kw in (dict(k=17), dict(T=1 << 62), dict(T=1 << 25), dict(R=1 << 40),
+               dict(D=1 << 62), dict(T=1 << 10, D=1 << 62)):
         assert call(**kw) == sg.ERR_UNSUPPORTED, kw
     assert call(T=0) == sg.OK
     back = lambda dy, dw, y=PTR: L.sg_moe_combine_backward(PTR, y, sg.F32, 8, PTR, None, 4, 2, 16, dy, dw, None)

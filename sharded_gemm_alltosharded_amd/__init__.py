@@ -534,6 +534,16 @@ def _out(out, name: str, shape, dtype, device):
     return _want(out, name, shape, _FLOATS, device)
 
 
+_freed: list = []
+
+
+def _free_experts():
+    """Release the layers given up.  That waits for the device, which a capture
+    does not allow: until it ends they stay."""
+    while _freed and not torch.cuda.is_current_stream_capturing():
+        _lib.sg_experts_free(_freed.pop())
+
+
 class Experts:
     """E sharded linear layers owned by the library (sg_experts*)."""
 
@@ -561,9 +571,10 @@ class Experts:
         _run(lib().sg_experts_update, self.device, self.handle, _at(weight))
 
     def free(self):
-        if self._h is not None and _lib is not None:
-            _lib.sg_experts_free(self._h)
-        self._h = None
+        h, self._h = self._h, None
+        if h is not None and _lib is not None:
+            _freed.append(h)
+            _free_experts()
 
     def __del__(self):
         try:
@@ -577,6 +588,7 @@ def _experts(make, device) -> Experts:
     h = C.c_void_p()
     with torch.cuda.device(device):
         _check(make(_stream(device), C.byref(h)))
+    _free_experts()
     return Experts(h, device)
 
 

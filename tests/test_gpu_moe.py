@@ -235,6 +235,7 @@ COLUMNS = [
     (8, 100, 62, 24, 4, 2, HF), (5, 700, 1000, 48, 2, 1, BF), (2, 300, 256, 130, 1, 2, HF), (6, 40, 520, 16, 8, 2, BF),
     (70, 90, 64, 16, 1, 2, BF), (4, 513, 320, 64, 3, 3, BF), (2, 1100, 192, 272, 1, 2, BF), (1, 300, 35, 7, 3, 2, BF),
     (100, 1300, 72, 24, 1, 2, HF), (130, 2000, 33, 5, 2, 2, BF),
+    (2, 2, 2048, 256, 1, 2, BF), (1, 5, 2051, 40, 2, 2, HF), (3, 17, 2500, 24, 1, 1, BF),
 ]
 
 
@@ -271,7 +272,7 @@ def test_experts_column(case):
 ROWS = [  # E, R, out, in / P, P, S, dtype
     (1, 1, 1, 8, 1, 1, BF), (1, 150, 64, 64, 2, 1, BF), (3, 5, 20, 32, 1, 1, HF), (4, 64, 33, 96, 3, 1, BF),
     (8, 100, 250, 31, 4, 1, HF), (5, 700, 72, 363, 2, 1, BF), (2, 300, 1000, 128, 8, 1, HF), (6, 40, 16, 40, 8, 2, BF),
-    (70, 90, 48, 64, 1, 1, BF), (3, 900, 300, 88, 4, 1, BF),
+    (70, 90, 48, 64, 1, 1, BF), (3, 900, 300, 88, 4, 1, BF), (1, 2, 32, 523, 4, 1, BF), (3, 4, 700, 1100, 2, 2, HF),
 ]
 
 
@@ -516,6 +517,24 @@ def test_results_past_2_to_the_32():
         ref.close(got[0, -64:], t @ v.T, ref.sum_bound(t.abs() @ v.abs().T, K), "last rows")
 
 
+def test_a_layer_given_up_in_a_capture_outlives_it():
+    g = gen(12)
+    w, x = normal(g, (1, 64, 128), BF), normal(g, (5, 128), BF).cuda()
+    keep, gone = (sg.shard_experts(w.cuda(), "all-to-sharded") for _ in range(2))
+    want = sg.experts_all_to_sharded(keep, x)
+    graph, out = torch.cuda.CUDAGraph(), torch.empty_like(want)
+    with torch.cuda.graph(graph):
+        del gone
+        sg.experts_all_to_sharded(keep, x, out=out)
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        assert torch.equal(out, want)
+    assert len(sg._freed) == 1
+    keep.free()
+    assert not sg._freed
+
+
 def test_row_map_needs_its_k():
     layer = sg.shard_experts(normal(gen(1), (1, 16, 64), BF).cuda(), "all-to-sharded")
     x, rows = normal(gen(2), (4, 64), BF).cuda(), torch.zeros(8, dtype=torch.int32, device="cuda")
@@ -575,6 +594,7 @@ def test_experts_update():
 CHAIN = [  # T, E, k, D, F, P, dtype
     (1, 8, 2, 256, 512, 8, BF), (3, 4, 4, 64, 96, 1, HF), (33, 64, 4, 128, 64, 4, BF), (300, 5, 3, 200, 366, 2, BF),
     (1000, 4, 2, 128, 256, 4, HF), (77, 3, 1, 70, 54, 2, BF), (20, 64, 2, 512, 74, 2, BF),
+    (2, 4, 2, 2056, 2100, 1, BF),
 ]
 
 

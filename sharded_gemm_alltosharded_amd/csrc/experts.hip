@@ -704,6 +704,15 @@ hipError_t stream_launch(const Grouped& p, hipStream_t s) {
 // widest group, and the fewest waves that give every compute unit seven (gate|up
 // of 32 rows, two pairs a wave: 83 us, one pair and eight waves: 158 us; down,
 // four waves for four blocks 49 us, eight for two 67 us).
+// Sixteen waves where compute units get one workgroup of eight at most, and each
+// wave still has a run of steps, of one block where that is enough for all (us,
+// eight / sixteen waves, one row of an expert; MXFP4 weights for two blocks have
+// no registers for sixteen, 22 / 30 us on the first):
+//                      16-bit     MXFP4     MXFP4 x MXFP4
+//   2 x (4096 x 14336)  48 / 40    22         18 / 16
+//   1 x (4096 x 14336)  44 / 29    19 / 15    15 / 12
+//   1 x (2048 x 8192)   23 / 16    11 / 9     8.5 / 7.1
+// and with half as many workgroups again as compute units 63 / 71.
 template <int MODE, bool SWIGLU, bool AL>
 hipError_t stream_mode(const Grouped& p, hipStream_t s) {
     constexpr int NB = SWIGLU ? 2 : 4;
@@ -719,6 +728,11 @@ hipError_t stream_mode(const Grouped& p, hipStream_t s) {
         if (blocks / NB * 2 >= want) return stream_launch<MODE, SWIGLU, 1, NB, 2, 4, AL>(p, s);
         if (blocks / NB * 4 >= want) return stream_launch<MODE, SWIGLU, 1, NB, 4, 4, AL>(p, s);
         if (blocks / NB * 8 >= want) return stream_launch<MODE, SWIGLU, 1, NB, 8, 8, AL>(p, s);
+    }
+    if (blocks <= NB / 2 * (int64_t)device_cus() && p.wsteps >= 64) {
+        if constexpr (!SWIGLU)
+            if (blocks <= (int64_t)device_cus()) return stream_launch<MODE, SWIGLU, 1, 1, 16, 16, AL>(p, s);
+        if constexpr (MODE != G_MX4) return stream_launch<MODE, SWIGLU, 1, NB / 2, 16, 16, AL>(p, s);
     }
     return stream_launch<MODE, SWIGLU, 1, NB / 2, 8, 8, AL>(p, s);
 }

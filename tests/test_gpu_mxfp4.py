@@ -101,6 +101,7 @@ def mx_weights(g, E, n, K):
 COLUMNS = [  # E, R, in, out / P / S, P, S
     (1, 1, 32, 1, 1, 1), (1, 200, 96, 16, 2, 2), (3, 5, 160, 20, 1, 2), (4, 64, 256, 33, 2, 2), (8, 100, 64, 24, 4, 2),
     (5, 700, 1024, 48, 2, 1), (2, 300, 288, 130, 1, 2), (40, 90, 416, 16, 1, 2), (1, 700, 640, 272, 1, 2),
+    (1, 3, 8192, 16, 1, 1), (2, 3, 8224, 144, 1, 2), (3, 3, 8320, 1400, 1, 1),
 ]
 
 
@@ -168,7 +169,7 @@ def test_mxfp4_wide_tiles(E, R, K, f, P, S, acts):
 
 ROWS = [  # E, R, out, in / P, P
     (1, 1, 1, 32, 1), (1, 150, 64, 96, 2), (3, 5, 20, 160, 1), (4, 64, 33, 64, 3), (8, 100, 250, 32, 4),
-    (3, 900, 300, 288, 2), (40, 70, 64, 128, 1),
+    (3, 900, 300, 288, 2), (40, 70, 64, 128, 1), (2, 2, 72, 2080, 4),
 ]
 
 

@@ -248,7 +248,7 @@ __global__ __launch_bounds__(64 * NWV) void grouped_stream_kernel(Grouped p) {
 
 // ---------------------------------------------------------------------------
 // Tile kernel: TM rows x BN weight rows (SwiGLU: BN / 2 gate and the BN / 2
-// matching up rows; transposed: BN columns of the weights), 2 x 4 waves, two or
+// matching up rows; transposed: BN columns of the weights), 2 x 4 waves, two to
 // four LDS stages.  Bound by the matrix unit for many rows of an expert.
 //
 // A k tile is 64 inputs (MXFP4 weights: 128; MXFP4 x MXFP4: 256, the same 128
@@ -288,7 +288,6 @@ struct Stages {
 // n tile nt of the rows of one slot; the stages may be larger than needed
 template <int MODE, bool SWIGLU, bool TRANS, int TM, int BN, int NS, bool AL>
 __device__ __forceinline__ void grouped_tile(const Grouped& p, const Slot s, const int nt, const Stages<NS>& stage) {
-    static_assert(AL || NS == 2, "rows staged through registers come one k tile ahead");
     using Shape = TileShape<MODE, TM, BN>;
     constexpr int WM = 2, WN = 4, NWV = WM * WN;
     constexpr int NBM = TM / WM / 16, NBN = BN / WN / 16;
@@ -356,7 +355,9 @@ __device__ __forceinline__ void grouped_tile(const Grouped& p, const Slot s, con
         if (ik + KT > p.kl && k >= p.kl) off = kOutside;
         dma16(buffer(base, bytes(a_bytes)), off, (uint32_t)(A4 ? ik / 2 : ik * 2), to);
     };
-    // rows of any alignment: through registers, into LDS when the k tile at hand is done
+    // rows of any alignment: through registers, into LDS a k tile later (of two
+    // stages: when the k tile at hand is done)
+    constexpr bool LATE = !AL && NS > 2;
     [[maybe_unused]] u32x4 av[LA];
     auto fetch_a = [&]() ALWAYS_INLINE {
 #pragma unroll
@@ -485,14 +486,19 @@ __device__ __forceinline__ void grouped_tile(const Grouped& p, const Slot s, con
             for (int i = 0; i < LA; ++i) load_a(nA, i);
         } else {
             fetch_a();
-            put_a(nA);
+            if constexpr (!LATE) put_a(nA);
         }
 #pragma unroll
         for (int i = 0; i < LW; ++i) load_w(nW, i);
         advance();
     };
-    // (of the loads that may stay in flight, a wave's scales are not counted)
-    constexpr int LATER = (NS - 2) * (LA + LW);
+    // (of the loads that may stay in flight, a wave's scales are not counted, nor
+    // rows that go into LDS behind the barrier)
+    constexpr int LATER = (NS - 2) * (LATE ? LW : LA + LW);
+    auto arrived = [&](auto uc) ALWAYS_INLINE {
+        stage_barrier<LATER>();
+        if constexpr (LATE) put_a(stage.A[(decltype(uc)::value + NS - 2) % NS]);
+    };
     auto step = [&](auto uc) ALWAYS_INLINE {
         constexpr int u = decltype(uc)::value, next = (u + NS - 1) % NS;
         const uint8_t *sA = stage.A[u], *sW = stage.W[u];
@@ -501,7 +507,7 @@ __device__ __forceinline__ void grouped_tile(const Grouped& p, const Slot s, con
         uint32_t *nSW = stage.SW[next], *nSA = stage.SA[next];
         // this wave's loads of the k tile have landed; behind the barrier every
         // wave's have, and every wave has read the k tile before
-        stage_barrier<LATER>();
+        arrived(uc);
         u32x4 wf[NBN], af[NBM];
         // MXFP4 weights: a lane's 32 codes and their scale serve the k tile's four steps
         [[maybe_unused]] u32x4 codes[NBN];
@@ -532,11 +538,12 @@ __device__ __forceinline__ void grouped_tile(const Grouped& p, const Slot s, con
             }
             multiply(sSW, sSA, kk, wf, af);
         });
-        if constexpr (!AL) put_a(nA);
+        if constexpr (!AL && !LATE) put_a(nA);
     };
     static_for<0, NS - 1>([&](auto uc) ALWAYS_INLINE {
         constexpr int u = decltype(uc)::value;
         issue(stage.A[u], stage.W[u], stage.SW[u], stage.SA[u]);
+        if constexpr (LATE && u < NS - 2) put_a(stage.A[u]);
     });
     if (wave_m * NBM * 16 < s.nrows) {
         for (int t = 0; t < nkt; t += NS)
@@ -548,7 +555,7 @@ __device__ __forceinline__ void grouped_tile(const Grouped& p, const Slot s, con
             static_for<0, NS>([&](auto uc) ALWAYS_INLINE {
                 constexpr int u = decltype(uc)::value, next = (u + NS - 1) % NS;
                 if (u > 0 && t + u >= nkt) return;
-                stage_barrier<LATER>();
+                arrived(uc);
                 issue(stage.A[next], stage.W[next], stage.SW[next], stage.SA[next]);
             });
     }
@@ -566,17 +573,19 @@ __device__ __forceinline__ void grouped_tile(const Grouped& p, const Slot s, con
 template <int MODE, bool SWIGLU, bool TRANS, int TM, int BN, int NS, bool AL>
 __global__ __launch_bounds__(512) void grouped_tile_kernel(Grouped p, int slots, int tiles_n, int cus) {
     using Shape = TileShape<MODE, TM, BN>;
-    constexpr bool R = NS == 4;  // (a ring of four, or two)
-    static_assert(NS == 2 || NS == 4, "stages");
+    constexpr bool R = NS >= 3, Q = NS == 4;  // (a ring of two, three or four)
+    static_assert(NS >= 2 && NS <= 4, "stages");
     __shared__ __attribute__((aligned(1024))) uint8_t sA0[Shape::A], sA1[Shape::A], sW0[Shape::W], sW1[Shape::W],
-        sA2[R ? Shape::A : 4], sA3[R ? Shape::A : 4], sW2[R ? Shape::W : 4], sW3[R ? Shape::W : 4];
+        sA2[R ? Shape::A : 4], sA3[Q ? Shape::A : 4], sW2[R ? Shape::W : 4], sW3[Q ? Shape::W : 4];
     __shared__ uint32_t sSW0[Shape::SW], sSW1[Shape::SW], sSA0[Shape::SA], sSA1[Shape::SA], sSW2[R ? Shape::SW : 1],
-        sSW3[R ? Shape::SW : 1], sSA2[R ? Shape::SA : 1], sSA3[R ? Shape::SA : 1];
+        sSW3[Q ? Shape::SW : 1], sSA2[R ? Shape::SA : 1], sSA3[Q ? Shape::SA : 1];
     Stages<NS> stage;
     stage.A[0] = sA0, stage.W[0] = sW0, stage.SW[0] = sSW0, stage.SA[0] = sSA0;
     stage.A[1] = sA1, stage.W[1] = sW1, stage.SW[1] = sSW1, stage.SA[1] = sSA1;
     if constexpr (R) {
         stage.A[2] = sA2, stage.W[2] = sW2, stage.SW[2] = sSW2, stage.SA[2] = sSA2;
+    }
+    if constexpr (Q) {
         stage.A[3] = sA3, stage.W[3] = sW3, stage.SW[3] = sSW3, stage.SA[3] = sSA3;
     }
     // The launch has room for every way the rows may fall on the experts; the
@@ -750,19 +759,23 @@ hipError_t tile_launch(const Grouped& p, hipStream_t s) {
     return hipGetLastError();
 }
 
-// Whether tiles of TM rows and 128 weight rows hardly fill the chip once: they
-// then take four stages, which leave a compute unit room for one workgroup
-// instead of two or three.  us with two / four stages, 8 x (4096 x 14336), 256
-// tiles: m = 32: 200 / 156, 96: 238 / 180; MXFP4 m = 32: 113 / 87; 8 x (28672 x
-// 4096, SwiGLU), 1792 tiles: m = 32: 332 / 324, 128: 471 / 503; 32 x (2048 x 2048,
-// SwiGLU), 512 tiles: m = 64: 58 / 69.
+// Tiles of TM rows and 128 weight rows; a quarter more rows than the average
+// expert's are reckoned with.
+template <bool SWIGLU, int TM>
+int64_t tiles_of(const Grouped& p) {
+    const int64_t experts = p.R < p.E ? p.R : p.E;
+    const int64_t slots = experts * ((p.R * (int64_t)5 / (4 * experts) + TM - 1) / TM);
+    return slots * ((p.nout + (SWIGLU ? 3 : 7)) / (SWIGLU ? 4 : 8));
+}
+
+// Whether these hardly fill the chip once: they then take four stages, which
+// leave a compute unit room for one workgroup instead of two or three.  us with
+// two / four stages, 8 x (4096 x 14336), 256 tiles: m = 32: 200 / 156, 96: 238 /
+// 180; MXFP4 m = 32: 113 / 87; 8 x (28672 x 4096, SwiGLU), 1792 tiles: m = 32: 332
+// / 324, 128: 471 / 503; 32 x (2048 x 2048, SwiGLU), 512 tiles: m = 64: 58 / 69.
 template <bool SWIGLU, int TM>
 bool few_tiles(const Grouped& p) {
-    const int64_t experts = p.R < p.E ? p.R : p.E;
-    // a quarter more rows than the average expert's are reckoned with
-    const int64_t slots = experts * ((p.R * (int64_t)5 / (4 * experts) + TM - 1) / TM);
-    const int64_t tiles = slots * ((p.nout + (SWIGLU ? 3 : 7)) / (SWIGLU ? 4 : 8));
-    return tiles * 5 <= (int64_t)device_cus() * 6;
+    return tiles_of<SWIGLU, TM>(p) * 5 <= (int64_t)device_cus() * 6;
 }
 
 // Tile by the rows of an expert, m = R / E on average (they differ: half as
@@ -773,7 +786,18 @@ bool few_tiles(const Grouped& p) {
 //   32 x (2048 x 2048, SwiGLU)  m = 32:  55  55  62   48:  66  57  64  128:  88  84  72   256: 146 118 125
 template <int MODE, bool SWIGLU, bool TRANS, bool AL>
 hipError_t tile_mode(const Grouped& p, hipStream_t s) {
-    if constexpr (!AL) {
+    if constexpr (!AL && MODE == G_MX4) {
+        return tile_launch<MODE, SWIGLU, TRANS, 128, 128, 2, false>(p, s);
+    } else if constexpr (!AL) {
+        // Rows through registers: times round the chip, of two or three workgroups
+        // a compute unit.  us, 128 x 128 / 64 x 128 / the latter in three stages:
+        // 8 x (2046 x 4094) m = 125: 100 76 73   gate|up of 8 x (8188 x 2046): 131 115 123
+        // 8 x (4094 x 4094) m = 500: 354 318 390   32 x (1022 x 2046) m = 188: 66 79 75
+        const int64_t cus = device_cus();
+        if (few_tiles<SWIGLU, 64>(p)) return tile_launch<MODE, SWIGLU, TRANS, 64, 128, 3, false>(p, s);
+        const int64_t wide = (tiles_of<SWIGLU, 128>(p) + 2 * cus - 1) / (2 * cus);
+        const int64_t narrow = (tiles_of<SWIGLU, 64>(p) + 3 * cus - 1) / (3 * cus);
+        if (3 * narrow <= 4 * wide) return tile_launch<MODE, SWIGLU, TRANS, 64, 128, 2, false>(p, s);
         return tile_launch<MODE, SWIGLU, TRANS, 128, 128, 2, false>(p, s);
     } else if constexpr (MODE == G_MX4) {
         // (turning codes into operands costs the narrow tile as much as its few
@@ -790,11 +814,13 @@ hipError_t tile_mode(const Grouped& p, hipStream_t s) {
         const int64_t tiles = (p.R / 256 + p.E / 2) * ((p.nout + 15) / 16) * (SWIGLU ? 2 : 1);
         if (p.R >= (int64_t)128 * p.E && tiles * 10 >= (int64_t)device_cus() * (MODE == G_MX4A4 ? 40 : 7))
             return tile_launch<MODE, SWIGLU, TRANS, 256, 256, 2, true>(p, s);
+        // (few narrow tiles go before few wide ones: 256 rows of 4096 x 4096 27 32, 500 rows
+        // of 2 x (2048 x 2048) 15 19)
+        if (few_tiles<SWIGLU, 64>(p)) return tile_launch<MODE, SWIGLU, TRANS, 64, 128, 4, true>(p, s);
         if (p.R > (int64_t)40 * p.E) {
             if (few_tiles<SWIGLU, 128>(p)) return tile_launch<MODE, SWIGLU, TRANS, 128, 128, 4, true>(p, s);
             return tile_launch<MODE, SWIGLU, TRANS, 128, 128, 2, true>(p, s);
         }
-        if (few_tiles<SWIGLU, 64>(p)) return tile_launch<MODE, SWIGLU, TRANS, 64, 128, 4, true>(p, s);
         return tile_launch<MODE, SWIGLU, TRANS, 64, 128, 2, true>(p, s);
     }
 }

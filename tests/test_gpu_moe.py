@@ -273,6 +273,7 @@ ROWS = [  # E, R, out, in / P, P, S, dtype
     (1, 1, 1, 8, 1, 1, BF), (1, 150, 64, 64, 2, 1, BF), (3, 5, 20, 32, 1, 1, HF), (4, 64, 33, 96, 3, 1, BF),
     (8, 100, 250, 31, 4, 1, HF), (5, 700, 72, 363, 2, 1, BF), (2, 300, 1000, 128, 8, 1, HF), (6, 40, 16, 40, 8, 2, BF),
     (70, 90, 48, 64, 1, 1, BF), (3, 900, 300, 88, 4, 1, BF), (1, 2, 32, 523, 4, 1, BF), (3, 4, 700, 1100, 2, 2, HF),
+    (2, 100, 24, 5, 3, 1, BF), (2, 1500, 1030, 1001, 1, 1, HF),
 ]
 
 

@@ -253,14 +253,14 @@ __global__ __launch_bounds__(64 * NWV) void grouped_stream_kernel(Grouped p) {
 //
 // A k tile is 64 inputs (MXFP4 weights: 128; MXFP4 x MXFP4: 256, the same 128
 // bytes a row).  Its operands go from memory straight into the stage that the
-// k tile before left (with four stages, three k tiles ahead): one barrier a k
-// tile, behind which every wave's loads of it have landed; the next loads are
-// issued between the two halves' operand reads and MFMAs.  With two waves a SIMD
-// the reads of one run beside the MFMAs of the other; a raised wave priority
-// around the MFMAs keeps them back to back (256 x 256, 8192 x 28672 x 4096: 1.08 -> 1.28 PFLOP/s, where the
-// vendor library's product of that size reaches 1.37).  Each stage is an array
-// of its own, so that the compiler sees that reads of one do not wait for the
-// loads into the other.
+// k tile before left (with three or four stages, two or three k tiles ahead): one
+// barrier a k tile, behind which every wave's loads of it have landed; the next
+// loads are issued between the two halves' operand reads and MFMAs.  With two
+// waves a SIMD the reads of one run beside the MFMAs of the other; a raised wave
+// priority around the MFMAs keeps them back to back (256 x 256, 8192 x 28672 x
+// 4096: 1.08 -> 1.28 PFLOP/s, where the vendor library's product of that size
+// reaches 1.37).  Each stage is an array of its own, so that the compiler sees that reads
+// of one do not wait for the loads into the other.
 //
 // LDS: rows of A as 128 bytes (MXFP4 weights: 256), 16-byte chunks
 // XOR-swizzled by (row >> 1) & 7 (row & 15), so that the sixteen rows of an

@@ -28,10 +28,13 @@ __device__ __forceinline__ u32x4 mx4_to_bf16(uint32_t w, float scale) {
 }
 
 // silu(g) u.  For 16-bit results (NEAR) on the hardware's exponential and
-// reciprocal, off by a few fp32 half steps, far below the result's own rounding:
-// e^-z = 2^t 2^r with t = -z log2 e rounded and r what the rounding left.  Beyond
-// |t| = 100 r is left out: 2^t then tells z from 0 or from z alone, and for
-// infinite t there is no r.
+// reciprocal: e^-z = 2^t 2^r with t = -z log2 e rounded and r what the rounding
+// left.  r knows log2 e to 1.93e-8 (its own fp32 rounding), so e^-z is off by
+// 1.93e-8 ln 2 |z|, at most 1.2e-6 = 20 half steps of fp32 where it is finite, and
+// a few half steps of the instructions: below 2^-19, where half a step of a
+// 16-bit result is 2^-11 or more.  Beyond |t| = 126 r is left out: 2^t then tells z
+// from 0 (t < 0), or silu is below 90 * 2^-126 (t > 0), where 2^t may be infinite,
+// silu 0, and an r of 0 times it a NaN.
 template <bool NEAR>
 __device__ __forceinline__ f32x4 swiglu4(f32x4 g, f32x4 u) {
     f32x4 v;
@@ -39,9 +42,8 @@ __device__ __forceinline__ f32x4 swiglu4(f32x4 g, f32x4 u) {
     for (int i = 0; i < 4; ++i) {
         if constexpr (NEAR) {
             const float z = g[i], t = -1.44269504f * z;
-            const float r = fabsf(t) < 100.f ? fmaf(-1.44269504f, z, -t) : 0.f;
             float e = __builtin_amdgcn_exp2f(t);
-            e = fmaf(e * r, 0.693147181f, e);
+            if (fabsf(t) < 126.f) e = fmaf(e * fmaf(-1.44269504f, z, -t), 0.693147181f, e);
             v[i] = z * __builtin_amdgcn_rcpf(1.0f + e) * u[i];
         } else {
             v[i] = silu_f32(g[i]) * u[i];

@@ -1,0 +1,90 @@
+"""The mixture-of-experts and MXFP4 operators where values, sizes and callers are
+unusual: gates far from zero, no tokens, rows of any alignment, infinities,
+pairs of different weights, layers given up by several threads, and activation
+slices that fill their 32-bit offsets.
+
+Tolerances as in test_gpu_moe.py."""
+import math
+import threading
+
+import pytest
+import torch
+
+import moe_ref as ref
+import sharded_gemm_alltosharded_amd as sg
+from test_gpu_moe import BF, F32, HF, gen, normal, offsets_of
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True, scope="module")
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    torch.cuda.set_device(0)
+    sg.lib()
+
+
+# gates c * a for the columns' c and the rows' a, one product each, so exact
+FAR_COLUMNS = [1.0, -1.0, 0.0, 64.0, -64.0, 0.5, -0.5]
+FAR_ROWS = [1.0, 16.0, 69.0, 70.0, 87.0, 88.0, 89.0, 96.0, 100.0, 104.0, 126.0, 128.0, 200.0]
+
+
+@pytest.mark.parametrize("tiles", [False, True])
+@pytest.mark.parametrize("kind", ["bf16", "fp16", "mxfp4", "mxfp4 x mxfp4"])
+def test_swiglu_epilogue_far_gates(kind, tiles):
+    """silu of gates down to where e^-z is no fp32 number, in the streaming kernel and in the tiles.
+
+    Where e^-z is beyond 2^126 its reciprocal is below the smallest normal fp32
+    number and may be 0: |silu(z)| = |z| / (1 + e^-z) < 90 * 2^-126 for those z
+    (z < -87.3, and |z| e^z falls from there on) may be lost, times |up|."""
+    dtype = HF if kind == "fp16" else BF
+    a = FAR_ROWS + ([] if kind == "fp16" else [2.0 ** 100])
+    P, K, f, up = 2, 96, len(FAR_COLUMNS) * 2, 1.5
+    E, R = (1, len(a) * 12) if tiles else (4, len(a))
+    x = torch.zeros((R, K), dtype=dtype)
+    x[:, 0] = torch.tensor(a).repeat(R // len(a)).to(dtype)
+    x[:, 40] = up  # (another scale block)
+    w = torch.zeros((E, 2, f, K))
+    w[:, 0, :, 0] = torch.tensor(FAR_COLUMNS * 2)
+    w[:, 1, :, 40] = 1.0
+    w = w.view(E, 2 * f, K)
+    off = offsets_of(gen(1), E, R)
+    kw, xv, call = {}, x, x.cuda()
+    if kind.startswith("mxfp4"):
+        codes, scales = ref.encode(w)
+        assert torch.equal(ref.decode(codes, scales), w.double())
+        layer = sg.shard_mxfp4_experts(codes.cuda(), scales.cuda(), "all-to-sharded", segments=2, P=P)
+        if kind != "mxfp4":
+            call, xs = sg.quantize_mxfp4(x.cuda())
+            kw, xv = {"x_scales": xs}, ref.decode(call.cpu(), xs.cpu())
+    else:
+        layer = sg.shard_experts(w.to(dtype).cuda(), "all-to-sharded", segments=2, P=P)
+    gate = xv[:, 0].double()[:, None] * torch.tensor(FAR_COLUMNS * 2, dtype=torch.float64)
+    u = xv[:, 40].double()[:, None].expand_as(gate)
+    zero = torch.zeros_like(gate)
+    bound = ref.swiglu_bound(gate, u, zero, zero, K)
+    # (e^-z of a rounded exponent: log2 e in fp32 is 1.93e-8 off, an e of relative error
+    # 1.93e-8 ln 2 |z| < 1.2e-6 where it is finite, 20 half steps; a few more of the
+    # hardware's exponential and reciprocal)
+    bound = bound + 32 * 2.0 ** -24 * (ref.silu(gate) * u).abs() + 90 * 2.0 ** -126 * u.abs()
+    want, bound = (v.view(R, P, f // P).transpose(0, 1) for v in (ref.silu(gate) * u, bound))
+    for out_dtype in (dtype, F32):
+        got = sg.experts_all_to_sharded(layer, call, off.cuda(), swiglu=True, out_dtype=out_dtype, **kw)
+        ref.close(got, want, bound, f"{kind} {out_dtype}")
+
+
+@pytest.mark.parametrize("T", [3, 200])
+def test_moe_mlp_of_far_gates(T):
+    """A token one of whose gates is -100 keeps its output."""
+    g = gen(T)
+    D, F = 64, 32
+    x, gu, dn = normal(g, (T, D), BF), normal(g, (1, 2 * F, D), BF, 0.1), normal(g, (1, D, F), BF, 0.1)
+    x[:, 0] = 1.0
+    gu[0, 5, :] = 0
+    gu[0, 5, 0] = -100.0
+    route = sg.moe_route(torch.zeros((T, 1), device="cuda"), 1)
+    lg = sg.shard_experts(gu.cuda(), "all-to-sharded", segments=2)
+    out = sg.moe_mlp(lg, sg.shard_experts(dn.cuda(), "sharded-to-all"), x.cuda(), route)
+    dn[0, :, 5] = 0  # silu(-100) is below 2^-137: no output of that column's counts
+    assert torch.equal(out, sg.moe_mlp(lg, sg.shard_experts(dn.cuda(), "sharded-to-all"), x.cuda(), route))

@@ -481,10 +481,10 @@ void route_v(const Route& r, hipStream_t s) {
         return;
     }
     const int ct = chunk_tokens_of(r.T, r.k);
-    const int chunks = (r.T + ct - 1) / ct;
-    launch(route_choose_kernel<V>, dim3(chunks), dim3(1024), 0, s, r, ct);
+    const int chunks = (r.T + ct - 1) / ct;  // (0 without tokens: the scan alone, which writes the offsets)
+    if (chunks) launch(route_choose_kernel<V>, dim3(chunks), dim3(1024), 0, s, r, ct);
     launch(route_scan_kernel, dim3(1), dim3(1024), 0, s, r, chunks);
-    launch(route_place_kernel, dim3(chunks), dim3(64), 0, s, r, ct);
+    if (chunks) launch(route_place_kernel, dim3(chunks), dim3(64), 0, s, r, ct);
 }
 
 }  // namespace

@@ -88,3 +88,13 @@ def test_moe_mlp_of_far_gates(T):
     out = sg.moe_mlp(lg, sg.shard_experts(dn.cuda(), "sharded-to-all"), x.cuda(), route)
     dn[0, :, 5] = 0  # silu(-100) is below 2^-137: no output of that column's counts
     assert torch.equal(out, sg.moe_mlp(lg, sg.shard_experts(dn.cuda(), "sharded-to-all"), x.cuda(), route))
+
+
+@pytest.mark.parametrize("E", [5, 256, 257, 300, 1024])
+@pytest.mark.parametrize("normalize", [True, False])
+def test_route_of_no_tokens(E, normalize):
+    z = torch.empty((0, E), device="cuda")
+    r = sg.moe_route(z, 2, normalize)
+    assert r.offsets.tolist() == [0] * (E + 1)
+    assert r.weights.shape == r.experts.shape == r.slots.shape == (0, 2) and r.rows.shape == (0,)
+    assert sg.moe_route_backward(z, r, torch.empty((0, 2), device="cuda"), normalize).shape == (0, E)

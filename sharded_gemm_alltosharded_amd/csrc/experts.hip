@@ -724,6 +724,8 @@ hipError_t stream_launch(const Grouped& p, hipStream_t s) {
 //   1 x (4096 x 14336)  44 / 29    19 / 15    15 / 12
 //   1 x (2048 x 8192)   23 / 16    11 / 9     8.5 / 7.1
 // and with half as many workgroups again as compute units 63 / 71.
+// (None of this looks at alignment: how many waves share the inputs decides the
+// order of the sums, and so the result's bits.)
 template <int MODE, bool SWIGLU, bool AL>
 hipError_t stream_mode(const Grouped& p, hipStream_t s) {
     constexpr int NB = SWIGLU ? 2 : 4;
@@ -734,7 +736,7 @@ hipError_t stream_mode(const Grouped& p, hipStream_t s) {
     if constexpr (MODE < G_MX4) {
         if constexpr (!SWIGLU)
             if (blocks * 2 > want) return stream_launch<MODE, SWIGLU, 1, NB / 2, 4, 4, AL>(p, s);
-    } else if constexpr (AL) {
+    } else {
         if (blocks / NB >= want) return stream_launch<MODE, SWIGLU, 1, NB, 1, 4, AL>(p, s);
         if (blocks / NB * 2 >= want) return stream_launch<MODE, SWIGLU, 1, NB, 2, 4, AL>(p, s);
         if (blocks / NB * 4 >= want) return stream_launch<MODE, SWIGLU, 1, NB, 4, 4, AL>(p, s);

@@ -98,3 +98,21 @@ def test_route_of_no_tokens(E, normalize):
     assert r.offsets.tolist() == [0] * (E + 1)
     assert r.weights.shape == r.experts.shape == r.slots.shape == (0, 2) and r.rows.shape == (0,)
     assert sg.moe_route_backward(z, r, torch.empty((0, 2), device="cuda"), normalize).shape == (0, E)
+
+
+# E, R, in, out, segments: as many output blocks as take one, two, four, eight
+# and sixteen waves for a block's inputs, and tiles
+@pytest.mark.parametrize("E,R,K,n,S", [(4, 6, 2048, 28672, 1), (2, 5, 2048, 28672, 1), (1, 3, 2048, 28672, 1),
+                                       (1, 2, 2048, 14336, 1), (4, 7, 4096, 28672, 2), (1, 2, 8192, 4096, 1),
+                                       (1, 3, 8192, 2048, 2), (1, 40, 2048, 4096, 2)])
+def test_mxfp4_results_do_not_depend_on_alignment(E, R, K, n, S):
+    g = torch.Generator("cuda").manual_seed(n + E)
+    codes = torch.randint(0, 256, (E, n, K // 2), generator=g, device="cuda", dtype=torch.int32).to(torch.uint8)
+    scales = torch.randint(118, 123, (E, n, K // 32), generator=g, device="cuda", dtype=torch.int32).to(torch.uint8)
+    layer = sg.shard_mxfp4_experts(codes, scales, "all-to-sharded", segments=S)
+    off = offsets_of(gen(E), E, R, empty=False).cuda()
+    for width, at in ((K + 3, 1), (K + 8, 8), (K + 4, 4)):
+        x = torch.randn((R, width), generator=g, device="cuda").to(BF)[:, at:at + K]
+        for swiglu in ([False, True] if S == 2 else [False]):
+            got = sg.experts_all_to_sharded(layer, x, off, swiglu=swiglu, out_dtype=F32)
+            assert torch.equal(got, sg.experts_all_to_sharded(layer, x.contiguous(), off, swiglu=swiglu, out_dtype=F32))

@@ -26,7 +26,8 @@ namespace sg {
 //    multiple of 16 and segment s stored in rows s kpad .. + kl.
 //  * Output columns come in 16-column blocks: block b lies in piece b / bps at
 //    column 16 (b % bps) of its f columns; piece i is part i % S of rank i / S.
-//    Rank r's columns start at out + r * o_rank, row stride ldo.
+//    Rank r's columns start at out + r * o_rank, row stride ldo.  The last `pad`
+//    of the f columns are stored as zeros.
 //  * swiglu: pieces 2r and 2r + 1 are rank r's gate and up rows; output block b
 //    is block b % bps of rank b / bps.
 // Rows behind offsets[E] are not written.
@@ -48,7 +49,7 @@ struct Grouped {
     int64_t wsc_expert;
     int wblocks, wsteps;  // 16-row blocks, steps a block
     int transposed, swiglu;
-    int bps, f, S, nout;  // output blocks (of pairs with swiglu): nout
+    int bps, f, pad, S, nout;  // output blocks (of pairs with swiglu): nout
     void* out;
     int out_dtype;
     int64_t ldo, o_rank;

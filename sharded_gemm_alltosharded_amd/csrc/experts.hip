@@ -71,7 +71,10 @@ __device__ __forceinline__ void store_typed(const Grouped& p, int ob0, int row0,
             const int m = 16 * j + (lane & 15);
             if (m >= nrows) return;
             const f32x4 q = value(ic, jc, std::bool_constant<DT != SG_F32>{});
-            const float v[4] = {q[0], q[1], q[2], q[3]};
+            float v[4] = {q[0], q[1], q[2], q[3]};
+            if (c + 4 > p.f - p.pad)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = c + e < p.f - p.pad ? v[e] : 0.f;
             store_cols<DT>(p.out, base + (int64_t)(row0 + m) * p.ldo, v, p.f - c);
         });
     });

@@ -207,7 +207,8 @@ void set_out(sg::Grouped& p, void* y, sg_dtype dt) {
 }
 
 // x (T, in) -> ranks' columns; ldh: columns of a rank's output row that are
-// stored (the layer's own, or more of its zero-padded rows)
+// stored (the layer's own, and zeros behind them: products with its zero-padded
+// rows would be NaN there for an infinite x)
 sg::Grouped column(const sg_experts* x, const void* a, const uint8_t* a_scales, int64_t T, int64_t ldx,
                    const int32_t* offsets, const int32_t* rows, int k, int64_t R, void* y, int swiglu, int64_t ldh,
                    sg_dtype dt) {
@@ -229,6 +230,7 @@ sg::Grouped column(const sg_experts* x, const void* a, const uint8_t* a_scales, 
     p.swiglu = swiglu;
     p.bps = (int)x->l.bps;
     p.f = (int)(swiglu ? ldh : x->l.f);
+    p.pad = (int)(p.f - x->l.f);
     p.S = swiglu ? 1 : x->l.S;
     p.nout = (int)(swiglu ? x->l.bps * x->l.P : x->l.blocks);
     p.ldo = swiglu ? ldh : x->l.f * x->l.S;

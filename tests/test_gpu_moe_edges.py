@@ -116,3 +116,22 @@ def test_mxfp4_results_do_not_depend_on_alignment(E, R, K, n, S):
         for swiglu in ([False, True] if S == 2 else [False]):
             got = sg.experts_all_to_sharded(layer, x, off, swiglu=swiglu, out_dtype=F32)
             assert torch.equal(got, sg.experts_all_to_sharded(layer, x.contiguous(), off, swiglu=swiglu, out_dtype=F32))
+
+
+@pytest.mark.parametrize("T", [3, 200])
+def test_moe_mlp_of_infinities(T):
+    """Infinities go through the chain as through its three calls, where the hidden
+    width is no multiple of the stored rows' eight columns."""
+    g = gen(T)
+    D, F, P = 64, 26, 2
+    x = normal(g, (T, D), BF).abs()
+    x[0, 3] = math.inf
+    w = lambda *s: normal(g, s, BF, 0.1).abs() + 0.01
+    lg = sg.shard_experts(w(1, 2 * F, D).cuda(), "all-to-sharded", segments=2, P=P)
+    ld = sg.shard_experts(w(1, D, F).cuda(), "sharded-to-all", P=P)
+    r = sg.moe_route(torch.zeros((T, 1), device="cuda"), 1)
+    h = sg.experts_all_to_sharded(lg, x.cuda(), r.offsets, r.rows, 1, swiglu=True)
+    want = sg.moe_combine(sg.experts_sharded_to_all(ld, h, r.offsets, out_dtype=F32), r.slots, r.weights, out_dtype=BF)
+    got = sg.moe_mlp(lg, ld, x.cuda(), r)
+    assert torch.isinf(want[0]).all() and torch.isfinite(want[1:]).all()
+    assert torch.equal(got, want)

@@ -470,7 +470,8 @@ sg_status sg_moe_combine_backward(const void* dout, const void* y, sg_dtype dtyp
  * sg_experts_all_to_sharded (SWIGLU), sg_experts_sharded_to_all (fp32 y) and
  * sg_moe_combine.
  *   gate_up all-to-sharded with segments = 2, down sharded-to-all with
- *   segments = 1, of one E, P and dtype (both MXFP4, or both not).
+ *   segments = 1, of one E, P and dtype (an MXFP4 layer's is bf16: the pair may
+ *   be of MXFP4, of bf16, or of one each).
  *   x (T, in_dims), row stride ldx; weights, offsets, rows, slots: a plan of
  *   T tokens and k choices; y (T, out_dims of down).
  *   workspace sg_moe_mlp_workspace(...) bytes, 16-byte aligned, no initial

@@ -135,3 +135,20 @@ def test_moe_mlp_of_infinities(T):
     got = sg.moe_mlp(lg, ld, x.cuda(), r)
     assert torch.isinf(want[0]).all() and torch.isfinite(want[1:]).all()
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("T,E,k,D,F,P", [(1, 4, 2, 64, 64, 2), (40, 6, 3, 96, 192, 2), (300, 2, 1, 96, 54, 2)])
+def test_moe_mlp_of_one_mxfp4_layer(T, E, k, D, F, P):
+    """MXFP4 gate|up with bf16 down, and the reverse: bitwise the three calls."""
+    g = gen(T)
+    x, r = normal(g, (T, D), BF).cuda(), sg.moe_route(normal(g, (T, E)).cuda(), k)
+    gu, dn = normal(g, (E, 2 * F, D), BF, 0.1).cuda(), normal(g, (E, D, F), BF, 0.1).cuda()
+    pairs = [(sg.shard_mxfp4_experts(*sg.quantize_mxfp4(gu), "all-to-sharded", segments=2, P=P),
+              sg.shard_experts(dn, "sharded-to-all", P=P))]
+    if F // P % 32 == 0:
+        pairs.append((sg.shard_experts(gu, "all-to-sharded", segments=2, P=P),
+                      sg.shard_mxfp4_experts(*sg.quantize_mxfp4(dn), "sharded-to-all", P=P)))
+    for lg, ld in pairs:
+        h = sg.experts_all_to_sharded(lg, x, r.offsets, r.rows, k, swiglu=True)
+        y = sg.experts_sharded_to_all(ld, h, r.offsets, out_dtype=F32)
+        assert torch.equal(sg.moe_mlp(lg, ld, x, r), sg.moe_combine(y, r.slots, r.weights, out_dtype=BF))

@@ -541,7 +541,11 @@ def _free_experts():
     """Release the layers given up.  That waits for the device, which a capture
     does not allow: until it ends they stay."""
     while _freed and not torch.cuda.is_current_stream_capturing():
-        _lib.sg_experts_free(_freed.pop())
+        try:
+            h = _freed.pop()
+        except IndexError:  # another thread took the last one since
+            return
+        _lib.sg_experts_free(h)
 
 
 class Experts:

@@ -152,3 +152,24 @@ def test_moe_mlp_of_one_mxfp4_layer(T, E, k, D, F, P):
         h = sg.experts_all_to_sharded(lg, x, r.offsets, r.rows, k, swiglu=True)
         y = sg.experts_sharded_to_all(ld, h, r.offsets, out_dtype=F32)
         assert torch.equal(sg.moe_mlp(lg, ld, x, r), sg.moe_combine(y, r.slots, r.weights, out_dtype=BF))
+
+
+def test_layers_given_up_by_several_threads():
+    w = normal(gen(14), (1, 32, 64), BF).cuda()
+    layers = [sg.shard_experts(w, "all-to-sharded") for _ in range(48)]
+    errors = []
+
+    def drop(some):
+        try:
+            torch.cuda.set_device(0)
+            for layer in some:
+                layer.free()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=drop, args=(layers[i::8],)) for i in range(8)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors and not sg._freed

@@ -200,3 +200,22 @@ def test_reference_mxfp4_by_hand():
 
 def test_reference_shard_rows():
     assert ref.shard_rows(12, 2, 3) == [[0, 1, 6, 7], [2, 3, 8, 9], [4, 5, 10, 11]]
+
+
+def test_a_layer_taken_by_another_thread_is_left_to_it(monkeypatch):
+    """Two threads release the layers given up: one may empty the list behind the other's look at it."""
+    released = []
+
+    class Lib:
+        sg_experts_free = staticmethod(released.append)
+
+    def other_thread():  # between the look and the taking
+        if len(sg._freed) == 1:
+            sg._freed.pop()
+        return False
+
+    monkeypatch.setattr(sg, "_lib", Lib)
+    monkeypatch.setattr(sg, "_freed", ["a", "b", "c"])
+    monkeypatch.setattr(sg.torch.cuda, "is_current_stream_capturing", other_thread)
+    sg._free_experts()
+    assert released == ["c", "b"] and not sg._freed

@@ -538,8 +538,8 @@ _freed: list = []
 
 
 def _free_experts():
-    """Release the layers given up.  That waits for the device, which a capture
-    does not allow: until it ends they stay."""
+    """Release the layers given up.  That waits for the device; those given up while
+    this thread captures, whose graph may hold calls on them, stay until it ends."""
     while _freed and not torch.cuda.is_current_stream_capturing():
         try:
             h = _freed.pop()

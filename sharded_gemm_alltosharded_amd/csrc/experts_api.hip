@@ -366,10 +366,14 @@ void sg_experts_free(sg_experts* x) {
     int d = x->device;
     (void)hipGetDevice(&d);
     if (d != x->device) (void)hipSetDevice(x->device);
-    // kernels queued on any stream may still read the weights
-    (void)hipDeviceSynchronize();
+    // Kernels queued on any stream may still read the weights: hipFree waits for
+    // the device.  In relaxed mode it does so beside a capture of any thread, which
+    // hipDeviceSynchronize would end.
+    hipStreamCaptureMode mode = hipStreamCaptureModeRelaxed;
+    (void)hipThreadExchangeStreamCaptureMode(&mode);
     if (x->w) (void)hipFree(x->w);
     if (x->wsc) (void)hipFree(x->wsc);
+    (void)hipThreadExchangeStreamCaptureMode(&mode);
     if (d != x->device) (void)hipSetDevice(d);
     delete x;
 }

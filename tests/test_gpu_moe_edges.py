@@ -173,3 +173,53 @@ def test_layers_given_up_by_several_threads():
     for t in threads:
         t.join()
     assert not errors and not sg._freed
+
+
+def test_a_layer_given_up_while_another_thread_captures():
+    g = gen(15)
+    w, x = normal(g, (1, 64, 128), BF).cuda(), normal(g, (5, 128), BF).cuda()
+    keep, gone = (sg.shard_experts(w, "all-to-sharded") for _ in range(2))
+    mx = sg.shard_mxfp4_experts(*sg.quantize_mxfp4(w), "all-to-sharded")
+    want = sg.experts_all_to_sharded(keep, x)
+    graph, out = torch.cuda.CUDAGraph(), torch.empty_like(want)
+    capturing, errors = threading.Event(), []
+
+    def drop():
+        try:
+            torch.cuda.set_device(0)
+            if capturing.wait(60):
+                gone.free()
+                mx.free()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    other = threading.Thread(target=drop)
+    other.start()
+    with torch.cuda.graph(graph):
+        capturing.set()
+        other.join()
+        sg.experts_all_to_sharded(keep, x, out=out)
+    assert not errors and not sg._freed
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        assert torch.equal(out, want)
+
+
+def test_giving_up_a_layer_waits_for_the_device():
+    g = gen(16)
+    layers = [sg.shard_experts(normal(g, (2, 512, 1024), BF).cuda(), "all-to-sharded") for _ in range(2)]
+    x = normal(g, (4096, 1024), BF).cuda()
+    off = torch.tensor([0, 2000, 4096], dtype=torch.int32).cuda()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    out = torch.empty((1, 4096, 512), dtype=BF, device="cuda")
+    with torch.cuda.stream(side):
+        for _ in range(400):
+            sg.experts_all_to_sharded(layers[0], x, off, out=out)
+        done = torch.cuda.Event()
+        done.record()
+    busy = not done.query()
+    layers[1].free()
+    assert busy and done.query()
+    layers[0].free()

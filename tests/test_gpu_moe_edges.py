@@ -223,3 +223,57 @@ def test_giving_up_a_layer_waits_for_the_device():
     layers[1].free()
     assert busy and done.query()
     layers[0].free()
+
+
+@pytest.mark.parametrize("R", [40, 5])
+def test_offsets_near_4_gib_of_tokens(R):
+    """Rows at the end of the largest slice of activations: forward, dW and MXFP4 weights, in tiles and streams."""
+    g = gen(R)
+    T, K, n, E = 1000, 200, 48, 2
+    ld = 2147450880 // T // 8 * 8  # T rows of ld fill the 4 GiB less 64 KiB that an offset reaches
+    x = normal(g, (T, K), BF)
+    wide = torch.zeros((T, ld), dtype=BF, device="cuda")
+    wide[:, ld - K:] = x.cuda()
+    for off8 in (0, 3):  # (rows of any alignment too)
+        big = wide[:, ld - K - off8:ld - off8] if off8 else wide[:, ld - K:]
+        small = big.contiguous()
+        off = offsets_of(g, E, R, empty=False).cuda()
+        rows = (T - 1 - torch.arange(R, dtype=torch.int32)).cuda()
+        layer = sg.shard_experts(normal(g, (E, n, K), BF, 0.1).cuda(), "all-to-sharded")
+        want = sg.experts_all_to_sharded(layer, small, off, rows, 1)
+        assert torch.equal(sg.experts_all_to_sharded(layer, big, off, rows, 1), want)
+        assert torch.isfinite(want).all() and want.any()
+        dy = normal(g, (1, R, n), BF).cuda()
+        for a, b in zip(sg.experts_all_to_sharded_backward(layer, big, dy, off, rows, 1),
+                        sg.experts_all_to_sharded_backward(layer, small, dy, off, rows, 1)):
+            assert torch.equal(a, b)
+        mx = sg.shard_mxfp4_experts(*sg.quantize_mxfp4(normal(g, (E, n, 192), BF, 0.1).cuda()), "all-to-sharded")
+        assert torch.equal(sg.experts_all_to_sharded(mx, big[:, :192], off, rows, 1),
+                           sg.experts_all_to_sharded(mx, small[:, :192].contiguous(), off, rows, 1))
+    with pytest.raises(sg.ShardGemmError) as e:  # a row's bytes more
+        sg.experts_all_to_sharded(layer, torch.as_strided(wide, (T, K), (ld + 40, 1)), off, rows, 1)
+    assert e.value.code == sg.ERR_UNSUPPORTED
+
+
+def test_offsets_near_4_gib_of_rows():
+    """The last rows of the largest packed slice: down product, both gradients of it, and the plain rows of dW."""
+    g = gen(13)
+    K, n = 2056, 16
+    R = 2147450880 // K
+    w = normal(g, (1, n, K), BF, 0.1)
+    down = sg.shard_experts(w.cuda(), "sharded-to-all")
+    h = torch.zeros((1, R, K), dtype=BF, device="cuda")
+    h[:, -300:] = normal(g, (1, 300, K), BF).cuda()
+    tail = h[:, -300:].contiguous()
+    y = sg.experts_sharded_to_all(down, h)
+    assert torch.equal(y[-300:], sg.experts_sharded_to_all(down, tail)) and not y[:-300].any()
+    dy = torch.zeros((R, n), dtype=BF, device="cuda")
+    dy[-300:] = normal(g, (300, n), BF).cuda()
+    _, dw = sg.experts_sharded_to_all_backward(down, h, dy, need_dx=False)
+    a, b = dy[-300:].cpu().double(), tail[0].cpu().double()
+    ref.close(dw[0, 0], a.T @ b, ref.sum_bound(a.abs().T @ b.abs(), 300), "dw")
+    col = sg.shard_experts(w.transpose(1, 2).contiguous().cuda(), "all-to-sharded")  # its dy is h
+    dx, dw = sg.experts_all_to_sharded_backward(col, dy, h)
+    assert torch.equal(dx[-300:], sg.experts_all_to_sharded_backward(col, dy[-300:], tail, need_dw=False)[0])
+    assert not dx[:-300].any()
+    ref.close(dw[0, 0], b.T @ a, ref.sum_bound(b.abs().T @ a.abs(), 300), "dw of columns")

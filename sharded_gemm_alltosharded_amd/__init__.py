@@ -620,8 +620,8 @@ def shard_mxfp4_experts(codes: torch.Tensor, scales: torch.Tensor, sharding, seg
 
 
 def _grouped(layer: Experts, offsets, rows, R, k=1):
-    if rows is not None and k is None:
-        _bad("rows are slots of k choices each: k is None")
+    if rows is not None and (k is None or k < 1):
+        _bad(f"rows are slots of k choices each: k is {k}")
     _want(offsets, "offsets", (layer.E + 1,), torch.int32, layer.device, optional=layer.E == 1)
     _want(rows, "rows", (R,), torch.int32, layer.device, optional=True)
 

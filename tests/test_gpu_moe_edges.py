@@ -277,3 +277,16 @@ def test_offsets_near_4_gib_of_rows():
     assert torch.equal(dx[-300:], sg.experts_all_to_sharded_backward(col, dy[-300:], tail, need_dw=False)[0])
     assert not dx[:-300].any()
     ref.close(dw[0, 0], b.T @ a, ref.sum_bound(b.abs().T @ a.abs(), 300), "dw of columns")
+
+
+@pytest.mark.parametrize("k", [0, -2])
+def test_row_map_of_no_choices_is_refused(k):
+    layer = sg.shard_experts(normal(gen(1), (1, 16, 64), BF).cuda(), "all-to-sharded")
+    x, rows = normal(gen(2), (4, 64), BF).cuda(), torch.zeros(8, dtype=torch.int32, device="cuda")
+    dy = torch.zeros((1, 8, 16), dtype=BF, device="cuda")
+    for call in (lambda: sg.experts_all_to_sharded(layer, x, rows=rows, k=k),
+                 lambda: sg.experts_all_to_sharded_backward(layer, x, dy, rows=rows, k=k),
+                 lambda: sg.experts_all_to_sharded_backward(layer, None, dy, rows=rows, k=k, need_dw=False)):
+        with pytest.raises(sg.ShardGemmError) as e:
+            call()
+        assert e.value.code == sg.ERR_INVALID_ARG

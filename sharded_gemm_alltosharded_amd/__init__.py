@@ -512,6 +512,8 @@ def _want(t, name: str, shape=None, dtype=None, device=None, optional=False):
 
 def _matrix(t, name: str, width=None, dtype=_FLOATS, device=None):
     """A (rows, width) argument whose rows may be strided: its row stride."""
+    if t is None:
+        _bad(f"{name} is None")
     if t.dim() != 2 or (width is not None and t.shape[1] != width):
         _bad(f"{name} has shape {tuple(t.shape)}, not (any, {width})")
     if t.dtype is not dtype and t.dtype not in (dtype if isinstance(dtype, tuple) else ()):
@@ -819,8 +821,8 @@ def moe_mlp(gate_up: Experts, down: Experts, x: torch.Tensor, route: Route, out_
 
 def quantize_mxfp4(x: torch.Tensor):
     """(..., n) values -> MXFP4 codes (..., n / 2) and scales (..., n / 32), uint8 (sg_quantize_mxfp4)."""
-    if x.dim() < 1:
-        _bad("x has no columns")
+    if x is None or x.dim() < 1:
+        _bad("x is None" if x is None else "x has no columns")
     n = x.shape[-1]
     if x.dim() == 2:
         ld = _matrix(x, "x")

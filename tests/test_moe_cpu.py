@@ -219,3 +219,12 @@ def test_a_layer_taken_by_another_thread_is_left_to_it(monkeypatch):
     monkeypatch.setattr(sg.torch.cuda, "is_current_stream_capturing", other_thread)
     sg._free_experts()
     assert released == ["c", "b"] and not sg._freed
+
+
+def test_missing_matrices_are_refused(L):
+    """None where a (rows, width) tensor belongs, as for every other argument."""
+    for call in (lambda: sg.moe_route(None, 2), lambda: sg.quantize_mxfp4(None),
+                 lambda: sg._matrix(None, "x", 64)):
+        with pytest.raises(sg.ShardGemmError, match="None") as e:
+            call()
+        assert e.value.code == sg.ERR_INVALID_ARG

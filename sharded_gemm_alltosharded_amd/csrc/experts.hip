@@ -54,7 +54,8 @@ __device__ __forceinline__ f32x4 swiglu4(f32x4 g, f32x4 u) {
 
 // Stores a wave's N x M result blocks: value(i, j) is this lane's four columns
 // 4 (lane >> 4) .. + 3 of output block ob0 + i, row row0 + 16 j + (lane & 15).
-template <int DT, int N, int M, typename F>
+// PAD: columns behind the piece's own may be asked for (p.pad; only SwiGLU has them).
+template <int DT, bool PAD, int N, int M, typename F>
 __device__ __forceinline__ void store_typed(const Grouped& p, int ob0, int row0, int nrows, F&& value) {
     const int lane = threadIdx.x & 63;
     static_for<0, N>([&](auto ic) {
@@ -66,24 +67,24 @@ __device__ __forceinline__ void store_typed(const Grouped& p, int ob0, int row0,
         const int c = 16 * blk + 4 * (lane >> 4);
         if (c >= p.f) return;
         const int64_t base = (int64_t)r * p.o_rank + s * p.f + c;
+        const int live = p.f - p.pad - c;
         static_for<0, M>([&](auto jc) {
             constexpr int j = decltype(jc)::value;
             const int m = 16 * j + (lane & 15);
             if (m >= nrows) return;
             const f32x4 q = value(ic, jc, std::bool_constant<DT != SG_F32>{});
-            float v[4] = {q[0], q[1], q[2], q[3]};
-            if (c + 4 > p.f - p.pad)
+            float v[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = c + e < p.f - p.pad ? v[e] : 0.f;
+            for (int e = 0; e < 4; ++e) v[e] = !PAD || e < live ? q[e] : 0.f;
             store_cols<DT>(p.out, base + (int64_t)(row0 + m) * p.ldo, v, p.f - c);
         });
     });
 }
-template <int N, int M, typename F>
+template <bool PAD, int N, int M, typename F>
 __device__ __forceinline__ void store_blocks(const Grouped& p, int ob0, int row0, int nrows, F&& value) {
-    if (p.out_dtype == SG_BF16) store_typed<SG_BF16, N, M>(p, ob0, row0, nrows, value);
-    else if (p.out_dtype == SG_F16) store_typed<SG_F16, N, M>(p, ob0, row0, nrows, value);
-    else store_typed<SG_F32, N, M>(p, ob0, row0, nrows, value);
+    if (p.out_dtype == SG_BF16) store_typed<SG_BF16, PAD, N, M>(p, ob0, row0, nrows, value);
+    else if (p.out_dtype == SG_F16) store_typed<SG_F16, PAD, N, M>(p, ob0, row0, nrows, value);
+    else store_typed<SG_F32, PAD, N, M>(p, ob0, row0, nrows, value);
 }
 
 // segment's first element of A
@@ -244,7 +245,7 @@ __global__ __launch_bounds__(64 * NWV) void grouped_stream_kernel(Grouped p) {
 #pragma unroll
                 for (int b = 0; b < MB; ++b) acc[i][b] += red[(((q * NG + ng) * NW + i) * MB + b) * 64 + lane];
     }
-    store_blocks<NB, MB>(p, ob0, s.row0, s.nrows, [&](auto ic, auto jc, auto near) {
+    store_blocks<SWIGLU, NB, MB>(p, ob0, s.row0, s.nrows, [&](auto ic, auto jc, auto near) {
         constexpr int n = decltype(ic)::value, b = decltype(jc)::value;
         if constexpr (!SWIGLU) return acc[n][b];
         else return swiglu4<decltype(near)::value>(acc[2 * n][b], acc[2 * n + 1][b]);
@@ -568,7 +569,7 @@ __device__ __forceinline__ void grouped_tile(const Grouped& p, const Slot s, con
 
     constexpr int NO = SWIGLU ? NBN / 2 : NBN;  // output blocks of a wave
     const int m0 = wave_m * NBM * 16;
-    store_blocks<NO, NBM>(p, nt * NO * WN + wave_n * NO, s.row0 + m0, s.nrows - m0, [&](auto ic, auto jc, auto near) {
+    store_blocks<SWIGLU, NO, NBM>(p, nt * NO * WN + wave_n * NO, s.row0 + m0, s.nrows - m0, [&](auto ic, auto jc, auto near) {
         constexpr int i = decltype(ic)::value, j = decltype(jc)::value;
         if constexpr (!SWIGLU) return acc[i][j];
         else return swiglu4<decltype(near)::value>(acc[2 * i][j], acc[2 * i + 1][j]);

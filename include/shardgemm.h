@@ -419,7 +419,8 @@ sg_status sg_experts_sharded_to_all_backward(const sg_experts* layer, const void
 
 /* SwiGLU on its own, on rank-local rows [gate; up] (what an all-to-sharded
  * layer with segments = 2 gives without the epilogue): gu (rows, 2 f) ->
- * h (rows, f) = silu(gate) * up; dh (rows, f) -> dgu (rows, 2 f).  One dtype. */
+ * h (rows, f) = silu(gate) * up; dh (rows, f) -> dgu (rows, 2 f).  One dtype, in
+ * which dgu is stored: one rounding of 16-bit gradients ahead of the layer's own. */
 sg_status sg_swiglu(const void* gu, sg_dtype dtype, int64_t rows, int64_t f, void* h, void* stream);
 sg_status sg_swiglu_backward(const void* gu, const void* dh, sg_dtype dtype, int64_t rows, int64_t f, void* dgu,
                              void* stream);
@@ -466,7 +467,7 @@ sg_status sg_moe_combine_backward(const void* dout, const void* y, sg_dtype dtyp
 
 /* The gated MLP over experts: y[t] = sum over t's slots of weight times
  * down_e(silu(x[t] W_gate,e^T) * (x[t] W_up,e^T)).  h is stored in the layers'
- * dtype, the down layer's rows in fp32; bitwise the chain of
+ * dtype (fp16: infinite beyond 65504), the down layer's rows in fp32; bitwise the chain of
  * sg_experts_all_to_sharded (SWIGLU), sg_experts_sharded_to_all (fp32 y) and
  * sg_moe_combine.
  *   gate_up all-to-sharded with segments = 2, down sharded-to-all with
@@ -491,7 +492,7 @@ size_t sg_moe_mlp_workspace(const sg_experts* gate_up, const sg_experts* down, i
  *   scales (rows, cols / 32). */
 sg_status sg_quantize_mxfp4(const void* x, sg_dtype dtype, int64_t rows, int64_t cols, int64_t ldx, uint8_t* codes,
                             uint8_t* scales, void* stream);
-/* The values it stands for, rounded to dtype (exact in fp32); x packed. */
+/* The values it stands for, rounded to dtype (exact in fp32 below 2^128); x packed. */
 sg_status sg_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, void* x,
                               sg_dtype dtype, void* stream);
 

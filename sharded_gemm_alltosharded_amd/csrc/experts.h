@@ -47,7 +47,7 @@ struct Grouped {
     int64_t w_expert;  // bytes from one expert's weights to the next
     const uint8_t* wsc;
     int64_t wsc_expert;
-    int wblocks, wsteps;  // 16-row blocks, steps a block
+    int wsteps;  // steps of a 16-row block
     int transposed, swiglu;
     int bps, f, pad, S, nout;  // output blocks (of pairs with swiglu): nout
     void* out;
@@ -122,7 +122,7 @@ hipError_t launch_combine(const void* y, int y_dtype, const int32_t* slots, cons
 hipError_t launch_combine_backward(const void* dout, const void* y, int dtype, const int32_t* slots,
                                    const float* weights, int64_t T, int k, int64_t D, int64_t R, void* dy, float* dw,
                                    hipStream_t s);
-// swiglu on (rows, 2 f) -> (rows, f); ldh: row stride of the output
+// swiglu on (rows, 2 f) -> (rows, f)
 hipError_t launch_swiglu(const void* gu, int dtype, int64_t rows, int64_t f, void* h, hipStream_t s);
 hipError_t launch_swiglu_backward(const void* gu, const void* dh, int dtype, int64_t rows, int64_t f, void* dgu,
                                   hipStream_t s);

@@ -734,7 +734,10 @@ template <int MODE, bool SWIGLU, bool AL>
 hipError_t stream_mode(const Grouped& p, hipStream_t s) {
     constexpr int NB = SWIGLU ? 2 : 4;
     const int64_t blocks = (int64_t)p.nout * (p.R < p.E ? p.R : p.E), want = 7 * (int64_t)device_cus();
-    // (MXFP4 activations whose scales the tiles cannot take come here with any rows)
+    // (MXFP4 activations whose scales the tiles cannot take come here with any rows:
+    // the weights are read once for every 32 of them.  us of K = 1984 / the same on
+    // tiles, K = 2048 / with bf16 activations: 4096 rows of 8192 weight rows 151 / 71
+    // / 159, of 8 x 4096 79 / 39 / 78, 256 rows of those 14 / 10 / 15)
     if constexpr (MODE == G_MX4A4)
         if (p.R > (int64_t)8 * p.E) return stream_launch<MODE, SWIGLU, 2, NB, 1, 4, AL>(p, s);
     if constexpr (MODE < G_MX4) {
@@ -786,8 +789,9 @@ bool few_tiles(const Grouped& p) {
     return tiles_of<SWIGLU, TM>(p) * 5 <= (int64_t)device_cus() * 6;
 }
 
-// Tile by the rows of an expert, m = R / E on average (they differ: half as
-// much again is reckoned with), and by whether the tiles fill the chip.  Times
+// Tile by the rows of an expert, m = R / E on average, and by whether the tiles
+// fill the chip (experts differ: half a tile more for each is reckoned with where
+// wide tiles are asked about, a quarter more rows in tiles_of).  Times
 // in us on bf16 experts, 64 x 128 / 128 x 128 / 256 x 256 tiles:
 //   8 x (28672 x 4096, SwiGLU)  m = 32: 339 335 407   96: 440 378 434  128: 604 471 464   256: 1010 765 717
 //   8 x (4096 x 14336)          m = 32: 200 204 318   96: 229 237 323  192: 434 271 360   256: 476 498 385
@@ -837,7 +841,8 @@ template <int MODE, bool AL>
 hipError_t by_mode(const Grouped& p, hipStream_t s) {
     if constexpr (MODE < G_MX4)
         if (p.transposed) return tile_mode<MODE, false, true, AL>(p, s);
-    // (an MXFP4 row's scales are staged four at a time)
+    // (an MXFP4 row's scales are staged four at a time, by aligned 4-byte loads: rows
+    // of no multiple of 128 inputs go to the streaming kernel however many they are)
     const bool tiles = p.R > (int64_t)8 * p.E && (MODE != G_MX4A4 || (p.kl % 128 == 0 && (uintptr_t)p.a_scales % 4 == 0));
     if (tiles) return p.swiglu ? tile_mode<MODE, true, false, AL>(p, s) : tile_mode<MODE, false, false, AL>(p, s);
     return p.swiglu ? stream_mode<MODE, true, AL>(p, s) : stream_mode<MODE, false, AL>(p, s);

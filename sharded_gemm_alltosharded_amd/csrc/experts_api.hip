@@ -192,7 +192,6 @@ void set_weights(sg::Grouped& p, const sg_experts* x) {
     p.w_expert = x->w_expert();
     p.wsc = x->wsc;
     p.wsc_expert = x->wsc_expert();
-    p.wblocks = (int)x->l.blocks;
     p.wsteps = (int)x->l.steps;
     p.E = (int)x->l.E;
 }
@@ -449,7 +448,8 @@ sg_status sg_moe_mlp(const sg_experts* g, const sg_experts* d, const void* x, in
     // of one type, and h in two parts would cost every down product a second pass.
     // One rounding of each h beside one of each y, of the same size and independent:
     // sqrt(2) times the error of h in 32 bits (rms 0.0023 to 0.0017 of y in bf16,
-    // 0.00030 to 0.00021 in fp16; 0.0026 at most, on a few hundred outputs).
+    // 0.00030 to 0.00021 in fp16; 0.0026 at most, on a few hundred outputs).  An h
+    // beyond 65504 is infinite in fp16.
     void* h = workspace;
     float* yr = (float*)((char*)workspace + up(R * g->l.P * ldh * 2, 256));
     st = launched(sg::launch_grouped(column(g, x, nullptr, T, ldx, offsets, rows, k, R, h, 1, ldh, g->dtype), s),

@@ -93,7 +93,7 @@ __device__ __forceinline__ void choose(const Route& r, int64_t t, Put put) {
     if (lane < r.k) put(lane, mine, w);
 }
 
-// lanes of the wave whose value equals this lane's (values below 1024)
+// lanes of the wave whose value equals this lane's (values below 2^bits)
 __device__ __forceinline__ uint64_t same_lanes(int v, int bits) {
     uint64_t m = ~0ull;
     for (int b = 0; b < bits; ++b) {

@@ -496,6 +496,81 @@ sg_status sg_quantize_mxfp4(const void* x, sg_dtype dtype, int64_t rows, int64_t
 sg_status sg_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, void* x,
                               sg_dtype dtype, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Training a gated block on activations kept in 8 bits.
+ *
+ * MX FP8 (OCP Microscaling): blocks of 32 adjacent values of a row share one E8M0
+ * scale byte s, each value an E4M3 code, worth code * 2^(s - 127): the format of
+ * sg_shard_mxfp8_linear.  s - 127 is the smallest integer, -127 at least, at which
+ * no magnitude of the block exceeds 448, so that nothing saturates; codes round to
+ * nearest even; a block holding an infinity or a NaN: s = 255 (NaN), codes 0.  The
+ * last block of a row may be short.
+ *   x (rows, cols) of dtype, row stride ldx; codes (rows, cols);
+ *   scales (rows, ceil(cols / 32)). */
+sg_status sg_quantize_mxfp8(const void* x, sg_dtype dtype, int64_t rows, int64_t cols, int64_t ldx, uint8_t* codes,
+                            uint8_t* scales, void* stream);
+/* The values it stands for, rounded to dtype (exact in fp32 below 2^128; fp16:
+ * infinite from 65520); x packed. */
+sg_status sg_dequantize_mxfp8(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, void* x,
+                              sg_dtype dtype, void* stream);
+
+/* The gated half of the block, forward: with g, u the gate and up rows that
+ * sg_experts_all_to_sharded gives, h = silu(g) * u and, kept for the backward pass,
+ * g and u in MX FP8 (quantized from the fp32 sums).
+ *   layer    bf16 or fp16, all-to-sharded, segments = 2 ([W_gate; W_up]); f =
+ *            out_dims / 2 / P.  x, T, ldx, offsets, rows, k, R as there.
+ *   h        (P, R, f) of the layer's dtype.
+ *   codes    (P, R, 2, f), scales (P, R, 2, ceil(f / 32)): gate, then up.
+ *   workspace sg_experts_gated_workspace(layer, R) bytes, 16-byte aligned (NULL
+ *            when that is 0), no initial contents; calls that share it must not
+ *            overlap. */
+sg_status sg_experts_gated(const sg_experts* layer, const void* x, int64_t T, int64_t ldx, const int32_t* offsets,
+                           const int32_t* rows, int k, int64_t R, void* h, uint8_t* codes, uint8_t* scales,
+                           void* workspace, size_t ws_bytes, void* stream);
+size_t sg_experts_gated_workspace(const sg_experts* layer, int64_t R);
+
+/* ... and backward: dh_r = dy W_down,r (fp32, not rounded), then the gradient of the
+ * kept gate and up rows, and h again from them (the down layer's input, for its
+ * weight gradient).
+ *   down     bf16 or fp16, sharded-to-all, segments = 1; f = in_dims / P.
+ *   dy       (R, out_dims) of the layer's dtype.
+ *   dgu      (P, R, 2 f) rows [gate; up]; h (P, R, f), both of the layer's dtype;
+ *            h may be NULL.
+ *   workspace as above, sg_experts_gated_backward_workspace(down, R) bytes. */
+sg_status sg_experts_gated_backward(const sg_experts* down, const void* dy, const uint8_t* codes, const uint8_t* scales,
+                                    const int32_t* offsets, int64_t R, void* dgu, void* h, void* workspace,
+                                    size_t ws_bytes, void* stream);
+size_t sg_experts_gated_backward_workspace(const sg_experts* down, int64_t R);
+
+/* The whole block, forward: y[m] = sum over r of h_r[m] W_down,r^T for every grouped
+ * row, and what the backward pass needs: x and the gate|up rows in MX FP8 (one byte
+ * and 1/32 a value; h is not kept).  A dense block is one of E == 1 with offsets NULL.
+ * Bitwise the chain of sg_quantize_mxfp8, sg_experts_gated and
+ * sg_experts_sharded_to_all.
+ *   gate_up, down a pair as for sg_moe_mlp, bf16 or fp16.
+ *   y        (R, out_dims of down) of y_dtype.
+ *   x_codes  (T, in_dims), x_scales (T, ceil(in_dims / 32)); gu_codes, gu_scales as
+ *            codes, scales of sg_experts_gated.
+ *   workspace sg_gated_mlp_workspace(...) bytes, 16-byte aligned. */
+sg_status sg_gated_mlp(const sg_experts* gate_up, const sg_experts* down, const void* x, int64_t T, int64_t ldx,
+                       const int32_t* offsets, const int32_t* rows, int k, int64_t R, void* y, sg_dtype y_dtype,
+                       uint8_t* x_codes, uint8_t* x_scales, uint8_t* gu_codes, uint8_t* gu_scales, void* workspace,
+                       size_t ws_bytes, void* stream);
+size_t sg_gated_mlp_workspace(const sg_experts* gate_up, const sg_experts* down, int64_t R);
+
+/* Its gradients, from what it kept: dx (R, in_dims), one row for every grouped row;
+ * dw_gate_up (E, P, 2 f, in_dims); dw_down (E, P, out_dims, f), of dw_dtype, laid out
+ * as the layers' shards.  Any may be NULL (not all).  x_codes and x_scales are needed
+ * for dw_gate_up only.  Bitwise the chain of sg_experts_gated_backward,
+ * sg_dequantize_mxfp8 and the two layers' backward calls.
+ *   workspace sg_gated_mlp_backward_workspace(...) bytes, 16-byte aligned. */
+sg_status sg_gated_mlp_backward(const sg_experts* gate_up, const sg_experts* down, const uint8_t* x_codes,
+                                const uint8_t* x_scales, int64_t T, const uint8_t* gu_codes, const uint8_t* gu_scales,
+                                const void* dy, const int32_t* offsets, const int32_t* rows, int k, int64_t R, void* dx,
+                                sg_dtype dx_dtype, void* dw_gate_up, void* dw_down, sg_dtype dw_dtype, void* workspace,
+                                size_t ws_bytes, void* stream);
+size_t sg_gated_mlp_backward_workspace(const sg_experts* gate_up, const sg_experts* down, int64_t T, int64_t R);
+
 /* Profiling: arm two hipEvent_t (created with timing enabled; either may be
  * NULL) for the next kernel this thread launches through the library, which
  * records start_event when that kernel begins and stop_event when it ends

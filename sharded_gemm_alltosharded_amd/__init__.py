@@ -26,6 +26,10 @@ kernels.  The entry points mirror include/shardgemm.h one to one:
     moe_combine                sg_moe_combine (+ _backward): the weighted sum over a token's experts
     moe_mlp                    sg_moe_mlp (+ sg_moe_mlp_workspace)
     quantize_mxfp4             sg_quantize_mxfp4; dequantize_mxfp4: sg_dequantize_mxfp4
+    quantize_mxfp8             sg_quantize_mxfp8; dequantize_mxfp8: sg_dequantize_mxfp8
+    experts_gated              sg_experts_gated (+ _backward): SwiGLU's half of the gated block, its
+                               gate|up rows kept in MX FP8 for the backward pass
+    gated_mlp                  sg_gated_mlp (+ _backward): the whole block
     Layer.info / Layer.shard   sg_layer_info / sg_layer_copy_shard
     time_next_launch           sg_time_next_launch (profiling)
 
@@ -122,6 +126,16 @@ def lib():
             "sg_moe_mlp_workspace": ([P, P, I64, I], SZ),
             "sg_quantize_mxfp4": ([P, I, I64, I64, I64, P, P, P], I),
             "sg_dequantize_mxfp4": ([P, P, I64, I64, P, I, P], I),
+            "sg_quantize_mxfp8": ([P, I, I64, I64, I64, P, P, P], I),
+            "sg_dequantize_mxfp8": ([P, P, I64, I64, P, I, P], I),
+            "sg_experts_gated": ([P, P, I64, I64, P, P, I, I64, P, P, P, P, SZ, P], I),
+            "sg_experts_gated_workspace": ([P, I64], SZ),
+            "sg_experts_gated_backward": ([P, P, P, P, P, I64, P, P, P, SZ, P], I),
+            "sg_experts_gated_backward_workspace": ([P, I64], SZ),
+            "sg_gated_mlp": ([P, P, P, I64, I64, P, P, I, I64, P, I, P, P, P, P, P, SZ, P], I),
+            "sg_gated_mlp_workspace": ([P, P, I64], SZ),
+            "sg_gated_mlp_backward": ([P, P, P, P, I64, P, P, P, P, P, I, I64, P, I, P, P, I, P, SZ, P], I),
+            "sg_gated_mlp_backward_workspace": ([P, P, I64, I64], SZ),
             "sg_time_next_launch": ([P, P], I),
             "sg_last_error": ([], C.c_char_p),
         }
@@ -847,3 +861,144 @@ def dequantize_mxfp4(codes: torch.Tensor, scales: torch.Tensor, out_dtype=torch.
     _run(lib().sg_dequantize_mxfp4, codes.device, _at(codes), _at(scales), x.numel() // n if n else 0, n, _at(x),
          _DT[out_dtype])
     return x
+
+
+# ---- the gated block on activations kept in 8 bits --------------------------
+
+def quantize_mxfp8(x: torch.Tensor):
+    """(..., n) values -> MX FP8 codes (..., n) and scales (..., ceil(n / 32)), uint8 (sg_quantize_mxfp8)."""
+    if x is None or x.dim() < 1:
+        _bad("x is None" if x is None else "x has no columns")
+    n = x.shape[-1]
+    if x.dim() == 2:
+        ld = _matrix(x, "x")
+    else:
+        _want(x, "x", None, _FLOATS)
+        ld = n
+    codes = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
+    scales = torch.empty((*x.shape[:-1], (n + 31) // 32), dtype=torch.uint8, device=x.device)
+    _run(lib().sg_quantize_mxfp8, x.device, _at(x), _DT[x.dtype], x.numel() // n if n else 0, n, ld, _at(codes),
+         _at(scales))
+    return codes, scales
+
+
+def dequantize_mxfp8(codes: torch.Tensor, scales: torch.Tensor, out_dtype=torch.float32) -> torch.Tensor:
+    """The values that codes (..., n) and scales (..., ceil(n / 32)) stand for (sg_dequantize_mxfp8)."""
+    _want(codes, "codes", None, torch.uint8)
+    if codes.dim() < 1:
+        _bad("codes has no columns")
+    n = codes.shape[-1]
+    _want(scales, "scales", (*codes.shape[:-1], (n + 31) // 32), torch.uint8, codes.device)
+    x = _out(None, "out", tuple(codes.shape), out_dtype, codes.device)
+    _run(lib().sg_dequantize_mxfp8, codes.device, _at(codes), _at(scales), x.numel() // n if n else 0, n, _at(x),
+         _DT[out_dtype])
+    return x
+
+
+class GatedSaved(NamedTuple):
+    """What a gated block keeps for its backward pass, in MX FP8 (sg_gated_mlp)."""
+    x_codes: torch.Tensor    # (T, in) uint8
+    x_scales: torch.Tensor   # (T, ceil(in / 32)) uint8
+    gu_codes: torch.Tensor   # (P, R, 2, f) uint8: the gate rows, the up rows
+    gu_scales: torch.Tensor  # (P, R, 2, ceil(f / 32)) uint8
+
+
+def _scratch(need: int, dev):
+    return torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
+
+
+def _kept(P, R, f, dev):
+    return (torch.empty((P, R, 2, f), dtype=torch.uint8, device=dev),
+            torch.empty((P, R, 2, (f + 31) // 32), dtype=torch.uint8, device=dev))
+
+
+def _want_kept(codes, scales, P, R, f, dev):
+    _want(codes, "codes", (P, R, 2, f), torch.uint8, dev)
+    _want(scales, "scales", (P, R, 2, (f + 31) // 32), torch.uint8, dev)
+
+
+def experts_gated(layer: Experts, x: torch.Tensor, offsets=None, rows=None, k: int | None = None):
+    """x (T, in) -> (h (P, R, f), codes (P, R, 2, f), scales): SwiGLU of the gate|up
+    product, and its gate and up rows kept in MX FP8 (sg_experts_gated).  rows, k as
+    in experts_all_to_sharded; f = out_dims / 2 / P."""
+    dev = layer.device
+    ld = _matrix(x, "x", layer.in_dims, layer.dtype, dev)
+    R = x.shape[0] if rows is None else rows.shape[0]
+    _grouped(layer, offsets, rows, R, k)
+    f = layer.out_dims // 2 // layer.P
+    h = torch.empty((layer.P, R, f), dtype=layer.dtype, device=dev)
+    codes, scales = _kept(layer.P, R, f, dev)
+    L = lib()
+    need = L.sg_experts_gated_workspace(layer.handle, R)
+    ws = _scratch(need, dev)
+    _run(L.sg_experts_gated, dev, layer.handle, _at(x), x.shape[0], ld, _at(offsets), _at(rows), k or 1, R, _at(h),
+         _at(codes), _at(scales), _at(ws), need)
+    return h, codes, scales
+
+
+def experts_gated_backward(down: Experts, dy: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, offsets=None,
+                           need_h: bool = True):
+    """dy (R, out) and the kept gate and up rows -> (dgu (P, R, 2 f), h (P, R, f) or
+    None): the gradient of the gate|up rows, and the down layer's input again
+    (sg_experts_gated_backward)."""
+    dev, f = down.device, down.in_dims // down.P
+    _want(dy, "dy", (None, down.out_dims), down.dtype, dev)
+    R = dy.shape[0]
+    _grouped(down, offsets, None, R)
+    _want_kept(codes, scales, down.P, R, f, dev)
+    dgu = torch.empty((down.P, R, 2 * f), dtype=down.dtype, device=dev)
+    h = torch.empty((down.P, R, f), dtype=down.dtype, device=dev) if need_h else None
+    L = lib()
+    need = L.sg_experts_gated_backward_workspace(down.handle, R)
+    ws = _scratch(need, dev)
+    _run(L.sg_experts_gated_backward, dev, down.handle, _at(dy), _at(codes), _at(scales), _at(offsets), R, _at(dgu),
+         _at(h), _at(ws), need)
+    return dgu, h
+
+
+def gated_mlp(gate_up: Experts, down: Experts, x: torch.Tensor, offsets=None, rows=None, k: int | None = None,
+              out_dtype=None, out: torch.Tensor | None = None):
+    """The gated block for training: x (T, in) -> (y (R, out), GatedSaved), y[m] =
+    down(silu(x W_gate^T) * (x W_up^T)) for every grouped row (sg_gated_mlp).  A dense
+    block is one expert: shard_experts(weight[None], ...), offsets None."""
+    dev = gate_up.device
+    ld = _matrix(x, "x", gate_up.in_dims, gate_up.dtype, dev)
+    T = x.shape[0]
+    R = T if rows is None else rows.shape[0]
+    _grouped(gate_up, offsets, rows, R, k)
+    out = _out(out, "out", (R, down.out_dims), out_dtype or down.dtype, dev)
+    x_codes = torch.empty((T, gate_up.in_dims), dtype=torch.uint8, device=dev)
+    x_scales = torch.empty((T, (gate_up.in_dims + 31) // 32), dtype=torch.uint8, device=dev)
+    gu_codes, gu_scales = _kept(gate_up.P, R, gate_up.out_dims // 2 // gate_up.P, dev)
+    L = lib()
+    need = L.sg_gated_mlp_workspace(gate_up.handle, down.handle, R)
+    ws = _scratch(need, dev)
+    _run(L.sg_gated_mlp, dev, gate_up.handle, down.handle, _at(x), T, ld, _at(offsets), _at(rows), k or 1, R, _at(out),
+         _DT[out.dtype], _at(x_codes), _at(x_scales), _at(gu_codes), _at(gu_scales), _at(ws), need)
+    return out, GatedSaved(x_codes, x_scales, gu_codes, gu_scales)
+
+
+def gated_mlp_backward(gate_up: Experts, down: Experts, saved: GatedSaved, dy: torch.Tensor, offsets=None, rows=None,
+                       k: int | None = None, need_dx: bool = True, need_dw: bool = True, dx_dtype=None,
+                       dw_dtype=torch.float32):
+    """Gradients of gated_mlp from what it kept: dy (R, out) -> (dx (R, in), one row
+    for every grouped row, dw_gate_up (E, P, 2 f, in), dw_down (E, P, out, f)); dx, or
+    both weights', may be skipped (None) (sg_gated_mlp_backward)."""
+    dev = gate_up.device
+    _want(dy, "dy", (None, down.out_dims), down.dtype, dev)
+    R, f, D = dy.shape[0], gate_up.out_dims // 2 // gate_up.P, gate_up.in_dims
+    _grouped(gate_up, offsets, rows, R, k)
+    _want(saved.x_codes, "x_codes", (None, D), torch.uint8, dev)
+    T = saved.x_codes.shape[0]
+    _want(saved.x_scales, "x_scales", (T, (D + 31) // 32), torch.uint8, dev)
+    _want_kept(saved.gu_codes, saved.gu_scales, gate_up.P, R, f, dev)
+    dx = _out(None, "dx", (R, D), dx_dtype or gate_up.dtype, dev) if need_dx else None
+    dwg = _out(None, "dw", (gate_up.E, gate_up.P, 2 * f, D), dw_dtype, dev) if need_dw else None
+    dwd = _out(None, "dw", (down.E, down.P, down.out_dims, down.in_dims // down.P), dw_dtype, dev) if need_dw else None
+    L = lib()
+    need = L.sg_gated_mlp_backward_workspace(gate_up.handle, down.handle, T, R)
+    ws = _scratch(need, dev)
+    _run(L.sg_gated_mlp_backward, dev, gate_up.handle, down.handle, _at(saved.x_codes), _at(saved.x_scales), T,
+         _at(saved.gu_codes), _at(saved.gu_scales), _at(dy), _at(offsets), _at(rows), k or 1, R, _at(dx),
+         _DT.get(dx_dtype or gate_up.dtype, -1), _at(dwg), _at(dwd), _DT.get(dw_dtype, -1), _at(ws), need)
+    return dx, dwg, dwd

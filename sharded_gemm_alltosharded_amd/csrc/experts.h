@@ -133,6 +133,19 @@ hipError_t launch_quantize_mxfp4(const void* x, int dtype, int64_t rows, int64_t
 hipError_t launch_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, void* x,
                                    int dtype, hipStream_t s);
 
+// MX FP8 activations (mxfp8.hip); a row of n values has mx8_blocks(n) scales
+__host__ __device__ inline int64_t mx8_blocks(int64_t n) { return (n + 31) / 32; }
+hipError_t launch_quantize_mxfp8(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ld, uint8_t* codes,
+                                 uint8_t* scales, hipStream_t s);
+hipError_t launch_dequantize_mxfp8(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, void* x,
+                                   int dtype, hipStream_t s);
+// the gated block where its products' epilogues do not do it: gate|up rows to h and
+// what is kept, and dh with what was kept to the gradient of the gate|up rows (and h)
+hipError_t launch_gated_keep(const float* gu, int64_t P, int64_t R, int64_t f, const int32_t* offsets, int E, void* h,
+                             int f16, uint8_t* codes, uint8_t* scales, hipStream_t s);
+hipError_t launch_gated_grad(const float* dh, const uint8_t* codes, const uint8_t* scales, int64_t P, int64_t R,
+                             int64_t f, const int32_t* offsets, int E, void* dgu, void* h, int f16, hipStream_t s);
+
 #ifdef __HIPCC__
 #define ALWAYS_INLINE __attribute__((always_inline))
 
@@ -250,6 +263,38 @@ __device__ __forceinline__ void load_cols(const void* x, int64_t at, float (&v)[
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = DT == SG_BF16 ? bf16_to_f32(h[e]) : f16_to_f32(h[e]);
     }
+}
+
+// ---- MX FP8 blocks (mxfp8.hip has the format) -------------------------------
+// magnitudes compare like their bit patterns; infinities and NaNs are the largest
+__device__ __forceinline__ uint32_t mx8_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+__device__ __forceinline__ bool mx8_bad(uint32_t m) { return m >= 0x7f800000u; }
+// exponent of a block whose largest magnitude has the bits m: 448 = 1.75 2^8
+// (zeros and subnormals fall below -127)
+__device__ __forceinline__ int mx8_exponent(uint32_t m) {
+    return max((int)(m >> 23) - 135 + ((m & 0x7fffffu) > 0x600000u), -127);
+}
+__device__ __forceinline__ uint8_t mx8_scale(uint32_t m) { return mx8_bad(m) ? 255 : (uint8_t)(mx8_exponent(m) + 127); }
+// four codes: x 2^-e is exact (a power of two) unless it falls below 2^-126, where
+// the code is 0 anyway
+__device__ __forceinline__ uint32_t mx8_codes(float a, float b, float c, float d, int e) {
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(ldexpf(a, -e), ldexpf(b, -e), 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(ldexpf(c, -e), ldexpf(d, -e), w, true);
+}
+__device__ __forceinline__ void mx8_values(uint32_t w, int s, float& a, float& b, float& c, float& d) {
+    const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
+    const float nan = __builtin_nanf("");
+    a = s == 255 ? nan : ldexpf(lo[0], s - 127), b = s == 255 ? nan : ldexpf(lo[1], s - 127);
+    c = s == 255 ? nan : ldexpf(hi[0], s - 127), d = s == 255 ? nan : ldexpf(hi[1], s - 127);
+}
+
+// h = g s u with s = 1 / (1 + e^-g), and its gradient: dg = dh u s (1 + g (1 - s)),
+// du = dh g s.  e^-|g| cannot overflow, and s keeps what it has far below zero.
+__device__ __forceinline__ void swiglu_grad(float g, float u, float dh, float& dg, float& du, float& h) {
+    const float e = expf(-fabsf(g)), s = (g < 0.f ? e : 1.0f) / (1.0f + e), a = g * s;
+    dg = dh * u * s * (1.0f + g * (1.0f - s));
+    du = dh * a;
+    h = a * u;
 }
 
 struct Slot {

@@ -1,6 +1,6 @@
-// C-ABI entry points of the mixture of experts and of MXFP4: validation, the
-// expert layers, and what each call hands to the grouped kernels.  Every check
-// runs on the host before any device work.
+// C-ABI entry points of the mixture of experts, of MXFP4 and of the gated block on
+// activations kept in MX FP8: validation, the expert layers, and what each call
+// hands to the grouped kernels.  Every check runs on the host before any device work.
 #include <stdarg.h>
 #include <stdio.h>
 
@@ -261,6 +261,32 @@ sg::Grouped row(const sg_experts* x, const void* h, const uint8_t* h_scales, int
     p.nout = (int)x->l.blocks;
     p.ldo = x->l.f;
     set_out(p, y, dt);
+    return p;
+}
+
+// dh_r = dy W_r of a sharded-to-all layer
+sg::Grouped row_dx(const sg_experts* x, const void* dy, const int32_t* offsets, int64_t R, void* dh,
+                          sg_dtype dh_dtype) {
+    const sg::ExpertsLayout& l = x->l;
+    sg::Grouped p{};
+    p.mode = mode_of(x, nullptr);
+    p.A = dy;
+    p.lda = l.out;
+    p.a_pieces = p.nseg = 1;
+    p.kl = (int)l.out;
+    p.kpad = (int)(l.bps * 16);
+    p.offsets = offsets;
+    p.kdiv = 1;
+    p.T = p.R = (int)R;
+    set_weights(p, x);
+    p.transposed = 1;
+    p.bps = (int)(l.kpad / 16);
+    p.f = (int)l.kl;
+    p.S = 1;
+    p.nout = p.bps * l.P;
+    p.ldo = l.kl;
+    p.o_rank = R * l.kl;
+    set_out(p, dh, dh_dtype);
     return p;
 }
 
@@ -545,28 +571,9 @@ sg_status sg_experts_sharded_to_all_backward(const sg_experts* x, const void* h,
     if (st) return st;
     const sg::ExpertsLayout& l = x->l;
     hipStream_t s = (hipStream_t)stream;
-    if (dh && R > 0) {
-        sg::Grouped p{};
-        p.mode = mode_of(x, nullptr);
-        p.A = dy;
-        p.lda = l.out;
-        p.a_pieces = p.nseg = 1;
-        p.kl = (int)l.out;
-        p.kpad = (int)(l.bps * 16);
-        p.offsets = offsets;
-        p.kdiv = 1;
-        p.T = p.R = (int)R;
-        set_weights(p, x);
-        p.transposed = 1;
-        p.bps = (int)(l.kpad / 16);
-        p.f = (int)l.kl;
-        p.S = 1;
-        p.nout = p.bps * l.P;
-        p.ldo = l.kl;
-        p.o_rank = R * l.kl;
-        set_out(p, dh, dh_dtype);
-        st = launched(sg::launch_grouped(p, s), "sg_experts_sharded_to_all_backward dx");
-    }
+    if (dh && R > 0)
+        st = launched(sg::launch_grouped(row_dx(x, dy, offsets, R, dh, dh_dtype), s),
+                      "sg_experts_sharded_to_all_backward dx");
     if (!st && dw) {
         sg::GroupedDw p{};
         p.f16 = x->dtype == SG_F16;
@@ -726,6 +733,204 @@ sg_status sg_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scales, int64
         return fail(SG_ERR_INVALID_ARG, "codes must be 4-byte, x 16-byte aligned");
     return launched(sg::launch_dequantize_mxfp4(codes, scales, rows, cols, x, dtype, (hipStream_t)stream),
                     "sg_dequantize_mxfp4");
+}
+
+// ---- the gated block on activations kept in 8 bits ---------------------------
+
+static sg_status check_mx8(sg_dtype dtype, int64_t rows, int64_t cols) {
+    if (!known(dtype)) return fail(SG_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
+    if (rows < 0 || cols < 0) return fail(SG_ERR_INVALID_ARG, "rows and cols must be >= 0");
+    if ((double)rows * (double)sg::mx8_blocks(cols) * 4 >= (double)(sg::kMaxBlocks - 1) * 256)
+        return fail(SG_ERR_UNSUPPORTED, "more values than one launch takes");
+    return SG_OK;
+}
+
+sg_status sg_quantize_mxfp8(const void* x, sg_dtype dtype, int64_t rows, int64_t cols, int64_t ldx, uint8_t* codes,
+                            uint8_t* scales, void* stream) {
+    sg::last_error().clear();
+    if (sg_status st = check_mx8(dtype, rows, cols)) return st;
+    if (ldx < cols) return fail(SG_ERR_INVALID_ARG, "row stride %lld is below the width %lld", (long long)ldx,
+                                (long long)cols);
+    if (rows == 0 || cols == 0) return SG_OK;
+    if (!x || !codes || !scales) return fail(SG_ERR_INVALID_ARG, "x, codes and scales must not be NULL");
+    return launched(sg::launch_quantize_mxfp8(x, dtype, rows, cols, ldx, codes, scales, (hipStream_t)stream),
+                    "sg_quantize_mxfp8");
+}
+
+sg_status sg_dequantize_mxfp8(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, void* x,
+                              sg_dtype dtype, void* stream) {
+    sg::last_error().clear();
+    if (sg_status st = check_mx8(dtype, rows, cols)) return st;
+    if (rows == 0 || cols == 0) return SG_OK;
+    if (!x || !codes || !scales) return fail(SG_ERR_INVALID_ARG, "x, codes and scales must not be NULL");
+    return launched(sg::launch_dequantize_mxfp8(codes, scales, rows, cols, x, dtype, (hipStream_t)stream),
+                    "sg_dequantize_mxfp8");
+}
+
+static sg_status check_gate_up(const sg_experts* g) {
+    if (sg_status st = check_layer(g, SG_ALL_TO_SHARDED, "a gated block")) return st;
+    if (g->mx) return fail(SG_ERR_UNSUPPORTED, "a gated block that keeps its activations needs bf16 or fp16 layers");
+    if (g->l.S != 2) return fail(SG_ERR_INVALID_ARG, "gate_up must be an all-to-sharded layer with segments = 2");
+    return SG_OK;
+}
+static sg_status check_down(const sg_experts* d) {
+    if (sg_status st = check_layer(d, SG_SHARDED_TO_ALL, "a gated block")) return st;
+    if (d->mx) return fail(SG_ERR_UNSUPPORTED, "a gated block that keeps its activations needs bf16 or fp16 layers");
+    if (d->l.S != 1) return fail(SG_ERR_INVALID_ARG, "down must be a sharded-to-all layer with segments = 1");
+    return SG_OK;
+}
+static sg_status check_ws(const char* what, const void* ws, size_t bytes, size_t need) {
+    if (need && (!ws || bytes < need || !aligned(ws, 16)))
+        return fail(SG_ERR_WORKSPACE, "%s needs %zu bytes of 16-byte aligned workspace (got %zu)", what, need,
+                    ws ? bytes : (size_t)0);
+    return SG_OK;
+}
+// rows of the block: f columns of P ranks, as many threads as a launch may have
+static sg_status check_gated_rows(int64_t P, int64_t R, int64_t f) {
+    if ((double)P * (double)R * (double)sg::mx8_blocks(f) * 4 >= (double)(sg::kMaxBlocks - 1) * 256)
+        return fail(SG_ERR_UNSUPPORTED, "more values than one launch takes");
+    return SG_OK;
+}
+
+size_t sg_experts_gated_workspace(const sg_experts* g, int64_t R) {
+    if (!g || g->l.mode != SG_ALL_TO_SHARDED || g->l.S != 2 || g->mx || R <= 0 || R > kMaxRows) return 0;
+    return (size_t)up(R * g->l.out * 4, 256);
+}
+
+sg_status sg_experts_gated(const sg_experts* g, const void* x, int64_t T, int64_t ldx, const int32_t* offsets,
+                           const int32_t* rows, int k, int64_t R, void* h, uint8_t* codes, uint8_t* scales,
+                           void* workspace, size_t ws_bytes, void* stream) {
+    sg::last_error().clear();
+    sg_status st = check_gate_up(g);
+    if (!st) st = check_rows(g, offsets, R);
+    if (!st) st = check_gather(T, ldx, g->l.in, rows, k, R);
+    if (!st) st = check_bytes(T, ldx, 4);
+    if (!st) st = check_gated_rows(g->l.P, R, g->l.f);
+    if (st) return st;
+    if (R == 0) return SG_OK;
+    if (T == 0) return fail(SG_ERR_INVALID_ARG, "%lld rows of no tokens", (long long)R);
+    if (!x || !h || !codes || !scales) return fail(SG_ERR_INVALID_ARG, "x, h, codes and scales must not be NULL");
+    if ((st = check_ws("sg_experts_gated", workspace, ws_bytes, sg_experts_gated_workspace(g, R)))) return st;
+    hipStream_t s = (hipStream_t)stream;
+    st = launched(sg::launch_grouped(column(g, x, nullptr, T, ldx, offsets, rows, k, R, workspace, 0, 0, SG_F32), s),
+                  "sg_experts_gated");
+    if (!st) st = launched(sg::launch_gated_keep((const float*)workspace, g->l.P, R, g->l.f, offsets, (int)g->l.E, h,
+                                                 g->dtype == SG_F16, codes, scales, s), "sg_experts_gated");
+    return st;
+}
+
+size_t sg_experts_gated_backward_workspace(const sg_experts* d, int64_t R) {
+    if (!d || d->l.mode != SG_SHARDED_TO_ALL || d->l.S != 1 || d->mx || R <= 0 || R > kMaxRows) return 0;
+    return (size_t)up(R * d->l.in * 4, 256);
+}
+
+sg_status sg_experts_gated_backward(const sg_experts* d, const void* dy, const uint8_t* codes, const uint8_t* scales,
+                                    const int32_t* offsets, int64_t R, void* dgu, void* h, void* workspace,
+                                    size_t ws_bytes, void* stream) {
+    sg::last_error().clear();
+    sg_status st = check_down(d);
+    if (!st) st = check_rows(d, offsets, R);
+    if (!st) st = check_bytes(R, d->l.out, 4);
+    if (!st) st = check_gated_rows(d->l.P, R, d->l.kl);
+    if (st) return st;
+    if (R == 0) return SG_OK;
+    if (!dy || !codes || !scales || !dgu) return fail(SG_ERR_INVALID_ARG, "dy, codes, scales and dgu must not be NULL");
+    if ((st = check_ws("sg_experts_gated_backward", workspace, ws_bytes, sg_experts_gated_backward_workspace(d, R))))
+        return st;
+    hipStream_t s = (hipStream_t)stream;
+    st = launched(sg::launch_grouped(row_dx(d, dy, offsets, R, workspace, SG_F32), s), "sg_experts_gated_backward");
+    if (!st) st = launched(sg::launch_gated_grad((const float*)workspace, codes, scales, d->l.P, R, d->l.kl, offsets,
+                                                 (int)d->l.E, dgu, h, d->dtype == SG_F16, s),
+                           "sg_experts_gated_backward");
+    return st;
+}
+
+size_t sg_gated_mlp_workspace(const sg_experts* g, const sg_experts* d, int64_t R) {
+    if (check_pair(g, d) || R <= 0 || R > kMaxRows) return 0;
+    return (size_t)up(R * d->l.in * 2, 256) + sg_experts_gated_workspace(g, R);
+}
+
+sg_status sg_gated_mlp(const sg_experts* g, const sg_experts* d, const void* x, int64_t T, int64_t ldx,
+                       const int32_t* offsets, const int32_t* rows, int k, int64_t R, void* y, sg_dtype y_dtype,
+                       uint8_t* x_codes, uint8_t* x_scales, uint8_t* gu_codes, uint8_t* gu_scales, void* workspace,
+                       size_t ws_bytes, void* stream) {
+    sg::last_error().clear();
+    sg_status st = check_pair(g, d);
+    if (!st) st = check_gate_up(g);
+    if (!st) st = check_down(d);
+    if (!st) st = check_rows(g, offsets, R);
+    if (!st) st = check_gather(T, ldx, g->l.in, rows, k, R);
+    if (!st) st = check_bytes(T, ldx, 4);
+    if (!st) st = check_bytes(R, d->l.kl, 4);
+    if (!st) st = check_gated_rows(g->l.P, R, g->l.f);
+    if (!st) st = check_mx8(g->dtype, T, g->l.in);
+    if (st) return st;
+    if (!known(y_dtype)) return fail(SG_ERR_INVALID_ARG, "unknown output dtype %d", (int)y_dtype);
+    if (R > 0 && T == 0) return fail(SG_ERR_INVALID_ARG, "%lld rows of no tokens", (long long)R);
+    if (T > 0 && (!x || !x_codes || !x_scales)) return fail(SG_ERR_INVALID_ARG, "x, x_codes and x_scales must not be NULL");
+    if (R > 0 && (!y || !gu_codes || !gu_scales))
+        return fail(SG_ERR_INVALID_ARG, "y, gu_codes and gu_scales must not be NULL");
+    if ((st = check_ws("sg_gated_mlp", workspace, ws_bytes, sg_gated_mlp_workspace(g, d, R)))) return st;
+    // h in the layers' 16 bits, as in sg_moe_mlp
+    const size_t hb = (size_t)up(R * d->l.in * 2, 256);
+    st = sg_quantize_mxfp8(x, g->dtype, T, g->l.in, ldx, x_codes, x_scales, stream);
+    if (!st && R) st = sg_experts_gated(g, x, T, ldx, offsets, rows, k, R, workspace, gu_codes, gu_scales,
+                                        (char*)workspace + hb, ws_bytes - hb, stream);
+    if (!st) st = sg_experts_sharded_to_all(d, workspace, nullptr, offsets, R, y, y_dtype, stream);
+    return st;
+}
+
+size_t sg_gated_mlp_backward_workspace(const sg_experts* g, const sg_experts* d, int64_t T, int64_t R) {
+    if (check_pair(g, d) || R <= 0 || R > kMaxRows || T < 0 || T > kMaxRows) return 0;
+    return (size_t)up(R * g->l.out * 2, 256) + (size_t)up(R * d->l.in * 2, 256) + (size_t)up(T * g->l.in * 2, 256) +
+           sg_experts_gated_backward_workspace(d, R);
+}
+
+sg_status sg_gated_mlp_backward(const sg_experts* g, const sg_experts* d, const uint8_t* x_codes,
+                                const uint8_t* x_scales, int64_t T, const uint8_t* gu_codes, const uint8_t* gu_scales,
+                                const void* dy, const int32_t* offsets, const int32_t* rows, int k, int64_t R, void* dx,
+                                sg_dtype dx_dtype, void* dw_gate_up, void* dw_down, sg_dtype dw_dtype, void* workspace,
+                                size_t ws_bytes, void* stream) {
+    sg::last_error().clear();
+    sg_status st = check_pair(g, d);
+    if (!st) st = check_gate_up(g);
+    if (!st) st = check_down(d);
+    if (!st) st = check_rows(g, offsets, R);
+    if (!st && dw_gate_up) st = check_gather(T, g->l.in, g->l.in, rows, k, R);
+    if (!st && dw_gate_up) st = check_bytes(T, g->l.in, 4);
+    if (!st && dw_gate_up) st = check_mx8(g->dtype, T, g->l.in);
+    if (!st) st = check_bytes(R, g->l.f * 2, 4);
+    if (!st) st = check_bytes(R, d->l.out, 4);
+    if (!st) st = check_gated_rows(g->l.P, R, g->l.f);
+    if (st) return st;
+    if (!dx && !dw_gate_up && !dw_down) return fail(SG_ERR_INVALID_ARG, "dx, dw_gate_up and dw_down are all NULL");
+    if (dx && !known(dx_dtype)) return fail(SG_ERR_INVALID_ARG, "unknown dx dtype %d", (int)dx_dtype);
+    if ((dw_gate_up || dw_down) && !known(dw_dtype)) return fail(SG_ERR_INVALID_ARG, "unknown dw dtype %d", (int)dw_dtype);
+    if (R > 0 && dw_gate_up && T == 0) return fail(SG_ERR_INVALID_ARG, "%lld rows of no tokens", (long long)R);
+    if (R > 0 && (!dy || !gu_codes || !gu_scales))
+        return fail(SG_ERR_INVALID_ARG, "dy, gu_codes and gu_scales must not be NULL");
+    if (R > 0 && dw_gate_up && (!x_codes || !x_scales))
+        return fail(SG_ERR_INVALID_ARG, "dw_gate_up needs x_codes and x_scales");
+    if ((st = check_ws("sg_gated_mlp_backward", workspace, ws_bytes, sg_gated_mlp_backward_workspace(g, d, T, R))))
+        return st;
+    char* at = (char*)workspace;
+    void* dgu = at;
+    void* h = at += up(R * g->l.out * 2, 256);
+    void* x = at += up(R * d->l.in * 2, 256);
+    if (dw_gate_up) at += up(T * g->l.in * 2, 256);
+    if (R > 0) {
+        // dgu is stored in the layers' 16 bits, once, the operand of both products
+        // behind it (a matrix instruction multiplies values of one type)
+        st = sg_experts_gated_backward(d, dy, gu_codes, gu_scales, offsets, R, dgu, dw_down ? h : nullptr, at,
+                                       ws_bytes - (size_t)(at - (char*)workspace), stream);
+        if (!st && dw_gate_up) st = sg_dequantize_mxfp8(x_codes, x_scales, T, g->l.in, x, g->dtype, stream);
+    }
+    if (!st && (dx || dw_gate_up))
+        st = sg_experts_all_to_sharded_backward(g, x, T, g->l.in, dgu, offsets, rows, k, R, dx, dx_dtype, dw_gate_up,
+                                                dw_dtype, stream);
+    if (!st && dw_down)
+        st = sg_experts_sharded_to_all_backward(d, h, dy, offsets, R, nullptr, dx_dtype, dw_down, dw_dtype, stream);
+    return st;
 }
 
 }  // extern "C"

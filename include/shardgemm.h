@@ -571,6 +571,63 @@ sg_status sg_gated_mlp_backward(const sg_experts* gate_up, const sg_experts* dow
                                 size_t ws_bytes, void* stream);
 size_t sg_gated_mlp_backward_workspace(const sg_experts* gate_up, const sg_experts* down, int64_t T, int64_t R);
 
+/* ---------------------------------------------------------------------------
+ * Low-rank adapters of many requests beside a shared projection.  Token t of a step
+ * goes with adapter a = which[t], or none:
+ *
+ *   y[t] = x[t] W^T (+ bias) + scale[a] (x[t] A_a^T) B_a^T
+ *
+ * beside any layer of bf16 or fp16 activations (dense, 4-bit or MX FP8).  The
+ * adapters' matrices are the unsharded layer's: all-to-sharded, B's rows go with the
+ * layer's (each rank has its part of every segment) and A is replicated;
+ * sharded-to-all, A's columns go with the layer's, x A^T summed over the ranks, and B
+ * is replicated.  Sums are fp32, and the output is rounded once.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    const void* A;      /* (n, rank, in_dims) of the layer's dtype, on the device */
+    const void* B;      /* (n, out_dims, rank) */
+    const float* scale; /* (n) fp32 on the device, or NULL: 1 */
+    int n, rank;        /* n <= 1024, rank <= 256 */
+} sg_adapters;
+
+/* The plan of a step: its tokens grouped by adapter, for every layer's calls of the
+ * step.  which (T) int32 on the device: 0 .. n - 1, anything else: no adapter.
+ * plan: sg_adapter_plan_ints(T, n) int32 on the device (0 for T or n out of range),
+ * to be passed with the same T and n.  T <= 2^25. */
+size_t sg_adapter_plan_ints(int64_t T, int n);
+sg_status sg_adapter_plan(const int32_t* which, int64_t T, int n, int32_t* plan, void* stream);
+
+/* Forward: x, y, out_layout, epilogue as in sg_all_to_sharded_ex (SG_IN_FULL), and
+ * as in sg_sharded_to_all; SwiGLU is taken of the sums.
+ *   workspace sg_adapted_workspace(layer, adapters, T) bytes, 16-byte aligned, no
+ *            initial contents; calls that share it must not overlap. */
+sg_status sg_adapted_all_to_sharded(const sg_layer* layer, const sg_adapters* adapters, const int32_t* plan,
+                                    const void* x, int64_t T, void* y, int out_layout, int epilogue, sg_dtype y_dtype,
+                                    void* workspace, size_t ws_bytes, void* stream);
+sg_status sg_adapted_sharded_to_all(const sg_layer* layer, const sg_adapters* adapters, const int32_t* plan,
+                                    const void* x_partial, int64_t T, void* y, sg_dtype y_dtype, void* workspace,
+                                    size_t ws_bytes, void* stream);
+size_t sg_adapted_workspace(const sg_layer* layer, const sg_adapters* adapters, int64_t T);
+
+/* Backward, the projection frozen (no SwiGLU): x and dy as in the layers' backward
+ * calls;
+ *   dA (n, rank, in_dims), dB (n, out_dims, rank) of d_dtype, zeros for an adapter
+ *      without tokens;
+ *   dx of dx_dtype, laid out as x, through W and the adapters (dense layers only,
+ *      else SG_ERR_UNSUPPORTED; on its first call the layer builds its transposed
+ *      copy, as for its own backward call).
+ * Any may be NULL (not all); x is needed for dA and dB only.
+ *   workspace sg_adapted_backward_workspace(layer, adapters, T) bytes, as above. */
+sg_status sg_adapted_all_to_sharded_backward(const sg_layer* layer, const sg_adapters* adapters, const int32_t* plan,
+                                             const void* x, const void* dy, int64_t T, void* dx, sg_dtype dx_dtype,
+                                             void* dA, void* dB, sg_dtype d_dtype, void* workspace, size_t ws_bytes,
+                                             void* stream);
+sg_status sg_adapted_sharded_to_all_backward(const sg_layer* layer, const sg_adapters* adapters, const int32_t* plan,
+                                             const void* x_partial, const void* dy, int64_t T, void* dx_partial,
+                                             sg_dtype dx_dtype, void* dA, void* dB, sg_dtype d_dtype, void* workspace,
+                                             size_t ws_bytes, void* stream);
+size_t sg_adapted_backward_workspace(const sg_layer* layer, const sg_adapters* adapters, int64_t T);
+
 /* Profiling: arm two hipEvent_t (created with timing enabled; either may be
  * NULL) for the next kernel this thread launches through the library, which
  * records start_event when that kernel begins and stop_event when it ends

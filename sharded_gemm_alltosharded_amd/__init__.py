@@ -30,6 +30,9 @@ kernels.  The entry points mirror include/shardgemm.h one to one:
     experts_gated              sg_experts_gated (+ _backward): SwiGLU's half of the gated block, its
                                gate|up rows kept in MX FP8 for the backward pass
     gated_mlp                  sg_gated_mlp (+ _backward): the whole block
+    adapter_plan               sg_adapter_plan: a step's tokens grouped by adapter
+    adapted_all_to_sharded     sg_adapted_all_to_sharded (+ _backward): low-rank adapters beside a layer
+    adapted_sharded_to_all     sg_adapted_sharded_to_all (+ _backward)
     Layer.info / Layer.shard   sg_layer_info / sg_layer_copy_shard
     time_next_launch           sg_time_next_launch (profiling)
 
@@ -136,6 +139,14 @@ def lib():
             "sg_gated_mlp_workspace": ([P, P, I64], SZ),
             "sg_gated_mlp_backward": ([P, P, P, P, I64, P, P, P, P, P, I, I64, P, I, P, P, I, P, SZ, P], I),
             "sg_gated_mlp_backward_workspace": ([P, P, I64, I64], SZ),
+            "sg_adapter_plan_ints": ([I64, I], SZ),
+            "sg_adapter_plan": ([P, I64, I, P, P], I),
+            "sg_adapted_workspace": ([P, P, I64], SZ),
+            "sg_adapted_all_to_sharded": ([P, P, P, P, I64, P, I, I, I, P, SZ, P], I),
+            "sg_adapted_sharded_to_all": ([P, P, P, P, I64, P, I, P, SZ, P], I),
+            "sg_adapted_backward_workspace": ([P, P, I64], SZ),
+            "sg_adapted_all_to_sharded_backward": ([P, P, P, P, P, I64, P, I, P, P, I, P, SZ, P], I),
+            "sg_adapted_sharded_to_all_backward": ([P, P, P, P, P, I64, P, I, P, P, I, P, SZ, P], I),
             "sg_time_next_launch": ([P, P], I),
             "sg_last_error": ([], C.c_char_p),
         }
@@ -1002,3 +1013,121 @@ def gated_mlp_backward(gate_up: Experts, down: Experts, saved: GatedSaved, dy: t
          _at(saved.gu_codes), _at(saved.gu_scales), _at(dy), _at(offsets), _at(rows), k or 1, R, _at(dx),
          _DT.get(dx_dtype or gate_up.dtype, -1), _at(dwg), _at(dwd), _DT.get(dw_dtype, -1), _at(ws), need)
     return dx, dwg, dwd
+
+
+# ---- low-rank adapters beside a shared projection ----------------------------
+
+class Adapters(NamedTuple):
+    """n low-rank adapters of one layer: y += scale[a] (x A[a]^T) B[a]^T (sg_adapters)."""
+    A: torch.Tensor                    # (n, rank, in_dims) of the layer's dtype
+    B: torch.Tensor                    # (n, out_dims, rank)
+    scale: torch.Tensor | None = None  # (n,) fp32; None: 1
+
+
+class AdapterPlan(NamedTuple):
+    """A step's tokens grouped by adapter (sg_adapter_plan)."""
+    data: torch.Tensor
+    T: int
+    n: int
+
+
+class _AdaptersArg(C.Structure):
+    _fields_ = [("A", C.c_void_p), ("B", C.c_void_p), ("scale", C.c_void_p), ("n", C.c_int), ("rank", C.c_int)]
+
+
+def adapter_plan(which: torch.Tensor, n: int) -> AdapterPlan:
+    """which (T,) int32, the adapter of each token (0 .. n - 1, anything else: none)
+    -> the plan that every layer's calls of the step take."""
+    _want(which, "which", (None,), torch.int32)
+    T, dev, L = which.shape[0], which.device, lib()
+    # (out of range: sg_adapter_plan says so)
+    data = torch.empty((max(1, L.sg_adapter_plan_ints(T, n)),), dtype=torch.int32, device=dev)
+    _run(L.sg_adapter_plan, dev, _at(which), T, n, _at(data))
+    return AdapterPlan(data, T, n)
+
+
+def _adapters(layer: Layer, ad: Adapters, plan: AdapterPlan, T: int):
+    if layer.handle is None:
+        _bad("the layer has been freed")
+    dev = layer.device
+    _want(ad.A, "A", (None, None, layer.in_dims), layer.dtype, dev)
+    n, rank = ad.A.shape[0], ad.A.shape[1]
+    _want(ad.B, "B", (n, layer.out_dims, rank), layer.dtype, dev)
+    _want(ad.scale, "scale", (n,), torch.float32, dev, optional=True)
+    if plan.T != T or plan.n != n:
+        _bad(f"the plan is of {plan.T} tokens and {plan.n} adapters, the call of {T} and {n}")
+    _want(plan.data, "plan", (max(1, lib().sg_adapter_plan_ints(T, n)),), torch.int32, dev)
+    return C.byref(_AdaptersArg(_at(ad.A), _at(ad.B), _at(ad.scale), n, rank))
+
+
+def adapted_all_to_sharded(layer: Layer, x: torch.Tensor, adapters: Adapters, plan: AdapterPlan, gather: bool = False,
+                           swiglu: bool = False, out_dtype=None, out: torch.Tensor | None = None) -> torch.Tensor:
+    """all_to_sharded with each token's adapter beside the layer: x (T, in) ->
+    (P, T, n / P) sharded, or (T, n) gathered (sg_adapted_all_to_sharded)."""
+    dev = layer.device
+    _want(x, "x", (None, layer.in_dims), layer.dtype, dev)
+    T = x.shape[0]
+    ad = _adapters(layer, adapters, plan, T)
+    n = layer.out_dims // 2 if swiglu else layer.out_dims
+    out = _out(out, "out", (T, n) if gather else (layer.P, T, n // layer.P), out_dtype or layer.dtype, dev)
+    L = lib()
+    need = L.sg_adapted_workspace(layer.handle, ad, T)
+    ws = _scratch(need, dev)
+    _run(L.sg_adapted_all_to_sharded, dev, layer.handle, ad, _at(plan.data), _at(x), T, _at(out),
+         OUT_FULL if gather else OUT_SHARDED, EPI_SWIGLU if swiglu else EPI_NONE, _DT[out.dtype], _at(ws), need)
+    return out
+
+
+def adapted_sharded_to_all(layer: Layer, x_partial: torch.Tensor, adapters: Adapters, plan: AdapterPlan, out_dtype=None,
+                           out: torch.Tensor | None = None) -> torch.Tensor:
+    """sharded_to_all with each token's adapter beside the layer: x_partial
+    (P, T, in / P) -> (T, out) (sg_adapted_sharded_to_all)."""
+    dev = layer.device
+    _want(x_partial, "x_partial", (layer.P, None, layer.in_dims // layer.P), layer.dtype, dev)
+    T = x_partial.shape[1]
+    ad = _adapters(layer, adapters, plan, T)
+    out = _out(out, "out", (T, layer.out_dims), out_dtype or layer.dtype, dev)
+    L = lib()
+    need = L.sg_adapted_workspace(layer.handle, ad, T)
+    ws = _scratch(need, dev)
+    _run(L.sg_adapted_sharded_to_all, dev, layer.handle, ad, _at(plan.data), _at(x_partial), T, _at(out), _DT[out.dtype],
+         _at(ws), need)
+    return out
+
+
+def _adapted_backward(fn, layer, x, x_shape, dy, T, adapters, plan, need_dx, need_d, dx_dtype, d_dtype):
+    dev = layer.device
+    if need_d:
+        _want(x, "x", x_shape, layer.dtype, dev)
+    ad = _adapters(layer, adapters, plan, T)
+    dx = _out(None, "dx", x_shape, dx_dtype or layer.dtype, dev) if need_dx else None
+    dA = _out(None, "dA", tuple(adapters.A.shape), d_dtype, dev) if need_d else None
+    dB = _out(None, "dB", tuple(adapters.B.shape), d_dtype, dev) if need_d else None
+    need = lib().sg_adapted_backward_workspace(layer.handle, ad, T)
+    ws = _scratch(need, dev)
+    _run(fn, dev, layer.handle, ad, _at(plan.data), _at(x) if need_d else None, _at(dy), T, _at(dx),
+         _DT.get(dx_dtype or layer.dtype, -1), _at(dA), _at(dB), _DT.get(d_dtype, -1), _at(ws), need)
+    return dx, dA, dB
+
+
+def adapted_all_to_sharded_backward(layer: Layer, x: torch.Tensor | None, dy: torch.Tensor, adapters: Adapters,
+                                    plan: AdapterPlan, need_dx: bool = True, need_d: bool = True, dx_dtype=None,
+                                    d_dtype=torch.float32):
+    """Gradients of adapted_all_to_sharded (no SwiGLU) with the layer frozen: dy
+    (P, T, out / P) -> (dx (T, in), dA, dB); dx, or the adapters', may be skipped (None)."""
+    _want(dy, "dy", (layer.P, None, layer.out_dims // layer.P), layer.dtype, layer.device)
+    T = dy.shape[1]
+    return _adapted_backward(lib().sg_adapted_all_to_sharded_backward, layer, x, (T, layer.in_dims), dy, T, adapters, plan,
+                             need_dx, need_d, dx_dtype, d_dtype)
+
+
+def adapted_sharded_to_all_backward(layer: Layer, x_partial: torch.Tensor | None, dy: torch.Tensor, adapters: Adapters,
+                                    plan: AdapterPlan, need_dx: bool = True, need_d: bool = True, dx_dtype=None,
+                                    d_dtype=torch.float32):
+    """Gradients of adapted_sharded_to_all with the layer frozen: dy (T, out) ->
+    (dx (P, T, in / P), dA, dB); dx, or the adapters', may be skipped (None)."""
+    _want(dy, "dy", (None, layer.out_dims), layer.dtype, layer.device)
+    T = dy.shape[0]
+    return _adapted_backward(lib().sg_adapted_sharded_to_all_backward, layer, x_partial,
+                             (layer.P, T, layer.in_dims // layer.P), dy, T, adapters, plan, need_dx, need_d, dx_dtype,
+                             d_dtype)

@@ -1,0 +1,307 @@
+// C-ABI entry points of the low-rank adapters: validation, workspaces, and the order
+// of the launches beside the shared projection's own call.  Every check runs on the
+// host before any device work.
+#include <stdarg.h>
+#include <stdio.h>
+
+#include "adapters.h"
+
+namespace {
+
+sg_status fail(sg_status st, const char* fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    sg::last_error() = buf;
+    return st;
+}
+
+sg_status launched(hipError_t e, const char* what) {
+    if (e == hipSuccess) return SG_OK;
+    return fail(e == hipErrorOutOfMemory ? SG_ERR_OOM : SG_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
+}
+
+bool known(int dt) { return dt == SG_F32 || dt == SG_BF16 || dt == SG_F16; }
+size_t up256(int64_t n) { return (size_t)((n + 255) / 256 * 256); }
+
+constexpr int64_t kMaxTokens = (int64_t)1 << 25;
+
+struct Geometry {
+    int64_t out, in;
+    int mode, S, P, quantized;
+    sg_dtype dtype;
+    bool column() const { return mode == SG_ALL_TO_SHARDED; }
+    int64_t part() const { return (column() ? out : in) / S / P; }
+};
+
+// the rank-sharded side's activation, (P, T, S part), and the replicated one's
+sg::Pieces sharded(const Geometry& g, int64_t T) {
+    const int64_t ld = g.S * g.part();
+    return {T * ld, ld, g.S, g.P, (int)g.part()};
+}
+sg::Pieces full(int64_t width) { return {0, width, 1, 1, (int)width}; }
+sg::Pieces x_pieces(const Geometry& g, int64_t T) { return g.column() ? full(g.in) : sharded(g, T); }
+sg::Pieces y_pieces(const Geometry& g, int64_t T) { return g.column() ? sharded(g, T) : full(g.out); }
+
+sg::Plan plan_of(const int32_t* plan, int64_t T, int n) {
+    const sg::PlanLayout l = sg::plan_layout(T, n);
+    return {plan + l.offsets, plan + l.rows, plan + l.tiles, (int)T, n, (int)sg::adapter_tiles(T, n),
+            sg::adapter_tile_rows(T, n)};
+}
+
+sg_status check_adapters(const sg_adapters* ad) {
+    if (!ad) return fail(SG_ERR_INVALID_ARG, "adapters is NULL");
+    if (ad->n < 1 || ad->rank < 1) return fail(SG_ERR_INVALID_ARG, "need n >= 1 adapters of rank >= 1 (got %d, %d)", ad->n,
+                                               ad->rank);
+    if (ad->n > sg::kMaxAdapters || ad->rank > sg::kMaxRank)
+        return fail(SG_ERR_UNSUPPORTED, "more than %d adapters, or ranks above %d, are not supported", sg::kMaxAdapters,
+                    sg::kMaxRank);
+    return SG_OK;
+}
+
+sg_status check_call(const sg_layer* l, int mode, const sg_adapters* ad, int64_t T, Geometry* g) {
+    if (!l) return fail(SG_ERR_INVALID_ARG, "layer is NULL");
+    if (sg_status st = sg_layer_info(l, &g->out, &g->in, &g->mode, &g->S, &g->P, &g->dtype, &g->quantized)) return st;
+    if (g->mode != mode)
+        return fail(SG_ERR_INVALID_ARG, mode == SG_ALL_TO_SHARDED ? "layer is sharded-to-all" : "layer is all-to-sharded");
+    if (g->dtype == SG_F32) return fail(SG_ERR_UNSUPPORTED, "adapters stand beside layers of bf16 or fp16 activations");
+    if (sg_status st = check_adapters(ad)) return st;
+    if (T < 0) return fail(SG_ERR_INVALID_ARG, "T must be >= 0");
+    if (T > kMaxTokens) return fail(SG_ERR_UNSUPPORTED, "more than 2^25 tokens are not supported");
+    const int64_t groups = (g->part() + 31) / 32 * g->S * g->P + ((g->column() ? g->in : g->out) + 31) / 32;
+    if (groups > 4 * 65535 || (double)(sg::adapter_tiles(T, ad->n) * 4) * (double)groups >= (double)sg::kMaxBlocks * 4)
+        return fail(SG_ERR_UNSUPPORTED, "more columns or tokens than one launch takes");
+    if (!ad->A || !ad->B) return fail(SG_ERR_INVALID_ARG, "A and B must not be NULL");
+    return SG_OK;
+}
+
+// U = X M^T in `slabs` parts, then used through M2
+struct Half {
+    sg::LowRank p;
+    size_t bytes;
+};
+Half half(const Geometry& g, const sg_adapters* ad, const int32_t* plan, int64_t T, bool of_x) {
+    Half h{};
+    sg::LowRank& p = h.p;
+    p.plan = plan_of(plan, T, ad->n);
+    p.f16 = g.dtype == SG_F16;
+    p.rank = ad->rank;
+    p.rp = (ad->rank + 15) / 16 * 16;
+    p.M = of_x ? ad->A : ad->B;
+    p.transposed = !of_x;
+    p.width = of_x ? g.in : g.out;
+    p.x = of_x ? x_pieces(g, T) : y_pieces(g, T);
+    p.slabs = T ? sg::shrink_slabs(p.plan, p.width, p.rank) : 1;
+    p.slab = T * p.rp;
+    p.scale = ad->scale;
+    h.bytes = up256(p.slab * p.slabs * 4);
+    return h;
+}
+
+size_t base_bytes(const sg_layer* l, const Geometry& g, int64_t T) {
+    return up256(T * g.out * 4) + (g.column() ? 0 : up256((int64_t)sg_sharded_to_all_workspace(l, T)));
+}
+
+sg_status check_ws(const char* what, const void* ws, size_t bytes, size_t need) {
+    if (need && (!ws || bytes < need || (uintptr_t)ws % 16))
+        return fail(SG_ERR_WORKSPACE, "%s needs %zu bytes of 16-byte aligned workspace (got %zu)", what, need,
+                    ws ? bytes : (size_t)0);
+    return SG_OK;
+}
+
+sg_status forward(const char* what, const sg_layer* l, const Geometry& g, const sg_adapters* ad, const int32_t* plan,
+                  const void* x, int64_t T, void* y, int out_layout, int epilogue, sg_dtype y_dtype, void* workspace,
+                  size_t ws_bytes, void* stream) {
+    if (!known(y_dtype)) return fail(SG_ERR_INVALID_ARG, "unknown output dtype %d", (int)y_dtype);
+    if (T == 0) return SG_OK;
+    if (!plan || !x || !y) return fail(SG_ERR_INVALID_ARG, "plan, x and y must not be NULL");
+    if (sg_status st = check_ws(what, workspace, ws_bytes, sg_adapted_workspace(l, ad, T))) return st;
+    hipStream_t s = (hipStream_t)stream;
+    Half u = half(g, ad, plan, T, true);
+    sg::LowRank& p = u.p;
+    p.U = (float*)workspace;
+    p.X = x;
+    sg_status st = launched(sg::launch_shrink(p, s), what);
+    if (st) return st;
+    // the projection's result stays in fp32 until the adapters' part is added, so that y
+    // is rounded once; an fp32 y holds it itself
+    const bool swiglu = epilogue == SG_EPI_SWIGLU, in_y = y_dtype == SG_F32 && !swiglu;
+    char* at = (char*)workspace + u.bytes;
+    float* base = in_y ? (float*)y : (float*)at;
+    at += up256(T * g.out * 4);
+    // (sharded unless y is both gathered and the sum's own place)
+    if (g.column()) {
+        st = sg_all_to_sharded_ex(l, x, SG_IN_FULL, T, base, in_y ? out_layout : SG_OUT_SHARDED, SG_EPI_NONE, SG_F32, stream);
+    } else {
+        st = sg_sharded_to_all_ex(l, x, T, base, SG_OUT_FULL, SG_F32, at, ws_bytes - (size_t)(at - (char*)workspace), stream);
+    }
+    if (st) return st;
+    p.M = ad->B;
+    p.width = g.out;
+    p.x = y_pieces(g, T);
+    p.base = base;
+    p.swiglu = swiglu;
+    p.out = y;
+    p.out_dtype = y_dtype;
+    const int64_t n = g.column() ? (swiglu ? g.out / 2 : g.out) / g.P : g.out;
+    p.out_ld = n;
+    p.out_rank = g.column() ? T * n : 0;
+    if (g.column() && out_layout == SG_OUT_FULL) {
+        p.out_ld = n * g.P;
+        p.out_rank = n;
+        if (in_y) p.x.ld = p.out_ld, p.x.rank = p.out_rank;
+    }
+    return launched(sg::launch_expand(p, s), what);
+}
+
+sg_status backward(const char* what, const sg_layer* l, const Geometry& g, const sg_adapters* ad, const int32_t* plan,
+                   const void* x, const void* dy, int64_t T, void* dx, sg_dtype dx_dtype, void* dA, void* dB,
+                   sg_dtype d_dtype, void* workspace, size_t ws_bytes, void* stream) {
+    if (!dx && !dA && !dB) return fail(SG_ERR_INVALID_ARG, "dx, dA and dB are all NULL");
+    if (dx && !known(dx_dtype)) return fail(SG_ERR_INVALID_ARG, "unknown dx dtype %d", (int)dx_dtype);
+    if ((dA || dB) && !known(d_dtype)) return fail(SG_ERR_INVALID_ARG, "unknown gradient dtype %d", (int)d_dtype);
+    if (dx && g.quantized) return fail(SG_ERR_UNSUPPORTED, "the input gradient is implemented for dense layers only");
+    if (T == 0 && !dA && !dB) return SG_OK;
+    if (!plan || (T && !dy)) return fail(SG_ERR_INVALID_ARG, "plan and dy must not be NULL");
+    if (T && (dA || dB) && !x) return fail(SG_ERR_INVALID_ARG, "dA and dB need x");
+    if (sg_status st = check_ws(what, workspace, ws_bytes, sg_adapted_backward_workspace(l, ad, T))) return st;
+    hipStream_t s = (hipStream_t)stream;
+    Half u = half(g, ad, plan, T, true), v = half(g, ad, plan, T, false);
+    u.p.U = (float*)workspace;
+    u.p.X = x;
+    v.p.U = (float*)((char*)workspace + u.bytes);
+    v.p.X = dy;
+    sg_status st = SG_OK;
+    if (T && (dx || dA)) {
+        st = launched(sg::launch_shrink(v.p, s), what);
+        if (!st) st = launched(sg::launch_finish(v.p, s), what);
+        v.p.slabs = 1;
+    }
+    if (!st && T && dB) {
+        st = launched(sg::launch_shrink(u.p, s), what);
+        if (!st) st = launched(sg::launch_finish(u.p, s), what);
+        u.p.slabs = 1;
+    }
+    if (!st && dA) {
+        sg::LowRank p = v.p;
+        p.M = ad->A;
+        p.transposed = 0;
+        p.width = g.in;
+        p.X = x;
+        p.x = x_pieces(g, T);
+        p.out = dA;
+        p.out_dtype = d_dtype;
+        st = launched(sg::launch_grad(p, s), what);
+    }
+    if (!st && dB) {
+        sg::LowRank p = u.p;
+        p.M = ad->B;
+        p.transposed = 1;
+        p.width = g.out;
+        p.X = dy;
+        p.x = y_pieces(g, T);
+        p.out = dB;
+        p.out_dtype = d_dtype;
+        st = launched(sg::launch_grad(p, s), what);
+    }
+    if (!st && T && dx) {
+        // as forward: the frozen projection's part in fp32, rounded once with the adapters'
+        float* base = dx_dtype == SG_F32 ? (float*)dx : (float*)((char*)workspace + u.bytes + v.bytes);
+        st = g.column() ? sg_all_to_sharded_backward(l, nullptr, dy, T, base, SG_F32, nullptr, SG_F32, nullptr, 0, stream)
+                        : sg_sharded_to_all_backward(l, nullptr, dy, T, base, SG_F32, nullptr, SG_F32, nullptr, 0, stream);
+        if (st) return st;
+        sg::LowRank p = v.p;
+        p.M = ad->A;
+        p.transposed = 1;  // (rank, in), its columns the output's
+        p.width = g.in;
+        p.x = x_pieces(g, T);
+        p.base = base;
+        p.out = dx;
+        p.out_dtype = dx_dtype;
+        p.out_ld = p.x.ld;
+        p.out_rank = p.x.rank;
+        st = launched(sg::launch_expand(p, s), what);
+    }
+    return st;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t sg_adapter_plan_ints(int64_t T, int n) {
+    if (T < 0 || T > kMaxTokens || n < 1 || n > sg::kMaxAdapters) return 0;
+    return (size_t)sg::plan_layout(T, n).ints;
+}
+
+sg_status sg_adapter_plan(const int32_t* which, int64_t T, int n, int32_t* plan, void* stream) {
+    sg::last_error().clear();
+    if (T < 0 || n < 1) return fail(SG_ERR_INVALID_ARG, "need T >= 0 and n >= 1");
+    if (T > kMaxTokens || n > sg::kMaxAdapters)
+        return fail(SG_ERR_UNSUPPORTED, "more than 2^25 tokens or %d adapters are not supported", sg::kMaxAdapters);
+    if (!plan || (T && !which)) return fail(SG_ERR_INVALID_ARG, "which and plan must not be NULL");
+    return launched(sg::launch_adapter_plan(which, T, n, plan, (hipStream_t)stream), "sg_adapter_plan");
+}
+
+size_t sg_adapted_workspace(const sg_layer* l, const sg_adapters* ad, int64_t T) {
+    Geometry g;
+    if (!l || !ad || T <= 0 || check_adapters(ad) || sg_layer_info(l, &g.out, &g.in, &g.mode, &g.S, &g.P, &g.dtype, &g.quantized))
+        return 0;
+    return half(g, ad, nullptr, T, true).bytes + base_bytes(l, g, T);
+}
+
+sg_status sg_adapted_all_to_sharded(const sg_layer* l, const sg_adapters* ad, const int32_t* plan, const void* x, int64_t T,
+                                    void* y, int out_layout, int epilogue, sg_dtype y_dtype, void* workspace,
+                                    size_t ws_bytes, void* stream) {
+    sg::last_error().clear();
+    Geometry g;
+    if (sg_status st = check_call(l, SG_ALL_TO_SHARDED, ad, T, &g)) return st;
+    if (out_layout != SG_OUT_FULL && out_layout != SG_OUT_SHARDED)
+        return fail(SG_ERR_INVALID_ARG, "unknown output layout %d", out_layout);
+    if (epilogue != SG_EPI_NONE && epilogue != SG_EPI_SWIGLU) return fail(SG_ERR_INVALID_ARG, "unknown epilogue %d", epilogue);
+    if (epilogue == SG_EPI_SWIGLU && g.S != 2)
+        return fail(SG_ERR_INVALID_ARG, "the SwiGLU epilogue needs a layer with segments = 2");
+    return forward("sg_adapted_all_to_sharded", l, g, ad, plan, x, T, y, out_layout, epilogue, y_dtype, workspace, ws_bytes,
+                   stream);
+}
+
+sg_status sg_adapted_sharded_to_all(const sg_layer* l, const sg_adapters* ad, const int32_t* plan, const void* x_partial,
+                                    int64_t T, void* y, sg_dtype y_dtype, void* workspace, size_t ws_bytes, void* stream) {
+    sg::last_error().clear();
+    Geometry g;
+    if (sg_status st = check_call(l, SG_SHARDED_TO_ALL, ad, T, &g)) return st;
+    return forward("sg_adapted_sharded_to_all", l, g, ad, plan, x_partial, T, y, SG_OUT_FULL, SG_EPI_NONE, y_dtype,
+                   workspace, ws_bytes, stream);
+}
+
+size_t sg_adapted_backward_workspace(const sg_layer* l, const sg_adapters* ad, int64_t T) {
+    Geometry g;
+    if (!l || !ad || T <= 0 || check_adapters(ad) || sg_layer_info(l, &g.out, &g.in, &g.mode, &g.S, &g.P, &g.dtype, &g.quantized))
+        return 0;
+    return half(g, ad, nullptr, T, true).bytes + half(g, ad, nullptr, T, false).bytes + up256(T * g.in * 4);
+}
+
+sg_status sg_adapted_all_to_sharded_backward(const sg_layer* l, const sg_adapters* ad, const int32_t* plan, const void* x,
+                                             const void* dy, int64_t T, void* dx, sg_dtype dx_dtype, void* dA, void* dB,
+                                             sg_dtype d_dtype, void* workspace, size_t ws_bytes, void* stream) {
+    sg::last_error().clear();
+    Geometry g;
+    if (sg_status st = check_call(l, SG_ALL_TO_SHARDED, ad, T, &g)) return st;
+    return backward("sg_adapted_all_to_sharded_backward", l, g, ad, plan, x, dy, T, dx, dx_dtype, dA, dB, d_dtype, workspace,
+                    ws_bytes, stream);
+}
+
+sg_status sg_adapted_sharded_to_all_backward(const sg_layer* l, const sg_adapters* ad, const int32_t* plan,
+                                             const void* x_partial, const void* dy, int64_t T, void* dx_partial,
+                                             sg_dtype dx_dtype, void* dA, void* dB, sg_dtype d_dtype, void* workspace,
+                                             size_t ws_bytes, void* stream) {
+    sg::last_error().clear();
+    Geometry g;
+    if (sg_status st = check_call(l, SG_SHARDED_TO_ALL, ad, T, &g)) return st;
+    return backward("sg_adapted_sharded_to_all_backward", l, g, ad, plan, x_partial, dy, T, dx_partial, dx_dtype, dA, dB,
+                    d_dtype, workspace, ws_bytes, stream);
+}
+
+}  // extern "C"

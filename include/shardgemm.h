@@ -535,18 +535,16 @@ size_t sg_experts_gated_workspace(const sg_experts* layer, int64_t R);
  *   down     bf16 or fp16, sharded-to-all, segments = 1; f = in_dims / P.
  *   dy       (R, out_dims) of the layer's dtype.
  *   dgu      (P, R, 2 f) rows [gate; up]; h (P, R, f), both of the layer's dtype;
- *            h may be NULL.
- *   workspace as above, sg_experts_gated_backward_workspace(down, R) bytes. */
+ *            h may be NULL. */
 sg_status sg_experts_gated_backward(const sg_experts* down, const void* dy, const uint8_t* codes, const uint8_t* scales,
-                                    const int32_t* offsets, int64_t R, void* dgu, void* h, void* workspace,
-                                    size_t ws_bytes, void* stream);
-size_t sg_experts_gated_backward_workspace(const sg_experts* down, int64_t R);
+                                    const int32_t* offsets, int64_t R, void* dgu, void* h, void* stream);
 
 /* The whole block, forward: y[m] = sum over r of h_r[m] W_down,r^T for every grouped
  * row, and what the backward pass needs: x and the gate|up rows in MX FP8 (one byte
  * and 1/32 a value; h is not kept).  A dense block is one of E == 1 with offsets NULL.
- * Bitwise the chain of sg_quantize_mxfp8, sg_experts_gated and
- * sg_experts_sharded_to_all.
+ * The chain of sg_quantize_mxfp8, sg_experts_gated and sg_experts_sharded_to_all,
+ * whose sums may be split over the inputs where the rows are few (what is kept is
+ * theirs bitwise, y up to fp32's last steps).
  *   gate_up, down a pair as for sg_moe_mlp, bf16 or fp16.
  *   y        (R, out_dims of down) of y_dtype.
  *   x_codes  (T, in_dims), x_scales (T, ceil(in_dims / 32)); gu_codes, gu_scales as
@@ -561,8 +559,8 @@ size_t sg_gated_mlp_workspace(const sg_experts* gate_up, const sg_experts* down,
 /* Its gradients, from what it kept: dx (R, in_dims), one row for every grouped row;
  * dw_gate_up (E, P, 2 f, in_dims); dw_down (E, P, out_dims, f), of dw_dtype, laid out
  * as the layers' shards.  Any may be NULL (not all).  x_codes and x_scales are needed
- * for dw_gate_up only.  Bitwise the chain of sg_experts_gated_backward,
- * sg_dequantize_mxfp8 and the two layers' backward calls.
+ * for dw_gate_up only.  The chain of sg_experts_gated_backward, sg_dequantize_mxfp8
+ * and the two layers' backward calls (weight gradients bitwise, dx as y above).
  *   workspace sg_gated_mlp_backward_workspace(...) bytes, 16-byte aligned. */
 sg_status sg_gated_mlp_backward(const sg_experts* gate_up, const sg_experts* down, const uint8_t* x_codes,
                                 const uint8_t* x_scales, int64_t T, const uint8_t* gu_codes, const uint8_t* gu_scales,

@@ -133,8 +133,7 @@ def lib():
             "sg_dequantize_mxfp8": ([P, P, I64, I64, P, I, P], I),
             "sg_experts_gated": ([P, P, I64, I64, P, P, I, I64, P, P, P, P, SZ, P], I),
             "sg_experts_gated_workspace": ([P, I64], SZ),
-            "sg_experts_gated_backward": ([P, P, P, P, P, I64, P, P, P, SZ, P], I),
-            "sg_experts_gated_backward_workspace": ([P, I64], SZ),
+            "sg_experts_gated_backward": ([P, P, P, P, P, I64, P, P, P], I),
             "sg_gated_mlp": ([P, P, P, I64, I64, P, P, I, I64, P, I, P, P, P, P, P, SZ, P], I),
             "sg_gated_mlp_workspace": ([P, P, I64], SZ),
             "sg_gated_mlp_backward": ([P, P, P, P, I64, P, P, P, P, P, I, I64, P, I, P, P, I, P, SZ, P], I),
@@ -959,11 +958,8 @@ def experts_gated_backward(down: Experts, dy: torch.Tensor, codes: torch.Tensor,
     _want_kept(codes, scales, down.P, R, f, dev)
     dgu = torch.empty((down.P, R, 2 * f), dtype=down.dtype, device=dev)
     h = torch.empty((down.P, R, f), dtype=down.dtype, device=dev) if need_h else None
-    L = lib()
-    need = L.sg_experts_gated_backward_workspace(down.handle, R)
-    ws = _scratch(need, dev)
-    _run(L.sg_experts_gated_backward, dev, down.handle, _at(dy), _at(codes), _at(scales), _at(offsets), R, _at(dgu),
-         _at(h), _at(ws), need)
+    _run(lib().sg_experts_gated_backward, dev, down.handle, _at(dy), _at(codes), _at(scales), _at(offsets), R, _at(dgu),
+         _at(h))
     return dgu, h
 
 

@@ -10,7 +10,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libshardgemm.so")
 SOURCES = ["api.hip", "generic.hip", "tile.hip", "skinny.hip", "q4.hip", "q4_wide.hip", "q4s.hip", "layout.hip",
-           "tile_dma.hip", "backward.hip", "q4tile.hip", "experts_api.hip", "experts.hip", "experts_dw.hip", "route.hip",
+           "tile_dma.hip", "backward.hip", "q4tile.hip", "experts_api.hip", "experts.hip", "experts_dw.hip", "experts_gated.hip", "route.hip",
            "mxfp4.hip", "mxfp8.hip",
            "adapters_api.hip", "adapters.hip", "adapters_expand.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -43,7 +43,8 @@ def _objdir():
 
 
 HEADERS = [os.path.join(CSRC, "internal.h"), os.path.join(CSRC, "q4_stream.h"), os.path.join(CSRC, "experts.h"),
-           os.path.join(CSRC, "adapters.h"),
+           os.path.join(CSRC, "grouped_tile.h"),
+           os.path.join(CSRC, "gated.h"), os.path.join(CSRC, "adapters.h"),
            os.path.join(os.path.dirname(HERE), "include", "shardgemm.h")]
 
 

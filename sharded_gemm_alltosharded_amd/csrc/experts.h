@@ -87,6 +87,8 @@ struct GroupedDw {
     int kdiv, T, R, E, P, O, I;
     uint32_t kmul;  // set by the launch
     int kshift;
+    int xw;         // columns of X that may be read: I, or more where its rows are padded
+    int of, ofp;    // pieces of the O columns of G: of of each ofp are the layer's (ofp 0: all)
     void* out;
     int out_dtype;
 };
@@ -138,13 +140,11 @@ __host__ __device__ inline int64_t mx8_blocks(int64_t n) { return (n + 31) / 32;
 hipError_t launch_quantize_mxfp8(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ld, uint8_t* codes,
                                  uint8_t* scales, hipStream_t s);
 hipError_t launch_dequantize_mxfp8(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, void* x,
-                                   int dtype, hipStream_t s);
-// the gated block where its products' epilogues do not do it: gate|up rows to h and
-// what is kept, and dh with what was kept to the gradient of the gate|up rows (and h)
-hipError_t launch_gated_keep(const float* gu, int64_t P, int64_t R, int64_t f, const int32_t* offsets, int E, void* h,
-                             int f16, uint8_t* codes, uint8_t* scales, hipStream_t s);
-hipError_t launch_gated_grad(const float* dh, const uint8_t* codes, const uint8_t* scales, int64_t P, int64_t R,
-                             int64_t f, const int32_t* offsets, int E, void* dgu, void* h, int f16, hipStream_t s);
+                                   int64_t ld, int dtype, hipStream_t s);
+// gate|up rows to h (rows of fp >= f columns, those behind f zeros) and what is kept,
+// where the product's epilogue does not do it
+hipError_t launch_gated_keep(const float* gu, int64_t P, int64_t R, int64_t f, int64_t fp, const int32_t* offsets, int E,
+                             void* h, int f16, uint8_t* codes, uint8_t* scales, hipStream_t s);
 
 #ifdef __HIPCC__
 #define ALWAYS_INLINE __attribute__((always_inline))
@@ -288,10 +288,15 @@ __device__ __forceinline__ void mx8_values(uint32_t w, int s, float& a, float& b
     c = s == 255 ? nan : ldexpf(hi[0], s - 127), d = s == 255 ? nan : ldexpf(hi[1], s - 127);
 }
 
-// h = g s u with s = 1 / (1 + e^-g), and its gradient: dg = dh u s (1 + g (1 - s)),
-// du = dh g s.  e^-|g| cannot overflow, and s keeps what it has far below zero.
+// h = g s u with s = 1 / (1 + e^-g), and its gradient, for 16-bit results:
+// dg = dh u s (1 + g (1 - s)), du = dh g s.  s from e^-|g|, which cannot overflow, on
+// the hardware's exponential: the square of 2^(t / 2), t = -|g| log2 e rounded, so that
+// it is not flushed before it leaves fp32's subnormals, times 1 + r ln 2 for the r that
+// t's rounding left.  Off by 2^-19 of itself at most (grouped_tile.h, swiglu4).
 __device__ __forceinline__ void swiglu_grad(float g, float u, float dh, float& dg, float& du, float& h) {
-    const float e = expf(-fabsf(g)), s = (g < 0.f ? e : 1.0f) / (1.0f + e), a = g * s;
+    const float z = fabsf(g), t = -1.44269504f * z, half = __builtin_amdgcn_exp2f(0.5f * t), e2 = half * half;
+    const float e = fmaf(e2 * fmaf(-1.44269504f, z, -t), 0.693147181f, e2);
+    const float s = (g < 0.f ? e : 1.0f) * __builtin_amdgcn_rcpf(1.0f + e), a = g * s;
     dg = dh * u * s * (1.0f + g * (1.0f - s));
     du = dh * a;
     h = a * u;

@@ -6,7 +6,7 @@
 
 #include <new>
 
-#include "experts.h"
+#include "gated.h"
 
 struct sg_experts {
     sg::ExpertsLayout l;
@@ -290,6 +290,80 @@ sg::Grouped row_dx(const sg_experts* x, const void* dy, const int32_t* offsets, 
     return p;
 }
 
+// dx = the ranks' sum of dy_r W_r of an all-to-sharded layer; dy (P, R, S, fp), each
+// piece's columns behind the layer's f zeros
+sg::Grouped column_dx(const sg_experts* x, const void* dy, int64_t fp, const int32_t* offsets, int64_t R, void* dx,
+                      sg_dtype dx_dtype) {
+    const sg::ExpertsLayout& l = x->l;
+    sg::Grouped p{};
+    p.mode = mode_of(x, nullptr);
+    p.A = dy;
+    p.lda = fp * l.S;
+    p.a_rank = R * fp * l.S;
+    p.a_pieces = l.S;
+    p.nseg = l.P * l.S;
+    p.kl = (int)fp;
+    p.kpad = (int)(l.bps * 16);
+    p.offsets = offsets;
+    p.kdiv = 1;
+    p.T = p.R = (int)R;
+    set_weights(p, x);
+    p.transposed = 1;
+    p.nout = p.bps = (int)(l.steps * 2);
+    p.f = (int)l.in;
+    p.S = 1;
+    p.ldo = l.in;
+    set_out(p, dx, dx_dtype);
+    return p;
+}
+
+// the weight gradients of the two layers
+sg::GroupedDw column_dw(const sg_experts* x, const void* a, int64_t T, int64_t ldx, const void* dy, const int32_t* offsets,
+                        const int32_t* rows, int k, int64_t R, void* dw, sg_dtype dw_dtype) {
+    const sg::ExpertsLayout& l = x->l;
+    const int64_t n = l.f * l.S;  // columns of a rank
+    sg::GroupedDw p{};
+    p.f16 = x->dtype == SG_F16;
+    p.G = dy;
+    p.ldg = n;
+    p.g_rank = R * n;
+    p.X = a;
+    p.ldx = ldx;
+    p.offsets = offsets;
+    p.rows = rows;
+    p.kdiv = rows ? k : 1;
+    p.T = (int)T;
+    p.R = (int)R;
+    p.E = (int)l.E;
+    p.P = l.P;
+    p.O = (int)n;
+    p.I = (int)l.in;
+    p.out = dw;
+    p.out_dtype = dw_dtype;
+    return p;
+}
+sg::GroupedDw row_dw(const sg_experts* x, const void* h, const void* dy, const int32_t* offsets, int64_t R, void* dw,
+                     sg_dtype dw_dtype) {
+    const sg::ExpertsLayout& l = x->l;
+    sg::GroupedDw p{};
+    p.f16 = x->dtype == SG_F16;
+    p.G = dy;
+    p.ldg = l.out;
+    p.X = h;
+    p.ldx = l.kl;
+    p.x_rank = R * l.kl;
+    p.offsets = offsets;
+    p.kdiv = 1;
+    p.T = p.R = (int)R;
+    p.E = (int)l.E;
+    p.P = l.P;
+    p.O = (int)l.out;
+    p.I = (int)l.kl;
+    p.out = dw;
+    p.out_dtype = dw_dtype;
+    return p;
+}
+
 // activations of a call on an MXFP4 layer
 sg_status check_acts(const sg_experts* x, const void* a, const uint8_t* scales, int64_t ldx) {
     if (scales && !x->mx) return fail(SG_ERR_INVALID_ARG, "MXFP4 activations need an MXFP4 layer");
@@ -511,51 +585,13 @@ sg_status sg_experts_all_to_sharded_backward(const sg_experts* x, const void* a,
     if (!st && dw) st = check_bytes(T, ldx, 4);
     if (st) return st;
     const sg::ExpertsLayout& l = x->l;
-    const int64_t n = l.f * l.S;  // columns of a rank
     hipStream_t s = (hipStream_t)stream;
-    if (dx && R > 0) {
-        sg::Grouped p{};
-        p.mode = mode_of(x, nullptr);
-        p.A = dy;
-        p.lda = n;
-        p.a_rank = R * n;
-        p.a_pieces = l.S;
-        p.nseg = l.P * l.S;
-        p.kl = (int)l.f;
-        p.kpad = (int)(l.bps * 16);
-        p.offsets = offsets;
-        p.kdiv = 1;
-        p.T = p.R = (int)R;
-        set_weights(p, x);
-        p.transposed = 1;
-        p.nout = p.bps = (int)(l.steps * 2);
-        p.f = (int)l.in;
-        p.S = 1;
-        p.ldo = l.in;
-        set_out(p, dx, dx_dtype);
-        st = launched(sg::launch_grouped(p, s), "sg_experts_all_to_sharded_backward dx");
-    }
-    if (!st && dw) {
-        sg::GroupedDw p{};
-        p.f16 = x->dtype == SG_F16;
-        p.G = dy;
-        p.ldg = n;
-        p.g_rank = R * n;
-        p.X = a;
-        p.ldx = ldx;
-        p.offsets = offsets;
-        p.rows = rows;
-        p.kdiv = rows ? k : 1;
-        p.T = (int)T;
-        p.R = (int)R;
-        p.E = (int)l.E;
-        p.P = l.P;
-        p.O = (int)n;
-        p.I = (int)l.in;
-        p.out = dw;
-        p.out_dtype = dw_dtype;
-        st = launched(sg::launch_grouped_dw(p, s), "sg_experts_all_to_sharded_backward dw");
-    }
+    if (dx && R > 0)
+        st = launched(sg::launch_grouped(column_dx(x, dy, l.f, offsets, R, dx, dx_dtype), s),
+                      "sg_experts_all_to_sharded_backward dx");
+    if (!st && dw)
+        st = launched(sg::launch_grouped_dw(column_dw(x, a, T, ldx, dy, offsets, rows, k, R, dw, dw_dtype), s),
+                      "sg_experts_all_to_sharded_backward dw");
     return st;
 }
 
@@ -569,30 +605,13 @@ sg_status sg_experts_sharded_to_all_backward(const sg_experts* x, const void* h,
     if (!st) st = check_bytes(R, x->l.out, 4);
     if (!st && dw) st = check_bytes(R, x->l.kl, 4);
     if (st) return st;
-    const sg::ExpertsLayout& l = x->l;
     hipStream_t s = (hipStream_t)stream;
     if (dh && R > 0)
         st = launched(sg::launch_grouped(row_dx(x, dy, offsets, R, dh, dh_dtype), s),
                       "sg_experts_sharded_to_all_backward dx");
-    if (!st && dw) {
-        sg::GroupedDw p{};
-        p.f16 = x->dtype == SG_F16;
-        p.G = dy;
-        p.ldg = l.out;
-        p.X = h;
-        p.ldx = l.kl;
-        p.x_rank = R * l.kl;
-        p.offsets = offsets;
-        p.kdiv = 1;
-        p.T = p.R = (int)R;
-        p.E = (int)l.E;
-        p.P = l.P;
-        p.O = (int)l.out;
-        p.I = (int)l.kl;
-        p.out = dw;
-        p.out_dtype = dw_dtype;
-        st = launched(sg::launch_grouped_dw(p, s), "sg_experts_sharded_to_all_backward dw");
-    }
+    if (!st && dw)
+        st = launched(sg::launch_grouped_dw(row_dw(x, h, dy, offsets, R, dw, dw_dtype), s),
+                      "sg_experts_sharded_to_all_backward dw");
     return st;
 }
 
@@ -763,7 +782,7 @@ sg_status sg_dequantize_mxfp8(const uint8_t* codes, const uint8_t* scales, int64
     if (sg_status st = check_mx8(dtype, rows, cols)) return st;
     if (rows == 0 || cols == 0) return SG_OK;
     if (!x || !codes || !scales) return fail(SG_ERR_INVALID_ARG, "x, codes and scales must not be NULL");
-    return launched(sg::launch_dequantize_mxfp8(codes, scales, rows, cols, x, dtype, (hipStream_t)stream),
+    return launched(sg::launch_dequantize_mxfp8(codes, scales, rows, cols, x, cols, dtype, (hipStream_t)stream),
                     "sg_dequantize_mxfp8");
 }
 
@@ -792,9 +811,43 @@ static sg_status check_gated_rows(int64_t P, int64_t R, int64_t f) {
     return SG_OK;
 }
 
+static bool fused(const sg_experts* g) { return sg::gated_fits(g->l.P, g->l.bps); }
+
 size_t sg_experts_gated_workspace(const sg_experts* g, int64_t R) {
     if (!g || g->l.mode != SG_ALL_TO_SHARDED || g->l.S != 2 || g->mx || R <= 0 || R > kMaxRows) return 0;
-    return (size_t)up(R * g->l.out * 4, 256);
+    return fused(g) ? 0 : (size_t)up(R * g->l.out * 4, 256);
+}
+
+// h's rows are ldh >= f columns apart, zeros behind f
+static sg_status gated(const sg_experts* g, const void* x, int64_t T, int64_t ldx, const int32_t* offsets,
+                       const int32_t* rows, int k, int64_t R, void* h, int64_t ldh, uint8_t* codes, uint8_t* scales,
+                       void* workspace, hipStream_t s) {
+    if (fused(g)) {
+        sg::Gated kept{};
+        kept.codes = codes;
+        kept.scales = scales;
+        kept.f = (int)g->l.f;
+        return launched(sg::launch_gated(column(g, x, nullptr, T, ldx, offsets, rows, k, R, h, 1, ldh, g->dtype), kept, s),
+                        "gated block");
+    }
+    sg_status st = launched(sg::launch_grouped(column(g, x, nullptr, T, ldx, offsets, rows, k, R, workspace, 0, 0, SG_F32), s),
+                            "gated block");
+    if (!st) st = launched(sg::launch_gated_keep((const float*)workspace, g->l.P, R, g->l.f, ldh, offsets, (int)g->l.E, h,
+                                                 g->dtype == SG_F16, codes, scales, s), "gated block");
+    return st;
+}
+
+// dgu's pieces and h's rows are fp >= f columns, zeros behind f
+static sg_status gated_backward(const sg_experts* d, const void* dy, const uint8_t* codes, const uint8_t* scales,
+                                const int32_t* offsets, int64_t R, void* dgu, void* h, int64_t fp, hipStream_t s) {
+    sg::Gated kept{};
+    kept.codes = (uint8_t*)codes;
+    kept.scales = (uint8_t*)scales;
+    kept.f = (int)d->l.kl;
+    kept.h = h;
+    sg::Grouped p = row_dx(d, dy, offsets, R, dgu, d->dtype);
+    p.f = (int)fp;
+    return launched(sg::launch_gated_backward(p, kept, s), "gated block");
 }
 
 sg_status sg_experts_gated(const sg_experts* g, const void* x, int64_t T, int64_t ldx, const int32_t* offsets,
@@ -811,22 +864,11 @@ sg_status sg_experts_gated(const sg_experts* g, const void* x, int64_t T, int64_
     if (T == 0) return fail(SG_ERR_INVALID_ARG, "%lld rows of no tokens", (long long)R);
     if (!x || !h || !codes || !scales) return fail(SG_ERR_INVALID_ARG, "x, h, codes and scales must not be NULL");
     if ((st = check_ws("sg_experts_gated", workspace, ws_bytes, sg_experts_gated_workspace(g, R)))) return st;
-    hipStream_t s = (hipStream_t)stream;
-    st = launched(sg::launch_grouped(column(g, x, nullptr, T, ldx, offsets, rows, k, R, workspace, 0, 0, SG_F32), s),
-                  "sg_experts_gated");
-    if (!st) st = launched(sg::launch_gated_keep((const float*)workspace, g->l.P, R, g->l.f, offsets, (int)g->l.E, h,
-                                                 g->dtype == SG_F16, codes, scales, s), "sg_experts_gated");
-    return st;
-}
-
-size_t sg_experts_gated_backward_workspace(const sg_experts* d, int64_t R) {
-    if (!d || d->l.mode != SG_SHARDED_TO_ALL || d->l.S != 1 || d->mx || R <= 0 || R > kMaxRows) return 0;
-    return (size_t)up(R * d->l.in * 4, 256);
+    return gated(g, x, T, ldx, offsets, rows, k, R, h, g->l.f, codes, scales, workspace, (hipStream_t)stream);
 }
 
 sg_status sg_experts_gated_backward(const sg_experts* d, const void* dy, const uint8_t* codes, const uint8_t* scales,
-                                    const int32_t* offsets, int64_t R, void* dgu, void* h, void* workspace,
-                                    size_t ws_bytes, void* stream) {
+                                    const int32_t* offsets, int64_t R, void* dgu, void* h, void* stream) {
     sg::last_error().clear();
     sg_status st = check_down(d);
     if (!st) st = check_rows(d, offsets, R);
@@ -835,19 +877,26 @@ sg_status sg_experts_gated_backward(const sg_experts* d, const void* dy, const u
     if (st) return st;
     if (R == 0) return SG_OK;
     if (!dy || !codes || !scales || !dgu) return fail(SG_ERR_INVALID_ARG, "dy, codes, scales and dgu must not be NULL");
-    if ((st = check_ws("sg_experts_gated_backward", workspace, ws_bytes, sg_experts_gated_backward_workspace(d, R))))
-        return st;
-    hipStream_t s = (hipStream_t)stream;
-    st = launched(sg::launch_grouped(row_dx(d, dy, offsets, R, workspace, SG_F32), s), "sg_experts_gated_backward");
-    if (!st) st = launched(sg::launch_gated_grad((const float*)workspace, codes, scales, d->l.P, R, d->l.kl, offsets,
-                                                 (int)d->l.E, dgu, h, d->dtype == SG_F16, s),
-                           "sg_experts_gated_backward");
-    return st;
+    return gated_backward(d, dy, codes, scales, offsets, R, dgu, h, d->l.kl, (hipStream_t)stream);
+}
+
+// A product of few rows and few tiles is split over its inputs (up to eight rows of an
+// expert it streams the weights, and splits them there)
+static int splits_of(const sg::Grouped& p) { return p.R > (int64_t)8 * p.E ? sg::grouped_splits(p) : 1; }
+static size_t split_bytes(const sg::Grouped& p) {
+    const int n = splits_of(p);
+    return n > 1 ? (size_t)up((int64_t)n * p.R * p.ldo * 4, 256) : 0;
+}
+static sg_status product(const sg::Grouped& p, void* workspace, const char* what, hipStream_t s) {
+    const int n = splits_of(p);
+    return launched(n > 1 ? sg::launch_grouped_split(p, n, (float*)workspace, s) : sg::launch_grouped(p, s), what);
 }
 
 size_t sg_gated_mlp_workspace(const sg_experts* g, const sg_experts* d, int64_t R) {
     if (check_pair(g, d) || R <= 0 || R > kMaxRows) return 0;
-    return (size_t)up(R * d->l.in * 2, 256) + sg_experts_gated_workspace(g, R);
+    const size_t a = sg_experts_gated_workspace(g, R);
+    const size_t b = split_bytes(row(d, nullptr, nullptr, h_stride(g), nullptr, R, nullptr, SG_F32));
+    return (size_t)up(R * g->l.P * h_stride(g) * 2, 256) + (a > b ? a : b);
 }
 
 sg_status sg_gated_mlp(const sg_experts* g, const sg_experts* d, const void* x, int64_t T, int64_t ldx,
@@ -861,7 +910,7 @@ sg_status sg_gated_mlp(const sg_experts* g, const sg_experts* d, const void* x, 
     if (!st) st = check_rows(g, offsets, R);
     if (!st) st = check_gather(T, ldx, g->l.in, rows, k, R);
     if (!st) st = check_bytes(T, ldx, 4);
-    if (!st) st = check_bytes(R, d->l.kl, 4);
+    if (!st) st = check_bytes(R, h_stride(g), 4);
     if (!st) st = check_gated_rows(g->l.P, R, g->l.f);
     if (!st) st = check_mx8(g->dtype, T, g->l.in);
     if (st) return st;
@@ -871,19 +920,23 @@ sg_status sg_gated_mlp(const sg_experts* g, const sg_experts* d, const void* x, 
     if (R > 0 && (!y || !gu_codes || !gu_scales))
         return fail(SG_ERR_INVALID_ARG, "y, gu_codes and gu_scales must not be NULL");
     if ((st = check_ws("sg_gated_mlp", workspace, ws_bytes, sg_gated_mlp_workspace(g, d, R)))) return st;
+    hipStream_t s = (hipStream_t)stream;
+    const int64_t ldh = h_stride(g);
+    if (T) st = launched(sg::launch_quantize_mxfp8(x, g->dtype, T, g->l.in, ldx, x_codes, x_scales, s), "sg_gated_mlp");
+    if (st || R == 0) return st;
     // h in the layers' 16 bits, as in sg_moe_mlp
-    const size_t hb = (size_t)up(R * d->l.in * 2, 256);
-    st = sg_quantize_mxfp8(x, g->dtype, T, g->l.in, ldx, x_codes, x_scales, stream);
-    if (!st && R) st = sg_experts_gated(g, x, T, ldx, offsets, rows, k, R, workspace, gu_codes, gu_scales,
-                                        (char*)workspace + hb, ws_bytes - hb, stream);
-    if (!st) st = sg_experts_sharded_to_all(d, workspace, nullptr, offsets, R, y, y_dtype, stream);
+    void* rest = (char*)workspace + up(R * g->l.P * ldh * 2, 256);
+    st = gated(g, x, T, ldx, offsets, rows, k, R, workspace, ldh, gu_codes, gu_scales, rest, s);
+    if (!st) st = product(row(d, workspace, nullptr, ldh, offsets, R, y, y_dtype), rest, "sg_gated_mlp down", s);
     return st;
 }
 
+// dgu (P, R, 2, fp), h (P, R, fp), x in 16 bits, and a split dx's parts
 size_t sg_gated_mlp_backward_workspace(const sg_experts* g, const sg_experts* d, int64_t T, int64_t R) {
     if (check_pair(g, d) || R <= 0 || R > kMaxRows || T < 0 || T > kMaxRows) return 0;
-    return (size_t)up(R * g->l.out * 2, 256) + (size_t)up(R * d->l.in * 2, 256) + (size_t)up(T * g->l.in * 2, 256) +
-           sg_experts_gated_backward_workspace(d, R);
+    const int64_t fp = h_stride(g), n = R * g->l.P * fp * 2;
+    return (size_t)up(2 * n, 256) + (size_t)up(n, 256) + (size_t)up(T * up(g->l.in, 8) * 2, 256) +
+           split_bytes(column_dx(g, nullptr, fp, nullptr, R, nullptr, SG_F32));
 }
 
 sg_status sg_gated_mlp_backward(const sg_experts* g, const sg_experts* d, const uint8_t* x_codes,
@@ -895,11 +948,12 @@ sg_status sg_gated_mlp_backward(const sg_experts* g, const sg_experts* d, const 
     sg_status st = check_pair(g, d);
     if (!st) st = check_gate_up(g);
     if (!st) st = check_down(d);
+    const int64_t fp = st ? 0 : h_stride(g), ldx = st ? 0 : up(g->l.in, 8);
     if (!st) st = check_rows(g, offsets, R);
-    if (!st && dw_gate_up) st = check_gather(T, g->l.in, g->l.in, rows, k, R);
-    if (!st && dw_gate_up) st = check_bytes(T, g->l.in, 4);
+    if (!st && dw_gate_up) st = check_gather(T, ldx, g->l.in, rows, k, R);
+    if (!st && dw_gate_up) st = check_bytes(T, ldx, 4);
     if (!st && dw_gate_up) st = check_mx8(g->dtype, T, g->l.in);
-    if (!st) st = check_bytes(R, g->l.f * 2, 4);
+    if (!st) st = check_bytes(R, fp * 2, 4);
     if (!st) st = check_bytes(R, d->l.out, 4);
     if (!st) st = check_gated_rows(g->l.P, R, g->l.f);
     if (st) return st;
@@ -913,23 +967,37 @@ sg_status sg_gated_mlp_backward(const sg_experts* g, const sg_experts* d, const 
         return fail(SG_ERR_INVALID_ARG, "dw_gate_up needs x_codes and x_scales");
     if ((st = check_ws("sg_gated_mlp_backward", workspace, ws_bytes, sg_gated_mlp_backward_workspace(g, d, T, R))))
         return st;
-    char* at = (char*)workspace;
-    void* dgu = at;
-    void* h = at += up(R * g->l.out * 2, 256);
-    void* x = at += up(R * d->l.in * 2, 256);
-    if (dw_gate_up) at += up(T * g->l.in * 2, 256);
+    hipStream_t s = (hipStream_t)stream;
+    const int64_t n = R * g->l.P * fp * 2;
+    char* dgu = (char*)workspace;
+    char* h = dgu + up(2 * n, 256);
+    char* x = h + up(n, 256);
+    char* rest = x + up(T * ldx * 2, 256);
+    // dgu is stored in the layers' 16 bits, once, the operand of both products behind it
+    // (a matrix instruction multiplies values of one type).  Rows of it, of h and of x
+    // begin on 16 bytes whatever f and in are.
     if (R > 0) {
-        // dgu is stored in the layers' 16 bits, once, the operand of both products
-        // behind it (a matrix instruction multiplies values of one type)
-        st = sg_experts_gated_backward(d, dy, gu_codes, gu_scales, offsets, R, dgu, dw_down ? h : nullptr, at,
-                                       ws_bytes - (size_t)(at - (char*)workspace), stream);
-        if (!st && dw_gate_up) st = sg_dequantize_mxfp8(x_codes, x_scales, T, g->l.in, x, g->dtype, stream);
+        st = gated_backward(d, dy, gu_codes, gu_scales, offsets, R, dgu, dw_down ? h : nullptr, fp, s);
+        if (!st && dx) st = product(column_dx(g, dgu, fp, offsets, R, dx, dx_dtype), rest, "sg_gated_mlp_backward dx", s);
+        if (!st && dw_gate_up)
+            st = launched(sg::launch_dequantize_mxfp8(x_codes, x_scales, T, g->l.in, x, ldx, g->dtype, s),
+                          "sg_gated_mlp_backward");
     }
-    if (!st && (dx || dw_gate_up))
-        st = sg_experts_all_to_sharded_backward(g, x, T, g->l.in, dgu, offsets, rows, k, R, dx, dx_dtype, dw_gate_up,
-                                                dw_dtype, stream);
-    if (!st && dw_down)
-        st = sg_experts_sharded_to_all_backward(d, h, dy, offsets, R, nullptr, dx_dtype, dw_down, dw_dtype, stream);
+    if (!st && dw_gate_up) {
+        sg::GroupedDw p = column_dw(g, x, T, ldx, dgu, offsets, rows, k, R, dw_gate_up, dw_dtype);
+        p.ldg = p.O = (int)(2 * fp);
+        p.g_rank = R * 2 * fp;
+        p.of = (int)g->l.f;
+        p.ofp = (int)fp;
+        p.xw = (int)ldx;
+        st = launched(sg::launch_grouped_dw(p, s), "sg_gated_mlp_backward dw_gate_up");
+    }
+    if (!st && dw_down) {
+        sg::GroupedDw p = row_dw(d, h, dy, offsets, R, dw_down, dw_dtype);
+        p.ldx = p.xw = (int)fp;
+        p.x_rank = R * fp;
+        st = launched(sg::launch_grouped_dw(p, s), "sg_gated_mlp_backward dw_down");
+    }
     return st;
 }
 

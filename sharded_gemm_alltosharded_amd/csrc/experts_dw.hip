@@ -50,7 +50,7 @@ __global__ __launch_bounds__(64 * WO * WI) void grouped_dw_kernel(GroupedDw p, i
     const uint16_t* G = (const uint16_t*)p.G + r * p.g_rank;
     const uint16_t* X = (const uint16_t*)p.X + r * p.x_rank;
     const __amdgpu_buffer_rsrc_t bg = buffer(G, ((int64_t)(p.R - 1) * p.ldg + p.O) * 2);
-    const __amdgpu_buffer_rsrc_t bx = buffer(X, ((int64_t)(p.T - 1) * p.ldx + p.I) * 2);
+    const __amdgpu_buffer_rsrc_t bx = buffer(X, ((int64_t)(p.T - 1) * p.ldx + p.xw) * 2);
 
     // load i of a wave: tile row (i NWV + wave) 64 / C + lane / C, LDS chunk lane
     // % C.  Byte offsets within a tile stay in registers; the tile's own is a
@@ -178,13 +178,18 @@ __global__ __launch_bounds__(64 * WO * WI) void grouped_dw_kernel(GroupedDw p, i
         wait_loads();  // none may still be writing this workgroup's LDS when it ends
     }
 
-    const int64_t base = (int64_t)er * p.O * p.I;
+    const int64_t base = (int64_t)er * (p.ofp ? p.O / p.ofp * p.of : p.O) * p.I;
     auto put = [&](auto dt) ALWAYS_INLINE {
         constexpr int DT = decltype(dt)::value;
         static_for<0, NBO>([&](auto jc) {
             constexpr int j = decltype(jc)::value;
-            const int o = o0 + wo + 16 * j + r16;
+            int o = o0 + wo + 16 * j + r16;
             if (o >= p.O) return;
+            if (p.ofp) {  // a piece's columns behind the layer's own are no rows of it
+                const int piece = o / p.ofp, k = o - piece * p.ofp;
+                if (k >= p.of) return;
+                o = piece * p.of + k;
+            }
             static_for<0, NBI / 2>([&](auto ic) {
                 constexpr int i = 2 * decltype(ic)::value;
                 const int c = i0 + wi + 16 * i + 8 * c16;
@@ -213,13 +218,13 @@ hipError_t dw_launch(const GroupedDw& p, hipStream_t s) {
 template <bool F16>
 hipError_t dw_type(const GroupedDw& p, hipStream_t s) {
     const bool al = (uintptr_t)p.G % 16 == 0 && (uintptr_t)p.X % 16 == 0 && p.ldg % 8 == 0 && p.ldx % 8 == 0 &&
-                    p.g_rank % 8 == 0 && p.x_rank % 8 == 0 && p.O % 8 == 0 && p.I % 8 == 0;
+                    p.g_rank % 8 == 0 && p.x_rank % 8 == 0 && p.O % 8 == 0 && p.xw % 8 == 0;
     if (!al) return dw_launch<F16, 128, 128, 2, 4, false>(p, s);
     // the wide tile where its tiles go round the chip several times (8 experts
     // of 28672 x 4096: 2.30 ms, 2.72 on the narrow one; 32 of 1024 x 704 over
     // 1500 x 4 rows, twice round: 35 us, 28 on the narrow one)
     const int64_t big = (int64_t)p.E * p.P * ((p.O + 255) / 256) * ((p.I + 255) / 256);
-    if (big >= 4 * device_cus()) return dw_launch<F16, 256, 256, 2, 4, true>(p, s);
+    if (big >= 3 * device_cus()) return dw_launch<F16, 256, 256, 2, 4, true>(p, s);
     return dw_launch<F16, 128, 128, 2, 4, true>(p, s);
 }
 
@@ -227,6 +232,7 @@ hipError_t dw_type(const GroupedDw& p, hipStream_t s) {
 
 hipError_t launch_grouped_dw(const GroupedDw& call, hipStream_t s) {
     GroupedDw p = call;
+    if (p.xw == 0) p.xw = p.I;
     // slot / kdiv as a multiplication: exact for slots below 2^31 (the error of
     // kmul, at most kdiv, times a slot stays below 2^(32 + kshift))
     if (p.kdiv > 1) {

@@ -6,8 +6,8 @@
 //   code = round to nearest even of x 2^-e  (never above 448: nothing saturates)
 //   a block that holds an infinity or a NaN: scale 255 (NaN), codes 0
 //
-// and what is computed from them row by row: SwiGLU of gate|up rows that are then
-// kept, and its gradient from the kept ones.  All of it is bound by HBM.
+// and SwiGLU of gate|up rows that are then kept, where the product's epilogue does not
+// do it (grouped_tile.h).  All of it is bound by HBM.
 #include "experts.h"
 
 namespace sg {
@@ -76,13 +76,13 @@ __global__ __launch_bounds__(256) void quantize8_kernel(const void* x, int64_t n
 
 template <int DT, bool WHOLE>
 __global__ __launch_bounds__(256) void dequantize8_kernel(const uint8_t* codes, const uint8_t* scales, int64_t n,
-                                                          int64_t blocks, int64_t cols, void* x) {
+                                                          int64_t blocks, int64_t cols, int64_t ld, void* x) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= n) return;
     const Place p = place(i, blocks, cols);
     float v[8];
     get_codes<WHOLE>(codes, p.row * cols + p.c, scales[i >> 2], p.left, v);
-    store_cols<DT>(x, p.row * cols + p.c, v, WHOLE ? 8 : p.left);
+    store_cols<DT>(x, p.row * ld + p.c, v, WHOLE ? 8 : p.left);
 }
 
 // rows outside the experts' are left alone
@@ -94,7 +94,7 @@ __device__ __forceinline__ bool in_groups(const int32_t* offsets, int E, int64_t
 // codes (P, R, 2, f), scales
 template <int DT>
 __global__ __launch_bounds__(256) void gated_keep_kernel(const float* gu, int64_t n, int64_t blocks, int64_t f,
-                                                         int64_t R, const int32_t* offsets, int E, void* h,
+                                                         int64_t fp, int64_t R, const int32_t* offsets, int E, void* h,
                                                          uint8_t* codes, uint8_t* scales) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= n) return;
@@ -112,29 +112,8 @@ __global__ __launch_bounds__(256) void gated_keep_kernel(const float* gu, int64_
         scales[p.row * 2 * blocks + blocks + b] = mx8_scale(mu);
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = silu_f32(g[e]) * u[e];
-    store_cols<DT>(h, p.row * f + p.c, v, p.left);
-}
-
-// dh (P, R, f) fp32 and the kept gate|up rows -> dgu (P, R, 2 f), and h again
-template <int DT>
-__global__ __launch_bounds__(256) void gated_grad_kernel(const float* dh, const uint8_t* codes, const uint8_t* scales,
-                                                         int64_t n, int64_t blocks, int64_t f, int64_t R,
-                                                         const int32_t* offsets, int E, void* dgu, void* h) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= n) return;
-    const Place p = place(i, blocks, f);
-    if (p.left == 0 || !in_groups(offsets, E, p.row % R)) return;
-    float d[8], g[8], u[8], a[8], b[8], v[8];
-    load_cols<SG_F32>(dh, p.row * f + p.c, d, p.left);
-    const int64_t sb = p.row * 2 * blocks + p.c / 32;
-    get_codes<false>(codes, p.row * 2 * f + p.c, scales[sb], p.left, g);
-    get_codes<false>(codes, p.row * 2 * f + f + p.c, scales[sb + blocks], p.left, u);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) swiglu_grad(g[e], u[e], d[e], a[e], b[e], v[e]);
-    store_cols<DT>(dgu, p.row * 2 * f + p.c, a, p.left);
-    store_cols<DT>(dgu, p.row * 2 * f + f + p.c, b, p.left);
-    if (h) store_cols<DT>(h, p.row * f + p.c, v, p.left);
+    for (int e = 0; e < 8; ++e) v[e] = silu_f32(g[e]) * u[e];  // (zeros behind the row's end)
+    store_cols<DT>(h, p.row * fp + p.c, v, (int)max(min(fp - p.c, (int64_t)8), (int64_t)0));
 }
 
 dim3 grid_of(int64_t n) { return dim3((unsigned)((n + 255) / 256)); }
@@ -163,32 +142,22 @@ hipError_t launch_quantize_mxfp8(const void* x, int dtype, int64_t rows, int64_t
 }
 
 hipError_t launch_dequantize_mxfp8(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, void* x,
-                                   int dtype, hipStream_t s) {
+                                   int64_t ld, int dtype, hipStream_t s) {
     const int64_t blocks = mx8_blocks(cols), n = rows * blocks * 4;
     by_type(dtype, cols % 32 == 0, [&](auto dt, auto whole) {
         launch(dequantize8_kernel<decltype(dt)::value, decltype(whole)::value>, grid_of(n), dim3(256), 0, s, codes,
-               scales, n, blocks, cols, x);
+               scales, n, blocks, cols, ld, x);
     });
     return hipGetLastError();
 }
 
-hipError_t launch_gated_keep(const float* gu, int64_t P, int64_t R, int64_t f, const int32_t* offsets, int E, void* h,
-                             int f16, uint8_t* codes, uint8_t* scales, hipStream_t s) {
+hipError_t launch_gated_keep(const float* gu, int64_t P, int64_t R, int64_t f, int64_t fp, const int32_t* offsets,
+                             int E, void* h, int f16, uint8_t* codes, uint8_t* scales, hipStream_t s) {
     const int64_t blocks = mx8_blocks(f), n = P * R * blocks * 4;
     if (f16)
-        launch(gated_keep_kernel<SG_F16>, grid_of(n), dim3(256), 0, s, gu, n, blocks, f, R, offsets, E, h, codes, scales);
+        launch(gated_keep_kernel<SG_F16>, grid_of(n), dim3(256), 0, s, gu, n, blocks, f, fp, R, offsets, E, h, codes, scales);
     else
-        launch(gated_keep_kernel<SG_BF16>, grid_of(n), dim3(256), 0, s, gu, n, blocks, f, R, offsets, E, h, codes, scales);
-    return hipGetLastError();
-}
-
-hipError_t launch_gated_grad(const float* dh, const uint8_t* codes, const uint8_t* scales, int64_t P, int64_t R,
-                             int64_t f, const int32_t* offsets, int E, void* dgu, void* h, int f16, hipStream_t s) {
-    const int64_t blocks = mx8_blocks(f), n = P * R * blocks * 4;
-    if (f16)
-        launch(gated_grad_kernel<SG_F16>, grid_of(n), dim3(256), 0, s, dh, codes, scales, n, blocks, f, R, offsets, E, dgu, h);
-    else
-        launch(gated_grad_kernel<SG_BF16>, grid_of(n), dim3(256), 0, s, dh, codes, scales, n, blocks, f, R, offsets, E, dgu, h);
+        launch(gated_keep_kernel<SG_BF16>, grid_of(n), dim3(256), 0, s, gu, n, blocks, f, fp, R, offsets, E, h, codes, scales);
     return hipGetLastError();
 }
 

@@ -42,12 +42,12 @@ def test_quantize_refuses(L):
 def test_missing_layers_are_refused(L):
     assert L.sg_experts_gated(None, PTR, 1, 8, None, None, 1, 1, PTR, PTR, PTR, PTR, 0, None) == sg.ERR_INVALID_ARG
     assert "layer is NULL" in err(L)
-    assert L.sg_experts_gated_backward(None, PTR, PTR, PTR, None, 1, PTR, PTR, PTR, 0, None) == sg.ERR_INVALID_ARG
+    assert L.sg_experts_gated_backward(None, PTR, PTR, PTR, None, 1, PTR, PTR, None) == sg.ERR_INVALID_ARG
     assert L.sg_gated_mlp(None, None, PTR, 1, 8, None, None, 1, 1, PTR, 1, PTR, PTR, PTR, PTR, PTR, 0,
                           None) == sg.ERR_INVALID_ARG
     assert L.sg_gated_mlp_backward(None, None, PTR, PTR, 1, PTR, PTR, PTR, None, None, 1, 1, PTR, 1, PTR, PTR, 1, PTR, 0,
                                    None) == sg.ERR_INVALID_ARG
-    assert L.sg_experts_gated_workspace(None, 4) == 0 and L.sg_experts_gated_backward_workspace(None, 4) == 0
+    assert L.sg_experts_gated_workspace(None, 4) == 0
     assert L.sg_gated_mlp_workspace(None, None, 4) == 0 and L.sg_gated_mlp_backward_workspace(None, None, 4, 4) == 0
 
 

@@ -201,6 +201,46 @@ def test_gated_backward(case):
     assert none is None and torch.equal(only[:, :end], dgu[:, :end])
 
 
+# the wide tiles, their quarters and the narrow ones, on rows that end inside them:
+# E, R, in, f, P, dtype
+WIDE = [(1, 2600, 96, 2304, 1, BF), (1, 2600, 72, 752, 4, HF), (3, 2000, 64, 2104, 1, HF), (2, 4700, 136, 1024, 2, BF),
+        (1, 700, 64, 8200, 1, BF), (1, 4100, 40, 2501, 1, BF)]
+
+
+@pytest.mark.parametrize("E,R,K,f,P,dtype", WIDE)
+def test_gated_wide_tiles(E, R, K, f, P, dtype):
+    """Sampled rows, forward and backward, at sizes that take the widest tiles."""
+    g = gen(R + f)
+    w = normal(g, (E, 2 * P * f, K), dtype, 1 / math.sqrt(K))
+    wd = normal(g, (E, K, P * f), dtype, 1 / math.sqrt(P * f))
+    x = normal(g, (R, K), dtype)
+    off = offsets_of(g, E, R)
+    off[-1] = R
+    pick = torch.unique(torch.cat([torch.randint(0, R, (60,), generator=g), off[1:].long() - 1,
+                                   torch.tensor([0, 127, 128, 255, 256, R - 1])]))
+    pick = pick[pick >= 0]
+    expert = torch.searchsorted(off[1:].contiguous(), pick.int(), right=True)
+    order = ref.shard_rows(2 * P * f, 2, P)
+    shard = lambda v: torch.stack([v[:, o] for o in order]).unflatten(-1, (2, f))  # noqa: E731
+    gu = shard(torch.stack([w[e].double() @ x[m].double() for m, e in zip(pick, expert)]))
+    mag = shard(torch.stack([w[e].double().abs() @ x[m].double().abs() for m, e in zip(pick, expert)]))
+    up = sg.shard_experts(w.cuda(), "all-to-sharded", segments=2, P=P)
+    down = sg.shard_experts(wd.cuda(), "sharded-to-all", P=P)
+    h, codes, scales = sg.experts_gated(up, x.cuda(), off.cuda())
+    (a, b), (ma, mb) = gu.unbind(2), mag.unbind(2)
+    at = pick.cuda()
+    ref.close(h[:, at], ref.silu(a) * b, ref.swiglu_bound(a, b, ma, mb, K), "h")
+    mx.check_kept(codes[:, at], scales[:, at], gu, ref.sum_bound(mag, K), "kept")
+    dgu, h2 = sg.experts_gated_backward(down, x.cuda(), codes, scales, off.cuda())
+    dh = torch.stack([x[m].double() @ wd[e].double() for m, e in zip(pick, expert)]).view(-1, P, f).transpose(0, 1)
+    md = torch.stack([x[m].double().abs() @ wd[e].double().abs() for m, e in zip(pick, expert)]).view(-1, P, f).transpose(0, 1)
+    gg, uu = mx.decode(codes[:, at].cpu(), scales[:, at].cpu()).unbind(2)
+    wants, bounds = mx.gated_grad(gg, uu, dh), mx.gated_bounds(gg, uu, dh, ref.sum_bound(md, K))
+    got = (dgu[:, at, :f].contiguous(), dgu[:, at, f:].contiguous(), h2[:, at])
+    for v, want, bound, name in zip(got, wants, bounds, ("dgate", "dup", "h")):
+        ref.close(v, want, bound, name)
+
+
 def test_gated_rows_behind_the_last_stay():
     g = gen(2)
     E, R, K, f, P = 3, 40, 64, 48, 2
@@ -222,9 +262,7 @@ def test_gated_rows_behind_the_last_stay():
     assert torch.isfinite(h[:, :23]).all() and (scales[:, :23] != 255).all()
     dgu = torch.full((P, R, 2 * f), 7.0, dtype=BF, device="cuda")
     h2 = torch.full((P, R, f), 7.0, dtype=BF, device="cuda")
-    ws = torch.empty(L.sg_experts_gated_backward_workspace(down.handle, R), dtype=torch.uint8, device="cuda")
-    assert L.sg_experts_gated_backward(down.handle, at(xc), at(codes), at(scales), at(off), R, at(dgu), at(h2), at(ws),
-                                       ws.numel(), s) == 0
+    assert L.sg_experts_gated_backward(down.handle, at(xc), at(codes), at(scales), at(off), R, at(dgu), at(h2), s) == 0
     assert (dgu[:, 23:] == 7).all() and (h2[:, 23:] == 7).all() and torch.isfinite(dgu[:, :23]).all()
 
 
@@ -244,17 +282,20 @@ def test_gated_infinities_are_kept_as_nan_blocks():
 
 # ---- the block --------------------------------------------------------------
 
-BLOCKS = [  # E, T, D, F, out, P, dtype
+BLOCKS = [  # E, T, D, F, out, P, dtype; the last ones' sums are split
     (1, 1, 8, 8, 8, 1, BF), (1, 77, 100, 726, 60, 2, HF), (1, 300, 256, 512, 256, 4, BF), (3, 150, 72, 96, 40, 2, BF),
-    (1, 1000, 136, 320, 136, 1, HF),
+    (1, 1000, 136, 320, 136, 1, HF), (1, 33, 77, 1030, 50, 2, BF), (1, 100, 1024, 2048, 512, 4, HF),
+    (1, 12, 200, 3000, 90, 3, BF),
 ]
 
 
 @pytest.mark.parametrize("E,T,D,F,N,P,dtype", BLOCKS)
 def test_block_is_the_chain_of_its_calls(E, T, D, F, N, P, dtype):
     g = gen(T + D)
-    gu = sg.shard_experts(normal(g, (E, 2 * F, D), dtype, 1 / math.sqrt(D)).cuda(), "all-to-sharded", segments=2, P=P)
-    dn = sg.shard_experts(normal(g, (E, N, F), dtype, 1 / math.sqrt(F)).cuda(), "sharded-to-all", P=P)
+    wg = normal(g, (E, 2 * F, D), dtype, 1 / math.sqrt(D))
+    gu = sg.shard_experts(wg.cuda(), "all-to-sharded", segments=2, P=P)
+    wd = normal(g, (E, N, F), dtype, 1 / math.sqrt(F))
+    dn = sg.shard_experts(wd.cuda(), "sharded-to-all", P=P)
     x = normal(g, (T, D), dtype).cuda()
     kw = {}
     R = T
@@ -269,14 +310,28 @@ def test_block_is_the_chain_of_its_calls(E, T, D, F, N, P, dtype):
     xc, xs = sg.quantize_mxfp8(x)
     for a, b in zip(kept, (xc, xs, codes, scales)):
         assert torch.equal(a, b)
-    assert torch.equal(y, sg.experts_sharded_to_all(dn, h, **off))
+    # y's and dx's sums may be split: fp32 sums of the same products, rounded alike
+    yw, w = sg.experts_sharded_to_all(dn, h, out_dtype=F32, **off).double().cpu(), P * F // P
+    mag = torch.zeros((R, N), dtype=torch.float64)
+    ends = torch.tensor([0, R]) if E == 1 else kw["offsets"].cpu()
+    full = h.double().cpu().transpose(0, 1).flatten(1).abs()
+    ref.product(full, wd.double().abs(), ends, torch.zeros_like(mag), mag)
+    ref.close(y, yw, 2 * ref.sum_bound(mag, w), "y")
     for dt in (dtype, F32):
         dx, dwg, dwd = sg.gated_mlp_backward(gu, dn, kept, dy, dx_dtype=dt, dw_dtype=dt, **kw)
         dgu, h2 = sg.experts_gated_backward(dn, dy, codes, scales, **off)
         x8 = sg.dequantize_mxfp8(xc, xs, out_dtype=dtype)
-        wx, wg = sg.experts_all_to_sharded_backward(gu, x8, dgu, dx_dtype=dt, dw_dtype=dt, **kw)
-        _, wd = sg.experts_sharded_to_all_backward(dn, h2, dy, need_dx=False, dw_dtype=dt, **off)
-        assert torch.equal(dx, wx) and torch.equal(dwg, wg) and torch.equal(dwd, wd)
+        _, ww = sg.experts_all_to_sharded_backward(gu, x8, dgu, dw_dtype=dt, **kw)
+        wx, _ = sg.experts_all_to_sharded_backward(gu, None, dgu, need_dw=False, dx_dtype=F32, **kw)
+        _, wn = sg.experts_sharded_to_all_backward(dn, h2, dy, need_dx=False, dw_dtype=dt, **off)
+        assert torch.equal(dwg, ww) and torch.equal(dwd, wn)
+        order = ref.shard_rows(2 * F, 2, P)
+        full = torch.zeros((R, 2 * F), dtype=torch.float64)
+        for r, o in enumerate(order):
+            full[:, o] = dgu[r].double().cpu().abs()
+        mx_ = torch.zeros((R, D), dtype=torch.float64)
+        ref.product(full, wg.double().transpose(1, 2), ends, torch.zeros_like(mx_), mx_)
+        ref.close(dx, wx.double().cpu(), 2 * ref.sum_bound(mx_, 2 * F), "dx")
     only, n1, n2 = sg.gated_mlp_backward(gu, dn, kept, dy, need_dw=False, dx_dtype=F32, **kw)
     assert n1 is None and n2 is None and torch.equal(only, dx)
     none, w1, w2 = sg.gated_mlp_backward(gu, dn, kept, dy, need_dx=False, **kw)

@@ -10,9 +10,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libshardgemm.so")
 SOURCES = ["api.hip", "generic.hip", "tile.hip", "skinny.hip", "q4.hip", "q4_wide.hip", "q4s.hip", "layout.hip",
-           "tile_dma.hip", "backward.hip", "q4tile.hip", "experts_api.hip", "experts.hip", "experts_dw.hip", "experts_gated.hip", "route.hip",
-           "mxfp4.hip", "mxfp8.hip",
-           "adapters_api.hip", "adapters.hip", "adapters_expand.hip"]
+           "tile_dma.hip", "backward.hip", "q4tile.hip", "experts_api.hip", "experts.hip", "experts_dw.hip", "experts_gated.hip",
+           "route.hip", "mxfp4.hip", "mxfp8.hip", "adapters_api.hip", "adapters.hip", "adapters_expand.hip",
+           "adapters_tile.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 

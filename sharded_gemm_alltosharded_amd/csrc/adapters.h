@@ -16,7 +16,8 @@ struct Pieces {
 // The plan of a step (ints): the tokens grouped by adapter (group n: those without
 // one), and the groups cut into tiles of adapter_tile_rows rows.
 //   offsets (n + 2), rows (T): the token of each grouped row, in token order for each
-//   group, tiles (adapter_tiles, 4): adapter, first row, rows; adapter -1 behind the last.
+//   group, ids (T): its adapter (n: none), tiles (adapter_tiles, 4): adapter, first row,
+//   rows; adapter -1 behind the last.
 constexpr int kMaxAdapters = 1024, kMaxRank = 256;
 // 16 rows where an adapter has few, else 64 (a tile reads its adapter's matrices once)
 inline int adapter_tile_rows(int64_t T, int n) { return T >= 32 * ((int64_t)n + 1) ? 64 : 16; }
@@ -24,14 +25,14 @@ inline int64_t adapter_tiles(int64_t T, int n) {
     return T / adapter_tile_rows(T, n) + (T < n + 1 ? T : n + 1);
 }
 struct PlanLayout {
-    int64_t offsets, rows, tiles, ints;
+    int64_t offsets, rows, ids, tiles, ints;
 };
 inline PlanLayout plan_layout(int64_t T, int n) {
-    const int64_t tiles = (n + 2 + T + 3) / 4 * 4;
-    return {0, n + 2, tiles, tiles + 4 * adapter_tiles(T, n)};
+    const int64_t tiles = (n + 2 + 2 * T + 3) / 4 * 4;
+    return {0, n + 2, n + 2 + T, tiles, tiles + 4 * adapter_tiles(T, n)};
 }
 struct Plan {
-    const int32_t *offsets, *rows, *tiles;
+    const int32_t *offsets, *rows, *ids, *tiles;
     int T, n, ntiles, tile_rows;
 };
 hipError_t launch_adapter_plan(const int32_t* which, int64_t T, int n, int32_t* plan, hipStream_t s);
@@ -40,12 +41,11 @@ hipError_t launch_adapter_plan(const int32_t* which, int64_t T, int n, int32_t* 
 // rank rounded up to 16.  M: an adapter's matrix, (rank, width) row-major, or
 // transposed (width, rank).
 //
-//   shrink: U[m][j] = sum over the columns k of X[t(m)][k] M[j][k]
-//   expand: out[t(m)][c] = base[t(m)][c] + scale_a sum_j U[m][j] M[j][c]; tokens
-//           without an adapter: base.  swiglu: column c of each rank is silu(gate) up
-//           of its columns c and f + c.
-//   grad:   G_a[j][c] = scale_a sum over the rows m of a of U[m][j] X[t(m)][c], laid
-//           out as M
+//   shrink: U[m][j] = scale_a sum over the columns k of X[t(m)][k] M[j][k]
+//   expand: out[t(m)][c] = base[t(m)][c] + sum_j U[m][j] M[j][c]; tokens without an
+//           adapter: base.  swiglu: column c of each rank is silu(gate) up of its
+//           columns c and f + c.
+//   grad:   G_a[j][c] = sum over the rows m of a of U[m][j] X[t(m)][c], laid out as M
 struct LowRank {
     Plan plan;
     int f16, rank, rp, slabs;
@@ -64,8 +64,32 @@ struct LowRank {
     int64_t out_rank, out_ld;  // expand
 };
 int shrink_slabs(const Plan& p, int64_t width, int rank);
+
+// expand in the epilogue of the product itself (grouped_tile.h): the projection's rows
+// are the plan's, and its sums never leave the registers before U's part is in.
+struct Adapted {
+    Plan plan;
+    const uint32_t __attribute__((ext_vector_type(4)))* operands;  // finish's
+    const int32_t* exponents;
+    int rank;
+    const void* M;    // (width, rank); of a transposed product (rank, width)
+    int64_t width;
+    int P;            // ranks of the output's columns: rank r's part s is the unsharded (s P + r)
+    // a layer's weights, fragment-major: bytes from one input segment's, and (transposed)
+    // from one rank's output columns, to the next
+    uint32_t wseg, wrank;
+};
+// transposed or not, p.rows the plan's; 16-byte rows of x
+hipError_t launch_adapted(const Grouped& p, const Adapted& d, hipStream_t s);
+// whether that beats the product's own kernel and expand behind it
+bool adapted_fills(const Grouped& p);
 hipError_t launch_shrink(const LowRank& p, hipStream_t s);
-hipError_t launch_finish(const LowRank& p, hipStream_t s);  // the slabs added into the first
+// The slabs added into the first; and, where operands is given, U split for the tiles'
+// matrix instructions: for every 16 grouped rows and 16 ranks a lane's 16 bytes (row l &
+// 15, ranks 8 (l >> 4 & 1) .. + 7, hi or from lane 32 on lo), of fp16 layers times
+// 2^-exponents[row].
+hipError_t launch_finish(const LowRank& p, void* operands, int32_t* exponents, hipStream_t s);
+inline size_t operand_bytes(int64_t T, int rank) { return (size_t)((T + 15) / 16 * ((rank + 15) / 16) * 1024); }
 hipError_t launch_expand(const LowRank& p, hipStream_t s);
 hipError_t launch_grad(const LowRank& p, hipStream_t s);
 

@@ -32,7 +32,7 @@ __device__ __forceinline__ uint64_t equal_lanes(int v, int bits) {
 // counts a run of tokens, the counts become first rows, each wave places its run.
 __global__ __launch_bounds__(1024) void adapter_plan_kernel(const int32_t* which, int T, int n, int tile_rows,
                                                             int ntiles, int32_t* offsets, int32_t* rows,
-                                                            int32_t* tiles) {
+                                                            int32_t* ids, int32_t* tiles) {
     __shared__ int first[16][kMaxAdapters + 1];  // counts, then the first row, of a wave's run and a group
     __shared__ int total[kMaxAdapters + 1];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, groups = n + 1;
@@ -91,7 +91,11 @@ __global__ __launch_bounds__(1024) void adapter_plan_kernel(const int32_t* which
     for (int i = 0; i < run; i += 64) {
         const int t = s0 + i + lane, g = group(t);
         const uint64_t same = equal_lanes(g + 1, bits);
-        if (g >= 0) rows[total[g] + first[wave][g] + __builtin_popcountll(same & ((1ull << lane) - 1))] = t;
+        if (g >= 0) {
+            const int at = total[g] + first[wave][g] + __builtin_popcountll(same & ((1ull << lane) - 1));
+            rows[at] = t;
+            ids[at] = g;
+        }
         // the wave's reads of `first` are done before its update (one wave, in order)
         __builtin_amdgcn_wave_barrier();
         if (g >= 0 && lane == __builtin_ctzll(same)) first[wave][g] += __builtin_popcountll(same);
@@ -100,23 +104,25 @@ __global__ __launch_bounds__(1024) void adapter_plan_kernel(const int32_t* which
 }
 
 // ---- shrink -----------------------------------------------------------------
-// U[slab][m][j] = sum over the slab's columns of X[t(m)][k] M[j][k].  Bound by
-// reading X (many rows of an adapter) or M (few).  Columns go in steps of 32,
-// one MFMA; slabs (blockIdx.y) and the four waves split them, a wave's steps
-// adjacent.  TR: M is (width, rank): a step's 32 rows pass through LDS and are read
+// U[slab][m][j] = scale_a sum over the slab's columns of X[t(m)][k] M[j][k].  Bound by
+// reading X (many rows of an adapter) or M (few).  Columns go in steps of 32, one MFMA;
+// slabs (blockIdx.y) and the NW waves split them, a wave's steps adjacent.  TR: M is (width, rank): a step's 32 rows pass through LDS and are read
 // transposed.
 template <bool F16, bool TR, int NR, int MB, bool AL>
 __global__ __launch_bounds__(256) void shrink_kernel(LowRank p) {
-    constexpr int U = NR + MB <= 3 ? 4 : 2;  // steps whose loads are out at once
-    __shared__ f32x4 red[3 * NR * MB * 64];
-    __shared__ __attribute__((aligned(16))) uint8_t stage[TR ? 4 * U * 32 * NR * 32 : 16];
+    constexpr int NW = 4, U = NR + MB <= 6 ? 4 : 2;  // waves; steps whose loads are out at once
+    // (the waves' sums go where their steps of M went)
+    constexpr int RED = (NW - 1) * NR * MB * 1024, ST = TR ? NW * U * NR * 1024 : 0;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[RED > ST ? RED : ST];
+    f32x4* red = (f32x4*)lds;
+    uint8_t* stage = lds;
     const Tile tile = tile_of(p.plan, blockIdx.x);
     if (tile.a < 0 || tile.a >= p.plan.n) return;
     const int lane = threadIdx.x & 63, r16 = lane & 15, c16 = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int j0 = blockIdx.z * NR * 16;
-    const int spp = (p.x.part + 31) / 32, steps = p.x.S * p.x.P * spp, parts = 4 * p.slabs;
-    const int w = blockIdx.y * 4 + wave;
+    const int spp = (p.x.part + 31) / 32, steps = p.x.S * p.x.P * spp, parts = NW * p.slabs;
+    const int w = blockIdx.y * NW + wave;
     const int st0 = (int)((int64_t)steps * w / parts), st1 = (int)((int64_t)steps * (w + 1) / parts);
 
     const uint16_t* X = (const uint16_t*)p.X;
@@ -163,7 +169,7 @@ __global__ __launch_bounds__(256) void shrink_kernel(LowRank p) {
             }
         }
         if constexpr (TR) {
-            uint8_t* mine = stage + wave * U * 1024 * NR;
+            uint8_t* mine = stage + wave * (U * 1024 * NR);
             lds_order();
 #pragma unroll
             for (int u = 0; u < U; ++u)
@@ -183,6 +189,7 @@ __global__ __launch_bounds__(256) void shrink_kernel(LowRank p) {
 #pragma unroll
                 for (int b = 0; b < MB; ++b) acc[i][b] = mfma16<F16>(mf[u][i], xf[u][b], acc[i][b]);
     }
+    if constexpr (TR) __syncthreads();
     if (wave > 0)
 #pragma unroll
         for (int i = 0; i < NR; ++i)
@@ -191,41 +198,92 @@ __global__ __launch_bounds__(256) void shrink_kernel(LowRank p) {
     __syncthreads();
     if (wave > 0) return;
     float* out = p.U + blockIdx.y * p.slab;
+    const float scale = p.scale ? p.scale[tile.a] : 1.0f;
 #pragma unroll
     for (int i = 0; i < NR; ++i)
 #pragma unroll
         for (int b = 0; b < MB; ++b) {
             f32x4 v = acc[i][b];
 #pragma unroll
-            for (int o = 0; o < 3; ++o) v += red[(o * NR * MB + i * MB + b) * 64 + lane];
+            for (int o = 0; o < NW - 1; ++o) v += red[(o * NR * MB + i * MB + b) * 64 + lane];
             const int j = j0 + 16 * i + 4 * c16;
-            if (live[b] && j < p.rp) *(f32x4*)(out + (int64_t)(tile.row0 + 16 * b + r16) * p.rp + j) = v;
+            if (live[b] && j < p.rp) *(f32x4*)(out + (int64_t)(tile.row0 + 16 * b + r16) * p.rp + j) = v * scale;
         }
 }
 
-__global__ __launch_bounds__(256) void finish_kernel(float* U, int64_t n4, int64_t slab, int slabs) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= n4) return;
-    f32x4 v = ((f32x4*)U)[i];
-    for (int q = 1; q < slabs; ++q) v += *(f32x4*)(U + q * slab + i * 4);
-    ((f32x4*)U)[i] = v;
+// A wave takes 16 rows: the slabs' sum, back into the first where there are several, and
+// the operands (adapters.h).  Lane l holds row l & 15, ranks 8 (l >> 4 & 1) .. + 7 of each
+// sixteen; lanes 32 apart hold the same.
+template <bool F16>
+__global__ __launch_bounds__(256) void finish_kernel(LowRank p, u32x4* operands, int32_t* exponents) {
+    const int lane = threadIdx.x & 63, r16 = lane & 15, c16 = lane >> 4;
+    const int64_t block = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), m = block * 16 + r16;
+    if (block * 16 >= p.plan.T) return;
+    const int chunks = p.rp / 16;
+    // (rows without an adapter hold nothing)
+    const bool in = m < p.plan.T && p.plan.ids[m] >= 0 && p.plan.ids[m] < p.plan.n;
+    auto sum = [&](int ch, f32x4 (&v)[2]) {
+        v[0] = v[1] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (!in) return;
+        const float* u = p.U + m * p.rp + ch * 16 + 8 * (c16 & 1);
+#pragma unroll 4
+        for (int q = 0; q < p.slabs; ++q) v[0] += *(const f32x4*)(u + q * p.slab), v[1] += *(const f32x4*)(u + q * p.slab + 4);
+    };
+    int ex = 0;
+    if (F16 && operands) {
+        float top = 0.f;
+        for (int ch = 0; ch < chunks; ++ch) {
+            f32x4 v[2];
+            sum(ch, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (ch * 16 + 8 * (c16 & 1) + e < p.rank) top = fmaxf(top, fabsf(v[e >> 2][e & 3]));
+        }
+        top = fmaxf(top, __shfl_xor(top, 16));
+        // (products of fp16 values are 2^-48 at least; the sums scaled with it must not overflow)
+        ex = max(range_exponent(top), -80);
+        if (in && lane < 16) exponents[m] = ex;
+    }
+    for (int ch = 0; ch < chunks; ++ch) {
+        f32x4 v[2];
+        sum(ch, v);
+        if (operands) {
+            u32x4 w;
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                uint16_t h0, l0, h1, l1;
+                const int j = ch * 16 + 8 * (c16 & 1) + e;
+                // (ranks behind the last hold nothing: an infinite x times zeros)
+                const float a = j < p.rank ? v[e >> 2][e & 3] : 0.f, b = j + 1 < p.rank ? v[e >> 2][(e & 3) + 1] : 0.f;
+                split16<F16>(F16 ? ldexpf(a, -ex) : a, h0, l0);
+                split16<F16>(F16 ? ldexpf(b, -ex) : b, h1, l1);
+                w[e / 2] = c16 < 2 ? h0 | ((uint32_t)h1 << 16) : l0 | ((uint32_t)l1 << 16);
+            }
+            operands[(block * chunks + ch) * 64 + lane] = w;
+        }
+        if (p.slabs > 1 && in && c16 < 2) {
+            float* u = p.U + m * p.rp + ch * 16 + 8 * c16;
+            *(f32x4*)u = v[0];
+            *(f32x4*)(u + 4) = v[1];
+        }
+    }
 }
 
 // ---- grad -------------------------------------------------------------------
-// G_a[j][c] = scale_a sum over a's rows m of U[m][j] X[t(m)][c].  Bound by reading X.
-// A workgroup takes 64 columns of one adapter, its waves every fourth 32 rows: X and
+// G_a[j][c] = sum over a's rows m of U[m][j] X[t(m)][c].  Bound by reading X.
+// A workgroup takes 64 columns of one adapter, its waves every eighth 32 rows: X and
 // the two halves of U go through LDS, a wave's own part of it, and are read
 // transposed.  For fp16 U's 32 rows are scaled by one power of two.
 template <bool F16, bool TR, int NR, bool AL>
-__global__ __launch_bounds__(256) void grad_kernel(LowRank p) {
+__global__ __launch_bounds__(512) void grad_kernel(LowRank p) {
+    constexpr int NW = 8;
     constexpr int XB = 4096, UB = 32 * 32 * NR, WAVE = XB + 2 * UB;  // bytes of X, of a half of U
-    constexpr int RED = 3 * 4 * NR * 64 * 16;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[4 * WAVE > RED ? 4 * WAVE : RED];
+    constexpr int RED = (NW - 1) * 4 * NR * 64 * 16;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[NW * WAVE > RED ? NW * WAVE : RED];
     const int a = blockIdx.y, lane = threadIdx.x & 63, r16 = lane & 15, c16 = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int gpp = (p.x.part + 63) / 64, q = blockIdx.x / gpp, c0 = (blockIdx.x - q * gpp) * 64, j0 = blockIdx.z * NR * 16;
     const int m0 = min(max(p.plan.offsets[a], 0), p.plan.T), m1 = max(min(p.plan.offsets[a + 1], p.plan.T), m0);
-    const float scale = p.scale ? p.scale[a] : 1.0f;
     const uint16_t* X = (const uint16_t*)p.X;
     const int64_t at = piece_at(p.x, q);
     uint8_t *sx = lds + wave * WAVE, *sh = sx + XB, *sl = sh + UB;
@@ -255,14 +313,14 @@ __global__ __launch_bounds__(256) void grad_kernel(LowRank p) {
     };
     int m = m0 + 32 * wave;
     if (m < m1) fetch(m);
-    for (; m < m1; m += 128) {
+    for (; m < m1; m += 32 * NW) {
         float top = 0.f;
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
             const int j = j0 + (lane + 64 * i) % (2 * NR) * 8;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float v = j + e < p.rank ? uv[i][e >> 2][e & 3] * scale : 0.f;
+                const float v = j + e < p.rank ? uv[i][e >> 2][e & 3] : 0.f;
                 uv[i][e >> 2][e & 3] = v;
                 top = fmaxf(top, fabsf(v));
             }
@@ -292,7 +350,7 @@ __global__ __launch_bounds__(256) void grad_kernel(LowRank p) {
             *(u32x4*)(sl + i * 1024 + lane * 16) = l;
         }
         lds_order();
-        if (m + 128 < m1) fetch(m + 128);
+        if (m + 32 * NW < m1) fetch(m + 32 * NW);
         const int row = 8 * c16 + (r16 >> 2);
         u32x4 xf[4], hf[NR], lf[NR];
         // (TR, results along the ranks: plain columns; else eight adjacent columns a lane)
@@ -331,7 +389,7 @@ __global__ __launch_bounds__(256) void grad_kernel(LowRank p) {
 #pragma unroll
         for (int j = 0; j < NR; ++j)
 #pragma unroll
-            for (int o = 0; o < 3; ++o) acc[i][j] += red[((o * 4 + i) * NR + j) * 64 + lane];
+            for (int o = 0; o < NW - 1; ++o) acc[i][j] += red[((o * 4 + i) * NR + j) * 64 + lane];
     const int64_t base = (int64_t)a * p.rank * p.width, col0 = (int64_t)q * p.x.part;
     by_out_type(p.out_dtype, [&](auto dt) {
         constexpr int OT = decltype(dt)::value;
@@ -367,14 +425,17 @@ __global__ __launch_bounds__(256) void grad_kernel(LowRank p) {
 hipError_t launch_adapter_plan(const int32_t* which, int64_t T, int n, int32_t* plan, hipStream_t s) {
     const PlanLayout l = plan_layout(T, n);
     launch(adapter_plan_kernel, dim3(1), dim3(1024), 0, s, which, (int)T, n, adapter_tile_rows(T, n),
-           (int)adapter_tiles(T, n), plan + l.offsets, plan + l.rows, plan + l.tiles);
+           (int)adapter_tiles(T, n), plan + l.offsets, plan + l.rows, plan + l.ids, plan + l.tiles);
     return hipGetLastError();
 }
 
-// as many slabs as give every compute unit two workgroups, of eight steps a wave at least
+// As many slabs as give every compute unit two workgroups, of four steps a wave at
+// least: a compute unit takes about 75 GB/s, so few of them are slow whatever their
+// waves (16 tokens of 16 adapters, 4096 inputs: 5 us, 9 in one slab of sixteen waves).
+// At most eight: every reader of U adds them up.
 int shrink_slabs(const Plan& p, int64_t width, int rank) {
     const int64_t blocks = (int64_t)p.ntiles * ((rank + 63) / 64), want = (2 * device_cus() + blocks - 1) / blocks;
-    const int64_t most = width / 1024;
+    const int64_t most = width / 512 < 8 ? width / 512 : 8;
     return (int)(want < most ? want : most > 1 ? most : 1);
 }
 
@@ -398,10 +459,11 @@ hipError_t launch_shrink(const LowRank& p, hipStream_t s) {
     });
 }
 
-hipError_t launch_finish(const LowRank& p, hipStream_t s) {
-    if (p.slabs == 1) return hipSuccess;
-    const int64_t n4 = (int64_t)p.plan.T * p.rp / 4;
-    launch(finish_kernel, dim3((unsigned)((n4 + 255) / 256)), dim3(256), 0, s, p.U, n4, p.slab, p.slabs);
+hipError_t launch_finish(const LowRank& p, void* operands, int32_t* exponents, hipStream_t s) {
+    if (p.slabs == 1 && !operands) return hipSuccess;
+    const dim3 grid((unsigned)(((p.plan.T + 15) / 16 + 3) / 4));
+    if (p.f16) launch(finish_kernel<true>, grid, dim3(256), 0, s, p, (u32x4*)operands, exponents);
+    else launch(finish_kernel<false>, grid, dim3(256), 0, s, p, (u32x4*)operands, exponents);
     return hipGetLastError();
 }
 
@@ -413,7 +475,7 @@ hipError_t launch_grad(const LowRank& p, hipStream_t s) {
         return by_bool(p.f16, [&](auto f16) {
             return by_bool(p.transposed, [&](auto tr) {
                 return by_bool(al, [&](auto a) {
-                    launch(grad_kernel<decltype(f16)::value, decltype(tr)::value, NR, decltype(a)::value>, grid, dim3(256), 0,
+                    launch(grad_kernel<decltype(f16)::value, decltype(tr)::value, NR, decltype(a)::value>, grid, dim3(512), 0,
                            s, p);
                     return hipGetLastError();
                 });

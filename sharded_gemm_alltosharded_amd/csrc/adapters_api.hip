@@ -47,7 +47,7 @@ sg::Pieces y_pieces(const Geometry& g, int64_t T) { return g.column() ? sharded(
 
 sg::Plan plan_of(const int32_t* plan, int64_t T, int n) {
     const sg::PlanLayout l = sg::plan_layout(T, n);
-    return {plan + l.offsets, plan + l.rows, plan + l.tiles, (int)T, n, (int)sg::adapter_tiles(T, n),
+    return {plan + l.offsets, plan + l.rows, plan + l.ids, plan + l.tiles, (int)T, n, (int)sg::adapter_tiles(T, n),
             sg::adapter_tile_rows(T, n)};
 }
 
@@ -100,15 +100,78 @@ Half half(const Geometry& g, const sg_adapters* ad, const int32_t* plan, int64_t
     return h;
 }
 
-size_t base_bytes(const sg_layer* l, const Geometry& g, int64_t T) {
-    return up256(T * g.out * 4) + (g.column() ? 0 : up256((int64_t)sg_sharded_to_all_workspace(l, T)));
-}
 
 sg_status check_ws(const char* what, const void* ws, size_t bytes, size_t need) {
     if (need && (!ws || bytes < need || (uintptr_t)ws % 16))
         return fail(SG_ERR_WORKSPACE, "%s needs %zu bytes of 16-byte aligned workspace (got %zu)", what, need,
                     ws ? bytes : (size_t)0);
     return SG_OK;
+}
+
+// The projection's product over the plan's rows, x W^T or (transposed) dy W, straight
+// from the layer's fragments; false where they, or the tokens, do not suit the tiles.
+bool tile_product(const sg_layer* l, const Geometry& g, const sg_adapters* ad, const sg::Plan& plan, int64_t T,
+                  bool transposed, bool swiglu, sg::Grouped* to, sg::Adapted* d) {
+    const sg::LayerView v = sg::layer_view(l);
+    const int64_t f = g.part(), rank_bytes = v.rows_r * v.cols_r * 2;  // f: of the sharded side
+    // whole 16-row blocks and 64-input tiles of every part, 32-column fragments of a
+    // transposed product's outputs, and 32-bit offsets
+    if (!v.wfrag || v.bias || g.out % 16 || g.in % 64 || f % (g.column() ? 16 : 64) || rank_bytes * g.P >= 0xffff0000ll ||
+        (double)T * (double)(g.in > g.out ? g.in : g.out) * 2 >= (double)0xffff0000ll)
+        return false;
+    sg::Grouped p{};
+    p.mode = g.dtype == SG_F16 ? sg::G_F16 : sg::G_BF16;
+    p.rows = plan.rows;
+    p.kdiv = 1;
+    p.T = p.R = (int)T;
+    p.E = 1;
+    p.W = (const uint8_t*)v.w;
+    p.w_expert = rank_bytes * g.P;
+    p.transposed = transposed;
+    p.swiglu = swiglu;
+    p.wsteps = (int)(v.cols_r / 32);
+    const bool in_sharded = g.column() == transposed;  // the product's input is the sharded side
+    const int64_t width = transposed ? g.out : g.in, cols = transposed ? g.in : g.out;
+    // input: ranks' pieces, or whole rows
+    p.a_pieces = in_sharded ? g.S : 1;
+    p.nseg = in_sharded ? g.S * g.P : 1;
+    p.kl = p.kpad = (int)(in_sharded ? f : width);
+    p.lda = in_sharded ? g.S * f : width;
+    p.a_rank = in_sharded ? T * g.S * f : 0;
+    if (in_sharded && !g.column()) {  // a rank's segments lie side by side in its matrix
+        p.a_pieces = 1;
+        p.nseg = g.P;
+        p.kl = p.kpad = (int)(g.S * f);
+    }
+    // output
+    const bool out_sharded = !in_sharded;
+    const int64_t fo = out_sharded ? f : cols;
+    p.f = (int)fo;
+    p.bps = (int)(fo / 16);
+    p.S = swiglu ? 1 : out_sharded ? g.S : 1;
+    p.nout = (int)(swiglu ? cols / 32 : cols / 16);
+    p.ldo = swiglu ? fo : out_sharded ? g.S * fo : cols;
+    p.o_rank = out_sharded ? T * p.ldo : 0;
+    d->plan = plan;
+    d->rank = ad->rank;
+    d->M = transposed ? ad->A : ad->B;
+    d->width = cols;
+    d->P = out_sharded ? g.P : 1;
+    // all-to-sharded: the ranks' rows are one stack; sharded-to-all: a matrix each
+    d->wseg = (uint32_t)rank_bytes;
+    d->wrank = (uint32_t)rank_bytes;
+    if (!sg::adapted_fills(p)) return false;
+    *to = p;
+    return true;
+}
+
+// U's sums, and its operands for the tiles, at `at` (operands_bytes)
+size_t operands_bytes(int64_t T, int rank) { return up256((int64_t)sg::operand_bytes(T, rank)) + up256(T * 4); }
+sg_status finish(const sg::LowRank& p, sg::Adapted* d, char* at, int64_t T, const char* what, hipStream_t s) {
+    int32_t* ex = (int32_t*)(at + up256((int64_t)sg::operand_bytes(T, p.rank)));
+    d->operands = (decltype(d->operands))at;
+    d->exponents = ex;
+    return launched(sg::launch_finish(p, at, ex, s), what);
 }
 
 sg_status forward(const char* what, const sg_layer* l, const Geometry& g, const sg_adapters* ad, const int32_t* plan,
@@ -125,6 +188,19 @@ sg_status forward(const char* what, const sg_layer* l, const Geometry& g, const 
     p.X = x;
     sg_status st = launched(sg::launch_shrink(p, s), what);
     if (st) return st;
+    const int64_t n = g.column() ? (epilogue == SG_EPI_SWIGLU ? g.out / 2 : g.out) / g.P : g.out;  // columns of a rank
+    const bool gathered = g.column() && out_layout == SG_OUT_FULL;
+    sg::Grouped q;
+    sg::Adapted d{};
+    if ((uintptr_t)x % 16 == 0 && (uintptr_t)ad->B % 16 == 0 &&
+        tile_product(l, g, ad, p.plan, T, false, epilogue == SG_EPI_SWIGLU, &q, &d)) {
+        q.A = x;
+        q.out = y;
+        q.out_dtype = y_dtype;
+        if (gathered) q.ldo = n * g.P, q.o_rank = n;
+        st = finish(p, &d, (char*)workspace + u.bytes, T, what, s);
+        return st ? st : launched(sg::launch_adapted(q, d, s), what);
+    }
     // the projection's result stays in fp32 until the adapters' part is added, so that y
     // is rounded once; an fp32 y holds it itself
     const bool swiglu = epilogue == SG_EPI_SWIGLU, in_y = y_dtype == SG_F32 && !swiglu;
@@ -145,10 +221,9 @@ sg_status forward(const char* what, const sg_layer* l, const Geometry& g, const 
     p.swiglu = swiglu;
     p.out = y;
     p.out_dtype = y_dtype;
-    const int64_t n = g.column() ? (swiglu ? g.out / 2 : g.out) / g.P : g.out;
     p.out_ld = n;
     p.out_rank = g.column() ? T * n : 0;
-    if (g.column() && out_layout == SG_OUT_FULL) {
+    if (gathered) {
         p.out_ld = n * g.P;
         p.out_rank = n;
         if (in_y) p.x.ld = p.out_ld, p.x.rank = p.out_rank;
@@ -173,15 +248,19 @@ sg_status backward(const char* what, const sg_layer* l, const Geometry& g, const
     u.p.X = x;
     v.p.U = (float*)((char*)workspace + u.bytes);
     v.p.X = dy;
+    char* rest = (char*)workspace + u.bytes + v.bytes;
+    sg::Grouped q;
+    sg::Adapted d{};
+    const bool tiles = T && dx && (uintptr_t)dy % 16 == 0 && tile_product(l, g, ad, v.p.plan, T, true, false, &q, &d);
     sg_status st = SG_OK;
     if (T && (dx || dA)) {
         st = launched(sg::launch_shrink(v.p, s), what);
-        if (!st) st = launched(sg::launch_finish(v.p, s), what);
+        if (!st) st = tiles ? finish(v.p, &d, rest, T, what, s) : launched(sg::launch_finish(v.p, nullptr, nullptr, s), what);
         v.p.slabs = 1;
     }
     if (!st && T && dB) {
         st = launched(sg::launch_shrink(u.p, s), what);
-        if (!st) st = launched(sg::launch_finish(u.p, s), what);
+        if (!st) st = launched(sg::launch_finish(u.p, nullptr, nullptr, s), what);
         u.p.slabs = 1;
     }
     if (!st && dA) {
@@ -206,9 +285,14 @@ sg_status backward(const char* what, const sg_layer* l, const Geometry& g, const
         p.out_dtype = d_dtype;
         st = launched(sg::launch_grad(p, s), what);
     }
-    if (!st && T && dx) {
+    if (!st && tiles) {
+        q.A = dy;
+        q.out = dx;
+        q.out_dtype = dx_dtype;
+        st = launched(sg::launch_adapted(q, d, s), what);
+    } else if (!st && T && dx) {
         // as forward: the frozen projection's part in fp32, rounded once with the adapters'
-        float* base = dx_dtype == SG_F32 ? (float*)dx : (float*)((char*)workspace + u.bytes + v.bytes);
+        float* base = dx_dtype == SG_F32 ? (float*)dx : (float*)rest;
         st = g.column() ? sg_all_to_sharded_backward(l, nullptr, dy, T, base, SG_F32, nullptr, SG_F32, nullptr, 0, stream)
                         : sg_sharded_to_all_backward(l, nullptr, dy, T, base, SG_F32, nullptr, SG_F32, nullptr, 0, stream);
         if (st) return st;
@@ -249,7 +333,10 @@ size_t sg_adapted_workspace(const sg_layer* l, const sg_adapters* ad, int64_t T)
     Geometry g;
     if (!l || !ad || T <= 0 || check_adapters(ad) || sg_layer_info(l, &g.out, &g.in, &g.mode, &g.S, &g.P, &g.dtype, &g.quantized))
         return 0;
-    return half(g, ad, nullptr, T, true).bytes + base_bytes(l, g, T);
+    // the projection's fp32 result and what its own call needs, or the operands of U
+    const size_t base = up256(T * g.out * 4) + (g.column() ? 0 : up256((int64_t)sg_sharded_to_all_workspace(l, T)));
+    const size_t ops = operands_bytes(T, ad->rank);
+    return half(g, ad, nullptr, T, true).bytes + (base > ops ? base : ops);
 }
 
 sg_status sg_adapted_all_to_sharded(const sg_layer* l, const sg_adapters* ad, const int32_t* plan, const void* x, int64_t T,
@@ -280,7 +367,8 @@ size_t sg_adapted_backward_workspace(const sg_layer* l, const sg_adapters* ad, i
     Geometry g;
     if (!l || !ad || T <= 0 || check_adapters(ad) || sg_layer_info(l, &g.out, &g.in, &g.mode, &g.S, &g.P, &g.dtype, &g.quantized))
         return 0;
-    return half(g, ad, nullptr, T, true).bytes + half(g, ad, nullptr, T, false).bytes + up256(T * g.in * 4);
+    const size_t base = up256(T * g.in * 4), ops = operands_bytes(T, ad->rank);
+    return half(g, ad, nullptr, T, true).bytes + half(g, ad, nullptr, T, false).bytes + (base > ops ? base : ops);
 }
 
 sg_status sg_adapted_all_to_sharded_backward(const sg_layer* l, const sg_adapters* ad, const int32_t* plan, const void* x,

@@ -6,7 +6,7 @@ namespace sg {
 namespace {
 
 // ---- expand -----------------------------------------------------------------
-// out[t(m)][c] = base[t(m)][c] + scale_a sum_j U[m][j] M[c][j].  Bound by reading
+// out[t(m)][c] = base[t(m)][c] + sum_j U[m][j] M[c][j].  Bound by reading
 // base and writing out.  A wave takes groups of 32 adjacent columns of one piece for
 // all rows of the tile; M's columns are dealt to the MFMA's rows so that a lane ends
 // up with eight adjacent ones (block i, row 4 c + e: column 8 c + 4 i + e).  TR: M is
@@ -26,7 +26,6 @@ __global__ __launch_bounds__(256) void expand_kernel(LowRank p, int groups, int 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int part = p.x.part, gpp = (part + 31) / 32, chunks = (p.rank + NR * 16 - 1) / (NR * 16);
     const uint16_t* M = (const uint16_t*)p.M + (adapted ? (int64_t)tile.a * p.rank * p.width : 0);
-    const float scale = adapted ? (p.scale ? p.scale[tile.a] : 1.0f) : 0.f;
 
     int64_t t[MB];
     bool live[MB];
@@ -50,12 +49,13 @@ __global__ __launch_bounds__(256) void expand_kernel(LowRank p, int groups, int 
                 f32x4 lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
                 if (live[b] && j < p.rp) {
                     const float* u = p.U + (int64_t)(tile.row0 + 16 * b + r16) * p.rp + j;
+#pragma unroll 4
                     for (int q = 0; q < p.slabs; ++q) lo += *(const f32x4*)(u + q * p.slab), hi += *(const f32x4*)(u + q * p.slab + 4);
                 }
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     // (ranks behind the last hold nothing: an infinite x times zeros)
-                    v[i][e] = j + e < p.rank ? scale * (e < 4 ? lo[e] : hi[e - 4]) : 0.f;
+                    v[i][e] = j + e < p.rank ? (e < 4 ? lo[e] : hi[e - 4]) : 0.f;
                     top = fmaxf(top, fabsf(v[i][e]));
                 }
             }

@@ -319,6 +319,9 @@ void set_weights(sg::Problem& p, const sg_layer* l) {
 }  // namespace
 
 std::string& sg::last_error() { return g_err; }
+sg::LayerView sg::layer_view(const sg_layer* l) {
+    return {l->w, !l->quantized && !l->mx && l->wfrag, l->bias != nullptr, l->rows_r, l->cols_r};
+}
 
 extern "C" {
 

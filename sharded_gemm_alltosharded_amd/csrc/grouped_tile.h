@@ -1,8 +1,9 @@
 // The grouped tile kernel (experts.h, Grouped): its code, and the choice of a tile.
 // experts.hip has the products that store their sums, experts_gated.hip those of the
-// gated block.
+// gated block, adapters_tile.hip those with low-rank adapters beside them.
 #pragma once
 
+#include "adapters.h"
 #include "gated.h"
 
 namespace sg {
@@ -58,8 +59,9 @@ __device__ __forceinline__ f32x4 swiglu4(f32x4 g, f32x4 u) {
 // Stores a wave's N x M result blocks: value(i, j) is this lane's four columns
 // 4 (lane >> 4) .. + 3 of output block ob0 + i, row row0 + 16 j + (lane & 15).
 // PAD: columns behind the piece's own may be asked for (p.pad; only SwiGLU has them).
-template <int DT, bool PAD, int N, int M, typename F>
-__device__ __forceinline__ void store_typed(const Grouped& p, int ob0, int row0, int nrows, F&& value) {
+// to_row(j): the output row of this lane's row of row block j.
+template <int DT, bool PAD, int N, int M, typename F, typename R>
+__device__ __forceinline__ void store_typed(const Grouped& p, int ob0, int row0, int nrows, F&& value, R&& to_row) {
     const int lane = threadIdx.x & 63;
     static_for<0, N>([&](auto ic) {
         constexpr int i = decltype(ic)::value;
@@ -79,15 +81,20 @@ __device__ __forceinline__ void store_typed(const Grouped& p, int ob0, int row0,
             float v[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = !PAD || e < live ? q[e] : 0.f;
-            store_cols<DT>(p.out, base + (int64_t)(row0 + m) * p.ldo, v, p.f - c);
+            store_cols<DT>(p.out, base + (int64_t)to_row(jc) * p.ldo, v, p.f - c);
         });
     });
 }
+template <bool PAD, int N, int M, typename F, typename R>
+__device__ __forceinline__ void store_blocks(const Grouped& p, int ob0, int row0, int nrows, F&& value, R&& to_row) {
+    if (p.out_dtype == SG_BF16) store_typed<SG_BF16, PAD, N, M>(p, ob0, row0, nrows, value, to_row);
+    else if (p.out_dtype == SG_F16) store_typed<SG_F16, PAD, N, M>(p, ob0, row0, nrows, value, to_row);
+    else store_typed<SG_F32, PAD, N, M>(p, ob0, row0, nrows, value, to_row);
+}
 template <bool PAD, int N, int M, typename F>
 __device__ __forceinline__ void store_blocks(const Grouped& p, int ob0, int row0, int nrows, F&& value) {
-    if (p.out_dtype == SG_BF16) store_typed<SG_BF16, PAD, N, M>(p, ob0, row0, nrows, value);
-    else if (p.out_dtype == SG_F16) store_typed<SG_F16, PAD, N, M>(p, ob0, row0, nrows, value);
-    else store_typed<SG_F32, PAD, N, M>(p, ob0, row0, nrows, value);
+    store_blocks<PAD, N, M>(p, ob0, row0, nrows, value,
+                            [&](auto jc) { return row0 + 16 * decltype(jc)::value + (int)(threadIdx.x & 15); });
 }
 
 // segment's first element of A
@@ -266,14 +273,127 @@ __device__ __forceinline__ void grad_blocks(const Grouped& p, const Gated& g, in
     });
 }
 
-// What becomes of a tile's sums (E_KEEP and E_GRAD: the gated block, gated.h)
-enum Epilogue { E_STORE = 0, E_KEEP = 1, E_GRAD = 2, E_SPLIT = 3 };
+// ---- adapters beside the product (adapters.h, Adapted) ------------------------
+// Adds U's rows through their adapters' matrices to the sums: after the inputs' steps,
+// one more for every sixteen ranks of every adapter that has rows here.  The operand of
+// a row is zero but for its own adapter.  Rows are grouped by adapter, so a tile of many
+// rows has few of them; of few rows, the matrices of several are loaded at once.
+// fp16: a row's operand is scaled by a power of two, and so are its sums here.
+template <bool F16, bool SWIGLU, bool TRANS, int N, int NBM, typename Acc>
+__device__ __forceinline__ void adapt_blocks(const Grouped& p, const Adapted& d, int ob0, int row0, int nrows, Acc& acc) {
+    constexpr int BA = N == 4 ? 1 : 4;         // adapters whose matrices are out at once
+    constexpr int JB = NBM < 4 ? NBM : 4;      // row blocks at a time (a lane a row)
+    const int lane = threadIdx.x & 63, r16 = lane & 15, c16 = lane >> 4;
+    const uint16_t* M = (const uint16_t*)d.M;
+    const int chunks = (d.rank + 15) / 16;
+    static_for<0, NBM / JB>([&](auto bc) ALWAYS_INLINE {
+        constexpr int j0 = decltype(bc)::value * JB;
+        const int first = row0 + 16 * j0, rows = min(nrows - 16 * j0, 16 * JB);
+        // the rows' adapters: of row `lane`, and of this lane's of each block
+        const int id = lane < rows ? d.plan.ids[first + lane] : -1;
+        const uint64_t all = __ballot(id >= 0 && id < d.plan.n);
+        if (!all) return;
+        int mine[JB];
+#pragma unroll
+        for (int j = 0; j < JB; ++j) mine[j] = __shfl(id, 16 * j + r16);
+        // (the operands of 16 rows and 16 ranks are 1 KB, a lane's 16 bytes)
+        auto load_u = [&](int j, int ch) ALWAYS_INLINE {
+            const bool in = mine[j] >= 0 && mine[j] < d.plan.n;
+            const u32x4 v = d.operands[in ? ((int64_t)(first / 16 + j) * chunks + ch) * 64 + lane : 0];
+            return in ? v : u32x4{0, 0, 0, 0};
+        };
+        [[maybe_unused]] int ex[JB];
+        if constexpr (F16) {
+#pragma unroll
+            for (int j = 0; j < JB; ++j)
+                ex[j] = mine[j] >= 0 && mine[j] < d.plan.n ? d.exponents[first + 16 * j + r16] : 0;
+            static_for<0, JB>([&](auto jc) ALWAYS_INLINE {
+                constexpr int j = decltype(jc)::value;
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[i][j0 + j][e] = ldexpf(acc[i][j0 + j][e], -ex[j]);
+            });
+        }
+        for (int ch = 0; ch < chunks; ++ch) {
+            uint64_t rem = all;
+            int a[BA];
+            u32x4 mf[BA][N];
+            auto load_matrices = [&]() ALWAYS_INLINE {
+                static_for<0, BA>([&](auto bc) ALWAYS_INLINE {
+                    constexpr int b = decltype(bc)::value;
+                    a[b] = -1;
+                    if (!rem) return;
+                    a[b] = __builtin_amdgcn_readlane(id, __builtin_ctzll(rem));
+                    rem &= ~__ballot(id == a[b]);
+                    const uint16_t* Ma = M + (int64_t)a[b] * d.rank * d.width;
+                    const int k = ch * 16 + 8 * (c16 & 1);
+                    static_for<0, N>([&](auto ic) ALWAYS_INLINE {
+                        constexpr int i = decltype(ic)::value;
+                        const int ob = ob0 + (SWIGLU ? i / 2 : i), piece = ob / p.bps, blk = ob - piece * p.bps;
+                        const int r = SWIGLU ? piece : piece / p.S, s = SWIGLU ? i & 1 : piece - r * p.S;
+                        const bool in = ob < p.nout && 16 * blk + r16 < p.f;
+                        const int64_t col = in ? (int64_t)(s * d.P + r) * p.f + 16 * blk + r16 : 0;  // unsharded
+                        if constexpr (TRANS) {
+#pragma unroll
+                            for (int e = 0; e < 8; e += 2) {
+                                const uint32_t lo = in && k + e < d.rank ? Ma[(int64_t)(k + e) * d.width + col] : 0;
+                                const uint32_t hi = in && k + e + 1 < d.rank ? Ma[(int64_t)(k + e + 1) * d.width + col] : 0;
+                                mf[b][i][e / 2] = lo | (hi << 16);
+                            }
+                        } else if (d.rank % 8 == 0) {
+                            const u32x4 v = *(const u32x4*)(in && k < d.rank ? Ma + col * d.rank + k : M);
+                            mf[b][i] = in && k < d.rank ? v : u32x4{0, 0, 0, 0};
+                        } else {
+                            mf[b][i] = row8<false>(Ma + col * d.rank, M, in && k < d.rank, k, d.rank);
+                        }
+                    });
+                });
+            };
+            load_matrices();
+            u32x4 uf[JB];
+#pragma unroll
+            for (int j = 0; j < JB; ++j) uf[j] = load_u(j, ch);
+            while (true) {
+                static_for<0, BA>([&](auto bc) ALWAYS_INLINE {
+                    constexpr int b = decltype(bc)::value;
+                    if (a[b] < 0) return;
+                    static_for<0, JB>([&](auto jc) ALWAYS_INLINE {
+                        constexpr int j = decltype(jc)::value;
+                        const bool own = mine[j] == a[b];
+                        if (!__ballot(own)) return;
+                        const u32x4 u = own ? uf[j] : u32x4{0, 0, 0, 0};
+#pragma unroll
+                        for (int i = 0; i < N; ++i) acc[i][j0 + j] = mfma16<F16>(mf[b][i], u, acc[i][j0 + j]);
+                    });
+                });
+                if (!rem) break;
+                load_matrices();
+            }
+        }
+        if constexpr (F16)
+            static_for<0, JB>([&](auto jc) ALWAYS_INLINE {
+                constexpr int j = decltype(jc)::value;
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[i][j0 + j][e] = ldexpf(acc[i][j0 + j][e], ex[j]);
+            });
+        asm volatile("" ::: "memory");  // (no load of the next row blocks' before)
+    });
+}
+
+// What becomes of a tile's sums (E_KEEP and E_GRAD: the gated block, gated.h; E_ADAPT:
+// adapters.h)
+enum Epilogue { E_STORE = 0, E_KEEP = 1, E_GRAD = 2, E_SPLIT = 3, E_ADAPT = 4 };
+template <int EPI>
+using Extra = std::conditional_t<EPI == E_ADAPT, Adapted, Gated>;
 
 // n tile nt of the rows of one slot; the stages may be larger than needed.  E_SPLIT:
 // part blockIdx.y of gridDim.y of the k tiles, stored in a slab of its own.
 template <int MODE, bool SWIGLU, bool TRANS, int TM, int BN, int NS, bool AL, int EPI>
 __device__ __forceinline__ void grouped_tile(const Grouped& p, const Slot s, const int nt, const Stages<NS>& stage,
-                                             const Gated& gated) {
+                                             const Extra<EPI>& extra) {
     using Shape = TileShape<MODE, TM, BN>;
     constexpr int WM = 2, WN = 4, NWV = WM * WN;
     constexpr int NBM = TM / WM / 16, NBN = BN / WN / 16;
@@ -377,11 +497,16 @@ __device__ __forceinline__ void grouped_tile(const Grouped& p, const Slot s, con
         if constexpr (TRANS) {
             const int kb = ik / 16 + f / (BN / 32), st = nt * (BN / 32) + f % (BN / 32);
             at = ((uint32_t)(iseg * (p.kpad / 16) + kb) * p.wsteps + st) * 1024u;
+            if constexpr (EPI == E_ADAPT) {  // (ranks' columns may be matrices of their own)
+                const int q = st / p.wsteps;
+                at = (uint32_t)q * extra.wrank + ((uint32_t)(iseg * (p.kpad / 16) + kb) * p.wsteps + st - q * p.wsteps) * 1024u;
+            }
             if constexpr (PERM) off = (uint32_t)(lane ^ (NBN == 4 ? (((f & 1) << 1) | (lane >> 5)) << 2 : (lane >> 4) << 2)) * 16;
-            if (kb >= p.kpad / 16 || st >= p.wsteps) off = kOutside, at = 0;
+            if (kb >= p.kpad / 16 || (EPI == E_ADAPT ? 2 * st >= p.nout : st >= p.wsteps)) off = kOutside, at = 0;
         } else {
             if constexpr (PERM) off = (uint32_t)(lane ^ ((f / FPB & 2) << 1)) * 16;
             at = wbase[i] + (uint32_t)(iseg * p.kpad + ik) / KST * 1024u;
+            if constexpr (EPI == E_ADAPT) at = wbase[i] + (uint32_t)iseg * extra.wseg + (uint32_t)ik / KST * 1024u;
             if (FPB * KST > KST && MX && ik + (f % FPB) * KST >= p.kpad) off = kOutside, at = 0;
         }
         dma16(buffer(W, bytes(p.w_expert)), off, at, sW + f * 1024);
@@ -581,30 +706,43 @@ __device__ __forceinline__ void grouped_tile(const Grouped& p, const Slot s, con
 
     constexpr int NO = SWIGLU ? NBN / 2 : NBN;  // output blocks of a wave
     const int m0 = wave_m * NBM * 16;
+    [[maybe_unused]] int rows_to[NBM];
     if constexpr (EPI == E_KEEP) {
-        keep_blocks<MODE == G_F16, NO, NBM, WN>(p, gated, nt * NO * WN + wave_n * NO, s.row0 + m0, s.nrows - m0, acc,
+        keep_blocks<MODE == G_F16, NO, NBM, WN>(p, extra, nt * NO * WN + wave_n * NO, s.row0 + m0, s.nrows - m0, acc,
                                                 (uint32_t*)stage.A[0]);
         if constexpr (NO == 2) return;
     } else if constexpr (EPI == E_GRAD) {
-        grad_blocks<MODE == G_F16, NO, NBM>(p, gated, nt * NO * WN + wave_n * NO, s.row0 + m0, s.nrows - m0, acc);
+        grad_blocks<MODE == G_F16, NO, NBM>(p, extra, nt * NO * WN + wave_n * NO, s.row0 + m0, s.nrows - m0, acc);
         return;
+    } else if constexpr (EPI == E_ADAPT) {
+#pragma unroll
+        for (int j = 0; j < NBM; ++j)  // (all at once, before the stores)
+            rows_to[j] = m0 + 16 * j + r16 < s.nrows ? token(extra.plan, s.row0 + m0 + 16 * j + r16) : 0;
+        adapt_blocks<MODE == G_F16, SWIGLU, TRANS, NBN, NBM>(p, extra, nt * NO * WN + wave_n * NO, s.row0 + m0, s.nrows - m0,
+                                                             acc);
     }
     const Grouped* to = &p;
     [[maybe_unused]] Grouped part;
     if constexpr (EPI == E_SPLIT) {
         part = p;
-        part.out = (float*)p.out + blockIdx.y * gated.slab;
+        part.out = (float*)p.out + blockIdx.y * extra.slab;
         to = &part;
     }
-    store_blocks<SWIGLU, NO, NBM>(*to, nt * NO * WN + wave_n * NO, s.row0 + m0, s.nrows - m0, [&](auto ic, auto jc, auto near) {
+    auto value = [&](auto ic, auto jc, auto near) {
         constexpr int i = decltype(ic)::value, j = decltype(jc)::value;
         if constexpr (!SWIGLU) return acc[i][j];
         else return swiglu4<decltype(near)::value>(acc[2 * i][j], acc[2 * i + 1][j]);
-    });
+    };
+    const int ob0 = nt * NO * WN + wave_n * NO;
+    if constexpr (EPI == E_ADAPT)
+        store_blocks<SWIGLU, NO, NBM>(*to, ob0, s.row0 + m0, s.nrows - m0, value,
+                                      [&](auto jc) { return rows_to[decltype(jc)::value]; });
+    else
+        store_blocks<SWIGLU, NO, NBM>(*to, ob0, s.row0 + m0, s.nrows - m0, value);
 }
 
 template <int MODE, bool SWIGLU, bool TRANS, int TM, int BN, int NS, bool AL, int EPI>
-__global__ __launch_bounds__(512) void grouped_tile_kernel(Grouped p, int slots, int tiles_n, int cus, Gated gated) {
+__global__ __launch_bounds__(512) void grouped_tile_kernel(Grouped p, int slots, int tiles_n, int cus, Extra<EPI> extra) {
     using Shape = TileShape<MODE, TM, BN>;
     constexpr bool R = NS >= 3, Q = NS == 4;  // (a ring of two, three or four)
     static_assert(NS >= 2 && NS <= 4, "stages");
@@ -646,7 +784,7 @@ __global__ __launch_bounds__(512) void grouped_tile_kernel(Grouped p, int slots,
     if ((int)blockIdx.x < tiles) {
         const Slot s = slot_of(xcd_remap(blockIdx.x, tiles), nt);
         if (s.e < 0) return;
-        grouped_tile<MODE, SWIGLU, TRANS, TM, BN, NS, AL, EPI>(p, s, nt, stage, gated);
+        grouped_tile<MODE, SWIGLU, TRANS, TM, BN, NS, AL, EPI>(p, s, nt, stage, extra);
     } else if constexpr (TM == 256) {
         if ((int)blockIdx.x >= tiles + 4 * rest) return;
         const int q = xcd_remap(blockIdx.x - tiles, 4 * rest);
@@ -654,20 +792,22 @@ __global__ __launch_bounds__(512) void grouped_tile_kernel(Grouped p, int slots,
         s.row0 += (q & 1) * 128;
         s.nrows = min(s.nrows - (q & 1) * 128, 128);
         if (s.e < 0 || s.nrows <= 0) return;
-        grouped_tile<MODE, SWIGLU, TRANS, 128, BN / 2, NS, AL, EPI>(p, s, 2 * nt + ((q >> 1) & 1), stage, gated);
+        grouped_tile<MODE, SWIGLU, TRANS, 128, BN / 2, NS, AL, EPI>(p, s, 2 * nt + ((q >> 1) & 1), stage, extra);
     }
 }
 
 template <int MODE, bool SWIGLU, bool TRANS, int TM, int BN, int NS, bool AL, int EPI = E_STORE>
-hipError_t tile_launch(const Grouped& p, hipStream_t s, const Gated& gated = Gated{}) {
+hipError_t tile_launch(const Grouped& p, hipStream_t s, const Extra<EPI>& extra = Extra<EPI>{}) {
     constexpr int NB = SWIGLU ? BN / 32 : BN / 16;
     const int64_t slots = p.R / TM + (p.R < p.E ? p.R : p.E);
     const int64_t tiles_n = (p.nout + NB - 1) / NB;
     const int cus = device_cus();
     const int64_t blocks = slots * tiles_n + (TM == 256 ? 3 * (cus / 2) : 0);
     if (blocks >= kMaxBlocks / 2) return hipErrorInvalidConfiguration;
-    launch(grouped_tile_kernel<MODE, SWIGLU, TRANS, TM, BN, NS, AL, EPI>,
-           dim3((unsigned)blocks, EPI == E_SPLIT ? gated.splits : 1), dim3(512), 0, s, p, (int)slots, (int)tiles_n, cus, gated);
+    int parts = 1;
+    if constexpr (EPI == E_SPLIT) parts = extra.splits;
+    launch(grouped_tile_kernel<MODE, SWIGLU, TRANS, TM, BN, NS, AL, EPI>, dim3((unsigned)blocks, parts), dim3(512), 0, s, p,
+           (int)slots, (int)tiles_n, cus, extra);
     return hipGetLastError();
 }
 
@@ -698,43 +838,43 @@ bool few_tiles(const Grouped& p) {
 //   8 x (4096 x 14336)          m = 32: 200 204 318   96: 229 237 323  192: 434 271 360   256: 476 498 385
 //   32 x (2048 x 2048, SwiGLU)  m = 32:  55  55  62   48:  66  57  64  128:  88  84  72   256: 146 118 125
 template <int MODE, bool SWIGLU, bool TRANS, bool AL, int EPI = E_STORE>
-hipError_t tile_mode(const Grouped& p, hipStream_t s, const Gated& gated = Gated{}) {
+hipError_t tile_mode(const Grouped& p, hipStream_t s, const Extra<EPI>& extra = Extra<EPI>{}) {
     if constexpr (!AL && MODE == G_MX4) {
-        return tile_launch<MODE, SWIGLU, TRANS, 128, 128, 2, false, EPI>(p, s, gated);
+        return tile_launch<MODE, SWIGLU, TRANS, 128, 128, 2, false, EPI>(p, s, extra);
     } else if constexpr (!AL) {
         // Rows through registers: times round the chip, of two or three workgroups
         // a compute unit.  us, 128 x 128 / 64 x 128 / the latter in three stages:
         // 8 x (2046 x 4094) m = 125: 100 76 73   gate|up of 8 x (8188 x 2046): 131 115 123
         // 8 x (4094 x 4094) m = 500: 354 318 390   32 x (1022 x 2046) m = 188: 66 79 75
         const int64_t cus = device_cus();
-        if (few_tiles<SWIGLU, 64>(p)) return tile_launch<MODE, SWIGLU, TRANS, 64, 128, 3, false, EPI>(p, s, gated);
+        if (few_tiles<SWIGLU, 64>(p)) return tile_launch<MODE, SWIGLU, TRANS, 64, 128, 3, false, EPI>(p, s, extra);
         const int64_t wide = (tiles_of<SWIGLU, 128>(p) + 2 * cus - 1) / (2 * cus);
         const int64_t narrow = (tiles_of<SWIGLU, 64>(p) + 3 * cus - 1) / (3 * cus);
-        if (3 * narrow <= 4 * wide) return tile_launch<MODE, SWIGLU, TRANS, 64, 128, 2, false, EPI>(p, s, gated);
-        return tile_launch<MODE, SWIGLU, TRANS, 128, 128, 2, false, EPI>(p, s, gated);
+        if (3 * narrow <= 4 * wide) return tile_launch<MODE, SWIGLU, TRANS, 64, 128, 2, false, EPI>(p, s, extra);
+        return tile_launch<MODE, SWIGLU, TRANS, 128, 128, 2, false, EPI>(p, s, extra);
     } else if constexpr (MODE == G_MX4) {
         // (turning codes into operands costs the narrow tile as much as its few
         // rows' products; gate|up, 64 x 128 / 128 x 256:  m = 64: 185 222  256: 552 531  1024: 1987 1742,
         // down  64: 126 174  256: 280 364  1024: 960 938)
         const int64_t tiles = (p.R / 128 + p.E / 2) * ((p.nout + 15) / 16) * (SWIGLU ? 2 : 1);
         if (p.R >= (int64_t)192 * p.E && tiles >= (int64_t)device_cus() * 6)
-            return tile_launch<MODE, SWIGLU, TRANS, 128, 256, 2, true, EPI>(p, s, gated);
-        if (few_tiles<SWIGLU, 64>(p)) return tile_launch<MODE, SWIGLU, TRANS, 64, 128, 4, true, EPI>(p, s, gated);
-        return tile_launch<MODE, SWIGLU, TRANS, 64, 128, 2, true, EPI>(p, s, gated);
+            return tile_launch<MODE, SWIGLU, TRANS, 128, 256, 2, true, EPI>(p, s, extra);
+        if (few_tiles<SWIGLU, 64>(p)) return tile_launch<MODE, SWIGLU, TRANS, 64, 128, 4, true, EPI>(p, s, extra);
+        return tile_launch<MODE, SWIGLU, TRANS, 64, 128, 2, true, EPI>(p, s, extra);
     } else {
         // (MXFP4 products are so short that a wave of tiles more costs them a
         // wider tile's gain: 512 rows of 8 experts, gate|up 461 429, down 221 256)
         const int64_t tiles = (p.R / 256 + p.E / 2) * ((p.nout + 15) / 16) * (SWIGLU ? 2 : 1);
         if (p.R >= (int64_t)128 * p.E && tiles * 10 >= (int64_t)device_cus() * (MODE == G_MX4A4 ? 40 : 7))
-            return tile_launch<MODE, SWIGLU, TRANS, 256, 256, 2, true, EPI>(p, s, gated);
+            return tile_launch<MODE, SWIGLU, TRANS, 256, 256, 2, true, EPI>(p, s, extra);
         // (few narrow tiles go before few wide ones: 256 rows of 4096 x 4096 27 32, 500 rows
         // of 2 x (2048 x 2048) 15 19)
-        if (few_tiles<SWIGLU, 64>(p)) return tile_launch<MODE, SWIGLU, TRANS, 64, 128, 4, true, EPI>(p, s, gated);
+        if (few_tiles<SWIGLU, 64>(p)) return tile_launch<MODE, SWIGLU, TRANS, 64, 128, 4, true, EPI>(p, s, extra);
         if (p.R > (int64_t)40 * p.E) {
-            if (few_tiles<SWIGLU, 128>(p)) return tile_launch<MODE, SWIGLU, TRANS, 128, 128, 4, true, EPI>(p, s, gated);
-            return tile_launch<MODE, SWIGLU, TRANS, 128, 128, 2, true, EPI>(p, s, gated);
+            if (few_tiles<SWIGLU, 128>(p)) return tile_launch<MODE, SWIGLU, TRANS, 128, 128, 4, true, EPI>(p, s, extra);
+            return tile_launch<MODE, SWIGLU, TRANS, 128, 128, 2, true, EPI>(p, s, extra);
         }
-        return tile_launch<MODE, SWIGLU, TRANS, 64, 128, 2, true, EPI>(p, s, gated);
+        return tile_launch<MODE, SWIGLU, TRANS, 64, 128, 2, true, EPI>(p, s, extra);
     }
 }
 

@@ -149,6 +149,14 @@ __host__ __device__ inline int64_t q4_group_offset(int64_t row, int64_t g, int64
     return (((row >> 5) * (groups >> 2) + (g >> 2)) * 32 + (row & 31)) * 4 + (g & 3);
 }
 
+// what other files need of a dense layer: its weights, fragment-major
+struct LayerView {
+    const void* w;
+    int wfrag, bias;
+    int64_t rows_r, cols_r;  // of one rank's matrix
+};
+LayerView layer_view(const sg_layer* l);
+
 // launchers (return hipError_t of the launch)
 hipError_t launch_generic(const Problem& p, hipStream_t s);
 hipError_t launch_tile(const Problem& p, hipStream_t s, int variant);

@@ -37,7 +37,7 @@ def test_plan_holds_every_grouping(L, T, n):
     """Offsets, rows and as many tiles as the tokens can make up, however they fall."""
     height = 64 if T >= 32 * (n + 1) else 16
     ints = L.sg_adapter_plan_ints(T, n)
-    tiles = (ints - (n + 2 + T + 3) // 4 * 4) // 4
+    tiles = (ints - (n + 2 + 2 * T + 3) // 4 * 4) // 4
     groups = min(T, n + 1)
     # the most tiles: every group but one has a single row in its last tile
     assert tiles >= (groups + (T - groups) // height if T else 0)

@@ -56,8 +56,10 @@ def test_plan(T, n):
     data = p.data.cpu().tolist()
     offsets, rows = aref.plan(which, n)
     assert data[:n + 2] == offsets and data[n + 2:n + 2 + T] == rows
+    group = [int(w) if 0 <= int(w) < n else n for w in which]
+    assert data[n + 2 + T:n + 2 + 2 * T] == [group[t] for t in rows]
     height = 64 if T >= 32 * (n + 1) else 16
-    at = (n + 2 + T + 3) // 4 * 4
+    at = (n + 2 + 2 * T + 3) // 4 * 4
     tiles = [tuple(data[i:i + 3]) for i in range(at, len(data) // 4 * 4, 4)]
     want = [(a, r, min(height, offsets[a + 1] - r)) for a in range(n + 1)
             for r in range(offsets[a], offsets[a + 1], height)]

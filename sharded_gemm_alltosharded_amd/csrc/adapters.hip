@@ -429,13 +429,13 @@ hipError_t launch_adapter_plan(const int32_t* which, int64_t T, int n, int32_t* 
     return hipGetLastError();
 }
 
-// As many slabs as give every compute unit two workgroups, of four steps a wave at
+// As many slabs as give every compute unit four workgroups, of four steps a wave at
 // least: a compute unit takes about 75 GB/s, so few of them are slow whatever their
 // waves (16 tokens of 16 adapters, 4096 inputs: 5 us, 9 in one slab of sixteen waves).
-// At most eight: every reader of U adds them up.
+// At most sixteen: somebody adds them up.
 int shrink_slabs(const Plan& p, int64_t width, int rank) {
-    const int64_t blocks = (int64_t)p.ntiles * ((rank + 63) / 64), want = (2 * device_cus() + blocks - 1) / blocks;
-    const int64_t most = width / 512 < 8 ? width / 512 : 8;
+    const int64_t blocks = (int64_t)p.ntiles * ((rank + 63) / 64), want = (4 * device_cus() + blocks - 1) / blocks;
+    const int64_t most = width / 512 < 16 ? width / 512 : 16;
     return (int)(want < most ? want : most > 1 ? most : 1);
 }
 

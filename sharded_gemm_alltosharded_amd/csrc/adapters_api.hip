@@ -201,6 +201,11 @@ sg_status forward(const char* what, const sg_layer* l, const Geometry& g, const 
         st = finish(p, &d, (char*)workspace + u.bytes, T, what, s);
         return st ? st : launched(sg::launch_adapted(q, d, s), what);
     }
+    // (many rows' sums are added up once, few by every workgroup that wants them)
+    if (p.plan.tile_rows > 16) {
+        if ((st = launched(sg::launch_finish(p, nullptr, nullptr, s), what))) return st;
+        p.slabs = 1;
+    }
     // the projection's result stays in fp32 until the adapters' part is added, so that y
     // is rounded once; an fp32 y holds it itself
     const bool swiglu = epilogue == SG_EPI_SWIGLU, in_y = y_dtype == SG_F32 && !swiglu;
@@ -251,7 +256,8 @@ sg_status backward(const char* what, const sg_layer* l, const Geometry& g, const
     char* rest = (char*)workspace + u.bytes + v.bytes;
     sg::Grouped q;
     sg::Adapted d{};
-    const bool tiles = T && dx && (uintptr_t)dy % 16 == 0 && tile_product(l, g, ad, v.p.plan, T, true, false, &q, &d);
+    const bool tiles = T && dx && (uintptr_t)dy % 16 == 0 && (uintptr_t)ad->A % 16 == 0 &&
+                       tile_product(l, g, ad, v.p.plan, T, true, false, &q, &d);
     sg_status st = SG_OK;
     if (T && (dx || dA)) {
         st = launched(sg::launch_shrink(v.p, s), what);

@@ -147,6 +147,7 @@ template <int NS>
 struct Stages {
     uint8_t *A[NS], *W[NS];
     uint32_t *SW[NS], *SA[NS];
+    uint8_t* M;  // adapt_blocks'
 };
 
 // ---- the gated block's epilogues (gated.h) ------------------------------------
@@ -280,12 +281,24 @@ __device__ __forceinline__ void grad_blocks(const Grouped& p, const Gated& g, in
 // rows has few of them; of few rows, the matrices of several are loaded at once.
 // fp16: a row's operand is scaled by a power of two, and so are its sums here.
 template <bool F16, bool SWIGLU, bool TRANS, int N, int NBM, typename Acc>
-__device__ __forceinline__ void adapt_blocks(const Grouped& p, const Adapted& d, int ob0, int row0, int nrows, Acc& acc) {
-    constexpr int BA = N == 4 ? 1 : 4;         // adapters whose matrices are out at once
-    constexpr int JB = NBM < 4 ? NBM : 4;      // row blocks at a time (a lane a row)
+__device__ __forceinline__ void adapt_blocks(const Grouped& p, const Adapted& d, int ob0, int row0, int nrows, Acc& acc,
+                                             uint8_t* lds) {
+    constexpr int BA = N == 4 ? 1 : TRANS ? 2 : 4;  // adapters whose matrices are out at once
+    constexpr int JB = NBM < 4 ? NBM : 4;           // row blocks at a time (a lane a row)
+    [[maybe_unused]] uint8_t* mine_lds = lds + (threadIdx.x >> 6) * (BA * N * 512);
     const int lane = threadIdx.x & 63, r16 = lane & 15, c16 = lane >> 4;
     const uint16_t* M = (const uint16_t*)d.M;
     const int chunks = (d.rank + 15) / 16;
+    // TRANS: the first of this lane's eight unsharded columns of block 2 i + lane / 32, -1
+    // where there is none
+    [[maybe_unused]] int col8[N / 2];
+    if constexpr (TRANS)
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            const int ob = ob0 + 2 * i + (lane >> 5), piece = ob / p.bps, c = 16 * (ob - piece * p.bps) + 8 * (lane & 1);
+            const int r = piece / p.S, s = piece - r * p.S;
+            col8[i] = ob < p.nout && c < p.f ? (s * d.P + r) * p.f + c : -1;
+        }
     static_for<0, NBM / JB>([&](auto bc) ALWAYS_INLINE {
         constexpr int j0 = decltype(bc)::value * JB;
         const int first = row0 + 16 * j0, rows = min(nrows - 16 * j0, 16 * JB);
@@ -327,28 +340,44 @@ __device__ __forceinline__ void adapt_blocks(const Grouped& p, const Adapted& d,
                     a[b] = __builtin_amdgcn_readlane(id, __builtin_ctzll(rem));
                     rem &= ~__ballot(id == a[b]);
                     const uint16_t* Ma = M + (int64_t)a[b] * d.rank * d.width;
-                    const int k = ch * 16 + 8 * (c16 & 1);
-                    static_for<0, N>([&](auto ic) ALWAYS_INLINE {
-                        constexpr int i = decltype(ic)::value;
-                        const int ob = ob0 + (SWIGLU ? i / 2 : i), piece = ob / p.bps, blk = ob - piece * p.bps;
-                        const int r = SWIGLU ? piece : piece / p.S, s = SWIGLU ? i & 1 : piece - r * p.S;
-                        const bool in = ob < p.nout && 16 * blk + r16 < p.f;
-                        const int64_t col = in ? (int64_t)(s * d.P + r) * p.f + 16 * blk + r16 : 0;  // unsharded
-                        if constexpr (TRANS) {
-#pragma unroll
-                            for (int e = 0; e < 8; e += 2) {
-                                const uint32_t lo = in && k + e < d.rank ? Ma[(int64_t)(k + e) * d.width + col] : 0;
-                                const uint32_t hi = in && k + e + 1 < d.rank ? Ma[(int64_t)(k + e + 1) * d.width + col] : 0;
-                                mf[b][i][e / 2] = lo | (hi << 16);
+                    [[maybe_unused]] const int k = ch * 16 + 8 * (c16 & 1);
+                    if constexpr (TRANS) {  // sixteen ranks of 16 columns, 32 bytes each, through LDS
+                        static_for<0, N / 2>([&](auto ic) ALWAYS_INLINE {
+                            constexpr int i = decltype(ic)::value;
+                            const int j = ch * 16 + (lane >> 1 & 15);
+                            const bool in = col8[i] >= 0 && j < d.rank;
+                            const u32x4 v = *(const u32x4*)(in ? Ma + (int64_t)j * d.width + col8[i] : M);
+                            mf[b][i] = in ? v : u32x4{0, 0, 0, 0};
+                        });
+                    } else {
+                        static_for<0, N>([&](auto ic) ALWAYS_INLINE {
+                            constexpr int i = decltype(ic)::value;
+                            const int ob = ob0 + (SWIGLU ? i / 2 : i), piece = ob / p.bps, blk = ob - piece * p.bps;
+                            const int r = SWIGLU ? piece : piece / p.S, s = SWIGLU ? i & 1 : piece - r * p.S;
+                            const bool in = ob < p.nout && 16 * blk + r16 < p.f;
+                            const int64_t col = in ? (int64_t)(s * d.P + r) * p.f + 16 * blk + r16 : 0;  // unsharded
+                            if (d.rank % 8 == 0) {
+                                const u32x4 v = *(const u32x4*)(in && k < d.rank ? Ma + col * d.rank + k : M);
+                                mf[b][i] = in && k < d.rank ? v : u32x4{0, 0, 0, 0};
+                            } else {
+                                mf[b][i] = row8<false>(Ma + col * d.rank, M, in && k < d.rank, k, d.rank);
                             }
-                        } else if (d.rank % 8 == 0) {
-                            const u32x4 v = *(const u32x4*)(in && k < d.rank ? Ma + col * d.rank + k : M);
-                            mf[b][i] = in && k < d.rank ? v : u32x4{0, 0, 0, 0};
-                        } else {
-                            mf[b][i] = row8<false>(Ma + col * d.rank, M, in && k < d.rank, k, d.rank);
-                        }
-                    });
+                        });
+                    }
                 });
+                if constexpr (TRANS) {
+                    lds_order();
+#pragma unroll
+                    for (int b = 0; b < BA; ++b)
+#pragma unroll
+                        for (int i = 0; i < N / 2; ++i) *(u32x4*)(mine_lds + (b * N / 2 + i) * 1024 + lane * 16) = mf[b][i];
+                    lds_order();
+#pragma unroll
+                    for (int b = 0; b < BA; ++b)
+#pragma unroll
+                        for (int i = 0; i < N; ++i)
+                            mf[b][i] = read_columns(mine_lds + (b * N + i) * 512, 8 * (c16 & 1) + (r16 >> 2), 32, 8 * (r16 & 3));
+                }
             };
             load_matrices();
             u32x4 uf[JB];
@@ -719,7 +748,7 @@ __device__ __forceinline__ void grouped_tile(const Grouped& p, const Slot s, con
         for (int j = 0; j < NBM; ++j)  // (all at once, before the stores)
             rows_to[j] = m0 + 16 * j + r16 < s.nrows ? token(extra.plan, s.row0 + m0 + 16 * j + r16) : 0;
         adapt_blocks<MODE == G_F16, SWIGLU, TRANS, NBN, NBM>(p, extra, nt * NO * WN + wave_n * NO, s.row0 + m0, s.nrows - m0,
-                                                             acc);
+                                                             acc, stage.M);
     }
     const Grouped* to = &p;
     [[maybe_unused]] Grouped part;
@@ -750,7 +779,11 @@ __global__ __launch_bounds__(512) void grouped_tile_kernel(Grouped p, int slots,
         sA2[R ? Shape::A : 4], sA3[Q ? Shape::A : 4], sW2[R ? Shape::W : 4], sW3[Q ? Shape::W : 4];
     __shared__ uint32_t sSW0[Shape::SW], sSW1[Shape::SW], sSA0[Shape::SA], sSA1[Shape::SA], sSW2[R ? Shape::SW : 1],
         sSW3[Q ? Shape::SW : 1], sSA2[R ? Shape::SA : 1], sSA3[Q ? Shape::SA : 1];
+    // (an array of its own, too: as part of a stage, it made the stages' reads wait for each
+    // other's loads)
+    __shared__ __attribute__((aligned(16))) uint8_t sM[EPI == E_ADAPT && TRANS ? 16384 : 4];
     Stages<NS> stage;
+    stage.M = sM;
     stage.A[0] = sA0, stage.W[0] = sW0, stage.SW[0] = sSW0, stage.SA[0] = sSA0;
     stage.A[1] = sA1, stage.W[1] = sW1, stage.SW[1] = sSW1, stage.SA[1] = sSA1;
     if constexpr (R) {

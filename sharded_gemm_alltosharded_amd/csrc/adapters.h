@@ -79,7 +79,7 @@ struct Adapted {
     // from one rank's output columns, to the next
     uint32_t wseg, wrank;
 };
-// transposed or not, p.rows the plan's; 16-byte rows of x
+// transposed or not, p.rows the plan's
 hipError_t launch_adapted(const Grouped& p, const Adapted& d, hipStream_t s);
 // whether that beats the product's own kernel and expand behind it
 bool adapted_fills(const Grouped& p);

@@ -108,61 +108,62 @@ sg_status check_ws(const char* what, const void* ws, size_t bytes, size_t need) 
     return SG_OK;
 }
 
-// The projection's product over the plan's rows, x W^T or (transposed) dy W, straight
-// from the layer's fragments; false where they, or the tokens, do not suit the tiles.
-bool tile_product(const sg_layer* l, const Geometry& g, const sg_adapters* ad, const sg::Plan& plan, int64_t T,
-                  bool transposed, bool swiglu, sg::Grouped* to, sg::Adapted* d) {
-    const sg::LayerView v = sg::layer_view(l);
-    const int64_t f = g.part(), rank_bytes = v.rows_r * v.cols_r * 2;  // f: of the sharded side
-    // whole 16-row blocks and 64-input tiles of every part, 32-column fragments of a
-    // transposed product's outputs, and 32-bit offsets
-    if (!v.wfrag || v.bias || g.out % 16 || g.in % 64 || f % (g.column() ? 16 : 64) || rank_bytes * g.P >= 0xffff0000ll ||
-        (double)T * (double)(g.in > g.out ? g.in : g.out) * 2 >= (double)0xffff0000ll)
-        return false;
-    sg::Grouped p{};
+// The projection's product over the plan's rows, x W^T or (transposed) dy W, from the
+// layer's fragments.  to->W null where they, or the tokens, do not suit the tiles.
+sg_status tile_product(const sg_layer* l, const Geometry& g, const sg_adapters* ad, const sg::Plan& plan, int64_t T,
+                       bool transposed, bool swiglu, hipStream_t stream, sg::Grouped* to, sg::Adapted* d) {
+    sg::Grouped& p = *to;
+    p = sg::Grouped{};
+    const int64_t f = g.part(), rank_width = g.S * f;  // of the sharded side
+    // (a rank's segments of a sharded-to-all layer lie side by side in its matrix: of whole
+    // blocks and without padding behind them, where there are several)
+    if (g.quantized || (!g.column() && g.S > 1 && (f % 16 || rank_width % 64)) ||
+        (double)T * (double)(g.in > g.out ? g.in : g.out) * 2 >= (double)0xffff0000ll ||
+        (double)((g.out + 15 + 16 * g.S * g.P) * (g.in + 63 + 64 * g.P)) * 2 >= (double)0xffff0000ll)
+        return SG_OK;
     p.mode = g.dtype == SG_F16 ? sg::G_F16 : sg::G_BF16;
     p.rows = plan.rows;
     p.kdiv = 1;
     p.T = p.R = (int)T;
     p.E = 1;
-    p.W = (const uint8_t*)v.w;
-    p.w_expert = rank_bytes * g.P;
     p.transposed = transposed;
     p.swiglu = swiglu;
-    p.wsteps = (int)(v.cols_r / 32);
     const bool in_sharded = g.column() == transposed;  // the product's input is the sharded side
     const int64_t width = transposed ? g.out : g.in, cols = transposed ? g.in : g.out;
-    // input: ranks' pieces, or whole rows
-    p.a_pieces = in_sharded ? g.S : 1;
-    p.nseg = in_sharded ? g.S * g.P : 1;
-    p.kl = p.kpad = (int)(in_sharded ? f : width);
-    p.lda = in_sharded ? g.S * f : width;
-    p.a_rank = in_sharded ? T * g.S * f : 0;
-    if (in_sharded && !g.column()) {  // a rank's segments lie side by side in its matrix
-        p.a_pieces = 1;
-        p.nseg = g.P;
-        p.kl = p.kpad = (int)(g.S * f);
-    }
-    // output
-    const bool out_sharded = !in_sharded;
-    const int64_t fo = out_sharded ? f : cols;
-    p.f = (int)fo;
-    p.bps = (int)(fo / 16);
-    p.S = swiglu ? 1 : out_sharded ? g.S : 1;
-    p.nout = (int)(swiglu ? cols / 32 : cols / 16);
-    p.ldo = swiglu ? fo : out_sharded ? g.S * fo : cols;
-    p.o_rank = out_sharded ? T * p.ldo : 0;
+    const int64_t rows16 = ((g.column() ? f : g.out) + 15) / 16 * 16;  // of a part, or of a rank's matrix
+    const int64_t cols64 = ((g.column() ? g.in : rank_width) + 63) / 64 * 64;
+    // input: the parts of an all-to-sharded layer's output, the ranks' rows of a
+    // sharded-to-all layer's input, or whole rows
+    p.a_pieces = in_sharded && g.column() ? g.S : 1;
+    p.nseg = !in_sharded ? 1 : g.column() ? g.S * g.P : g.P;
+    p.kl = (int)(!in_sharded ? width : g.column() ? f : rank_width);
+    p.kpad = (int)(transposed ? rows16 : cols64);
+    p.lda = in_sharded ? rank_width : width;
+    p.a_rank = in_sharded ? T * rank_width : 0;
+    // output: parts of f columns each; the one of a rank of a sharded-to-all layer with the
+    // padding of its matrix
+    const bool parts = !in_sharded && (g.column() || g.S > 1);
+    p.S = swiglu || !parts ? 1 : g.S;
+    p.f = (int)(parts ? f : in_sharded ? cols : rank_width);
+    p.bps = (int)(parts ? (f + 15) / 16 : transposed ? cols64 / 16 : rows16 / 16);
+    p.nout = (int)(p.bps * (in_sharded ? 1 : g.P) * (parts && !swiglu ? g.S : 1));
+    p.ldo = in_sharded ? cols : swiglu ? f : rank_width;
+    p.o_rank = in_sharded ? 0 : T * p.ldo;
     d->plan = plan;
     d->rank = ad->rank;
     d->M = transposed ? ad->A : ad->B;
     d->width = cols;
-    d->P = out_sharded ? g.P : 1;
-    // all-to-sharded: the ranks' rows are one stack; sharded-to-all: a matrix each
-    d->wseg = (uint32_t)rank_bytes;
-    d->wrank = (uint32_t)rank_bytes;
-    if (!sg::adapted_fills(p)) return false;
-    *to = p;
-    return true;
+    d->P = in_sharded ? 1 : g.P;
+    if (!sg::adapted_fills(p)) return SG_OK;
+    sg::LayerTiles v;
+    if (sg_status st = launched(sg::layer_tiles(l, stream, &v), "weight layout")) return st;
+    if (v.bias) return SG_OK;
+    const int64_t matrix = v.blocks * v.steps * 1024;
+    p.W = (const uint8_t*)v.w;
+    p.w_expert = matrix * (g.column() ? 1 : g.P);
+    p.wsteps = (int)v.steps;
+    d->wseg = d->wrank = (uint32_t)matrix;
+    return SG_OK;
 }
 
 // U's sums, and its operands for the tiles, at `at` (operands_bytes)
@@ -192,8 +193,8 @@ sg_status forward(const char* what, const sg_layer* l, const Geometry& g, const 
     const bool gathered = g.column() && out_layout == SG_OUT_FULL;
     sg::Grouped q;
     sg::Adapted d{};
-    if ((uintptr_t)x % 16 == 0 && (uintptr_t)ad->B % 16 == 0 &&
-        tile_product(l, g, ad, p.plan, T, false, epilogue == SG_EPI_SWIGLU, &q, &d)) {
+    if ((st = tile_product(l, g, ad, p.plan, T, false, epilogue == SG_EPI_SWIGLU, s, &q, &d))) return st;
+    if (q.W) {
         q.A = x;
         q.out = y;
         q.out_dtype = y_dtype;
@@ -254,11 +255,11 @@ sg_status backward(const char* what, const sg_layer* l, const Geometry& g, const
     v.p.U = (float*)((char*)workspace + u.bytes);
     v.p.X = dy;
     char* rest = (char*)workspace + u.bytes + v.bytes;
-    sg::Grouped q;
+    sg::Grouped q{};
     sg::Adapted d{};
-    const bool tiles = T && dx && (uintptr_t)dy % 16 == 0 && (uintptr_t)ad->A % 16 == 0 &&
-                       tile_product(l, g, ad, v.p.plan, T, true, false, &q, &d);
     sg_status st = SG_OK;
+    if (T && dx && (st = tile_product(l, g, ad, v.p.plan, T, true, false, s, &q, &d))) return st;
+    const bool tiles = T && dx && q.W;
     if (T && (dx || dA)) {
         st = launched(sg::launch_shrink(v.p, s), what);
         if (!st) st = tiles ? finish(v.p, &d, rest, T, what, s) : launched(sg::launch_finish(v.p, nullptr, nullptr, s), what);

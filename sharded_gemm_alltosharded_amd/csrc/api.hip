@@ -7,7 +7,7 @@
 #include <mutex>
 #include <string>
 
-#include "internal.h"
+#include "experts.h"
 
 struct sg_layer {
     int mode, segments, P, quantized;
@@ -27,6 +27,7 @@ struct sg_layer {
     // the first backward call that reads them): all-to-sharded, P matrices
     // W_r^T (cols_r, rows_r); sharded-to-all, the stack of W_r^T, (in, out)
     void* wt;
+    void* wx;  // the weights for the grouped tiles, where the stored ones are not (layer_tiles)
     std::mutex wt_mu;
 };
 
@@ -119,6 +120,7 @@ void free_layer(sg_layer* l) {
     if (l->ms) (void)hipFree(l->ms);
     if (l->bias) (void)hipFree(l->bias);
     if (l->wt) (void)hipFree(l->wt);
+    if (l->wx) (void)hipFree(l->wx);
     delete l;
 }
 
@@ -319,8 +321,56 @@ void set_weights(sg::Problem& p, const sg_layer* l) {
 }  // namespace
 
 std::string& sg::last_error() { return g_err; }
-sg::LayerView sg::layer_view(const sg_layer* l) {
-    return {l->w, !l->quantized && !l->mx && l->wfrag, l->bias != nullptr, l->rows_r, l->cols_r};
+
+hipError_t sg::layer_tiles(const sg_layer* lc, hipStream_t st, LayerTiles* out) {
+    sg_layer* l = const_cast<sg_layer*>(lc);  // the copy is a cache of the layer's own weights
+    *out = LayerTiles{};
+    if (l->quantized || l->mx || l->dtype == SG_F32) return hipSuccess;
+    const bool col = l->mode == SG_ALL_TO_SHARDED;
+    ExpertsLayout x{};
+    x.mode = SG_ALL_TO_SHARDED;
+    x.S = 1;
+    x.E = col ? 1 : l->P;
+    x.P = col ? l->P * l->segments : 1;
+    x.out = l->out_dims;
+    x.in = x.kl = l->cols_r;
+    x.f = x.out / x.P;
+    x.bps = (x.f + 15) / 16;
+    x.kpad = (x.kl + 63) / 64 * 64;
+    x.blocks = x.bps * x.P;
+    x.steps = x.kpad / 32;
+    out->blocks = x.blocks;
+    out->steps = x.steps;
+    out->bias = l->bias != nullptr;
+    if (l->wfrag && x.f % 16 == 0 && x.kl % 64 == 0) {
+        out->w = l->w;
+        return hipSuccess;
+    }
+    std::lock_guard<std::mutex> lock(l->wt_mu);
+    if (!l->wx) {
+        hipStreamCaptureStatus capturing = hipStreamCaptureStatusNone;
+        hipError_t e = hipStreamIsCapturing(st, &capturing);
+        if (e != hipSuccess || capturing != hipStreamCaptureStatusNone) return e;
+        const void* rowmajor = l->w;
+        void *tmp = nullptr, *wx = nullptr;
+        if (l->wfrag) {
+            e = hipMalloc(&tmp, (size_t)(l->P * l->rows_r * l->cols_r) * 2);
+            if (e == hipSuccess)
+                e = sg::frag_transform(tmp, l->w, col ? 1 : l->P, col ? l->out_dims : l->rows_r, l->cols_r, 0, st);
+            rowmajor = tmp;
+        }
+        if (e == hipSuccess) e = hipMalloc(&wx, (size_t)(x.E * x.blocks * x.steps) * 1024);
+        if (e == hipSuccess) e = sg::experts_pack(wx, rowmajor, x, st);
+        if (e == hipSuccess) e = hipStreamSynchronize(st);
+        if (tmp) (void)hipFree(tmp);
+        if (e != hipSuccess) {
+            if (wx) (void)hipFree(wx);
+            return e;
+        }
+        l->wx = wx;
+    }
+    out->w = l->wx;
+    return hipSuccess;
 }
 
 extern "C" {

@@ -276,8 +276,8 @@ __device__ __forceinline__ void grad_blocks(const Grouped& p, const Gated& g, in
 
 // ---- adapters beside the product (adapters.h, Adapted) ------------------------
 // Adds U's rows through their adapters' matrices to the sums: after the inputs' steps,
-// one more for every sixteen ranks of every adapter that has rows here.  The operand of
-// a row is zero but for its own adapter.  Rows are grouped by adapter, so a tile of many
+// one more for every sixteen ranks of every adapter that has rows here, which keeps the
+// sums of its own rows.  Rows are grouped by adapter, so a tile of many
 // rows has few of them; of few rows, the matrices of several are loaded at once.
 // fp16: a row's operand is scaled by a power of two, and so are its sums here.
 template <bool F16, bool SWIGLU, bool TRANS, int N, int NBM, typename Acc>
@@ -291,13 +291,15 @@ __device__ __forceinline__ void adapt_blocks(const Grouped& p, const Adapted& d,
     const int chunks = (d.rank + 15) / 16;
     // TRANS: the first of this lane's eight unsharded columns of block 2 i + lane / 32, -1
     // where there is none
-    [[maybe_unused]] int col8[N / 2];
+    [[maybe_unused]] int col8[N / 2], base8[N / 2];  // (base8: the part's first)
+    [[maybe_unused]] const bool whole = (uintptr_t)M % 16 == 0 && (TRANS ? d.width % 8 == 0 && p.f % 8 == 0 : d.rank % 8 == 0);
     if constexpr (TRANS)
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) {
             const int ob = ob0 + 2 * i + (lane >> 5), piece = ob / p.bps, c = 16 * (ob - piece * p.bps) + 8 * (lane & 1);
             const int r = piece / p.S, s = piece - r * p.S;
-            col8[i] = ob < p.nout && c < p.f ? (s * d.P + r) * p.f + c : -1;
+            base8[i] = (s * d.P + r) * p.f;
+            col8[i] = ob < p.nout && c < p.f ? base8[i] + c : -1;
         }
     static_for<0, NBM / JB>([&](auto bc) ALWAYS_INLINE {
         constexpr int j0 = decltype(bc)::value * JB;
@@ -346,8 +348,12 @@ __device__ __forceinline__ void adapt_blocks(const Grouped& p, const Adapted& d,
                             constexpr int i = decltype(ic)::value;
                             const int j = ch * 16 + (lane >> 1 & 15);
                             const bool in = col8[i] >= 0 && j < d.rank;
-                            const u32x4 v = *(const u32x4*)(in ? Ma + (int64_t)j * d.width + col8[i] : M);
-                            mf[b][i] = in ? v : u32x4{0, 0, 0, 0};
+                            if (whole) {
+                                const u32x4 v = *(const u32x4*)(in ? Ma + (int64_t)j * d.width + col8[i] : M);
+                                mf[b][i] = in ? v : u32x4{0, 0, 0, 0};
+                            } else {
+                                mf[b][i] = row8<false>(Ma + (in ? (int64_t)j * d.width + base8[i] : 0), M, in, col8[i] - base8[i], p.f);
+                            }
                         });
                     } else {
                         static_for<0, N>([&](auto ic) ALWAYS_INLINE {
@@ -356,7 +362,7 @@ __device__ __forceinline__ void adapt_blocks(const Grouped& p, const Adapted& d,
                             const int r = SWIGLU ? piece : piece / p.S, s = SWIGLU ? i & 1 : piece - r * p.S;
                             const bool in = ob < p.nout && 16 * blk + r16 < p.f;
                             const int64_t col = in ? (int64_t)(s * d.P + r) * p.f + 16 * blk + r16 : 0;  // unsharded
-                            if (d.rank % 8 == 0) {
+                            if (whole) {
                                 const u32x4 v = *(const u32x4*)(in && k < d.rank ? Ma + col * d.rank + k : M);
                                 mf[b][i] = in && k < d.rank ? v : u32x4{0, 0, 0, 0};
                             } else {
@@ -390,10 +396,20 @@ __device__ __forceinline__ void adapt_blocks(const Grouped& p, const Adapted& d,
                     static_for<0, JB>([&](auto jc) ALWAYS_INLINE {
                         constexpr int j = decltype(jc)::value;
                         const bool own = mine[j] == a[b];
-                        if (!__ballot(own)) return;
+                        const uint64_t owners = __ballot(own);
+                        if (!owners) return;
                         const u32x4 u = own ? uf[j] : u32x4{0, 0, 0, 0};
+                        if (owners == ~0ull) {
 #pragma unroll
-                        for (int i = 0; i < N; ++i) acc[i][j0 + j] = mfma16<F16>(mf[b][i], u, acc[i][j0 + j]);
+                            for (int i = 0; i < N; ++i) acc[i][j0 + j] = mfma16<F16>(mf[b][i], u, acc[i][j0 + j]);
+                        } else {  // (an infinite matrix times the other rows' zeros is NaN)
+#pragma unroll
+                            for (int i = 0; i < N; ++i) {
+                                const f32x4 v = mfma16<F16>(mf[b][i], u, acc[i][j0 + j]);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) acc[i][j0 + j][e] = own ? v[e] : acc[i][j0 + j][e];
+                            }
+                        }
                     });
                 });
                 if (!rem) break;

@@ -149,13 +149,17 @@ __host__ __device__ inline int64_t q4_group_offset(int64_t row, int64_t g, int64
     return (((row >> 5) * (groups >> 2) + (g >> 2)) * 32 + (row & 31)) * 4 + (g & 3);
 }
 
-// what other files need of a dense layer: its weights, fragment-major
-struct LayerView {
-    const void* w;
-    int wfrag, bias;
-    int64_t rows_r, cols_r;  // of one rank's matrix
+// A dense 16-bit layer's weights for the grouped tiles, in the expert layers' layout
+// (experts.h): matrices of 16-row blocks of `steps` 32-input steps.  All-to-sharded: one
+// matrix, every part of f rows padded to whole blocks; sharded-to-all: one a rank, of
+// `blocks` blocks.  The stored weights where they are that already, else a copy that the
+// layer builds on its first call (which allocates and synchronises the stream) and holds.
+struct LayerTiles {
+    const void* w;  // null: no such layer, or its copy is not there and the stream is captured
+    int64_t blocks, steps;
+    int bias;
 };
-LayerView layer_view(const sg_layer* l);
+hipError_t layer_tiles(const sg_layer* l, hipStream_t s, LayerTiles* out);
 
 // launchers (return hipError_t of the launch)
 hipError_t launch_generic(const Problem& p, hipStream_t s);

@@ -4,8 +4,8 @@ sizes that fill nothing, tokens without an adapter.
 
 Tolerances (adapters_ref): x A^T is an fp32 sum; as an operand it is split into two
 16-bit halves, off by 2^-16 (bf16) or 2^-22 (fp16) of itself; then an fp32 sum of
-2 rank products, the projection's fp32 result added, and one rounding.  The
-projection's own part is the layer's own fp32 result."""
+2 rank products more beside the projection's own, and one rounding.  (Beside
+quantized layers the projection's part is the layer's own fp32 result.)"""
 import math
 
 import pytest
@@ -75,6 +75,11 @@ CASES = [
     (70, 512, 96, 1, 4, 2, 2, 64, BF), (130, 72, 130, 0, 1, 2, 1, 100, HF), (300, 264, 520, 0, 2, 2, 3, 32, BF),
     (300, 264, 200, 1, 2, 1, 3, 4, HF), (700, 130, 77, 0, 7, 1, 6, 24, BF), (640, 2048, 64, 1, 8, 1, 2, 16, BF),
     (200, 4096, 48, 0, 2, 1, 1, 40, HF), (90, 64, 64, 0, 1, 1, 60, 200, BF), (1100, 40, 3000, 0, 1, 1, 2, 8, HF),
+    # enough tiles for the products with the adapters in their epilogue: forward, backward
+    (300, 100, 3003, 0, 3, 1, 3, 12, BF), (300, 36, 2820, 0, 2, 2, 2, 20, HF), (300, 45, 2900, 1, 3, 1, 2, 9, BF),
+    (300, 2900, 45, 0, 3, 1, 3, 16, HF), (300, 2904, 50, 1, 2, 1, 3, 8, BF), (300, 2816, 64, 1, 2, 2, 2, 16, BF),
+    (300, 2900, 64, 1, 2, 2, 2, 7, HF), (12, 64, 20480, 0, 4, 2, 30, 16, BF), (60, 20480, 72, 0, 1, 1, 9, 36, HF),
+    (1500, 128, 4100, 0, 2, 2, 3, 16, HF), (1500, 4100, 96, 0, 2, 1, 3, 40, BF), (1500, 64, 4224, 0, 1, 2, 90, 8, BF),
 ]
 
 
@@ -89,7 +94,14 @@ def case_of(T, i, o, mode, P, S, n, r, dtype, which=None):
     order = ref.shard_rows(o if mode == 0 else i, S, P)
     shard = lambda v: torch.stack([v[:, q] for q in order])  # noqa: E731
     xs, dys = (x, shard(dy)) if mode == 0 else (shard(x), dy)
+    layer.weight = w.double()  # for the tests
     return layer, sg.Adapters(A.cuda(), B.cuda(), scale.cuda()), which, xs, dys, x.double(), dy.double(), order, shard
+
+
+def exact_base(layer, x, shard=None):
+    """x W^T and its bound as an fp32 sum."""
+    v, e = x @ layer.weight.T, ref.sum_bound(x.abs() @ layer.weight.abs().T, x.shape[1])
+    return (shard(v), shard(e)) if shard else (v, e)
 
 
 def base_of(layer, x, mode):
@@ -104,19 +116,19 @@ def test_forward(case):
     plan = sg.adapter_plan(which.cuda(), n)
     d, e = aref.delta(x, which, ad.A.cpu(), ad.B.cpu(), ad.scale.cpu(), dtype)
     d, e = (shard(d), shard(e)) if mode == 0 else (d, e)
-    base = base_of(layer, xs, mode)
+    base, eb = exact_base(layer, x, shard if mode == 0 else None)
     call = sg.adapted_all_to_sharded if mode == 0 else sg.adapted_sharded_to_all
+    # (the sums of both parts in one: the adapters' 2 rank + 1 steps act on the base, too)
+    eb = eb + (2 * r + 4) * 2.0 ** -24 * (base.abs() + d.abs() + e)
     for out in (dtype, F32):
         y = call(layer, xs.cuda(), ad, plan, out_dtype=out)
-        ref.close(y, base + d, e + 2.0 ** -24 * (base.abs() + d.abs() + e), f"y {out}")
-    none = (which < 0) | (which >= n)
-    assert torch.equal(y.cpu()[..., none, :].double(), base[..., none, :])
+        ref.close(y, base + d, e + eb, f"y {out}")
     assert torch.equal(y, call(layer, xs.cuda(), ad, plan, out_dtype=F32))  # the same run to run
     one = sg.Adapters(ad.A, ad.B)  # scale 1
     y1 = call(layer, xs.cuda(), one, plan, out_dtype=F32)
     d1, e1 = aref.delta(x, which, ad.A.cpu(), ad.B.cpu(), torch.ones(n), dtype)
     d1, e1 = (shard(d1), shard(e1)) if mode == 0 else (d1, e1)
-    ref.close(y1, base + d1, e1 + 2.0 ** -24 * (base.abs() + d1.abs() + e1), "scale 1")
+    ref.close(y1, base + d1, e1 + eb + (2 * r + 4) * 2.0 ** -24 * d1.abs(), "scale 1")
     if mode == 0:
         z = sg.adapted_all_to_sharded(layer, xs.cuda(), ad, plan, gather=True, out_dtype=F32)
         assert torch.equal(z.view(T, P, -1).transpose(0, 1), y)
@@ -130,9 +142,9 @@ def test_forward_swiglu(case):
     layer, ad, which, xs, _, x, _, order, shard = case_of(*case)
     plan = sg.adapter_plan(which.cuda(), n)
     d, e = aref.delta(x, which, ad.A.cpu(), ad.B.cpu(), ad.scale.cpu(), dtype)
-    base = base_of(layer, xs, 0)
-    z, e = base + shard(d), shard(e)
-    e = e + 2.0 ** -24 * (z.abs() + e)
+    base, eb = exact_base(layer, x, shard)
+    z, e = base + shard(d), shard(e) + eb
+    e = e + (2 * r + 4) * 2.0 ** -24 * (base.abs() + shard(d).abs() + e)
     f = z.shape[-1] // 2
     (a, b), (ea, eb) = z.split(f, -1), e.split(f, -1)
     want = ref.silu(a) * b
@@ -186,17 +198,16 @@ def test_backward(case):
     layer, ad, which, xs, dys, x, dy, order, shard = case_of(*case)
     plan = sg.adapter_plan(which.cuda(), n)
     (dx, ex), (dA, eA), (dB, eB) = aref.gradients(x, dy, which, ad.A.cpu(), ad.B.cpu(), ad.scale.cpu(), dtype)
+    base, eb = dy @ layer.weight, ref.sum_bound(dy.abs() @ layer.weight.abs(), o)
+    ex = ex + eb + (2 * r + 4) * 2.0 ** -24 * (base.abs() + dx.abs() + ex)
     if mode == 0:
-        base = sg.all_to_sharded_backward(layer, None, dys.cuda(), need_dw=False, dx_dtype=F32)[0]
         back = sg.adapted_all_to_sharded_backward
     else:
-        base = sg.sharded_to_all_backward(layer, None, dys.cuda(), need_dw=False, dx_dtype=F32)[0]
-        dx, ex = shard(dx), shard(ex)
+        base, dx, ex = shard(base), shard(dx), shard(ex)
         back = sg.adapted_sharded_to_all_backward
-    base = base.double().cpu()
     for dt in (dtype, F32):
         gx, gA, gB = back(layer, xs.cuda(), dys.cuda(), ad, plan, dx_dtype=dt, d_dtype=dt)
-        ref.close(gx, base + dx, ex + 2.0 ** -24 * (base.abs() + dx.abs() + ex), f"dx {dt}")
+        ref.close(gx, base + dx, ex, f"dx {dt}")
         ref.close(gA, dA, eA, f"dA {dt}")
         ref.close(gB, dB, eB, f"dB {dt}")
     only, n1, n2 = back(layer, None, dys.cuda(), ad, plan, need_d=False, dx_dtype=F32)
@@ -246,12 +257,12 @@ def test_fp16_far_from_one(size):
     ref.close(gB, dB, eB, "dB")
 
 
-@pytest.mark.parametrize("T", [20, 300])
-def test_tokens_stay_apart(T):
+@pytest.mark.parametrize("T,i,o", [(20, 72, 104), (300, 72, 104), (300, 72, 3000), (300, 2904, 40), (40, 64, 17000)])
+def test_tokens_stay_apart(T, i, o):
     """An infinite or NaN token reaches no other one, nor other adapters' gradients;
     an infinite adapter reaches its own tokens only."""
     g = gen(T)
-    i, o, n, r = 72, 104, 3, 12
+    n, r = 3, 12
     layer = sg.shard_linear(normal(g, (o, i), BF, 0.1).cuda(), 0)
     A, B = normal(g, (n, r, i), BF, 0.1), normal(g, (n, o, r), BF, 0.1)
     which = torch.randint(0, n, (T,), generator=g, dtype=torch.int32)
@@ -295,11 +306,11 @@ def test_no_tokens_and_no_adapters():
     assert torch.equal(sg.adapted_all_to_sharded(layer, x, ad, plan), sg.all_to_sharded(layer, x))
 
 
-@pytest.mark.parametrize("T", [24, 400])
-def test_bad_plans_stay_inside(T):
+@pytest.mark.parametrize("T,i,o", [(24, 64, 96), (400, 64, 96), (400, 64, 3000), (400, 3000, 64), (24, 64, 17000)])
+def test_bad_plans_stay_inside(T, i, o):
     """A plan of any contents leads out of no array (its results are unspecified)."""
     g = gen(2)
-    i, o, n, r = 64, 96, 2, 16
+    n, r = 2, 16
     layer = sg.shard_linear(normal(g, (o, i), BF).cuda(), 0)
     ad = sg.Adapters(normal(g, (n, r, i), BF).cuda(), normal(g, (n, o, r), BF).cuda())
     x, dy = normal(g, (T, i), BF).cuda(), normal(g, (1, T, o), BF).cuda()
@@ -313,9 +324,9 @@ def test_bad_plans_stay_inside(T):
         assert (guard[0] == 7).all() and (guard[2] == 7).all()
 
 
-def test_on_another_stream_and_in_graphs():
+@pytest.mark.parametrize("i,o,n,r,T", [(256, 384, 4, 16, 30), (200, 6000, 4, 12, 300)])
+def test_on_another_stream_and_in_graphs(i, o, n, r, T):
     g = gen(5)
-    i, o, n, r, T = 256, 384, 4, 16, 30
     layer = sg.shard_linear(normal(g, (o, i), BF, 0.1).cuda(), 0, segments=2, P=2)
     down = sg.shard_linear(normal(g, (i, o // 2), BF, 0.1).cuda(), 1, P=2)
     ad = sg.Adapters(normal(g, (n, r, i), BF, 0.1).cuda(), normal(g, (n, o, r), BF, 0.1).cuda())

@@ -78,7 +78,12 @@ struct Adapted {
     // a layer's weights, fragment-major: bytes from one input segment's, and (transposed)
     // from one rank's output columns, to the next
     uint32_t wseg, wrank;
+    int again;        // segment from which on the inputs are the first ones' again (none: 0)
 };
+// 4-bit weights (`matrices` of rows x cols, in parts of `part` rows each) as two 16-bit
+// ones in the tiles' layout, hi + lo, the lo behind all the hi ones
+hipError_t launch_q4_tiles(const LayerCodes& q, int f16, int64_t matrices, int64_t rows, int64_t part, int64_t cols,
+                           void* out, hipStream_t s);
 // transposed or not, p.rows the plan's
 hipError_t launch_adapted(const Grouped& p, const Adapted& d, hipStream_t s);
 // whether that beats the product's own kernel and expand behind it

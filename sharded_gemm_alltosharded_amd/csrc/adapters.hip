@@ -269,6 +269,34 @@ __global__ __launch_bounds__(256) void finish_kernel(LowRank p, u32x4* operands,
     }
 }
 
+// ---- 4-bit weights for the tiles --------------------------------------------
+// w = scale q + bias in fp32, split in hi + lo.  A wave writes a 16-row block's step of
+// 32 inputs, a lane its eight (one word of codes).
+template <bool F16>
+__global__ __launch_bounds__(256) void q4_tiles_kernel(LayerCodes q, int64_t frags, int64_t blocks, int64_t steps,
+                                                       int64_t rows, int64_t part, int64_t cols, u32x4* hi, u32x4* lo) {
+    const int64_t fr = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (fr >= frags) return;
+    const int lane = threadIdx.x & 63;
+    const int64_t st = fr % steps, b = fr / steps % blocks, m = fr / (steps * blocks);
+    const int64_t bps = (part + 15) / 16, j = b % bps * 16 + (lane & 15), k = st * 32 + 8 * (lane >> 4);
+    u32x4 h = {0, 0, 0, 0}, l = h;
+    if (j < part && k < cols) {
+        const int64_t row = m * rows + b / bps * part + j;
+        const uint32_t w = q.codes[row * (cols / 8) + k / 8];
+        const float scale = f16_to_f32(q.scales[row * (cols / 64) + k / 64]), bias = f16_to_f32(q.biases[row * (cols / 64) + k / 64]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            uint16_t a, c;
+            split16<F16>(fmaf(scale, (float)((w >> (4 * q4_nibble_pos(e))) & 15u), bias), a, c);
+            h[e / 2] |= (uint32_t)a << (16 * (e & 1));
+            l[e / 2] |= (uint32_t)c << (16 * (e & 1));
+        }
+    }
+    hi[fr * 64 + lane] = h;
+    lo[fr * 64 + lane] = l;
+}
+
 // ---- grad -------------------------------------------------------------------
 // G_a[j][c] = sum over a's rows m of U[m][j] X[t(m)][c].  Bound by reading X.
 // A workgroup takes 64 columns of one adapter, its waves every eighth 32 rows: X and
@@ -464,6 +492,16 @@ hipError_t launch_finish(const LowRank& p, void* operands, int32_t* exponents, h
     const dim3 grid((unsigned)(((p.plan.T + 15) / 16 + 3) / 4));
     if (p.f16) launch(finish_kernel<true>, grid, dim3(256), 0, s, p, (u32x4*)operands, exponents);
     else launch(finish_kernel<false>, grid, dim3(256), 0, s, p, (u32x4*)operands, exponents);
+    return hipGetLastError();
+}
+
+hipError_t launch_q4_tiles(const LayerCodes& q, int f16, int64_t matrices, int64_t rows, int64_t part, int64_t cols,
+                           void* out, hipStream_t s) {
+    const int64_t blocks = rows / part * ((part + 15) / 16), steps = (cols + 63) / 64 * 2, frags = matrices * blocks * steps;
+    u32x4 *hi = (u32x4*)out, *lo = hi + frags * 64;
+    const dim3 grid((unsigned)((frags + 3) / 4));
+    if (f16) launch(q4_tiles_kernel<true>, grid, dim3(256), 0, s, q, frags, blocks, steps, rows, part, cols, hi, lo);
+    else launch(q4_tiles_kernel<false>, grid, dim3(256), 0, s, q, frags, blocks, steps, rows, part, cols, hi, lo);
     return hipGetLastError();
 }
 

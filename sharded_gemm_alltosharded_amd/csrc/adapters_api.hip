@@ -5,6 +5,7 @@
 #include <stdio.h>
 
 #include "adapters.h"
+#include "gated.h"
 
 namespace {
 
@@ -108,21 +109,20 @@ sg_status check_ws(const char* what, const void* ws, size_t bytes, size_t need) 
     return SG_OK;
 }
 
-// The projection's product over the plan's rows, x W^T or (transposed) dy W, from the
-// layer's fragments.  to->W null where they, or the tokens, do not suit the tiles.
-sg_status tile_product(const sg_layer* l, const Geometry& g, const sg_adapters* ad, const sg::Plan& plan, int64_t T,
-                       bool transposed, bool swiglu, hipStream_t stream, sg::Grouped* to, sg::Adapted* d) {
+// The projection's product on the grouped tiles, x W^T or (transposed) dy W: what it is
+// but for its weights.  False where they, or the tokens, do not suit the tiles.
+bool tile_product(const sg_layer* l, const Geometry& g, int64_t T, bool transposed, bool swiglu, sg::Grouped* to) {
     sg::Grouped& p = *to;
     p = sg::Grouped{};
     const int64_t f = g.part(), rank_width = g.S * f;  // of the sharded side
     // (a rank's segments of a sharded-to-all layer lie side by side in its matrix: of whole
     // blocks and without padding behind them, where there are several)
-    if (g.quantized || (!g.column() && g.S > 1 && (f % 16 || rank_width % 64)) ||
+    if (T <= 8 || (g.quantized && (transposed || !sg::layer_codes(l).codes)) ||
+        (!g.column() && g.S > 1 && (f % 16 || rank_width % 64)) ||
         (double)T * (double)(g.in > g.out ? g.in : g.out) * 2 >= (double)0xffff0000ll ||
-        (double)((g.out + 15 + 16 * g.S * g.P) * (g.in + 63 + 64 * g.P)) * 2 >= (double)0xffff0000ll)
-        return SG_OK;
+        (double)((g.out + 15 + 16 * g.S * g.P) * (g.in + 63 + 64 * g.P)) * (g.quantized ? 4 : 2) >= (double)0xffff0000ll)
+        return false;
     p.mode = g.dtype == SG_F16 ? sg::G_F16 : sg::G_BF16;
-    p.rows = plan.rows;
     p.kdiv = 1;
     p.T = p.R = (int)T;
     p.E = 1;
@@ -149,21 +149,69 @@ sg_status tile_product(const sg_layer* l, const Geometry& g, const sg_adapters* 
     p.nout = (int)(p.bps * (in_sharded ? 1 : g.P) * (parts && !swiglu ? g.S : 1));
     p.ldo = in_sharded ? cols : swiglu ? f : rank_width;
     p.o_rank = in_sharded ? 0 : T * p.ldo;
-    d->plan = plan;
-    d->rank = ad->rank;
-    d->M = transposed ? ad->A : ad->B;
-    d->width = cols;
-    d->P = in_sharded ? 1 : g.P;
-    if (!sg::adapted_fills(p)) return SG_OK;
-    sg::LayerTiles v;
-    if (sg_status st = launched(sg::layer_tiles(l, stream, &v), "weight layout")) return st;
+    return true;
+}
+
+// (a 4-bit layer's: hi and lo)
+size_t weight_bytes(const Geometry& g) {
+    if (!g.quantized) return 0;
+    const int64_t blocks = g.column() ? (g.part() + 15) / 16 * g.S * g.P : (g.out + 15) / 16;
+    return (size_t)(2 * (g.column() ? 1 : g.P) * blocks * (((g.column() ? g.in : g.in / g.P) + 63) / 64 * 2) * 1024);
+}
+
+// Its weights; of a 4-bit layer at `at` (weight_bytes).  p.W stays null where there are none.
+sg_status tile_weights(const sg_layer* l, const Geometry& g, void* at, hipStream_t s, sg::Grouped* to, sg::Adapted* d) {
+    sg::Grouped& p = *to;
+    sg::LayerTiles v{};
+    if (g.quantized) {
+        const int64_t cols = g.column() ? g.in : g.in / g.P;
+        v.blocks = g.column() ? (g.part() + 15) / 16 * g.S * g.P : (g.out + 15) / 16;
+        v.steps = (cols + 63) / 64 * 2;
+        v.w = at;
+        if (sg_status st = launched(sg::launch_q4_tiles(sg::layer_codes(l), g.dtype == SG_F16, g.column() ? 1 : g.P, g.out,
+                                                        g.column() ? g.part() : g.out, cols, at, s), "4-bit weights"))
+            return st;
+        d->again = p.nseg;  // the same inputs through the lo halves
+        p.nseg *= 2;
+    } else if (sg_status st = launched(sg::layer_tiles(l, s, &v), "weight layout")) {
+        return st;
+    }
     if (v.bias) return SG_OK;
     const int64_t matrix = v.blocks * v.steps * 1024;
     p.W = (const uint8_t*)v.w;
-    p.w_expert = matrix * (g.column() ? 1 : g.P);
+    p.w_expert = matrix * (g.column() ? 1 : g.P) * (g.quantized ? 2 : 1);
     p.wsteps = (int)v.steps;
     d->wseg = d->wrank = (uint32_t)matrix;
     return SG_OK;
+}
+
+// the adapters' part of the epilogue
+void set_adapted(const Geometry& g, const sg_adapters* ad, const sg::Plan& plan, sg::Grouped* p, sg::Adapted* d) {
+    const bool in_sharded = g.column() == (bool)p->transposed;
+    p->rows = plan.rows;
+    d->plan = plan;
+    d->rank = ad->rank;
+    d->M = p->transposed ? ad->A : ad->B;
+    d->width = p->transposed ? g.in : g.out;
+    d->P = in_sharded ? 1 : g.P;
+}
+
+// Fewer tiles than fill the chip: the projection's part by itself, its sums split over
+// the inputs, in fp32.  (A transposed product's weights and a sharded-to-all layer's
+// ranks lie as the plain tiles have them only where there is one matrix.)
+bool split_product(const Geometry& g, const sg::Grouped& p) {
+    return !g.quantized && (g.column() || g.P == 1) && !sg::adapted_fills(p);
+}
+size_t split_bytes(const sg::Grouped& p) {
+    const int n = sg::grouped_splits(p);
+    return n > 1 ? up256(n * sg::grouped_outputs(p) * 4) : 0;
+}
+sg_status launch_split(sg::Grouped p, const void* a, float* out, void* ws, const char* what, hipStream_t s) {
+    p.A = a;
+    p.out = out;
+    p.out_dtype = SG_F32;
+    const int n = sg::grouped_splits(p);
+    return launched(n > 1 ? sg::launch_grouped_split(p, n, (float*)ws, s) : sg::launch_grouped(p, s), what);
 }
 
 // U's sums, and its operands for the tiles, at `at` (operands_bytes)
@@ -191,15 +239,23 @@ sg_status forward(const char* what, const sg_layer* l, const Geometry& g, const 
     if (st) return st;
     const int64_t n = g.column() ? (epilogue == SG_EPI_SWIGLU ? g.out / 2 : g.out) / g.P : g.out;  // columns of a rank
     const bool gathered = g.column() && out_layout == SG_OUT_FULL;
+    const bool swiglu = epilogue == SG_EPI_SWIGLU;
+    char* rest = (char*)workspace + u.bytes;
     sg::Grouped q;
     sg::Adapted d{};
-    if ((st = tile_product(l, g, ad, p.plan, T, false, epilogue == SG_EPI_SWIGLU, s, &q, &d))) return st;
-    if (q.W) {
+    bool tiles = tile_product(l, g, T, false, swiglu, &q), split = false;
+    if (tiles && !sg::adapted_fills(q)) tiles = false, split = tile_product(l, g, T, false, false, &q) && split_product(g, q);
+    if (tiles || split) {
+        if ((st = tile_weights(l, g, rest + operands_bytes(T, ad->rank), s, &q, &d))) return st;
+        if (!q.W) tiles = split = false;
+    }
+    if (tiles) {
+        set_adapted(g, ad, p.plan, &q, &d);
         q.A = x;
         q.out = y;
         q.out_dtype = y_dtype;
         if (gathered) q.ldo = n * g.P, q.o_rank = n;
-        st = finish(p, &d, (char*)workspace + u.bytes, T, what, s);
+        st = finish(p, &d, rest, T, what, s);
         return st ? st : launched(sg::launch_adapted(q, d, s), what);
     }
     // (many rows' sums are added up once, few by every workgroup that wants them)
@@ -209,12 +265,14 @@ sg_status forward(const char* what, const sg_layer* l, const Geometry& g, const 
     }
     // the projection's result stays in fp32 until the adapters' part is added, so that y
     // is rounded once; an fp32 y holds it itself
-    const bool swiglu = epilogue == SG_EPI_SWIGLU, in_y = y_dtype == SG_F32 && !swiglu;
-    char* at = (char*)workspace + u.bytes;
+    const bool in_y = y_dtype == SG_F32 && !swiglu && !(split && gathered);
+    char* at = rest;
     float* base = in_y ? (float*)y : (float*)at;
     at += up256(T * g.out * 4);
     // (sharded unless y is both gathered and the sum's own place)
-    if (g.column()) {
+    if (split) {
+        st = launch_split(q, x, base, at, what, s);
+    } else if (g.column()) {
         st = sg_all_to_sharded_ex(l, x, SG_IN_FULL, T, base, in_y ? out_layout : SG_OUT_SHARDED, SG_EPI_NONE, SG_F32, stream);
     } else {
         st = sg_sharded_to_all_ex(l, x, T, base, SG_OUT_FULL, SG_F32, at, ws_bytes - (size_t)(at - (char*)workspace), stream);
@@ -258,8 +316,14 @@ sg_status backward(const char* what, const sg_layer* l, const Geometry& g, const
     sg::Grouped q{};
     sg::Adapted d{};
     sg_status st = SG_OK;
-    if (T && dx && (st = tile_product(l, g, ad, v.p.plan, T, true, false, s, &q, &d))) return st;
-    const bool tiles = T && dx && q.W;
+    bool tiles = T && dx && tile_product(l, g, T, true, false, &q), split = false;
+    if (tiles) {
+        split = split_product(g, q);
+        tiles = sg::adapted_fills(q);
+        if (tiles || split)
+            if ((st = tile_weights(l, g, nullptr, s, &q, &d))) return st;
+        if (!q.W) tiles = split = false;
+    }
     if (T && (dx || dA)) {
         st = launched(sg::launch_shrink(v.p, s), what);
         if (!st) st = tiles ? finish(v.p, &d, rest, T, what, s) : launched(sg::launch_finish(v.p, nullptr, nullptr, s), what);
@@ -293,6 +357,7 @@ sg_status backward(const char* what, const sg_layer* l, const Geometry& g, const
         st = launched(sg::launch_grad(p, s), what);
     }
     if (!st && tiles) {
+        set_adapted(g, ad, v.p.plan, &q, &d);
         q.A = dy;
         q.out = dx;
         q.out_dtype = dx_dtype;
@@ -300,8 +365,9 @@ sg_status backward(const char* what, const sg_layer* l, const Geometry& g, const
     } else if (!st && T && dx) {
         // as forward: the frozen projection's part in fp32, rounded once with the adapters'
         float* base = dx_dtype == SG_F32 ? (float*)dx : (float*)rest;
-        st = g.column() ? sg_all_to_sharded_backward(l, nullptr, dy, T, base, SG_F32, nullptr, SG_F32, nullptr, 0, stream)
-                        : sg_sharded_to_all_backward(l, nullptr, dy, T, base, SG_F32, nullptr, SG_F32, nullptr, 0, stream);
+        if (split) st = launch_split(q, dy, base, rest + up256(T * g.in * 4), what, s);
+        else st = g.column() ? sg_all_to_sharded_backward(l, nullptr, dy, T, base, SG_F32, nullptr, SG_F32, nullptr, 0, stream)
+                             : sg_sharded_to_all_backward(l, nullptr, dy, T, base, SG_F32, nullptr, SG_F32, nullptr, 0, stream);
         if (st) return st;
         sg::LowRank p = v.p;
         p.M = ad->A;
@@ -341,8 +407,13 @@ size_t sg_adapted_workspace(const sg_layer* l, const sg_adapters* ad, int64_t T)
     if (!l || !ad || T <= 0 || check_adapters(ad) || sg_layer_info(l, &g.out, &g.in, &g.mode, &g.S, &g.P, &g.dtype, &g.quantized))
         return 0;
     // the projection's fp32 result and what its own call needs, or the operands of U
-    const size_t base = up256(T * g.out * 4) + (g.column() ? 0 : up256((int64_t)sg_sharded_to_all_workspace(l, T)));
-    const size_t ops = operands_bytes(T, ad->rank);
+    size_t own = g.column() ? 0 : up256((int64_t)sg_sharded_to_all_workspace(l, T)), ops = operands_bytes(T, ad->rank);
+    sg::Grouped q;
+    if (tile_product(l, g, T, false, false, &q)) {
+        if (split_product(g, q) && split_bytes(q) > own) own = split_bytes(q);
+        ops += weight_bytes(g);
+    }
+    const size_t base = up256(T * g.out * 4) + own;
     return half(g, ad, nullptr, T, true).bytes + (base > ops ? base : ops);
 }
 
@@ -374,7 +445,10 @@ size_t sg_adapted_backward_workspace(const sg_layer* l, const sg_adapters* ad, i
     Geometry g;
     if (!l || !ad || T <= 0 || check_adapters(ad) || sg_layer_info(l, &g.out, &g.in, &g.mode, &g.S, &g.P, &g.dtype, &g.quantized))
         return 0;
-    const size_t base = up256(T * g.in * 4), ops = operands_bytes(T, ad->rank);
+    const size_t ops = operands_bytes(T, ad->rank);
+    size_t base = up256(T * g.in * 4);
+    sg::Grouped q;
+    if (tile_product(l, g, T, true, false, &q) && split_product(g, q)) base += split_bytes(q);
     return half(g, ad, nullptr, T, true).bytes + half(g, ad, nullptr, T, false).bytes + (base > ops ? base : ops);
 }
 

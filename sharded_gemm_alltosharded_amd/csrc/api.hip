@@ -373,6 +373,11 @@ hipError_t sg::layer_tiles(const sg_layer* lc, hipStream_t st, LayerTiles* out) 
     return hipSuccess;
 }
 
+sg::LayerCodes sg::layer_codes(const sg_layer* l) {
+    if (!l->quantized || l->mx || l->qfrag) return LayerCodes{};
+    return {(const uint32_t*)l->w, l->qs, l->qb};
+}
+
 extern "C" {
 
 const char* sg_last_error(void) { return g_err.c_str(); }

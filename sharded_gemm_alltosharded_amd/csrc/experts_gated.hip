@@ -28,9 +28,9 @@ template <int OT>
 __global__ __launch_bounds__(256) void split_sum_kernel(const float* ws, int splits, int64_t slab, int64_t N,
                                                         const int32_t* offsets, int E, int64_t R, void* out) {
     const int64_t per = (N + 7) / 8, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= R * per) return;
+    if (i >= slab / N * per) return;
     const int64_t m = i / per, c = (i - m * per) * 8;
-    if (offsets && (m < offsets[0] || m >= offsets[E])) return;
+    if (offsets && (m % R < offsets[0] || m % R >= offsets[E])) return;
     const int left = (int)min(N - c, (int64_t)8);
     float v[8], w[8];
     load_cols<SG_F32>(ws, m * N + c, v, left);
@@ -58,18 +58,23 @@ int grouped_splits(const Grouped& p) {
     return (int)(want < most ? want : most > 1 ? most : 1);
 }
 
+int64_t grouped_outputs(const Grouped& p) {
+    const int ranks = p.o_rank ? p.nout / (p.bps * p.S) : 1;
+    return (int64_t)p.R * p.ldo * ranks;
+}
+
 hipError_t launch_grouped_split(const Grouped& call, int splits, float* ws, hipStream_t s) {
     Grouped p = call;
     p.out = ws;
     p.out_dtype = SG_F32;
     Gated g{};
     g.splits = splits;
-    g.slab = (int64_t)p.R * p.ldo;
+    g.slab = grouped_outputs(p);
     hipError_t e;
     if (p.mode == G_F16) e = p.transposed ? split_mode<G_F16, true>(p, g, s) : split_mode<G_F16, false>(p, g, s);
     else e = p.transposed ? split_mode<G_BF16, true>(p, g, s) : split_mode<G_BF16, false>(p, g, s);
     if (e != hipSuccess) return e;
-    const dim3 grid((unsigned)(((int64_t)p.R * ((p.ldo + 7) / 8) + 255) / 256));
+    const dim3 grid((unsigned)((g.slab / p.ldo * ((p.ldo + 7) / 8) + 255) / 256));
     if (call.out_dtype == SG_F32)
         launch(split_sum_kernel<SG_F32>, grid, dim3(256), 0, s, ws, splits, g.slab, p.ldo, p.offsets, p.E, p.R, call.out);
     else if (call.out_dtype == SG_BF16)

@@ -25,8 +25,9 @@ hipError_t launch_gated(const Grouped& p, const Gated& g, hipStream_t s);
 hipError_t launch_gated_backward(const Grouped& p, const Gated& g, hipStream_t s);
 
 // A product of few tiles, its inputs split over more workgroups: parts of fp32 sums in
-// slabs of R ldo values, added in order.  1: not worth it.
+// slabs of R ldo values for each rank of the output, added in order.  1: not worth it.
 int grouped_splits(const Grouped& p);
+int64_t grouped_outputs(const Grouped& p);  // values of a slab
 hipError_t launch_grouped_split(const Grouped& p, int splits, float* ws, hipStream_t s);
 
 #ifdef __HIPCC__

@@ -599,6 +599,8 @@ __device__ __forceinline__ void grouped_tile(const Grouped& p, const Slot s, con
         ++iseg;
         ia += p.kl;
         if (++ipiece == p.a_pieces) ipiece = 0, irank += p.a_rank, ia = irank;
+        if constexpr (EPI == E_ADAPT)
+            if (iseg == extra.again) ia = irank = 0;
     };
 
     f32x4 acc[NBN][NBM];

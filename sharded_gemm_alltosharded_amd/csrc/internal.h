@@ -160,6 +160,12 @@ struct LayerTiles {
     int bias;
 };
 hipError_t layer_tiles(const sg_layer* l, hipStream_t s, LayerTiles* out);
+// A 4-bit layer whose codes no matrix-core kernel takes (row-major); codes null: any other.
+struct LayerCodes {
+    const uint32_t* codes;
+    const uint16_t *scales, *biases;
+};
+LayerCodes layer_codes(const sg_layer* l);
 
 // launchers (return hipError_t of the launch)
 hipError_t launch_generic(const Problem& p, hipStream_t s);

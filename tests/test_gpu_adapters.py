@@ -156,33 +156,46 @@ def test_forward_swiglu(case):
 
 
 @pytest.mark.parametrize("T", [1, 8, 40, 200])
-@pytest.mark.parametrize("kind", ["q4", "mx8"])
-@pytest.mark.parametrize("mode", [0, 1])
-def test_beside_quantized_layers(mode, kind, T):
+@pytest.mark.parametrize("kind", ["q4", "q4 f16", "mx8"])
+@pytest.mark.parametrize("mode,i,o", [(0, 512, 256), (1, 512, 256), (0, 576, 6020), (1, 640, 6016)])
+def test_beside_quantized_layers(mode, i, o, kind, T):
+    """4-bit layers whose codes come in whole runs of 256 inputs, and others."""
     g = gen(T + mode)
-    i, o, P, n, r = 512, 256, 2, 3, 16
-    if kind == "q4":
+    P, n, r = 2, 3, 16
+    dtype = HF if kind == "q4 f16" else BF
+    if kind != "mx8":
         w = torch.randint(-2 ** 31, 2 ** 31, (o, i // 8), generator=g, dtype=torch.int64).to(torch.int32)
         sc = (torch.rand((o, i // 64), generator=g) * 0.01).half()
-        layer = sg.shard_quantized_linear(w.cuda(), sc.view(torch.int16).cuda(), (-7 * sc).view(torch.int16).cuda(), i, mode,
-                                          P=P)
+        qb = (-7 * sc).half()
+        layer = sg.shard_quantized_linear(w.cuda(), sc.view(torch.int16).cuda(), qb.view(torch.int16).cuda(), i, mode, P=P,
+                                          act_dtype=dtype)
+        q = ((w.long() & 0xffffffff)[..., None] >> (4 * torch.arange(8)) & 15).flatten(1).double()
+        sq, b = sc.double().repeat_interleave(64, 1) * q, qb.double().repeat_interleave(64, 1)
+        W, size = sq + b, sq.abs() + b.abs()
     else:
-        layer = sg.shard_mxfp8_linear(*(v.cuda() for v in mx.encode(normal(g, (o, i), F32, 0.05))), mode, P=P)
-    A, B = normal(g, (n, r, i), BF, 0.05), normal(g, (n, o, r), BF, 0.2)
+        codes, scales = mx.encode(normal(g, (o, i), F32, 0.05))
+        layer = sg.shard_mxfp8_linear(codes.cuda(), scales.cuda(), mode, P=P)
+        W = mx.decode(codes, scales)
+        size = W.abs()
+    A, B = normal(g, (n, r, i), dtype, 0.05), normal(g, (n, o, r), dtype, 0.2)
     scale, which = torch.rand(n, generator=g), draw_which(g, T, n)
-    x, dy = normal(g, (T, i), BF), normal(g, (T, o), BF)
+    x, dy = normal(g, (T, i), dtype), normal(g, (T, o), dtype)
     order = ref.shard_rows(o if mode == 0 else i, 1, P)
     shard = lambda v: torch.stack([v[:, q] for q in order])  # noqa: E731
     xs, dys = (x, shard(dy)) if mode == 0 else (shard(x), dy)
     ad, plan = sg.Adapters(A.cuda(), B.cuda(), scale.cuda()), sg.adapter_plan(which.cuda(), n)
-    d, e = aref.delta(x.double(), which, A, B, scale, BF)
-    d, e = (shard(d), shard(e)) if mode == 0 else (d, e)
-    base = base_of(layer, xs, mode)
+    d, e = aref.delta(x.double(), which, A, B, scale, dtype)
+    # the projection: fp32 sums of the codes' and the biases' products, or of the weights
+    # in two halves (2^-16 or 2^-22 of them)
+    base = x.double() @ W.T
+    e = e + (aref.SPLIT[dtype] + (2 * i + 2 * r + 8) * 2.0 ** -24) * (x.double().abs() @ size.T + d.abs())
+    d, e, base = (shard(d), shard(e), shard(base)) if mode == 0 else (d, e, base)
     call = sg.adapted_all_to_sharded if mode == 0 else sg.adapted_sharded_to_all
-    ref.close(call(layer, xs.cuda(), ad, plan), base + d, e + 2.0 ** -24 * (base.abs() + d.abs() + e), "y")
+    for out in (dtype, F32):
+        ref.close(call(layer, xs.cuda(), ad, plan, out_dtype=out), base + d, e, "y")
     back = sg.adapted_all_to_sharded_backward if mode == 0 else sg.adapted_sharded_to_all_backward
     none, dA, dB = back(layer, xs.cuda(), dys.cuda(), ad, plan, need_dx=False)
-    _, (wA, eA), (wB, eB) = aref.gradients(x.double(), dy.double(), which, A, B, scale, BF)
+    _, (wA, eA), (wB, eB) = aref.gradients(x.double(), dy.double(), which, A, B, scale, dtype)
     assert none is None
     ref.close(dA, wA, eA, "dA")
     ref.close(dB, wB, eB, "dB")

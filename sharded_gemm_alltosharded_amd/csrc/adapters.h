@@ -80,9 +80,9 @@ struct Adapted {
     uint32_t wseg, wrank;
     int again;        // segment from which on the inputs are the first ones' again (none: 0)
 };
-// 4-bit weights (`matrices` of rows x cols, in parts of `part` rows each) as two 16-bit
-// ones in the tiles' layout, hi + lo, the lo behind all the hi ones
-hipError_t launch_q4_tiles(const LayerCodes& q, int f16, int64_t matrices, int64_t rows, int64_t part, int64_t cols,
+// Quantized weights (`matrices` of rows x cols, in parts of `part` rows each) as 16-bit
+// tiles: 4-bit ones as two, hi and behind it lo, MX FP8 ones as one.
+hipError_t launch_code_tiles(const LayerCodes& q, int f16, int64_t matrices, int64_t rows, int64_t part, int64_t cols,
                            void* out, hipStream_t s);
 // transposed or not, p.rows the plan's
 hipError_t launch_adapted(const Grouped& p, const Adapted& d, hipStream_t s);

@@ -269,11 +269,13 @@ __global__ __launch_bounds__(256) void finish_kernel(LowRank p, u32x4* operands,
     }
 }
 
-// ---- 4-bit weights for the tiles --------------------------------------------
-// w = scale q + bias in fp32, split in hi + lo.  A wave writes a 16-row block's step of
-// 32 inputs, a lane its eight (one word of codes).
-template <bool F16>
-__global__ __launch_bounds__(256) void q4_tiles_kernel(LayerCodes q, int64_t frags, int64_t blocks, int64_t steps,
+// ---- quantized weights for the tiles ----------------------------------------
+// 4-bit: w = scale q + bias in fp32, split in hi + lo (scale and bias are multiples of
+// fp16's smallest step, 2^-24, so that fp16's two halves lose nothing of small weights
+// either).  MX FP8: w = 2^s code, exact in bf16 alone.  A wave writes a 16-row block's
+// step of 32 inputs, a lane its eight.
+template <bool F16, bool MX>
+__global__ __launch_bounds__(256) void code_tiles_kernel(LayerCodes q, int64_t frags, int64_t blocks, int64_t steps,
                                                        int64_t rows, int64_t part, int64_t cols, u32x4* hi, u32x4* lo) {
     const int64_t fr = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
     if (fr >= frags) return;
@@ -283,6 +285,15 @@ __global__ __launch_bounds__(256) void q4_tiles_kernel(LayerCodes q, int64_t fra
     u32x4 h = {0, 0, 0, 0}, l = h;
     if (j < part && k < cols) {
         const int64_t row = m * rows + b / bps * part + j;
+        if constexpr (MX) {
+            const uint2 w = *(const uint2*)(q.codes8 + row * cols + k);
+            const float scale = e8m0_to_f32(q.scales8[row * (cols / 32) + k / 32]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                h[e / 2] |= (uint32_t)to16<false>(scale * e4m3_to_f32((uint8_t)((e < 4 ? w.x : w.y) >> (8 * (e & 3))))) << (16 * (e & 1));
+            hi[fr * 64 + lane] = h;
+            return;
+        }
         const uint32_t w = q.codes[row * (cols / 8) + k / 8];
         const float scale = f16_to_f32(q.scales[row * (cols / 64) + k / 64]), bias = f16_to_f32(q.biases[row * (cols / 64) + k / 64]);
 #pragma unroll
@@ -294,7 +305,7 @@ __global__ __launch_bounds__(256) void q4_tiles_kernel(LayerCodes q, int64_t fra
         }
     }
     hi[fr * 64 + lane] = h;
-    lo[fr * 64 + lane] = l;
+    if constexpr (!MX) lo[fr * 64 + lane] = l;
 }
 
 // ---- grad -------------------------------------------------------------------
@@ -495,13 +506,14 @@ hipError_t launch_finish(const LowRank& p, void* operands, int32_t* exponents, h
     return hipGetLastError();
 }
 
-hipError_t launch_q4_tiles(const LayerCodes& q, int f16, int64_t matrices, int64_t rows, int64_t part, int64_t cols,
+hipError_t launch_code_tiles(const LayerCodes& q, int f16, int64_t matrices, int64_t rows, int64_t part, int64_t cols,
                            void* out, hipStream_t s) {
     const int64_t blocks = rows / part * ((part + 15) / 16), steps = (cols + 63) / 64 * 2, frags = matrices * blocks * steps;
     u32x4 *hi = (u32x4*)out, *lo = hi + frags * 64;
     const dim3 grid((unsigned)((frags + 3) / 4));
-    if (f16) launch(q4_tiles_kernel<true>, grid, dim3(256), 0, s, q, frags, blocks, steps, rows, part, cols, hi, lo);
-    else launch(q4_tiles_kernel<false>, grid, dim3(256), 0, s, q, frags, blocks, steps, rows, part, cols, hi, lo);
+    if (q.codes8) launch(code_tiles_kernel<false, true>, grid, dim3(256), 0, s, q, frags, blocks, steps, rows, part, cols, hi, lo);
+    else if (f16) launch(code_tiles_kernel<true, false>, grid, dim3(256), 0, s, q, frags, blocks, steps, rows, part, cols, hi, lo);
+    else launch(code_tiles_kernel<false, false>, grid, dim3(256), 0, s, q, frags, blocks, steps, rows, part, cols, hi, lo);
     return hipGetLastError();
 }
 

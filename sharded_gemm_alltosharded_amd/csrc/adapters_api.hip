@@ -117,7 +117,7 @@ bool tile_product(const sg_layer* l, const Geometry& g, int64_t T, bool transpos
     const int64_t f = g.part(), rank_width = g.S * f;  // of the sharded side
     // (a rank's segments of a sharded-to-all layer lie side by side in its matrix: of whole
     // blocks and without padding behind them, where there are several)
-    if (T <= 8 || (g.quantized && (transposed || !sg::layer_codes(l).codes)) ||
+    if ((T <= 8 && !g.quantized) || (g.quantized && (transposed || !sg::layer_codes(l, T).any())) ||
         (!g.column() && g.S > 1 && (f % 16 || rank_width % 64)) ||
         (double)T * (double)(g.in > g.out ? g.in : g.out) * 2 >= (double)0xffff0000ll ||
         (double)((g.out + 15 + 16 * g.S * g.P) * (g.in + 63 + 64 * g.P)) * (g.quantized ? 4 : 2) >= (double)0xffff0000ll)
@@ -152,14 +152,14 @@ bool tile_product(const sg_layer* l, const Geometry& g, int64_t T, bool transpos
     return true;
 }
 
-// (a 4-bit layer's: hi and lo)
+// of a quantized layer (hi and lo of a 4-bit one's)
 size_t weight_bytes(const Geometry& g) {
     if (!g.quantized) return 0;
     const int64_t blocks = g.column() ? (g.part() + 15) / 16 * g.S * g.P : (g.out + 15) / 16;
     return (size_t)(2 * (g.column() ? 1 : g.P) * blocks * (((g.column() ? g.in : g.in / g.P) + 63) / 64 * 2) * 1024);
 }
 
-// Its weights; of a 4-bit layer at `at` (weight_bytes).  p.W stays null where there are none.
+// Its weights; of a quantized layer at `at` (weight_bytes).  p.W stays null where there are none.
 sg_status tile_weights(const sg_layer* l, const Geometry& g, void* at, hipStream_t s, sg::Grouped* to, sg::Adapted* d) {
     sg::Grouped& p = *to;
     sg::LayerTiles v{};
@@ -168,11 +168,14 @@ sg_status tile_weights(const sg_layer* l, const Geometry& g, void* at, hipStream
         v.blocks = g.column() ? (g.part() + 15) / 16 * g.S * g.P : (g.out + 15) / 16;
         v.steps = (cols + 63) / 64 * 2;
         v.w = at;
-        if (sg_status st = launched(sg::launch_q4_tiles(sg::layer_codes(l), g.dtype == SG_F16, g.column() ? 1 : g.P, g.out,
-                                                        g.column() ? g.part() : g.out, cols, at, s), "4-bit weights"))
+        const sg::LayerCodes codes = sg::layer_codes(l, to->T);
+        if (sg_status st = launched(sg::launch_code_tiles(codes, g.dtype == SG_F16, g.column() ? 1 : g.P, g.out,
+                                                          g.column() ? g.part() : g.out, cols, at, s), "weight codes"))
             return st;
-        d->again = p.nseg;  // the same inputs through the lo halves
-        p.nseg *= 2;
+        if (codes.codes) {  // the same inputs through the lo halves
+            d->again = p.nseg;
+            p.nseg *= 2;
+        }
     } else if (sg_status st = launched(sg::layer_tiles(l, s, &v), "weight layout")) {
         return st;
     }
@@ -244,7 +247,8 @@ sg_status forward(const char* what, const sg_layer* l, const Geometry& g, const 
     sg::Grouped q;
     sg::Adapted d{};
     bool tiles = tile_product(l, g, T, false, swiglu, &q), split = false;
-    if (tiles && !sg::adapted_fills(q)) tiles = false, split = tile_product(l, g, T, false, false, &q) && split_product(g, q);
+    if (tiles && !g.quantized && !sg::adapted_fills(q))
+        tiles = false, split = tile_product(l, g, T, false, false, &q) && split_product(g, q);
     if (tiles || split) {
         if ((st = tile_weights(l, g, rest + operands_bytes(T, ad->rank), s, &q, &d))) return st;
         if (!q.W) tiles = split = false;

@@ -373,9 +373,15 @@ hipError_t sg::layer_tiles(const sg_layer* lc, hipStream_t st, LayerTiles* out) 
     return hipSuccess;
 }
 
-sg::LayerCodes sg::layer_codes(const sg_layer* l) {
-    if (!l->quantized || l->mx || l->qfrag) return LayerCodes{};
-    return {(const uint32_t*)l->w, l->qs, l->qb};
+sg::LayerCodes sg::layer_codes(const sg_layer* l, int64_t tokens) {
+    LayerCodes c{};
+    if (l->bias) return c;
+    if (l->mx) {
+        if (!l->wfrag && tokens <= 32 && l->dtype == SG_BF16) c.codes8 = (const uint8_t*)l->w, c.scales8 = l->ms;
+    } else if (l->quantized && !l->qfrag) {
+        c.codes = (const uint32_t*)l->w, c.scales = l->qs, c.biases = l->qb;
+    }
+    return c;
 }
 
 extern "C" {

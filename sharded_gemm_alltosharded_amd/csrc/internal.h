@@ -160,12 +160,15 @@ struct LayerTiles {
     int bias;
 };
 hipError_t layer_tiles(const sg_layer* l, hipStream_t s, LayerTiles* out);
-// A 4-bit layer whose codes no matrix-core kernel takes (row-major); codes null: any other.
+// A layer without bias whose row-major codes only the generic kernel takes: 4-bit, or MX FP8
+// of bf16 activations (which hold its weights exactly) up to 32 tokens.  Codes null: any other.
 struct LayerCodes {
-    const uint32_t* codes;
+    const uint32_t* codes;  // 4-bit
     const uint16_t *scales, *biases;
+    const uint8_t *codes8, *scales8;  // MX FP8
+    bool any() const { return codes || codes8; }
 };
-LayerCodes layer_codes(const sg_layer* l);
+LayerCodes layer_codes(const sg_layer* l, int64_t tokens);
 
 // launchers (return hipError_t of the launch)
 hipError_t launch_generic(const Problem& p, hipStream_t s);

@@ -203,6 +203,59 @@ def test_beside_quantized_layers(mode, i, o, kind, T):
         back(layer, xs.cuda(), dys.cuda(), ad, plan)
 
 
+@pytest.mark.parametrize("swiglu,bias", [(False, False), (False, True), (True, False)])
+@pytest.mark.parametrize("T", [3, 22, 33])
+@pytest.mark.parametrize("kind", ["q4", "mx8"])
+@pytest.mark.parametrize("mode,i,o,P", [(0, 1344, 512, 4), (1, 1408, 176, 2), (0, 832, 488, 1), (1, 768, 40, 8)])
+def test_quantized_layers_of_odd_sizes(mode, i, o, P, kind, T, swiglu, bias):
+    """Layers whose codes no matrix-core kernel takes, up to 32 tokens and behind; with biases."""
+    if swiglu and mode:
+        pytest.skip("the epilogue is the all-to-sharded layer's")
+    g = gen(T + o)
+    n, r = 3, 12
+    be = normal(g, (o,), BF) if bias else None
+    b = be.cuda() if bias else None
+    if kind == "q4":
+        w = torch.randint(-2 ** 31, 2 ** 31, (o, i // 8), generator=g, dtype=torch.int64).to(torch.int32)
+        sc = (torch.rand((o, i // 64), generator=g) * 0.01).half()
+        qb = (-7 * sc).half()
+        if mode and i // P % 64:
+            pytest.skip("a group of 64 in two ranks")
+        layer = sg.shard_quantized_linear(w.cuda(), sc.view(torch.int16).cuda(), qb.view(torch.int16).cuda(), i, mode, P=P,
+                                          act_dtype=BF, bias=b, segments=2 if swiglu else 1)
+        q = ((w.long() & 0xffffffff)[..., None] >> (4 * torch.arange(8)) & 15).flatten(1).double()
+        sq, qb = sc.double().repeat_interleave(64, 1) * q, qb.double().repeat_interleave(64, 1)
+        W, size = sq + qb, sq.abs() + qb.abs()
+    else:
+        codes, scales = mx.encode(normal(g, (o, i), F32, 0.05))
+        layer = sg.shard_mxfp8_linear(codes.cuda(), scales.cuda(), mode, P=P, bias=b, segments=2 if swiglu else 1)
+        W = mx.decode(codes, scales)
+        size = W.abs()
+    A, B = normal(g, (n, r, i), BF, 0.05), normal(g, (n, o, r), BF, 0.2)
+    scale, which = torch.rand(n, generator=g), draw_which(g, T, n)
+    x = normal(g, (T, i), BF)
+    order = ref.shard_rows(o if mode == 0 else i, 1, P)
+    ad, plan = sg.Adapters(A.cuda(), B.cuda(), scale.cuda()), sg.adapter_plan(which.cuda(), n)
+    d, e = aref.delta(x.double(), which, A, B, scale, BF)
+    base = x.double() @ W.T + (be.double() if bias else 0)
+    # fp32 sums of the codes' and the biases' products, or of the weights in two halves (2^-16)
+    e = e + (aref.SPLIT[BF] + (2 * i + 2 * r + 8) * 2.0 ** -24) * (x.double().abs() @ size.T + d.abs())
+    e = e + 4 * 2.0 ** -24 * base.abs()
+    want, bound = base + d, e
+    if swiglu:  # through the derivatives (|silu'| < 1.1), and fp32's steps of silu
+        (a, b), (ea, eb) = want.chunk(2, 1), e.chunk(2, 1)
+        want = ref.silu(a) * b
+        bound = 1.1 * (b.abs() + eb) * ea + (ref.silu(a).abs() + 1.1 * ea) * eb + 16 * 2.0 ** -24 * want.abs()
+        order = ref.shard_rows(o // 2, 1, P)
+    shard = lambda v: torch.stack([v[:, q] for q in order])  # noqa: E731
+    xs = (shard(x) if mode else x).cuda()
+    want, bound = (want, bound) if mode else (shard(want), shard(bound))
+    for out in (BF, F32):
+        y = (sg.adapted_sharded_to_all(layer, xs, ad, plan, out_dtype=out) if mode
+             else sg.adapted_all_to_sharded(layer, xs, ad, plan, swiglu=swiglu, out_dtype=out))
+        ref.close(y, want, bound, "y")
+
+
 # ---- backward ---------------------------------------------------------------
 
 @pytest.mark.parametrize("case", CASES)

@@ -580,6 +580,15 @@ size_t sg_gated_mlp_backward_workspace(const sg_experts* gate_up, const sg_exper
  * layer's (each rank has its part of every segment) and A is replicated;
  * sharded-to-all, A's columns go with the layer's, x A^T summed over the ranks, and B
  * is replicated.  Sums are fp32, and the output is rounded once.
+ *
+ * From nine tokens on, and backward, the product of a projection without bias runs on
+ * the expert layers' tiles.  A dense one whose weights are not stored for them (a rank's parts
+ * no multiple of 16 rows, or its inputs none of 64) builds a copy that is, of the same
+ * size, on its first such call: that allocates and synchronises, and a call captured
+ * into a graph before the copy exists runs the layer's own kernels instead.  The copy
+ * is held until sg_layer_free.  4-bit layers that have no matrix-core kernel are turned
+ * into 16-bit weights, in two halves, inside the call; fp16 ones need weights below
+ * 65504 there.
  * ------------------------------------------------------------------------- */
 typedef struct {
     const void* A;      /* (n, rank, in_dims) of the layer's dtype, on the device */
@@ -612,8 +621,8 @@ size_t sg_adapted_workspace(const sg_layer* layer, const sg_adapters* adapters, 
  *   dA (n, rank, in_dims), dB (n, out_dims, rank) of d_dtype, zeros for an adapter
  *      without tokens;
  *   dx of dx_dtype, laid out as x, through W and the adapters (dense layers only,
- *      else SG_ERR_UNSUPPORTED; on its first call the layer builds its transposed
- *      copy, as for its own backward call).
+ *      else SG_ERR_UNSUPPORTED; where the layer's own backward kernels run, it builds
+ *      its transposed copy on the first call, as for its own backward call).
  * Any may be NULL (not all); x is needed for dA and dB only.
  *   workspace sg_adapted_backward_workspace(layer, adapters, T) bytes, as above. */
 sg_status sg_adapted_all_to_sharded_backward(const sg_layer* layer, const sg_adapters* adapters, const int32_t* plan,

@@ -342,6 +342,7 @@ hipError_t sg::layer_tiles(const sg_layer* lc, hipStream_t st, LayerTiles* out) 
     out->blocks = x.blocks;
     out->steps = x.steps;
     out->bias = l->bias != nullptr;
+    if (out->bias) return hipSuccess;  // the tiles add none
     if (l->wfrag && x.f % 16 == 0 && x.kl % 64 == 0) {
         out->w = l->w;
         return hipSuccess;

@@ -588,7 +588,8 @@ size_t sg_gated_mlp_backward_workspace(const sg_experts* gate_up, const sg_exper
  * into a graph before the copy exists runs the layer's own kernels instead.  The copy
  * is held until sg_layer_free.  4-bit layers that have no matrix-core kernel are turned
  * into 16-bit weights, in two halves, inside the call; fp16 ones need weights below
- * 65504 there.
+ * 65504 there, and an infinite input makes its token's outputs NaN where the layer's
+ * own call may give infinities.
  * ------------------------------------------------------------------------- */
 typedef struct {
     const void* A;      /* (n, rank, in_dims) of the layer's dtype, on the device */

@@ -4,8 +4,8 @@ sizes that fill nothing, tokens without an adapter.
 
 Tolerances (adapters_ref): x A^T is an fp32 sum; as an operand it is split into two
 16-bit halves, off by 2^-16 (bf16) or 2^-22 (fp16) of itself; then an fp32 sum of
-2 rank products more beside the projection's own, and one rounding.  (Beside
-quantized layers the projection's part is the layer's own fp32 result.)"""
+2 rank products more beside the projection's own, and one rounding.  Quantized
+weights: as their codes, or in two such halves."""
 import math
 
 import pytest
@@ -430,6 +430,36 @@ def test_on_another_stream_and_in_graphs(i, o, n, r, T):
             step(xs[0], ws[0])
             torch.cuda.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(out, want[k])), k
+
+
+@pytest.mark.parametrize("T", [5, 30])
+@pytest.mark.parametrize("kind", ["q4", "mx8"])
+def test_quantized_layers_of_odd_sizes_in_graphs(kind, T):
+    g = gen(T)
+    i, o, n, r = 448, 240, 3, 16
+    if kind == "q4":
+        w = torch.randint(-2 ** 31, 2 ** 31, (o, i // 8), generator=g, dtype=torch.int64).to(torch.int32)
+        sc = (torch.rand((o, i // 64), generator=g) * 0.01).half()
+        layer = sg.shard_quantized_linear(w.cuda(), sc.view(torch.int16).cuda(), (-7 * sc).half().view(torch.int16).cuda(), i,
+                                          0, P=2, act_dtype=BF)
+    else:
+        codes, scales = mx.encode(normal(g, (o, i), F32, 0.05))
+        layer = sg.shard_mxfp8_linear(codes.cuda(), scales.cuda(), 0, P=2)
+    ad = sg.Adapters(normal(g, (n, r, i), BF, 0.1).cuda(), normal(g, (n, o, r), BF, 0.1).cuda())
+    xs, ws = [normal(g, (T, i), BF).cuda() for _ in range(3)], [draw_which(g, T, n).cuda() for _ in range(3)]
+    x, which = xs[0].clone(), ws[0].clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):  # the layer's first adapted call: nothing of it is built before
+        out = sg.adapted_all_to_sharded(layer, x, ad, sg.adapter_plan(which, n))
+    want = [sg.adapted_all_to_sharded(layer, a, ad, sg.adapter_plan(b, n)) for a, b in zip(xs, ws)]
+    for k in (1, 2, 0, 1):
+        x.copy_(xs[k])
+        which.copy_(ws[k])
+        graph.replay()
+        sg.adapted_all_to_sharded(layer, xs[0], ad, sg.adapter_plan(ws[0], n))
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[k]), k
 
 
 def test_adapters_trained_on_a_kept_input():

@@ -171,9 +171,15 @@ sg_status check_rows(const sg_experts* x, const int32_t* offsets, int64_t R) {
     return SG_OK;
 }
 
-sg_status check_gather(int64_t T, int64_t ldx, int64_t width, const int32_t* rows, int k, int64_t R) {
-    if (T < 0 || k < 1) return fail(SG_ERR_INVALID_ARG, "T must be >= 0 and k >= 1");
+sg_status check_tokens(int64_t T) {
+    if (T < 0) return fail(SG_ERR_INVALID_ARG, "T must be >= 0");
     if (T > kMaxRows) return fail(SG_ERR_UNSUPPORTED, "more than 2^30 tokens are not supported");
+    return SG_OK;
+}
+
+sg_status check_gather(int64_t T, int64_t ldx, int64_t width, const int32_t* rows, int k, int64_t R) {
+    if (sg_status st = check_tokens(T)) return st;
+    if (k < 1) return fail(SG_ERR_INVALID_ARG, "k must be >= 1");
     if (ldx < width) return fail(SG_ERR_INVALID_ARG, "row stride %lld of x is below its width %lld", (long long)ldx,
                                  (long long)width);
     if (!rows && R > T) return fail(SG_ERR_INVALID_ARG, "%lld rows of %lld tokens need a row map", (long long)R,
@@ -950,6 +956,7 @@ sg_status sg_gated_mlp_backward(const sg_experts* g, const sg_experts* d, const 
     if (!st) st = check_down(d);
     const int64_t fp = st ? 0 : h_stride(g), ldx = st ? 0 : up(g->l.in, 8);
     if (!st) st = check_rows(g, offsets, R);
+    if (!st) st = check_tokens(T);  // the workspace holds x whatever is asked for
     if (!st && dw_gate_up) st = check_gather(T, ldx, g->l.in, rows, k, R);
     if (!st && dw_gate_up) st = check_bytes(T, ldx, 4);
     if (!st && dw_gate_up) st = check_mx8(g->dtype, T, g->l.in);

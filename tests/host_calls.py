@@ -1,0 +1,91 @@
+"""Calls of the library on the stand-in runtime (host_stub.cpp), one function a test of
+test_host_calls_cpu.py, each in a process of its own:
+
+    python host_calls.py STUB LIBRARY FUNCTION
+"""
+import ctypes as C
+import sys
+
+BF16, F16 = 1, 2
+COLUMN, ROW = 0, 1
+INVALID, UNSUPPORTED, OOM = 1, 4, 6
+
+
+class Stub(C.Structure):
+    _fields_ = [(n, C.c_int64) for n in ("launches", "mallocs", "syncs", "device", "largest", "stream_captured",
+                                         "other_capture", "ended", "live")]
+
+
+class Adapters(C.Structure):
+    _fields_ = [("A", C.c_void_p), ("B", C.c_void_p), ("scale", C.c_void_p), ("n", C.c_int), ("rank", C.c_int)]
+
+
+def ready(stub, library):
+    global S, L, PTR
+    S = Stub.in_dll(C.CDLL(stub, mode=C.RTLD_GLOBAL), "stub")
+    L = C.CDLL(library)
+    L.sg_last_error.restype = C.c_char_p
+    for name in ("sg_gated_mlp_workspace", "sg_gated_mlp_backward_workspace", "sg_adapted_workspace",
+                 "sg_adapted_backward_workspace", "sg_adapter_plan_ints"):
+        getattr(L, name).restype = C.c_size_t
+    global memory
+    memory = C.create_string_buffer(1 << 22)
+    PTR = C.addressof(memory) // 256 * 256 + 256
+
+
+def wide(args):
+    """Integers as 64-bit ones (those that fit 32 bits alike), pointers as they are."""
+    return [C.c_int64(a) if isinstance(a, int) else a for a in args]
+
+
+def call(name, *args):
+    return getattr(L, name)(*wide(args))
+
+
+def error():
+    return L.sg_last_error().decode()
+
+
+def ok(status):
+    assert status == 0, (status, error())
+
+
+def experts(E, out, width, mode, segments, P):
+    h = C.c_void_p()
+    ok(call("sg_shard_experts", PTR, BF16, E, out, width, mode, segments, P, None, C.byref(h)))
+    return h
+
+
+def linear(out, width, mode, segments=1, P=1, bias=None, dtype=BF16):
+    h = C.c_void_p()
+    ok(call("sg_shard_linear", PTR, dtype, out, width, bias, mode, segments, P, None, C.byref(h)))
+    return h
+
+
+def block_backward_tokens():
+    """A block's backward call refuses every T that its workspace is not sized for."""
+    up, down = experts(1, 64, 32, COLUMN, 2, 1), experts(1, 32, 32, ROW, 1, 1)
+
+    def back(T, R, dx, dwg, dwd, ws=PTR, n=1 << 20):
+        return call("sg_gated_mlp_backward", up, down, PTR, PTR, T, PTR, PTR, PTR, None, None, 1, R, dx, BF16, dwg, dwd,
+                    BF16, ws, n, None)
+
+    before = S.launches
+    for T in (-1, -(1 << 40), (1 << 30) + 1, 1 << 62):
+        assert call("sg_gated_mlp_backward_workspace", up, down, T, 4) == 0
+        for dx, dwg, dwd in ((PTR, None, None), (None, None, PTR), (PTR, None, PTR), (None, PTR, None)):
+            for ws, n in ((None, 0), (PTR, 1 << 20)):
+                st = back(T, 4, dx, dwg, dwd, ws, n)
+                assert st == (INVALID if T < 0 else UNSUPPORTED), (T, st, error())
+    assert S.launches == before
+    assert back(4, 4, PTR, None, None, None, 0) == 5  # no workspace
+    assert S.launches == before
+    ok(back(4, 4, PTR, None, None))
+    ok(back(0, 4, PTR, None, PTR))
+    assert S.launches > before
+
+
+if __name__ == "__main__":
+    ready(*sys.argv[1:3])
+    globals()[sys.argv[3]]()
+    print("ok")

@@ -352,6 +352,7 @@ hipError_t sg::layer_tiles(const sg_layer* lc, hipStream_t st, LayerTiles* out) 
         hipStreamCaptureStatus capturing = hipStreamCaptureStatusNone;
         hipError_t e = hipStreamIsCapturing(st, &capturing);
         if (e != hipSuccess || capturing != hipStreamCaptureStatusNone) return e;
+        RelaxedCapture relaxed;
         const void* rowmajor = l->w;
         void *tmp = nullptr, *wx = nullptr;
         if (l->wfrag) {

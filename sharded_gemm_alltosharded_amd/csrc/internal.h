@@ -122,6 +122,16 @@ ArmedEvents& armed_events();
 // the calling thread's sg_last_error() message
 std::string& last_error();
 
+// While it lives, this thread allocates, frees and waits beside whatever capture another
+// thread has open; in the mode that threads start in, that fails and ends the capture.
+struct RelaxedCapture {
+    hipStreamCaptureMode mode = hipStreamCaptureModeRelaxed;
+    RelaxedCapture() { (void)hipThreadExchangeStreamCaptureMode(&mode); }
+    ~RelaxedCapture() { (void)hipThreadExchangeStreamCaptureMode(&mode); }
+    RelaxedCapture(const RelaxedCapture&) = delete;
+    RelaxedCapture& operator=(const RelaxedCapture&) = delete;
+};
+
 #ifdef __HIPCC__
 template <typename K, typename... Args>
 inline void launch(K kernel, dim3 grid, dim3 block, size_t lds, hipStream_t s, Args... args) {

@@ -25,6 +25,7 @@ def ready(stub, library):
     S = Stub.in_dll(C.CDLL(stub, mode=C.RTLD_GLOBAL), "stub")
     L = C.CDLL(library)
     L.sg_last_error.restype = C.c_char_p
+    # (integers travel as 64 bits: the callee reads as many as it declares)
     for name in ("sg_gated_mlp_workspace", "sg_gated_mlp_backward_workspace", "sg_adapted_workspace",
                  "sg_adapted_backward_workspace", "sg_adapter_plan_ints"):
         getattr(L, name).restype = C.c_size_t
@@ -83,6 +84,50 @@ def block_backward_tokens():
     ok(back(4, 4, PTR, None, None))
     ok(back(0, 4, PTR, None, PTR))
     assert S.launches > before
+
+
+def adapted(layer, mode, T=16, status=0, n=2, rank=8):
+    ad = Adapters(PTR, PTR, None, n, rank)
+    ref = C.byref(ad)
+    need = call("sg_adapted_workspace", layer, ref, T)
+    if mode == COLUMN:
+        st = call("sg_adapted_all_to_sharded", layer, ref, PTR, PTR, T, PTR, 1, 0, BF16, PTR, need, None)
+    else:
+        st = call("sg_adapted_sharded_to_all", layer, ref, PTR, PTR, T, PTR, BF16, PTR, need, None)
+    assert st == status, (st, error())
+
+
+def adapted_backward(layer, mode, T=16, status=0, n=2, rank=8, dx=True):
+    ad = Adapters(PTR, PTR, None, n, rank)
+    ref = C.byref(ad)
+    need = call("sg_adapted_backward_workspace", layer, ref, T)
+    name = "sg_adapted_all_to_sharded_backward" if mode == COLUMN else "sg_adapted_sharded_to_all_backward"
+    st = call(name, layer, ref, PTR, PTR, PTR, T, PTR if dx else None, BF16, PTR, PTR, BF16, PTR, need, None)
+    assert st == status, (st, error())
+
+
+# out, in, mode, P: stored row-major, and in fragments that are not the tiles'
+COPIED = [(40, 72, COLUMN, 1), (48, 96, COLUMN, 2), (80, 32, ROW, 1)]
+
+
+def first_adapted_call_beside_a_capture():
+    """The copy of a layer's weights is built without ending a capture of another thread."""
+    for out, width, mode, P in COPIED:
+        for f in (adapted, adapted_backward):
+            layer = linear(out, width, mode, P=P)
+            mallocs = S.mallocs
+            S.other_capture = 1
+            f(layer, mode)
+            S.other_capture = 0
+            assert S.ended == 0 and S.mallocs > mallocs, (out, width, mode, P)
+            mallocs = S.mallocs
+            f(layer, mode)  # it is there
+            assert S.mallocs == mallocs
+    layer = linear(*COPIED[0][:2], COLUMN)
+    mallocs, launches = S.mallocs, S.launches
+    S.stream_captured = 1  # the call's own stream: nothing is built, the layer's own kernels run
+    adapted(layer, COLUMN)
+    assert S.ended == 0 and S.mallocs == mallocs and S.launches > launches
 
 
 if __name__ == "__main__":

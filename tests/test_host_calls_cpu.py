@@ -34,3 +34,7 @@ def calls(stub, name):
 
 def test_block_backward_refuses_token_counts(stub):
     calls(stub, "block_backward_tokens")
+
+
+def test_first_adapted_call_beside_a_capture(stub):
+    calls(stub, "first_adapted_call_beside_a_capture")

@@ -240,8 +240,9 @@ sg_status sg_mlp_static(const sg_layer* gate_up, const sg_layer* down, const voi
  * that the layer builds on the first backward call that reads it (16-bit
  * layers whose out_dims/P is a multiple of 32 and in_dims of 16; the same
  * bytes as the weights again, held until sg_layer_free; that first call
- * allocates and synchronises the stream).  Backward calls on one layer must not
- * run concurrently with its first one.
+ * allocates and synchronises the stream; a call captured into a graph before the
+ * copy exists builds none and runs on the vector units).  Backward calls on one
+ * layer must not run concurrently with its first one.
  * dx or dw may be NULL (not both).  Dense layers only (SG_ERR_UNSUPPORTED for
  * 4-bit and MX FP8 layers); no bias gradient.  fp32 accumulation; the rank sum
  * is deterministic.  B = 0 is a no-op. */

@@ -988,10 +988,17 @@ bool wt_ok(const sg_layer* l) {
     return !l->quantized && !l->mx && l->dtype != SG_F32 && l->rows_r % 32 == 0 && l->cols_r % 16 == 0;
 }
 
-sg_status ensure_wt(const sg_layer* lc, hipStream_t st) {
+// *out: the copy, built by the first call; null where that is being captured (it would
+// allocate and wait), whose product then runs on the vector units
+sg_status ensure_wt(const sg_layer* lc, hipStream_t st, const void** out) {
     sg_layer* l = const_cast<sg_layer*>(lc);  // the copy is a cache of the layer's own weights
     std::lock_guard<std::mutex> lock(l->wt_mu);
+    *out = l->wt;
     if (l->wt) return SG_OK;
+    hipStreamCaptureStatus capturing = hipStreamCaptureStatusNone;
+    HIP_TRY(hipStreamIsCapturing(st, &capturing), "transposed shard copy");
+    if (capturing != hipStreamCaptureStatusNone) return SG_OK;
+    sg::RelaxedCapture relaxed;
     const size_t bytes = (size_t)(l->P * l->rows_r * l->cols_r) * dtype_size(l->dtype);
     void* rowmajor = l->w;
     void* tmp = nullptr;
@@ -1013,7 +1020,7 @@ sg_status ensure_wt(const sg_layer* lc, hipStream_t st) {
         if (wt) (void)hipFree(wt);
         return hip_fail(e, "transposed shard copy");
     }
-    l->wt = wt;
+    *out = l->wt = wt;
     return SG_OK;
 }
 
@@ -1133,11 +1140,12 @@ sg_status sg_all_to_sharded_backward(const sg_layer* l, const void* x, const voi
                     dw_ws_bytes(l, B));
     hipStream_t st = (hipStream_t)stream;
     if (dx) {
-        if (wt_ok(l) && aligned16(dy) && aligned16(dx)) {
+        const void* wt = nullptr;
+        if (wt_ok(l) && aligned16(dy) && aligned16(dx))
+            if (sg_status s2 = ensure_wt(l, st, &wt)) return s2;
+        if (wt) {
             // the sum_gradients all_sum: dx = sum_r dY_r W_r, a sharded-to-all
             // product on the transposed shards, ranks summed in order
-            sg_status s2 = ensure_wt(l, st);
-            if (s2 != SG_OK) return s2;
             sg::Problem p{};
             p.A = dy;
             p.lda = l->rows_r;
@@ -1146,7 +1154,7 @@ sg_status sg_all_to_sharded_backward(const sg_layer* l, const void* x, const voi
             p.Kseg = (int)l->rows_r;
             p.nseg = l->P;
             p.dtype = l->dtype;
-            p.W = l->wt;
+            p.W = wt;
             p.ldw = l->rows_r;
             p.w_seg = l->cols_r * l->rows_r;
             p.wfrag = 1;
@@ -1221,11 +1229,12 @@ sg_status sg_sharded_to_all_backward(const sg_layer* l, const void* x_partial, c
                     dw_ws_bytes(l, B));
     hipStream_t st = (hipStream_t)stream;
     if (dx_partial) {
-        if (wt_ok(l) && aligned16(dy) && aligned16(dx_partial)) {
+        const void* wt = nullptr;
+        if (wt_ok(l) && aligned16(dy) && aligned16(dx_partial))
+            if (sg_status s2 = ensure_wt(l, st, &wt)) return s2;
+        if (wt) {
             // every rank receives the full dY: dX_r = dY W_r, an all-to-sharded
             // product on the stacked W_r^T with a sharded output
-            sg_status s2 = ensure_wt(l, st);
-            if (s2 != SG_OK) return s2;
             sg::Problem p{};
             p.A = dy;
             p.lda = l->out_dims;
@@ -1233,7 +1242,7 @@ sg_status sg_sharded_to_all_backward(const sg_layer* l, const void* x_partial, c
             p.Kseg = (int)l->out_dims;
             p.nseg = 1;
             p.dtype = l->dtype;
-            p.W = l->wt;
+            p.W = wt;
             p.ldw = l->out_dims;
             p.wfrag = 1;
             p.wsteps = l->out_dims / 32;

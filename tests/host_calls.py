@@ -130,6 +130,29 @@ def first_adapted_call_beside_a_capture():
     assert S.ended == 0 and S.mallocs == mallocs and S.launches > launches
 
 
+def backward(layer, mode, B=4):
+    name = "sg_all_to_sharded_backward" if mode == COLUMN else "sg_sharded_to_all_backward"
+    ok(call(name, layer, None, PTR, B, PTR, BF16, None, BF16, None, 0, None))
+
+
+def first_backward_call_beside_a_capture():
+    """The transposed copy, too; a call captured before it is there builds none."""
+    for mode in (COLUMN, ROW):
+        for f in (backward, lambda x, m: adapted_backward(x, m, T=4)):
+            for out, width in ((64, 64), (64, 80)):  # stored in fragments and row-major
+                layer = linear(out, width, mode)
+                S.stream_captured, mallocs, launches = 1, S.mallocs, S.launches
+                f(layer, mode)
+                assert S.ended == 0 and S.mallocs == mallocs and S.launches > launches
+                S.stream_captured, S.other_capture = 0, 1
+                f(layer, mode)
+                assert S.ended == 0 and S.mallocs > mallocs
+                S.stream_captured, S.other_capture, mallocs = 1, 0, S.mallocs
+                f(layer, mode)  # it is there
+                S.stream_captured = 0
+                assert S.ended == 0 and S.mallocs == mallocs
+
+
 if __name__ == "__main__":
     ready(*sys.argv[1:3])
     globals()[sys.argv[3]]()

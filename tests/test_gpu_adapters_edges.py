@@ -5,6 +5,7 @@ import threading
 import pytest
 import torch
 
+import moe_ref as ref
 import sharded_gemm_alltosharded_amd as sg
 
 pytestmark = pytest.mark.gpu
@@ -75,3 +76,32 @@ def test_first_adapted_call_while_another_thread_captures(i, o):
         torch.cuda.synchronize()
         assert torch.equal(out, plain)
     del hold
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("mode,i,o", [(0, 64, 96), (0, 80, 64), (1, 64, 96), (1, 96, 64)])
+def test_first_backward_call_captured(mode, i, o, dtype):
+    """A backward call captured before the layer has its transposed copy: the vector units' sums."""
+    g = gen(i + o + mode)
+    B, P = 20, 2
+    w = normal(g, (o, i), dtype, 1 / math.sqrt(o))
+    layer = sg.shard_linear(w.cuda(), mode, P=P)
+    dys = [normal(g, (P, B, o // P) if mode == 0 else (B, o), dtype).cuda() for _ in range(3)]
+    dy, graph = dys[0].clone(), torch.cuda.CUDAGraph()
+    back = sg.all_to_sharded_backward if mode == 0 else sg.sharded_to_all_backward
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        out, _ = back(layer, None, dy, need_dw=False, dx_dtype=F32)
+    for k in (1, 2, 0):
+        dy.copy_(dys[k])
+        graph.replay()
+        eager, _ = back(layer, None, dys[k], need_dw=False, dx_dtype=F32)
+        torch.cuda.synchronize()
+        full = dys[k].double().cpu()
+        if mode == 0:
+            full = full.transpose(0, 1).flatten(1)
+        want, mag = full @ w.double(), full.abs() @ w.double().abs()
+        if mode == 1:
+            want, mag = (v.view(B, P, i // P).transpose(0, 1) for v in (want, mag))
+        for got, name in ((out, "captured"), (eager, "eager")):
+            ref.close(got, want, ref.sum_bound(mag, o), name)

@@ -38,3 +38,7 @@ def test_block_backward_refuses_token_counts(stub):
 
 def test_first_adapted_call_beside_a_capture(stub):
     calls(stub, "first_adapted_call_beside_a_capture")
+
+
+def test_first_backward_call_beside_a_capture(stub):
+    calls(stub, "first_backward_call_beside_a_capture")

@@ -367,7 +367,9 @@ hipError_t sg::layer_tiles(const sg_layer* lc, hipStream_t st, LayerTiles* out) 
         if (tmp) (void)hipFree(tmp);
         if (e != hipSuccess) {
             if (wx) (void)hipFree(wx);
-            return e;
+            if (e != hipErrorOutOfMemory) return e;
+            (void)hipGetLastError();  // (or the next launch's check would find it)
+            return hipSuccess;
         }
         l->wx = wx;
     }

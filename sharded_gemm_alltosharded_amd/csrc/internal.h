@@ -165,7 +165,8 @@ __host__ __device__ inline int64_t q4_group_offset(int64_t row, int64_t g, int64
 // `blocks` blocks.  The stored weights where they are that already, else a copy that the
 // layer builds on its first call (which allocates and synchronises the stream) and holds.
 struct LayerTiles {
-    const void* w;  // null: no such layer, or its copy is not there and the stream is captured
+    const void* w;  // null: no such layer, or its copy is not there and the stream is
+                    // captured, or there is no memory for it
     int64_t blocks, steps;
     int bias;
 };

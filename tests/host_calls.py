@@ -153,6 +153,23 @@ def first_backward_call_beside_a_capture():
                 assert S.ended == 0 and S.mallocs == mallocs
 
 
+def no_memory_for_a_copy():
+    """Without memory for the copy of its weights (or for the way there) a layer's own kernels run."""
+    for out, width, mode, P in COPIED:
+        weights = out * width * 2
+        for f in (adapted, lambda x, m: adapted_backward(x, m, T=16)):
+            for largest in (0, weights):  # (the copy is padded: larger)
+                layer = linear(out, width, mode, P=P)
+                live, launches = S.live, S.launches
+                S.largest = largest
+                f(layer, mode)
+                f(layer, mode)  # (the failure is not found again by a launch)
+                S.largest = 1 << 60
+                assert S.live == live and S.launches > launches
+                f(layer, mode)
+                assert S.live == live + 1, (S.live, live)
+
+
 if __name__ == "__main__":
     ready(*sys.argv[1:3])
     globals()[sys.argv[3]]()

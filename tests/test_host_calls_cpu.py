@@ -42,3 +42,7 @@ def test_first_adapted_call_beside_a_capture(stub):
 
 def test_first_backward_call_beside_a_capture(stub):
     calls(stub, "first_backward_call_beside_a_capture")
+
+
+def test_no_memory_for_a_copy(stub):
+    calls(stub, "no_memory_for_a_copy")

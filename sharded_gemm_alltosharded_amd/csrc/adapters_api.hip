@@ -67,6 +67,11 @@ sg_status check_call(const sg_layer* l, int mode, const sg_adapters* ad, int64_t
     if (sg_status st = sg_layer_info(l, &g->out, &g->in, &g->mode, &g->S, &g->P, &g->dtype, &g->quantized)) return st;
     if (g->mode != mode)
         return fail(SG_ERR_INVALID_ARG, mode == SG_ALL_TO_SHARDED ? "layer is sharded-to-all" : "layer is all-to-sharded");
+    int d = -1;
+    if (hipGetDevice(&d) != hipSuccess || d != sg::layer_device(l)) {
+        (void)hipGetLastError();
+        return fail(SG_ERR_INVALID_ARG, "the layer lives on device %d, the current device is %d", sg::layer_device(l), d);
+    }
     if (g->dtype == SG_F32) return fail(SG_ERR_UNSUPPORTED, "adapters stand beside layers of bf16 or fp16 activations");
     if (sg_status st = check_adapters(ad)) return st;
     if (T < 0) return fail(SG_ERR_INVALID_ARG, "T must be >= 0");

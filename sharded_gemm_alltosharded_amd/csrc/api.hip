@@ -321,6 +321,7 @@ void set_weights(sg::Problem& p, const sg_layer* l) {
 }  // namespace
 
 std::string& sg::last_error() { return g_err; }
+int sg::layer_device(const sg_layer* l) { return l->device; }
 
 hipError_t sg::layer_tiles(const sg_layer* lc, hipStream_t st, LayerTiles* out) {
     sg_layer* l = const_cast<sg_layer*>(lc);  // the copy is a cache of the layer's own weights

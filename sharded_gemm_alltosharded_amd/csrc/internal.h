@@ -159,6 +159,7 @@ __host__ __device__ inline int64_t q4_group_offset(int64_t row, int64_t g, int64
     return (((row >> 5) * (groups >> 2) + (g >> 2)) * 32 + (row & 31)) * 4 + (g & 3);
 }
 
+int layer_device(const sg_layer* l);
 // A dense 16-bit layer's weights for the grouped tiles, in the expert layers' layout
 // (experts.h): matrices of 16-row blocks of `steps` 32-input steps.  All-to-sharded: one
 // matrix, every part of f rows padded to whole blocks; sharded-to-all: one a rank, of

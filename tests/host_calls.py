@@ -170,6 +170,21 @@ def no_memory_for_a_copy():
                 assert S.live == live + 1, (S.live, live)
 
 
+def adapted_calls_on_another_device():
+    """Refused, as the expert calls are: what they build and launch would lie on the wrong one."""
+    for mode in (COLUMN, ROW):
+        layer = linear(40, 72, mode)
+        mallocs, launches = S.mallocs, S.launches
+        for T in (0, 1, 16):
+            for f in (adapted, adapted_backward):
+                S.device = 1
+                f(layer, mode, T=T, status=INVALID)
+                assert "device 0" in error() and "device is 1" in error()
+        assert S.mallocs == mallocs and S.launches == launches
+        S.device = 0
+        adapted(layer, mode)
+
+
 if __name__ == "__main__":
     ready(*sys.argv[1:3])
     globals()[sys.argv[3]]()

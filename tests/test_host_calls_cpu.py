@@ -46,3 +46,7 @@ def test_first_backward_call_beside_a_capture(stub):
 
 def test_no_memory_for_a_copy(stub):
     calls(stub, "no_memory_for_a_copy")
+
+
+def test_adapted_calls_on_another_device(stub):
+    calls(stub, "adapted_calls_on_another_device")

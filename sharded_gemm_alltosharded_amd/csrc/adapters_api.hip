@@ -243,8 +243,7 @@ sg_status forward(const char* what, const sg_layer* l, const Geometry& g, const 
     sg::LowRank& p = u.p;
     p.U = (float*)workspace;
     p.X = x;
-    sg_status st = launched(sg::launch_shrink(p, s), what);
-    if (st) return st;
+    sg_status st = SG_OK;
     const int64_t n = g.column() ? (epilogue == SG_EPI_SWIGLU ? g.out / 2 : g.out) / g.P : g.out;  // columns of a rank
     const bool gathered = g.column() && out_layout == SG_OUT_FULL;
     const bool swiglu = epilogue == SG_EPI_SWIGLU;
@@ -264,15 +263,12 @@ sg_status forward(const char* what, const sg_layer* l, const Geometry& g, const 
         q.out = y;
         q.out_dtype = y_dtype;
         if (gathered) q.ldo = n * g.P, q.o_rank = n;
-        st = finish(p, &d, rest, T, what, s);
+        st = launched(sg::launch_shrink(p, s), what);
+        if (!st) st = finish(p, &d, rest, T, what, s);
         return st ? st : launched(sg::launch_adapted(q, d, s), what);
     }
-    // (many rows' sums are added up once, few by every workgroup that wants them)
-    if (p.plan.tile_rows > 16) {
-        if ((st = launched(sg::launch_finish(p, nullptr, nullptr, s), what))) return st;
-        p.slabs = 1;
-    }
-    // the projection's result stays in fp32 until the adapters' part is added, so that y
+    // The projection first: its own call may refuse what this one lets through.  The
+    // projection's result stays in fp32 until the adapters' part is added, so that y
     // is rounded once; an fp32 y holds it itself
     const bool in_y = y_dtype == SG_F32 && !swiglu && !(split && gathered);
     char* at = rest;
@@ -285,6 +281,12 @@ sg_status forward(const char* what, const sg_layer* l, const Geometry& g, const 
         st = sg_all_to_sharded_ex(l, x, SG_IN_FULL, T, base, in_y ? out_layout : SG_OUT_SHARDED, SG_EPI_NONE, SG_F32, stream);
     } else {
         st = sg_sharded_to_all_ex(l, x, T, base, SG_OUT_FULL, SG_F32, at, ws_bytes - (size_t)(at - (char*)workspace), stream);
+    }
+    if (!st) st = launched(sg::launch_shrink(p, s), what);
+    // (many rows' sums are added up once, few by every workgroup that wants them)
+    if (!st && p.plan.tile_rows > 16) {
+        st = launched(sg::launch_finish(p, nullptr, nullptr, s), what);
+        p.slabs = 1;
     }
     if (st) return st;
     p.M = ad->B;
@@ -333,7 +335,15 @@ sg_status backward(const char* what, const sg_layer* l, const Geometry& g, const
             if ((st = tile_weights(l, g, nullptr, s, &q, &d))) return st;
         if (!q.W) tiles = split = false;
     }
-    if (T && (dx || dA)) {
+    // as forward: the frozen projection's part in fp32, rounded once with the adapters',
+    // and before any other launch
+    float* base = dx_dtype == SG_F32 ? (float*)dx : (float*)rest;
+    if (T && dx && !tiles) {
+        if (split) st = launch_split(q, dy, base, rest + up256(T * g.in * 4), what, s);
+        else st = g.column() ? sg_all_to_sharded_backward(l, nullptr, dy, T, base, SG_F32, nullptr, SG_F32, nullptr, 0, stream)
+                             : sg_sharded_to_all_backward(l, nullptr, dy, T, base, SG_F32, nullptr, SG_F32, nullptr, 0, stream);
+    }
+    if (!st && T && (dx || dA)) {
         st = launched(sg::launch_shrink(v.p, s), what);
         if (!st) st = tiles ? finish(v.p, &d, rest, T, what, s) : launched(sg::launch_finish(v.p, nullptr, nullptr, s), what);
         v.p.slabs = 1;
@@ -372,12 +382,6 @@ sg_status backward(const char* what, const sg_layer* l, const Geometry& g, const
         q.out_dtype = dx_dtype;
         st = launched(sg::launch_adapted(q, d, s), what);
     } else if (!st && T && dx) {
-        // as forward: the frozen projection's part in fp32, rounded once with the adapters'
-        float* base = dx_dtype == SG_F32 ? (float*)dx : (float*)rest;
-        if (split) st = launch_split(q, dy, base, rest + up256(T * g.in * 4), what, s);
-        else st = g.column() ? sg_all_to_sharded_backward(l, nullptr, dy, T, base, SG_F32, nullptr, SG_F32, nullptr, 0, stream)
-                             : sg_sharded_to_all_backward(l, nullptr, dy, T, base, SG_F32, nullptr, SG_F32, nullptr, 0, stream);
-        if (st) return st;
         sg::LowRank p = v.p;
         p.M = ad->A;
         p.transposed = 1;  // (rank, in), its columns the output's

@@ -185,6 +185,24 @@ def adapted_calls_on_another_device():
         adapted(layer, mode)
 
 
+def projections_that_cannot_be_launched():
+    """What the projection's own call refuses is refused before anything is launched."""
+    T = 1 << 25
+    row = linear(200, 35, ROW, bias=PTR)  # (biases: the layer's own kernels)
+    column = linear(200, 35, COLUMN, bias=PTR)
+    for layer, mode in ((row, ROW), (column, COLUMN)):
+        ad = Adapters(PTR, PTR, None, 1, 8)
+        ref = C.byref(ad)
+        launches, huge = S.launches, 1 << 60
+        name = "sg_adapted_all_to_sharded" if mode == COLUMN else "sg_adapted_sharded_to_all"
+        tail = (1, 0, BF16) if mode == COLUMN else (BF16,)
+        assert call(name, layer, ref, PTR, PTR, T, PTR, *tail, PTR, huge, None) != 0
+        assert S.launches == launches, (mode, "forward")
+        for d in (PTR, None):
+            assert call(name + "_backward", layer, ref, PTR, PTR, PTR, T, PTR, BF16, d, d, BF16, PTR, huge, None) != 0
+            assert S.launches == launches, (mode, "backward")
+
+
 if __name__ == "__main__":
     ready(*sys.argv[1:3])
     globals()[sys.argv[3]]()

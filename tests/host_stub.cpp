@@ -126,7 +126,9 @@ hipError_t __hipPopCallConfiguration(dim3* grid, dim3* block, size_t* lds, hipSt
     *grid = config.grid, *block = config.block, *lds = config.lds, *s = config.stream;
     return hipSuccess;
 }
-hipError_t hipLaunchKernel(const void*, dim3, dim3, void**, size_t, hipStream_t) {
+hipError_t hipLaunchKernel(const void*, dim3 grid, dim3 block, void**, size_t, hipStream_t) {
+    if (!grid.x || !grid.y || !grid.z || grid.y > 65535 || grid.z > 65535 || (uint64_t)grid.x * block.x >= (uint64_t)1 << 32)
+        return told(hipErrorInvalidConfiguration);
     ++stub.launches;
     return hipSuccess;
 }

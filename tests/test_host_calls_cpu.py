@@ -50,3 +50,7 @@ def test_no_memory_for_a_copy(stub):
 
 def test_adapted_calls_on_another_device(stub):
     calls(stub, "adapted_calls_on_another_device")
+
+
+def test_projections_that_cannot_be_launched(stub):
+    calls(stub, "projections_that_cannot_be_launched")

@@ -157,11 +157,12 @@ bool tile_product(const sg_layer* l, const Geometry& g, int64_t T, bool transpos
     return true;
 }
 
-// of a quantized layer (hi and lo of a 4-bit one's)
+// 16-bit matrices that a layer's weights make up: hi and lo of a 4-bit one's
+int halves(const Geometry& g) { return g.quantized == 1 ? 2 : 1; }
 size_t weight_bytes(const Geometry& g) {
     if (!g.quantized) return 0;
     const int64_t blocks = g.column() ? (g.part() + 15) / 16 * g.S * g.P : (g.out + 15) / 16;
-    return (size_t)(2 * (g.column() ? 1 : g.P) * blocks * (((g.column() ? g.in : g.in / g.P) + 63) / 64 * 2) * 1024);
+    return (size_t)(halves(g) * (g.column() ? 1 : g.P) * blocks * (((g.column() ? g.in : g.in / g.P) + 63) / 64 * 2) * 1024);
 }
 
 // Its weights; of a quantized layer at `at` (weight_bytes).  p.W stays null where there are none.
@@ -187,7 +188,7 @@ sg_status tile_weights(const sg_layer* l, const Geometry& g, void* at, hipStream
     if (v.bias) return SG_OK;
     const int64_t matrix = v.blocks * v.steps * 1024;
     p.W = (const uint8_t*)v.w;
-    p.w_expert = matrix * (g.column() ? 1 : g.P) * (g.quantized ? 2 : 1);
+    p.w_expert = matrix * (g.column() ? 1 : g.P) * halves(g);
     p.wsteps = (int)v.steps;
     d->wseg = d->wrank = (uint32_t)matrix;
     return SG_OK;

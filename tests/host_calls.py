@@ -203,6 +203,31 @@ def projections_that_cannot_be_launched():
             assert S.launches == launches, (mode, "backward")
 
 
+def quantized(out, width, mode, P, bits, dtype=BF16):
+    h = C.c_void_p()
+    if bits == 8:
+        ok(call("sg_shard_mxfp8_linear", PTR, PTR, out, width, dtype, None, mode, 1, P, None, C.byref(h)))
+    else:
+        ok(call("sg_shard_quantized_linear", PTR, PTR, PTR, out, width, 64, 4, dtype, None, mode, 1, P, None, C.byref(h)))
+    return h
+
+
+def workspace_of_decoded_weights():
+    """MX FP8 weights become one 16-bit matrix, 4-bit ones two: the workspace holds no more."""
+    T, n, rank = 22, 2, 8
+    ad = Adapters(PTR, PTR, None, n, rank)
+    for out, width, mode, P in ((416, 448, COLUMN, 1), (208, 896, ROW, 2)):
+        ranks = P if mode == ROW else 1
+        one = ranks * ((out + 15) // 16) * ((width // ranks + 63) // 64 * 2) * 1024
+        for bits, matrices in ((8, 1), (4, 2)):
+            layer = quantized(out, width, mode, P, bits)
+            need = call("sg_adapted_workspace", layer, C.byref(ad), T)
+            # beside them: x A^T in up to sixteen slabs of 16 floats a token, its operands and exponents
+            rest = 16 * T * 16 * 4 + 32 * 64 + T * 4 + 4 * 256
+            assert matrices * one <= need <= matrices * one + rest, (bits, need, one)
+            adapted(layer, mode, T=T)
+
+
 if __name__ == "__main__":
     ready(*sys.argv[1:3])
     globals()[sys.argv[3]]()

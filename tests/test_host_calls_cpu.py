@@ -54,3 +54,7 @@ def test_adapted_calls_on_another_device(stub):
 
 def test_projections_that_cannot_be_launched(stub):
     calls(stub, "projections_that_cannot_be_launched")
+
+
+def test_workspace_of_decoded_weights(stub):
+    calls(stub, "workspace_of_decoded_weights")

@@ -561,7 +561,9 @@ size_t sg_gated_mlp_workspace(const sg_experts* gate_up, const sg_experts* down,
  * dw_gate_up (E, P, 2 f, in_dims); dw_down (E, P, out_dims, f), of dw_dtype, laid out
  * as the layers' shards.  Any may be NULL (not all).  x_codes and x_scales are needed
  * for dw_gate_up only.  The chain of sg_experts_gated_backward, sg_dequantize_mxfp8
- * and the two layers' backward calls (weight gradients bitwise, dx as y above).
+ * and the two layers' backward calls (weight gradients bitwise, dx as y above), but for
+ * kept fp16 inputs from 63488 on: E4M3 rounds them to 65536, which the weight gradient
+ * takes as 65504, where sg_dequantize_mxfp8 gives an infinity.
  *   workspace sg_gated_mlp_backward_workspace(...) bytes, 16-byte aligned. */
 sg_status sg_gated_mlp_backward(const sg_experts* gate_up, const sg_experts* down, const uint8_t* x_codes,
                                 const uint8_t* x_scales, int64_t T, const uint8_t* gu_codes, const uint8_t* gu_scales,

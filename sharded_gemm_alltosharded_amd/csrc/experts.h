@@ -139,8 +139,9 @@ hipError_t launch_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scales, 
 __host__ __device__ inline int64_t mx8_blocks(int64_t n) { return (n + 31) / 32; }
 hipError_t launch_quantize_mxfp8(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ld, uint8_t* codes,
                                  uint8_t* scales, hipStream_t s);
+// kept16: values that were kept from dtype's own (what E4M3 rounds beyond fp16 is fp16's largest)
 hipError_t launch_dequantize_mxfp8(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, void* x,
-                                   int64_t ld, int dtype, hipStream_t s);
+                                   int64_t ld, int dtype, bool kept16, hipStream_t s);
 // gate|up rows to h (rows of fp >= f columns, those behind f zeros) and what is kept,
 // where the product's epilogue does not do it
 hipError_t launch_gated_keep(const float* gu, int64_t P, int64_t R, int64_t f, int64_t fp, const int32_t* offsets, int E,

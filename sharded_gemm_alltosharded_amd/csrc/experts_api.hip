@@ -788,7 +788,7 @@ sg_status sg_dequantize_mxfp8(const uint8_t* codes, const uint8_t* scales, int64
     if (sg_status st = check_mx8(dtype, rows, cols)) return st;
     if (rows == 0 || cols == 0) return SG_OK;
     if (!x || !codes || !scales) return fail(SG_ERR_INVALID_ARG, "x, codes and scales must not be NULL");
-    return launched(sg::launch_dequantize_mxfp8(codes, scales, rows, cols, x, cols, dtype, (hipStream_t)stream),
+    return launched(sg::launch_dequantize_mxfp8(codes, scales, rows, cols, x, cols, dtype, false, (hipStream_t)stream),
                     "sg_dequantize_mxfp8");
 }
 
@@ -987,7 +987,7 @@ sg_status sg_gated_mlp_backward(const sg_experts* g, const sg_experts* d, const 
         st = gated_backward(d, dy, gu_codes, gu_scales, offsets, R, dgu, dw_down ? h : nullptr, fp, s);
         if (!st && dx) st = product(column_dx(g, dgu, fp, offsets, R, dx, dx_dtype), rest, "sg_gated_mlp_backward dx", s);
         if (!st && dw_gate_up)
-            st = launched(sg::launch_dequantize_mxfp8(x_codes, x_scales, T, g->l.in, x, ldx, g->dtype, s),
+            st = launched(sg::launch_dequantize_mxfp8(x_codes, x_scales, T, g->l.in, x, ldx, g->dtype, true, s),
                           "sg_gated_mlp_backward");
     }
     if (!st && dw_gate_up) {

@@ -76,14 +76,19 @@ __global__ __launch_bounds__(256) void quantize8_kernel(const void* x, int64_t n
     if ((i & 3) == 0) scales[i >> 2] = mx8_scale(m);
 }
 
+// kept16: the values were kept from DT's own.  E4M3 rounds fp16's largest ones, from 63488
+// on, to 65536; they come back as 65504, half a step of fp16 away, not as infinities.
 template <int DT, bool WHOLE>
 __global__ __launch_bounds__(256) void dequantize8_kernel(const uint8_t* codes, const uint8_t* scales, int64_t n,
-                                                          int64_t blocks, int64_t cols, int64_t ld, void* x) {
+                                                          int64_t blocks, int64_t cols, int64_t ld, void* x, bool kept16) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= n) return;
     const Place p = place(i, blocks, cols);
     float v[8];
     get_codes<WHOLE>(codes, p.row * cols + p.c, scales[i >> 2], p.left, v);
+    if (DT == SG_F16 && kept16)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = fabsf(v[e]) == 65536.f ? copysignf(65504.f, v[e]) : v[e];
     store_cols<DT>(x, p.row * ld + p.c, v, WHOLE ? 8 : p.left);
 }
 
@@ -144,11 +149,11 @@ hipError_t launch_quantize_mxfp8(const void* x, int dtype, int64_t rows, int64_t
 }
 
 hipError_t launch_dequantize_mxfp8(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, void* x,
-                                   int64_t ld, int dtype, hipStream_t s) {
+                                   int64_t ld, int dtype, bool kept16, hipStream_t s) {
     const int64_t blocks = mx8_blocks(cols), n = rows * blocks * 4;
     by_type(dtype, cols % 32 == 0, [&](auto dt, auto whole) {
         launch(dequantize8_kernel<decltype(dt)::value, decltype(whole)::value>, grid_of(n), dim3(256), 0, s, codes,
-               scales, n, blocks, cols, ld, x);
+               scales, n, blocks, cols, ld, x, kept16);
     });
     return hipGetLastError();
 }

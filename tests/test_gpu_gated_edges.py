@@ -1,0 +1,64 @@
+"""The gated block on activations kept in 8 bits at the ends of its types' ranges."""
+import math
+
+import pytest
+import torch
+
+import moe_ref as ref
+import mx8_ref as mx
+import sharded_gemm_alltosharded_amd as sg
+
+pytestmark = pytest.mark.gpu
+
+BF, HF, F32 = torch.bfloat16, torch.float16, torch.float32
+
+
+@pytest.fixture(autouse=True, scope="module")
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    torch.cuda.set_device(0)
+    sg.lib()
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def normal(g, shape, dtype=F32, scale=1.0):
+    return (torch.randn(shape, generator=g) * scale).to(dtype)
+
+
+@pytest.mark.parametrize("D", [64, 77])
+def test_weight_gradients_of_fp16s_largest_inputs(D):
+    """E4M3 rounds fp16's values from 63488 on to 65536, which fp16 does not hold: the
+    weight gradient's operand is 65504, half a step of fp16 (2^-11) away."""
+    g = gen(D)
+    T, F = 40, 48
+    gu = sg.shard_experts(normal(g, (1, 2 * F, D), HF, 1e-4).cuda(), "all-to-sharded", segments=2)
+    dn = sg.shard_experts(normal(g, (1, D, F), HF, 0.1).cuda(), "sharded-to-all")
+    x = normal(g, (T, D), HF)
+    x[3, 5], x[4, 6], x[5, D - 1], x[6, 0], x[7, 1] = 65504, -65504, 63488, -64000, 63456
+    dy = normal(g, (T, D), HF, 0.1).cuda()
+    _, kept = sg.gated_mlp(gu, dn, x.cuda())
+    x8 = mx.decode(*(v.cpu() for v in kept[:2]))
+    assert x8.abs().max() == 65536 and (x8.abs() == 65536).sum() == 4 and x8[7, 1] == 61440
+    dgu, _ = sg.experts_gated_backward(dn, dy, kept.gu_codes, kept.gu_scales)
+    d = dgu[0].double().cpu()
+    assert torch.isfinite(d).all()
+    want = d.T @ x8
+    # The matrix instruction aligns products by their operands' exponents, and a subnormal's
+    # is the smallest normal's, 2^-14: fp32's steps are those of products that large.  (Row 7,
+    # gate row 29 of 64 columns: -3 2^-24 times 61440, aligned as 2^-14 2^15 = 2, whose half
+    # step is 2^-23, beside terms of 0.017: off by 2.5e-7, two of them.)
+    floor = torch.where(d == 0, 0.0, d.abs().clamp(min=2.0 ** -14)).double()
+    bound = ref.sum_bound(floor.T @ x8.abs(), T) + 2.0 ** -11 * d.abs().T @ torch.where(x8.abs() == 65536, 65536.0, 0.0).double()
+    dx, dw, _ = sg.gated_mlp_backward(gu, dn, kept, dy)
+    ref.close(dw[0, 0], want, bound, "dw gate_up")
+    assert torch.isfinite(dx).all()
+    # what an infinite input kept is NaN, and spoils its own block's columns alone
+    x[9, 0] = math.inf
+    _, kept = sg.gated_mlp(gu, dn, x.cuda())
+    kept = kept._replace(gu_codes=torch.zeros_like(kept.gu_codes) + 40, gu_scales=torch.full_like(kept.gu_scales, 127))
+    _, dw, _ = sg.gated_mlp_backward(gu, dn, kept, dy, need_dx=False)
+    assert torch.isnan(dw[0, 0, :, :32]).all() and torch.isfinite(dw[0, 0, :, 32:]).all()

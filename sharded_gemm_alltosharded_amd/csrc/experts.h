@@ -293,9 +293,10 @@ __device__ __forceinline__ void mx8_values(uint32_t w, int s, float& a, float& b
 // dg = dh u s (1 + g (1 - s)), du = dh g s.  s from e^-|g|, which cannot overflow, on
 // the hardware's exponential: the square of 2^(t / 2), t = -|g| log2 e rounded, so that
 // it is not flushed before it leaves fp32's subnormals, times 1 + r ln 2 for the r that
-// t's rounding left.  Off by 2^-19 of itself at most (grouped_tile.h, swiglu4).
+// t's rounding left.  Off by 2^-19 of itself at most (grouped_tile.h, swiglu4).  e^-|g| is
+// 0 long before |g| = 256; beyond 2^127.5 t would be infinite, and r not a number.
 __device__ __forceinline__ void swiglu_grad(float g, float u, float dh, float& dg, float& du, float& h) {
-    const float z = fabsf(g), t = -1.44269504f * z, half = __builtin_amdgcn_exp2f(0.5f * t), e2 = half * half;
+    const float z = fminf(fabsf(g), 256.f), t = -1.44269504f * z, half = __builtin_amdgcn_exp2f(0.5f * t), e2 = half * half;
     const float e = fmaf(e2 * fmaf(-1.44269504f, z, -t), 0.693147181f, e2);
     const float s = (g < 0.f ? e : 1.0f) * __builtin_amdgcn_rcpf(1.0f + e), a = g * s;
     dg = dh * u * s * (1.0f + g * (1.0f - s));

@@ -62,3 +62,26 @@ def test_weight_gradients_of_fp16s_largest_inputs(D):
     kept = kept._replace(gu_codes=torch.zeros_like(kept.gu_codes) + 40, gu_scales=torch.full_like(kept.gu_scales, 127))
     _, dw, _ = sg.gated_mlp_backward(gu, dn, kept, dy, need_dx=False)
     assert torch.isnan(dw[0, 0, :, :32]).all() and torch.isfinite(dw[0, 0, :, 32:]).all()
+
+
+@pytest.mark.parametrize("P,f", [(1, 64), (2, 16), (3, 5)])
+def test_gradients_of_the_largest_gates(P, f):
+    """Kept gates up to the largest, 448 2^119: the sigmoid is 1 or 0 there, and finite all it is multiplied by."""
+    g = gen(f)
+    T, D = 24, 32
+    w = normal(g, (1, D, P * f), BF, 0.1)
+    dn = sg.shard_experts(w.cuda(), "sharded-to-all", P=P)
+    gu = torch.full((P, T, 2, f), 0.75, dtype=torch.float64)
+    gates = [448 * 2.0 ** k for k in (-1, 0, 20, 100, 117, 118, 119)] + [a * 2.0 ** 119 for a in (352, 384, 416)]
+    for i, v in enumerate(gates):
+        gu[:, i, 0], gu[:, i + len(gates), 0] = v, -v
+    codes, scales = mx.encode(gu)
+    gg, uu = mx.decode(codes, scales).unbind(2)
+    assert torch.equal(gg, gu[:, :, 0])
+    dy = normal(g, (T, D), BF, 0.01)
+    dgu, h = sg.experts_gated_backward(dn, dy.cuda(), codes.cuda(), scales.cuda())
+    dh, mag = ((a @ b).view(T, P, f).transpose(0, 1) for a, b in
+               ((dy.double(), w[0].double()), (dy.double().abs(), w[0].double().abs())))
+    wants, bounds = mx.gated_grad(gg, uu, dh), mx.gated_bounds(gg, uu, dh, ref.sum_bound(mag, D))
+    for v, want, bound, name in zip((dgu[..., :f], dgu[..., f:], h), wants, bounds, ("dgate", "dup", "h")):
+        ref.close(v.contiguous(), want, bound, name)

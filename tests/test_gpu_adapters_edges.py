@@ -5,6 +5,7 @@ import threading
 import pytest
 import torch
 
+import adapters_ref as aref
 import moe_ref as ref
 import sharded_gemm_alltosharded_amd as sg
 
@@ -105,3 +106,125 @@ def test_first_backward_call_captured(mode, i, o, dtype):
             want, mag = (v.view(B, P, i // P).transpose(0, 1) for v in (want, mag))
         for got, name in ((out, "captured"), (eager, "eager")):
             ref.close(got, want, ref.sum_bound(mag, o), name)
+
+
+# ---- the widest tiles ---------------------------------------------------------
+# 4100 tokens beside outputs (backward: inputs) of some 4400 columns take tiles of 256 x 256,
+# those behind the last time round 256 compute units their quarters; the last tile has four
+# rows.  T, in, out, mode, P, S, adapters, rank, type
+FORWARD = [(4100, 72, 4416, 0, 2, 3, 5, 40, BF), (4100, 64, 4413, 0, 3, 1, 200, 20, HF), (4100, 128, 4400, 1, 2, 1, 3, 12, BF),
+           (4100, 64, 4400, 1, 1, 1, 70, 100, HF), (5300, 40, 4608, 0, 1, 2, 1, 8, HF)]
+SWIGLU = [(4100, 72, 4400, 0, 2, 2, 3, 24, BF), (4100, 64, 4404, 0, 1, 2, 150, 100, HF), (4100, 64, 4416, 0, 3, 2, 900, 16, BF)]
+BACKWARD = [(4100, 4408, 96, 0, 2, 1, 3, 17, BF), (4100, 4400, 64, 0, 1, 2, 150, 40, HF), (4100, 4416, 64, 1, 2, 1, 4, 48, HF),
+            (4100, 4480, 72, 1, 2, 2, 90, 16, BF), (4100, 4401, 64, 0, 1, 1, 2, 9, BF)]
+
+
+def wide_case(T, i, o, mode, P, S, n, r, dtype):
+    g = gen(T + i + o + r)
+    w = normal(g, (o, i), dtype, 1 / math.sqrt(i))
+    ad = sg.Adapters(normal(g, (n, r, i), dtype, 1 / math.sqrt(i)).cuda(), normal(g, (n, o, r), dtype, 1 / math.sqrt(r)).cuda(),
+                     (torch.rand(n, generator=g) + 0.5).cuda())
+    which = torch.randint(-1, n, (T,), generator=g, dtype=torch.int32)
+    x, dy = normal(g, (T, i), dtype), normal(g, (T, o), dtype)
+    # tokens at the borders of tiles and quarters in the plan's order, and others
+    _, rows = aref.plan(which, n)
+    at = [m for k in range(0, T, 128) for m in (k - 1, k, k + 15, k + 16) if 0 <= m < T] + [T - 1]
+    pick = torch.tensor(sorted({rows[m] for m in at} | set(torch.randint(0, T, (60,), generator=g).tolist())))
+    order = ref.shard_rows(o if mode == 0 else i, S, P)
+    shard = lambda v: torch.stack([v[:, q] for q in order])  # noqa: E731
+    return w, ad, which, x, dy, pick, shard, sg.adapter_plan(which.cuda(), n)
+
+
+def adapted_rows(w, ad, which, x, pick, r, dtype):
+    """x W^T and the adapters' part for the picked tokens, and the sum's bound."""
+    v = x[pick].double()
+    d, e = aref.delta(v, which[pick], ad.A.cpu(), ad.B.cpu(), ad.scale.cpu(), dtype)
+    base, eb = v @ w.double().T, ref.sum_bound(v.abs() @ w.double().abs().T, v.shape[1])
+    return base + d, e + eb + (2 * r + 4) * 2.0 ** -24 * (base.abs() + d.abs() + e)
+
+
+@pytest.mark.parametrize("case", FORWARD)
+def test_wide_tiles_forward(case):
+    T, i, o, mode, P, S, n, r, dtype = case
+    w, ad, which, x, _, pick, shard, plan = wide_case(*case)
+    layer = sg.shard_linear(w.cuda(), mode, segments=S, P=P)
+    want, bound = adapted_rows(w, ad, which, x, pick, r, dtype)
+    if mode == 0:
+        want, bound = shard(want), shard(bound)
+    for out in (dtype, F32):
+        if mode == 0:
+            y = sg.adapted_all_to_sharded(layer, x.cuda(), ad, plan, out_dtype=out)
+            z = sg.adapted_all_to_sharded(layer, x.cuda(), ad, plan, out_dtype=out, gather=True)
+            assert torch.equal(z.view(T, P, -1).transpose(0, 1), y)
+            ref.close(y[:, pick.cuda()], want, bound, f"y {out}")
+        else:
+            y = sg.adapted_sharded_to_all(layer, shard(x).cuda(), ad, plan, out_dtype=out)
+            ref.close(y[pick.cuda()], want, bound, f"y {out}")
+        assert torch.isfinite(y).all()
+
+
+@pytest.mark.parametrize("case", SWIGLU)
+def test_wide_tiles_swiglu(case):
+    T, i, o, mode, P, S, n, r, dtype = case
+    w, ad, which, x, _, pick, shard, plan = wide_case(*case)
+    layer = sg.shard_linear(w.cuda(), mode, segments=S, P=P)
+    z, e = adapted_rows(w, ad, which, x, pick, r, dtype)
+    (a, b), (ea, eb) = shard(z).chunk(2, -1), shard(e).chunk(2, -1)
+    want = ref.silu(a) * b
+    bound = 1.1 * (b.abs() + eb) * ea + (ref.silu(a).abs() + 1.1 * ea) * eb + 16 * 2.0 ** -24 * want.abs()
+    for out in (dtype, F32):
+        h = sg.adapted_all_to_sharded(layer, x.cuda(), ad, plan, swiglu=True, out_dtype=out)
+        ref.close(h[:, pick.cuda()], want, bound, f"h {out}")
+        assert torch.isfinite(h).all()
+
+
+@pytest.mark.parametrize("case", BACKWARD)
+def test_wide_tiles_backward(case):
+    T, i, o, mode, P, S, n, r, dtype = case
+    w, ad, which, x, dy, pick, shard, plan = wide_case(*case)
+    layer = sg.shard_linear(w.cuda(), mode, segments=S, P=P)
+    v = dy[pick].double()
+    (dx, ex), _, _ = aref.gradients(x[pick].double(), v, which[pick], ad.A.cpu(), ad.B.cpu(), ad.scale.cpu(), dtype)
+    base, eb = v @ w.double(), ref.sum_bound(v.abs() @ w.double().abs(), o)
+    want, bound = base + dx, ex + eb + (2 * r + 4) * 2.0 ** -24 * (base.abs() + dx.abs() + ex)
+    for out in (dtype, F32):
+        if mode == 0:
+            got, _, _ = sg.adapted_all_to_sharded_backward(layer, None, shard(dy).cuda(), ad, plan, need_d=False, dx_dtype=out)
+            ref.close(got[pick.cuda()], want, bound, f"dx {out}")
+        else:
+            got, _, _ = sg.adapted_sharded_to_all_backward(layer, None, dy.cuda(), ad, plan, need_d=False, dx_dtype=out)
+            ref.close(got[:, pick.cuda()], shard(want), shard(bound), f"dx {out}")
+        assert torch.isfinite(got).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("mode,i,o,P,S,swiglu", [(0, 576, 4416, 2, 1, False), (0, 448, 4416, 1, 2, True), (1, 640, 4400, 2, 1, False)])
+def test_wide_tiles_of_odd_4_bit_layers(mode, i, o, P, S, swiglu, dtype):
+    """Weights in two halves: the inputs twice through the tiles."""
+    T, n, r = 4100, 6, 24
+    _, ad, which, x, _, pick, shard, plan = wide_case(T, i, o, mode, P, S, n, r, dtype)
+    g = gen(i + o)
+    words = torch.randint(-2 ** 31, 2 ** 31, (o, i // 8), generator=g, dtype=torch.int64).to(torch.int32)
+    sc = ((0.5 + torch.rand((o, i // 64), generator=g)) / (8 * math.sqrt(i))).half()
+    qb = (-7.5 * sc).half()
+    layer = sg.shard_quantized_linear(words.cuda(), sc.view(torch.int16).cuda(), qb.view(torch.int16).cuda(), i, mode,
+                                      segments=S, P=P, act_dtype=dtype)
+    q = ((words.long() & 0xffffffff)[..., None] >> (4 * torch.arange(8)) & 15).flatten(1).double()
+    sq, b = sc.double().repeat_interleave(64, 1) * q, qb.double().repeat_interleave(64, 1)
+    z, e = adapted_rows(sq + b, ad, which, x, pick, r, dtype)
+    # the weights in two halves, and twice as many products
+    e = e + (aref.SPLIT[dtype] + (i + 4) * 2.0 ** -24) * (x[pick].double().abs() @ (sq.abs() + b.abs()).T)
+    if swiglu:
+        (a, c), (ea, ec) = shard(z).chunk(2, -1), shard(e).chunk(2, -1)
+        z = ref.silu(a) * c
+        e = 1.1 * (c.abs() + ec) * ea + (ref.silu(a).abs() + 1.1 * ea) * ec + 16 * 2.0 ** -24 * z.abs()
+    elif mode == 0:
+        z, e = shard(z), shard(e)
+    for out in (dtype, F32):
+        if mode == 0:
+            y = sg.adapted_all_to_sharded(layer, x.cuda(), ad, plan, swiglu=swiglu, out_dtype=out)
+            ref.close(y[:, pick.cuda()], z, e, f"y {out}")
+        else:
+            y = sg.adapted_sharded_to_all(layer, shard(x).cuda(), ad, plan, out_dtype=out)
+            ref.close(y[pick.cuda()], z, e, f"y {out}")
+        assert torch.isfinite(y).all()

@@ -220,11 +220,20 @@ hipError_t dw_type(const GroupedDw& p, hipStream_t s) {
     const bool al = (uintptr_t)p.G % 16 == 0 && (uintptr_t)p.X % 16 == 0 && p.ldg % 8 == 0 && p.ldx % 8 == 0 &&
                     p.g_rank % 8 == 0 && p.x_rank % 8 == 0 && p.O % 8 == 0 && p.xw % 8 == 0;
     if (!al) return dw_launch<F16, 128, 128, 2, 4, false>(p, s);
-    // the wide tile where its tiles go round the chip several times (8 experts
-    // of 28672 x 4096: 2.30 ms, 2.72 on the narrow one; 32 of 1024 x 704 over
-    // 1500 x 4 rows, twice round: 35 us, 28 on the narrow one)
+    // The wide tile where its tiles go round the chip four times (8 experts of 28672 x
+    // 4096: 2.30 ms, 2.72 on the narrow one; 32 of 1024 x 704 over 1500 x 4 rows, twice
+    // round: 35 us, 28 on the narrow one).  Three times round, it gains over many rows of
+    // an expert and loses over few; us, wide / narrow, by those rows:
+    //                        32      128     512     1024    1536    2048    4096
+    //   64 x (1024 x 768)    45 34   59 44   96 91   158 152
+    //   8 x (2304 x 2568)    44 34   51 39   87 77   133 123 178 171 227 221 426 444
+    //   8 x (2560 x 2560)    45 39   52 45   89 86   136 138 180 183 230 238 432 470
+    //   32 x (1280 x 1536)   44 42   56 50   95 102  153 174 214 253
+    //   1 x (4096 x 14336)   43 39   50 45   89 85   139 140 184 194 233 253 417 469
+    //   8 x (2816 x 2816)    44 45   52 51   91 97   143 158 190 217 250 288 455 560
     const int64_t big = (int64_t)p.E * p.P * ((p.O + 255) / 256) * ((p.I + 255) / 256);
-    if (big >= 3 * device_cus()) return dw_launch<F16, 256, 256, 2, 4, true>(p, s);
+    if (big >= 4 * device_cus() || (big >= 3 * device_cus() && p.R >= (int64_t)2048 * p.E))
+        return dw_launch<F16, 256, 256, 2, 4, true>(p, s);
     return dw_launch<F16, 128, 128, 2, 4, true>(p, s);
 }
 

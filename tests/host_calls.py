@@ -13,7 +13,7 @@ INVALID, UNSUPPORTED, OOM = 1, 4, 6
 
 class Stub(C.Structure):
     _fields_ = [(n, C.c_int64) for n in ("launches", "mallocs", "syncs", "device", "largest", "stream_captured",
-                                         "other_capture", "ended", "live")]
+                                         "other_capture", "ended", "live", "blocks")]
 
 
 class Adapters(C.Structure):
@@ -226,6 +226,26 @@ def workspace_of_decoded_weights():
             rest = 16 * T * 16 * 4 + 32 * 64 + T * 4 + 4 * 256
             assert matrices * one <= need <= matrices * one + rest, (bits, need, one)
             adapted(layer, mode, T=T)
+
+
+def weight_gradient_tiles():
+    """Tiles of 256 x 256 from four times round the chip's 256 compute units on, and from
+    three where an expert has many rows; else of 128 x 128."""
+    for E, O, I, times in ((64, 1024, 768, 3), (8, 2560, 2560, 3.125), (1, 4096, 14336, 3.5), (16, 1792, 1792, 3.0625),
+                           (16, 2048, 2048, 4), (8, 2048, 2048, 2)):
+        layer = experts(E, O, I, COLUMN, 1, 1)
+
+        def blocks(n):  # of an expert's tiles, in eights
+            return E * ((-(-O // n) * -(-I // n) + 7) // 8 * 8)
+
+        for m in (1, 32, 512, 2047, 2048, 4096):
+            R = m * E
+            if R * max(O, I) * 2 >= 0xffff0000:
+                continue
+            ok(call("sg_experts_all_to_sharded_backward", layer, PTR, R, I, PTR, PTR, None, 1, R, None, BF16, PTR, BF16,
+                    None))
+            wide = times >= 4 or (times >= 3 and m >= 2048)
+            assert S.blocks == blocks(256 if wide else 128), (E, O, I, m, S.blocks)
 
 
 if __name__ == "__main__":

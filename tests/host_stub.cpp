@@ -35,7 +35,8 @@ struct {
     int64_t other_capture;   // another thread's capture is open ...
     int64_t ended;           // ... until a call that it does not allow
     int64_t live;            // allocations not freed
-} stub = {0, 0, 0, 0, INT64_MAX, 0, 0, 0, 0};
+    int64_t blocks;          // workgroups of the last launch
+} stub = {0, 0, 0, 0, INT64_MAX, 0, 0, 0, 0, 0};
 
 // what no other thread may do while one captures, but for threads in relaxed mode
 static bool forbidden() {
@@ -130,6 +131,7 @@ hipError_t hipLaunchKernel(const void*, dim3 grid, dim3 block, void**, size_t, h
     if (!grid.x || !grid.y || !grid.z || grid.y > 65535 || grid.z > 65535 || (uint64_t)grid.x * block.x >= (uint64_t)1 << 32)
         return told(hipErrorInvalidConfiguration);
     ++stub.launches;
+    stub.blocks = (int64_t)grid.x * grid.y * grid.z;
     return hipSuccess;
 }
 

@@ -58,3 +58,7 @@ def test_projections_that_cannot_be_launched(stub):
 
 def test_workspace_of_decoded_weights(stub):
     calls(stub, "workspace_of_decoded_weights")
+
+
+def test_weight_gradient_tiles(stub):
+    calls(stub, "weight_gradient_tiles")

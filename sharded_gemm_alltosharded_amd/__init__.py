@@ -187,10 +187,25 @@ def time_next_launch(start: "torch.cuda.Event", stop: "torch.cuda.Event"):
     _check(lib().sg_time_next_launch(C.c_void_p(start.cuda_event), C.c_void_p(stop.cuda_event)))
 
 
+_freed_layers: list = []
+
+
+def _release(given_up: list, free):
+    """Release the layers given up.  That waits for the device; those given up while
+    this thread captures, whose graph may hold calls on them, stay until it ends."""
+    while given_up and not torch.cuda.is_current_stream_capturing():
+        try:
+            h = given_up.pop()
+        except IndexError:  # another thread took the last one since
+            return
+        free(h)
+
+
 class Layer:
     """A sharded layer owned by the library (sg_layer*)."""
 
     def __init__(self, handle: C.c_void_p, device: torch.device):
+        _release(_freed_layers, lib().sg_layer_free)
         self._h = handle
         self.device = device
         o, i, m, s, p, d, q = (C.c_int64(), C.c_int64(), C.c_int(), C.c_int(), C.c_int(), C.c_int(), C.c_int())
@@ -207,9 +222,10 @@ class Layer:
         return self._h
 
     def free(self):
-        if self._h is not None and _lib is not None:
-            _lib.sg_layer_free(self._h)
-        self._h = None
+        h, self._h = self._h, None
+        if h is not None and _lib is not None:
+            _freed_layers.append(h)
+            _release(_freed_layers, _lib.sg_layer_free)
 
     def __del__(self):
         try:
@@ -564,14 +580,7 @@ _freed: list = []
 
 
 def _free_experts():
-    """Release the layers given up.  That waits for the device; those given up while
-    this thread captures, whose graph may hold calls on them, stay until it ends."""
-    while _freed and not torch.cuda.is_current_stream_capturing():
-        try:
-            h = _freed.pop()
-        except IndexError:  # another thread took the last one since
-            return
-        _lib.sg_experts_free(h)
+    _release(_freed, _lib.sg_experts_free)
 
 
 class Experts:

@@ -112,8 +112,12 @@ sg_status copy_shards(void* dst, const void* src, int64_t rows, int64_t cols, si
 
 void free_layer(sg_layer* l) {
     if (!l) return;
-    // kernels queued on any stream may still read the shards
-    (void)hipDeviceSynchronize();
+    int d = l->device;
+    (void)hipGetDevice(&d);
+    if (d != l->device) (void)hipSetDevice(l->device);
+    // Kernels queued on any stream may still read the shards: hipFree waits for the device.
+    // (hipDeviceSynchronize would end a capture that another thread has open.)
+    sg::RelaxedCapture relaxed;
     if (l->w) (void)hipFree(l->w);
     if (l->qs) (void)hipFree(l->qs);
     if (l->qb) (void)hipFree(l->qb);
@@ -121,6 +125,7 @@ void free_layer(sg_layer* l) {
     if (l->bias) (void)hipFree(l->bias);
     if (l->wt) (void)hipFree(l->wt);
     if (l->wx) (void)hipFree(l->wx);
+    if (d != l->device) (void)hipSetDevice(d);
     delete l;
 }
 

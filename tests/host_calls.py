@@ -228,6 +228,25 @@ def workspace_of_decoded_weights():
             adapted(layer, mode, T=T)
 
 
+def layers_given_up_beside_a_capture():
+    """A layer's release, its copies' too, does not end a capture of another thread."""
+    live = S.live
+    for make in (lambda: linear(48, 96, COLUMN, P=2, bias=PTR), lambda: linear(48, 96, COLUMN, P=2),
+                 lambda: quantized(64, 256, ROW, 1, 4), lambda: quantized(64, 256, ROW, 1, 8)):
+        layer = make()
+        if S.live == live + 1:  # the dense one without a bias: its copies
+            adapted(layer, COLUMN)
+        S.other_capture = 1
+        call("sg_layer_free", layer)
+        S.other_capture = 0
+        assert S.ended == 0 and S.live == live
+    layer = linear(48, 96, COLUMN)
+    S.device = 1
+    call("sg_layer_free", layer)
+    assert S.device == 1 and S.live == live
+    call("sg_layer_free", None)
+
+
 def weight_gradient_tiles():
     """Tiles of 256 x 256 from four times round the chip's 256 compute units on, and from
     three where an expert has many rows; else of 128 x 128."""

@@ -84,6 +84,10 @@ hipError_t hipStreamSynchronize(hipStream_t) {
 }
 hipError_t hipDeviceSynchronize() {
     ++stub.syncs;
+    if (stub.stream_captured || stub.other_capture) {  // in every mode
+        stub.ended = 1;
+        return told(hipErrorStreamCaptureUnsupported);
+    }
     return hipSuccess;
 }
 hipError_t hipStreamIsCapturing(hipStream_t, hipStreamCaptureStatus* s) {

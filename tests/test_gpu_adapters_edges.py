@@ -108,6 +108,83 @@ def test_first_backward_call_captured(mode, i, o, dtype):
             ref.close(got, want, ref.sum_bound(mag, o), name)
 
 
+# ---- layers given up ----------------------------------------------------------
+
+def test_a_layer_given_up_in_a_capture_outlives_it():
+    g = gen(12)
+    w, x = normal(g, (64, 128), BF).cuda(), normal(g, (5, 128), BF).cuda()
+    keep, gone = (sg.shard_linear(w, "all-to-sharded") for _ in range(2))
+    want = sg.all_to_sharded(keep, x)
+    graph, out = torch.cuda.CUDAGraph(), torch.empty_like(want)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        del gone
+        sg.all_to_sharded(keep, x, out=out)
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    assert len(sg._freed_layers) == 1
+    again = sg.shard_linear(w, "all-to-sharded")
+    assert not sg._freed_layers and torch.equal(sg.all_to_sharded(again, x), want)
+
+
+def test_a_layer_given_up_while_another_thread_captures():
+    g = gen(15)
+    w, x = normal(g, (80, 96), BF).cuda(), normal(g, (20, 96), BF).cuda()
+    keep, gone = (sg.shard_linear(w, "all-to-sharded") for _ in range(2))
+    codes, scales = sg.quantize_mxfp8(w)
+    mx8 = sg.shard_mxfp8_linear(codes, scales, "all-to-sharded")
+    ad = sg.Adapters(normal(g, (1, 8, 96), BF).cuda(), normal(g, (1, 80, 8), BF).cuda())
+    plan = sg.adapter_plan(torch.zeros(20, dtype=torch.int32, device="cuda"), 1)
+    sg.adapted_all_to_sharded(gone, x, ad, plan)  # (it then holds a copy, too)
+    want = sg.all_to_sharded(keep, x)
+    graph, out = torch.cuda.CUDAGraph(), torch.empty_like(want)
+    torch.cuda.synchronize()
+    capturing, errors = threading.Event(), []
+
+    def drop():
+        try:
+            torch.cuda.set_device(0)
+            if capturing.wait(60):
+                gone.free()
+                mx8.free()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    other = threading.Thread(target=drop)
+    other.start()
+    with torch.cuda.graph(graph):
+        capturing.set()
+        other.join()
+        sg.all_to_sharded(keep, x, out=out)
+    assert not errors and not sg._freed_layers
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+
+
+def test_giving_up_a_layer_waits_for_the_device():
+    g = gen(16)
+    layers = [sg.shard_linear(normal(g, (1024, 1024), BF).cuda(), "all-to-sharded") for _ in range(2)]
+    x = normal(g, (4096, 1024), BF).cuda()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    out = torch.empty((1, 4096, 1024), dtype=BF, device="cuda")
+    with torch.cuda.stream(side):
+        for _ in range(1000):
+            sg.all_to_sharded(layers[0], x, out=out)
+        done = torch.cuda.Event()
+        done.record()
+    busy = not done.query()
+    layers[1].free()
+    assert busy and done.query()
+    layers[0].free()
+
+
 # ---- the widest tiles ---------------------------------------------------------
 # 4100 tokens beside outputs (backward: inputs) of some 4400 columns take tiles of 256 x 256,
 # those behind the last time round 256 compute units their quarters; the last tile has four

@@ -62,3 +62,7 @@ def test_workspace_of_decoded_weights(stub):
 
 def test_weight_gradient_tiles(stub):
     calls(stub, "weight_gradient_tiles")
+
+
+def test_layers_given_up_beside_a_capture(stub):
+    calls(stub, "layers_given_up_beside_a_capture")

@@ -108,9 +108,9 @@ __global__ __launch_bounds__(1024) void adapter_plan_kernel(const int32_t* which
 // U[slab][m][j] = scale_a sum over the slab's columns of X[t(m)][k] M[j][k].  Bound by
 // reading X (many rows of an adapter) or M (few).  Columns go in steps of 32, one MFMA;
 // slabs (blockIdx.y) and the NW waves split them, a wave's steps adjacent.  TR: M is
-// (width, rank): a step's 32 rows pass through LDS and are read transposed.  Up to sixteen
-// slabs, for a compute unit takes in some 75 GB/s only: 4096 rows of 28672 (235 MB)
-// 64 us, with eight 75; of 4096 columns 18 us; sixteen tokens of 4096 4.8 us.
+// (width, rank): a step's 32 rows pass through LDS and are read transposed.  4096 rows of 28672
+// (235 MB) in sixteen slabs 64 us, in eight 75; of 4096 columns 18 us; sixteen tokens of
+// 4096 4.8 us.
 template <bool F16, bool TR, int NR, int MB, bool AL>
 __global__ __launch_bounds__(256) void shrink_kernel(LowRank p) {
     constexpr int NW = 4, U = NR + MB <= 6 ? 4 : 2;  // waves; steps whose loads are out at once
@@ -275,8 +275,8 @@ __global__ __launch_bounds__(256) void finish_kernel(LowRank p, u32x4* operands,
 // ---- quantized weights for the tiles ----------------------------------------
 // 4-bit: w = scale q + bias in fp32, split in hi + lo (scale and bias are multiples of
 // fp16's smallest step, 2^-24, so that fp16's two halves lose nothing of small weights
-// either).  MX FP8: w = 2^s code, exact in bf16 alone.  A wave writes a 16-row block's
-// step of 32 inputs, a lane its eight.
+// either).  MX FP8: w = 2^s code, exact in bf16 alone, from its smallest value, 2^-133, on.
+// A wave writes a 16-row block's step of 32 inputs, a lane its eight.
 template <bool F16, bool MX>
 __global__ __launch_bounds__(256) void code_tiles_kernel(LayerCodes q, int64_t frags, int64_t blocks, int64_t steps,
                                                        int64_t rows, int64_t part, int64_t cols, u32x4* hi, u32x4* lo) {
@@ -473,9 +473,9 @@ hipError_t launch_adapter_plan(const int32_t* which, int64_t T, int n, int32_t* 
 }
 
 // As many slabs as give every compute unit four workgroups, of four steps a wave at
-// least: a compute unit takes about 75 GB/s, so few of them are slow whatever their
-// waves (16 tokens of 16 adapters, 4096 inputs: 5 us, 9 in one slab of sixteen waves).
-// At most sixteen: somebody adds them up.
+// least.  With few tokens that is what counts: a compute unit takes about 75 GB/s, so few
+// of them are slow whatever their waves (16 tokens of 16 adapters, 4096 inputs: 5 us, 9 in
+// one slab of sixteen waves).  At most sixteen: somebody adds them up.
 int shrink_slabs(const Plan& p, int64_t width, int rank) {
     const int64_t blocks = (int64_t)p.ntiles * ((rank + 63) / 64), want = (4 * device_cus() + blocks - 1) / blocks;
     const int64_t most = width / 512 < 16 ? width / 512 : 16;

@@ -20,8 +20,9 @@ hipError_t launch_adapted(const Grouped& p, const Adapted& d, hipStream_t s) {
 }
 
 // From nine rows on (up to eight stream the weights faster), where tiles of 64 x 128
-// give half of the compute units one: fewer are split over their inputs by the layer's
-// own call.
+// give half of the compute units one.  Fewer are split over their inputs, in the plain
+// grouped product (adapters_api.hip, split_product) or, of a sharded-to-all layer on
+// several ranks, in the layer's own call.
 bool adapted_fills(const Grouped& p) {
     return p.R > 8 && (p.swiglu ? tiles_of<true, 64>(p) : tiles_of<false, 64>(p)) * 2 > device_cus();
 }

@@ -930,7 +930,9 @@ sg_status sg_gated_mlp(const sg_experts* g, const sg_experts* d, const void* x, 
     const int64_t ldh = h_stride(g);
     if (T) st = launched(sg::launch_quantize_mxfp8(x, g->dtype, T, g->l.in, ldx, x_codes, x_scales, s), "sg_gated_mlp");
     if (st || R == 0) return st;
-    // h in the layers' 16 bits, as in sg_moe_mlp
+    // h is rounded to the layers' 16 bits, as in sg_moe_mlp and for its reason: it is the
+    // down product's operand, whose two halves would cost a second pass (sqrt(2) times the
+    // error of y that h in 32 bits would leave)
     void* rest = (char*)workspace + up(R * g->l.P * ldh * 2, 256);
     st = gated(g, x, T, ldx, offsets, rows, k, R, workspace, ldh, gu_codes, gu_scales, rest, s);
     if (!st) st = product(row(d, workspace, nullptr, ldh, offsets, R, y, y_dtype), rest, "sg_gated_mlp down", s);
@@ -980,9 +982,10 @@ sg_status sg_gated_mlp_backward(const sg_experts* g, const sg_experts* d, const 
     char* h = dgu + up(2 * n, 256);
     char* x = h + up(n, 256);
     char* rest = x + up(T * ldx * 2, 256);
-    // dgu is stored in the layers' 16 bits, once, the operand of both products behind it
-    // (a matrix instruction multiplies values of one type).  Rows of it, of h and of x
-    // begin on 16 bytes whatever f and in are.
+    // dgu is stored in the layers' 16 bits, once, the operand of both products behind it,
+    // and h again (a matrix instruction multiplies values of one type; two halves would cost
+    // each product a second pass): sqrt(2) times the error of dx and dW.  Rows of it, of h
+    // and of x begin on 16 bytes whatever f and in are.
     if (R > 0) {
         st = gated_backward(d, dy, gu_codes, gu_scales, offsets, R, dgu, dw_down ? h : nullptr, fp, s);
         if (!st && dx) st = product(column_dx(g, dgu, fp, offsets, R, dx, dx_dtype), rest, "sg_gated_mlp_backward dx", s);

@@ -305,3 +305,64 @@ def test_wide_tiles_of_odd_4_bit_layers(mode, i, o, P, S, swiglu, dtype):
             y = sg.adapted_sharded_to_all(layer, shard(x).cuda(), ad, plan, out_dtype=out)
             ref.close(y[pick.cuda()], z, e, f"y {out}")
         assert torch.isfinite(y).all()
+
+
+# ---- arguments of any alignment, gathered SwiGLU ------------------------------
+
+def shifted(t, by=1):
+    """The same values, packed, `by` elements behind a 16-byte border."""
+    flat = torch.empty(t.numel() + 8, dtype=t.dtype, device="cuda")
+    v = flat[by:by + t.numel()].view(t.shape)
+    v.copy_(t)
+    return v
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("T,i,o,mode,P,S,n,r", [(5, 64, 96, 0, 2, 1, 3, 16), (40, 256, 192, 0, 2, 3, 3, 8), (40, 256, 96, 1, 2, 1, 2, 24),
+                                                (300, 64, 4096, 0, 2, 2, 3, 16), (300, 4096, 64, 0, 1, 1, 70, 8),
+                                                (300, 4096, 64, 1, 2, 1, 3, 16), (300, 64, 4096, 1, 1, 1, 3, 40)])
+def test_arguments_of_any_alignment(T, i, o, mode, P, S, n, r, dtype):
+    w, ad, which, x, dy, _, shard, plan = wide_case(T, i, o, mode, P, S, n, r, dtype)
+    layer = sg.shard_linear(w.cuda(), mode, segments=S, P=P)
+    every = torch.arange(T)
+    want, bound = adapted_rows(w, ad, which, x, every, r, dtype)
+    (dx, ex), (dA, eA), (dB, eB) = aref.gradients(x.double(), dy.double(), which, ad.A.cpu(), ad.B.cpu(), ad.scale.cpu(), dtype)
+    base, eb = dy.double() @ w.double(), ref.sum_bound(dy.double().abs() @ w.double().abs(), o)
+    dx, ex = base + dx, ex + eb + (2 * r + 4) * 2.0 ** -24 * (base.abs() + dx.abs() + ex)
+    if mode == 0:
+        want, bound, xs, dys = shard(want), shard(bound), x, shard(dy)
+        call, back = sg.adapted_all_to_sharded, sg.adapted_all_to_sharded_backward
+    else:
+        dx, ex, xs, dys = shard(dx), shard(ex), shard(x), dy
+        call, back = sg.adapted_sharded_to_all, sg.adapted_sharded_to_all_backward
+    odd = sg.Adapters(shifted(ad.A), shifted(ad.B, 3), shifted(ad.scale))
+    for out in (dtype, F32):
+        y = shifted(torch.zeros(want.shape, dtype=out, device="cuda"))
+        ref.close(call(layer, shifted(xs), odd, plan, out=y), want, bound, f"y {out}")
+        assert y.data_ptr() % 16
+        gx, gA, gB = back(layer, shifted(xs, 5), shifted(dys), odd, plan, dx_dtype=out, d_dtype=out)
+        ref.close(gx, dx, ex, f"dx {out}")
+        ref.close(gA, dA, eA, f"dA {out}")
+        ref.close(gB, dB, eB, f"dB {out}")
+
+
+@pytest.mark.parametrize("kind", ["dense", "bias", "q4"])
+@pytest.mark.parametrize("T,i,o,P", [(3, 64, 96, 2), (20, 128, 256, 4), (300, 64, 4128, 3)])
+def test_gathered_swiglu(T, i, o, P, kind):
+    """The gathered layout holds what the sharded one does."""
+    g = gen(T + o)
+    if kind == "q4":
+        words = torch.randint(-2 ** 31, 2 ** 31, (o, i // 8), generator=g, dtype=torch.int64).to(torch.int32)
+        sc = (torch.rand((o, i // 64), generator=g) * 0.01).half()
+        layer = sg.shard_quantized_linear(words.cuda(), sc.view(torch.int16).cuda(), (-7 * sc).half().view(torch.int16).cuda(), i,
+                                          0, segments=2, P=P, act_dtype=BF)
+    else:
+        layer = sg.shard_linear(normal(g, (o, i), BF, 0.1).cuda(), 0, segments=2, P=P,
+                                bias=normal(g, (o,), BF).cuda() if kind == "bias" else None)
+    ad = sg.Adapters(normal(g, (3, 12, i), BF, 0.1).cuda(), normal(g, (3, o, 12), BF, 0.1).cuda())
+    plan = sg.adapter_plan(torch.randint(-1, 3, (T,), generator=g, dtype=torch.int32).cuda(), 3)
+    x = normal(g, (T, i), BF).cuda()
+    for out in (BF, F32):
+        h = sg.adapted_all_to_sharded(layer, x, ad, plan, swiglu=True, out_dtype=out)
+        z = sg.adapted_all_to_sharded(layer, x, ad, plan, swiglu=True, gather=True, out_dtype=out)
+        assert torch.equal(z.view(T, P, -1).transpose(0, 1), h) and h.any() and torch.isfinite(h).all()

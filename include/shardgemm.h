@@ -584,15 +584,16 @@ size_t sg_gated_mlp_backward_workspace(const sg_experts* gate_up, const sg_exper
  * sharded-to-all, A's columns go with the layer's, x A^T summed over the ranks, and B
  * is replicated.  Sums are fp32, and the output is rounded once.
  *
- * From nine tokens on, and backward, the product of a projection without bias runs on
- * the expert layers' tiles.  A dense one whose weights are not stored for them (a
- * rank's parts no multiple of 16 rows, or its inputs none of 64) builds a copy that
- * is, of the same size, on its first such call: that allocates and synchronises.  A
- * call captured into a graph before the copy exists, or without memory for it, runs
- * the layer's own kernels instead.  The copy is held until sg_layer_free.  4-bit
- * layers that have no matrix-core kernel are turned into 16-bit weights, in two
- * halves, inside the call; fp16 ones need weights below 65504 there, and an infinite
- * input makes its token's outputs NaN where the layer's own call may give infinities.
+ * From nine tokens on, the product of a projection without bias (backward: of any
+ * dense one) runs on the expert layers' tiles.  A dense one whose weights are not
+ * stored for them (a rank's parts no multiple of 16 rows, or its inputs none of 64)
+ * builds a copy that is, of the same size, on its first such call: that allocates and
+ * synchronises.  A call captured into a graph before the copy exists, or without
+ * memory for it, runs the layer's own kernels instead.  The copy is held until
+ * sg_layer_free.  4-bit layers that have no matrix-core kernel are turned into 16-bit
+ * weights, in two halves, inside the call; fp16 ones need weights below 65504 there,
+ * and an infinite input makes its token's outputs NaN where the layer's own call may
+ * give infinities.
  * ------------------------------------------------------------------------- */
 typedef struct {
     const void* A;      /* (n, rank, in_dims) of the layer's dtype, on the device */

@@ -182,10 +182,10 @@ sg_status tile_weights(const sg_layer* l, const Geometry& g, void* at, hipStream
             d->again = p.nseg;
             p.nseg *= 2;
         }
-    } else if (sg_status st = launched(sg::layer_tiles(l, s, &v), "weight layout")) {
+    } else if (sg_status st = launched(sg::layer_tiles(l, !p.transposed, s, &v), "weight layout")) {
         return st;
     }
-    if (v.bias) return SG_OK;
+    if (!v.w) return SG_OK;
     const int64_t matrix = v.blocks * v.steps * 1024;
     p.W = (const uint8_t*)v.w;
     p.w_expert = matrix * (g.column() ? 1 : g.P) * halves(g);

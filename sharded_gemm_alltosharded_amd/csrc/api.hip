@@ -328,10 +328,10 @@ void set_weights(sg::Problem& p, const sg_layer* l) {
 std::string& sg::last_error() { return g_err; }
 int sg::layer_device(const sg_layer* l) { return l->device; }
 
-hipError_t sg::layer_tiles(const sg_layer* lc, hipStream_t st, LayerTiles* out) {
+hipError_t sg::layer_tiles(const sg_layer* lc, bool forward, hipStream_t st, LayerTiles* out) {
     sg_layer* l = const_cast<sg_layer*>(lc);  // the copy is a cache of the layer's own weights
     *out = LayerTiles{};
-    if (l->quantized || l->mx || l->dtype == SG_F32) return hipSuccess;
+    if (l->quantized || l->mx || l->dtype == SG_F32 || (forward && l->bias)) return hipSuccess;
     const bool col = l->mode == SG_ALL_TO_SHARDED;
     ExpertsLayout x{};
     x.mode = SG_ALL_TO_SHARDED;
@@ -347,8 +347,6 @@ hipError_t sg::layer_tiles(const sg_layer* lc, hipStream_t st, LayerTiles* out) 
     x.steps = x.kpad / 32;
     out->blocks = x.blocks;
     out->steps = x.steps;
-    out->bias = l->bias != nullptr;
-    if (out->bias) return hipSuccess;  // the tiles add none
     if (l->wfrag && x.f % 16 == 0 && x.kl % 64 == 0) {
         out->w = l->w;
         return hipSuccess;

@@ -169,9 +169,9 @@ struct LayerTiles {
     const void* w;  // null: no such layer, or its copy is not there and the stream is
                     // captured, or there is no memory for it
     int64_t blocks, steps;
-    int bias;
 };
-hipError_t layer_tiles(const sg_layer* l, hipStream_t s, LayerTiles* out);
+// forward: not for a layer with a bias, which the tiles do not add (dx has none)
+hipError_t layer_tiles(const sg_layer* l, bool forward, hipStream_t s, LayerTiles* out);
 // A layer without bias whose row-major codes only the generic kernel takes: 4-bit, or MX FP8
 // of bf16 activations (which hold its weights exactly) up to 32 tokens.  Codes null: any other.
 struct LayerCodes {

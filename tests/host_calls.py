@@ -228,6 +228,19 @@ def workspace_of_decoded_weights():
             adapted(layer, mode, T=T)
 
 
+def input_gradients_beside_a_bias():
+    """No bias enters dx: it takes the same kernels, and no transposed copy, as without one."""
+    for mode, P in ((COLUMN, 1), (COLUMN, 2), (ROW, 1)):
+        seen = []
+        for bias in (None, PTR):
+            layer = linear(64, 128, mode, P=P, bias=bias)
+            mallocs, launches = S.mallocs, S.launches
+            adapted_backward(layer, mode, T=16)
+            seen.append((S.mallocs - mallocs, S.launches - launches, S.blocks))
+            adapted(layer, mode, T=16)
+        assert seen[0] == seen[1] and seen[0][0] == 0, seen
+
+
 def layers_given_up_beside_a_capture():
     """A layer's release, its copies' too, does not end a capture of another thread."""
     live = S.live

@@ -366,3 +366,21 @@ def test_gathered_swiglu(T, i, o, P, kind):
         h = sg.adapted_all_to_sharded(layer, x, ad, plan, swiglu=True, out_dtype=out)
         z = sg.adapted_all_to_sharded(layer, x, ad, plan, swiglu=True, gather=True, out_dtype=out)
         assert torch.equal(z.view(T, P, -1).transpose(0, 1), h) and h.any() and torch.isfinite(h).all()
+
+
+@pytest.mark.parametrize("T,i,o,mode,P,S,n,r,dtype", [(5, 96, 64, 0, 2, 1, 2, 8, BF), (40, 72, 104, 0, 2, 2, 3, 12, HF), (300, 4100, 96, 0, 2, 1, 3, 40, BF),
+                                                      (40, 96, 64, 1, 1, 1, 2, 8, HF), (300, 2900, 48, 1, 2, 1, 3, 16, BF), (4100, 4408, 96, 0, 1, 3, 5, 8, HF)])
+def test_gradients_beside_a_bias(T, i, o, mode, P, S, n, r, dtype):
+    w, ad, which, x, dy, pick, shard, plan = wide_case(T, i, o, mode, P, S, n, r, dtype)
+    layer = sg.shard_linear(w.cuda(), mode, segments=S, P=P, bias=normal(gen(1), (o,), dtype, 100.0).cuda())
+    v = dy[pick].double()
+    (dx, ex), _, _ = aref.gradients(x[pick].double(), v, which[pick], ad.A.cpu(), ad.B.cpu(), ad.scale.cpu(), dtype)
+    base, eb = v @ w.double(), ref.sum_bound(v.abs() @ w.double().abs(), o)
+    want, bound = base + dx, ex + eb + (2 * r + 4) * 2.0 ** -24 * (base.abs() + dx.abs() + ex)
+    for out in (dtype, F32):
+        if mode == 0:
+            got, _, _ = sg.adapted_all_to_sharded_backward(layer, None, shard(dy).cuda(), ad, plan, need_d=False, dx_dtype=out)
+            ref.close(got[pick.cuda()], want, bound, f"dx {out}")
+        else:
+            got, _, _ = sg.adapted_sharded_to_all_backward(layer, None, dy.cuda(), ad, plan, need_d=False, dx_dtype=out)
+            ref.close(got[:, pick.cuda()], shard(want), shard(bound), f"dx {out}")

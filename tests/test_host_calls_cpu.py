@@ -66,3 +66,7 @@ def test_weight_gradient_tiles(stub):
 
 def test_layers_given_up_beside_a_capture(stub):
     calls(stub, "layers_given_up_beside_a_capture")
+
+
+def test_input_gradients_beside_a_bias(stub):
+    calls(stub, "input_gradients_beside_a_bias")

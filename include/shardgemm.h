@@ -337,7 +337,9 @@ sg_status sg_layer_info(const sg_layer* layer, int64_t* out_dims, int64_t* in_di
 sg_status sg_layer_copy_shard(const sg_layer* layer, int r, int what, void* dst, size_t dst_bytes,
                               void* stream);
 
-/* Release a layer and its device memory (NULL is ignored). */
+/* Release a layer and its device memory (NULL is ignored).  Waits for the device, beside
+ * whatever is being captured; a graph that holds calls on the layer must not run after it
+ * (sg_experts_free alike). */
 void sg_layer_free(sg_layer* layer);
 
 /* ---------------------------------------------------------------------------
